@@ -305,6 +305,82 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_sample(const moe_w4a16_sampler* cfg, co
                                                 float* pmax, uint8_t* accept, void* workspace,
                                                 size_t workspace_bytes, void* stream);
 
+/* ---- the layer in 16 bits, with gradients ------------------------------------
+ * The steps around the experts on rows that the caller owns, and their gradients,
+ * for making or fine-tuning a layer before its weights are quantised (model card
+ * "srswti/axe-diffusion-ksl-xe": the unquantised experts the W4A16 weights are made
+ * from).  With moe_w4a16_route in front:
+ *   route -> dispatch -> linear (gate and up) -> linear (down) -> combine_rows
+ * and backwards
+ *   combine_rows_backward -> linear_backward -> linear_backward -> dispatch_backward.
+ * Conventions as for every call above; in addition outputs must not overlap inputs
+ * unless said so. */
+
+/* Types of rows and weights. */
+#define MOE_W4A16_FP16 0
+#define MOE_W4A16_BF16 1
+#define MOE_W4A16_FP32 2
+
+/* Rows of tokens and of (token, choice) pairs.
+ *   tokens   T >= 0        experts  E, 1..256       top_k  k, 1..min(E, 8), T*k <= 2^22
+ *   hidden   d, columns of a row, a multiple of 8, 8..65536
+ *   type     MOE_W4A16_FP16, _BF16 or _FP32: type of the rows */
+typedef struct {
+  int32_t tokens, experts, top_k, hidden, type;
+} moe_w4a16_rows;
+
+/* Device workspace bytes of moe_w4a16_dispatch (0 on an invalid cfg); scratch, no state. */
+MOE_W4A16_API size_t moe_w4a16_dispatch_workspace_bytes(const moe_w4a16_rows* cfg);
+
+/* Tokens sorted by expert.  Pair p = t*k + r is token t's choice r.  An id outside
+ * 0..E-1 drops its pair (a padded token, an expert that is full); a token may choose
+ * an expert more than once.
+ *   topk_idx        int32 [T][k]  expert of each pair (any router's; moe_w4a16_route's
+ *                                 gives that call's expert_offsets and pair_list)
+ *   x               type [T][d]
+ *   expert_offsets  int32 [E+1]   written: expert e's rows are offsets[e] .. offsets[e+1]-1
+ *   pair_list       int32 [T*k]   written: the pair of each row, p ascending inside an
+ *                                 expert; -1 from offsets[E] on
+ *   pair_pos        int32 [T][k]  written: the row of each pair, -1 for a dropped one
+ *   rows            type [T*k][d] written: rows[pair_pos[p]] = x[p / k]; rows from
+ *                                 offsets[E] on are left as they were
+ * With T = 0 only expert_offsets is used (and cleared). */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_dispatch(const moe_w4a16_rows* cfg, const int32_t* topk_idx, const void* x,
+                                                  int32_t* expert_offsets, int32_t* pair_list, int32_t* pair_pos,
+                                                  void* rows, void* workspace, size_t workspace_bytes,
+                                                  void* stream);
+
+/* The gradient of dispatch: grad_x[t] = sum_r grad_rows[pair_pos[t*k+r]], in rank
+ * order in fp32, rounded once; a token without kept pairs gets zeros.
+ *   grad_rows  type [T*k][d]    grad_x  type [T][d], written */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_dispatch_backward(const moe_w4a16_rows* cfg, const int32_t* pair_pos,
+                                                           const void* grad_rows, void* grad_x, void* stream);
+
+/* Rows back to their tokens: out[t] = residual[t] + sum_r w[t][r] rows[pair_pos[t*k+r]],
+ * the sum in rank order in fp32 (fused multiply-adds from 0), then the residual, rounded
+ * once.  Dropped pairs (pair_pos outside 0..T*k-1) add nothing.
+ *   topk_w  fp32 [T][k]    rows  type [T*k][d]    residual  type [T][d] or NULL
+ *   out     type [T][d], written; may be residual itself */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_combine_rows(const moe_w4a16_rows* cfg, const int32_t* pair_pos,
+                                                      const float* topk_w, const void* rows, const void* residual,
+                                                      void* out, void* stream);
+
+/* The gradient of combine_rows (that of the residual is grad_out itself), each output
+ * NULL where it is not wanted (one at least is):
+ *   grad_rows    type [T*k][d]  rows[pair_pos[p]] gets w[p] grad_out[p / k]; other rows are
+ *                               left as they were
+ *   grad_topk_w  fp32 [T][k]    <grad_out[t], rows[pair_pos[p]]>, 0 for a dropped pair
+ *   grad_logits  fp32 [T][E]    the gradient of the router logits when topk_w is the softmax
+ *                               over the selected k (moe_w4a16_route): w_r (dw_r - sum_j w_j dw_j)
+ *                               at expert topk_idx[t][r] of a kept pair (summed where a token
+ *                               chose an expert twice), 0 elsewhere
+ *   topk_idx     int32 [T][k], read for grad_logits only (may be NULL without it) */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_combine_rows_backward(const moe_w4a16_rows* cfg, const int32_t* topk_idx,
+                                                               const int32_t* pair_pos, const float* topk_w,
+                                                               const void* rows, const void* grad_out,
+                                                               void* grad_rows, float* grad_topk_w,
+                                                               float* grad_logits, void* stream);
+
 /* ---- host-side weight helpers (no GPU needed) ---------------------------- */
 
 /* Canonical packing of uint4 codes (dg-w4a16-v1 style, model card

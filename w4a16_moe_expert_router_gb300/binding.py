@@ -27,7 +27,10 @@ EXPORTED = ("moe_w4a16_workspace_bytes", "moe_w4a16_workspace_init", "moe_w4a16_
             "moe_w4a16_gate_up", "moe_w4a16_down", "moe_w4a16_combine", "moe_w4a16_read_error", "moe_w4a16_pack", "moe_w4a16_unpack", "moe_w4a16_prepared_bytes",
             "moe_w4a16_prepare", "moe_w4a16_unprepare", "moe_w4a16_status_string", "moe_w4a16_forward_noalloc",
             "moe_w4a16_selftest_wait_timeout", "moe_w4a16_sampler_workspace_bytes", "moe_w4a16_sample",
-            "moe_w4a16_block_front", "moe_w4a16_block", "moe_w4a16_noalloc_read_error")
+            "moe_w4a16_block_front", "moe_w4a16_block", "moe_w4a16_noalloc_read_error",
+            "moe_w4a16_dispatch_workspace_bytes", "moe_w4a16_dispatch", "moe_w4a16_dispatch_backward",
+            "moe_w4a16_combine_rows", "moe_w4a16_combine_rows_backward")
+FP16, BF16, FP32 = 0, 1, 2
 
 NOALLOC_SCRATCH_BYTES = 40 << 20  # MOE_W4A16_NOALLOC_SCRATCH_BYTES
 
@@ -47,6 +50,10 @@ class Sampler(ctypes.Structure):
     _fields_ = [("positions", ctypes.c_int32), ("vocab", ctypes.c_int32), ("inv_temperature", ctypes.c_float),
                 ("rule", ctypes.c_int32), ("bound", ctypes.c_float), ("step", ctypes.c_uint32),
                 ("noise", ctypes.c_int32), ("seed", ctypes.c_uint64)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "experts", "top_k", "hidden", "type")]
 
 
 class Weights(ctypes.Structure):
@@ -105,6 +112,16 @@ def lib() -> ctypes.CDLL:
             L.moe_w4a16_sampler_workspace_bytes.restype = sz
             L.moe_w4a16_sample.argtypes = [P(Sampler), vp, vp, vp, vp, vp, vp, vp, sz, vp]
             L.moe_w4a16_sample.restype = st
+            L.moe_w4a16_dispatch_workspace_bytes.argtypes = [P(Rows)]
+            L.moe_w4a16_dispatch_workspace_bytes.restype = sz
+            L.moe_w4a16_dispatch.argtypes = [P(Rows), vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            L.moe_w4a16_dispatch.restype = st
+            L.moe_w4a16_dispatch_backward.argtypes = [P(Rows), vp, vp, vp, vp]
+            L.moe_w4a16_dispatch_backward.restype = st
+            L.moe_w4a16_combine_rows.argtypes = [P(Rows), vp, vp, vp, vp, vp, vp]
+            L.moe_w4a16_combine_rows.restype = st
+            L.moe_w4a16_combine_rows_backward.argtypes = [P(Rows), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+            L.moe_w4a16_combine_rows_backward.restype = st
             L.moe_w4a16_read_error.argtypes = [vp, sz, vp, P(ctypes.c_int)]
             L.moe_w4a16_read_error.restype = st
             L.moe_w4a16_pack.argtypes = [vp, i64, i64, vp]
@@ -277,6 +294,94 @@ def moe_w4a16_sample(cfg: Sampler, logits, revealed, token, entropy, pmax, accep
     _check(lib().moe_w4a16_sample(ctypes.byref(cfg), _dptr(logits), _dptr(revealed), _dptr(token), _dptr(entropy),
                                   _dptr(pmax), _dptr(accept), _dptr(workspace), _nbytes(workspace), _stream(stream)),
            "moe_w4a16_sample")
+
+
+# ------------------------------------------- the layer in 16 bits, with gradients
+#
+# These calls take tensors of several types, so a tensor is checked before its
+# address is passed on: type, number of elements, contiguity, and that it lives on
+# the current CUDA device (raw addresses are passed on as they are).
+
+_TORCH_TYPES = None
+
+
+def _types():
+    global _TORCH_TYPES
+    if _TORCH_TYPES is None:
+        import torch
+        _TORCH_TYPES = ((torch.float16, torch.bfloat16, torch.float32), torch.int32, torch.float32,
+                        torch.cuda.current_device)
+    return _TORCH_TYPES
+
+
+def _tptr(t, dtype, n, dev, where) -> int | None:
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise MoeW4A16Error(ERR_SHAPE, f"{where}: a contiguous {dtype} tensor of {n} elements is wanted, got "
+                                       f"{t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}")
+    if t.get_device() != dev:
+        raise MoeW4A16Error(ERR_DEVICE, f"{where}: a tensor lives on {t.device}, the call runs on cuda:{dev}")
+    return t.data_ptr()
+
+
+def make_rows(tokens, experts, top_k, hidden, type=0) -> Rows:
+    return Rows(tokens, experts, top_k, hidden, type)
+
+
+def moe_w4a16_dispatch_workspace_bytes(cfg: Rows) -> int:
+    return int(lib().moe_w4a16_dispatch_workspace_bytes(ctypes.byref(cfg)))
+
+
+def _rows_types(cfg: Rows, where: str):
+    if not 0 <= cfg.type <= 2:
+        raise MoeW4A16Error(ERR_SHAPE, where)
+    kinds, i32, f32, current = _types()
+    return kinds[cfg.type], i32, f32, current()
+
+
+def moe_w4a16_dispatch(cfg: Rows, topk_idx, x, expert_offsets, pair_list, pair_pos, rows, workspace,
+                       stream=None) -> None:
+    w = "moe_w4a16_dispatch"
+    dt, i32, _, dev = _rows_types(cfg, w)
+    n = cfg.tokens * cfg.top_k
+    _check(lib().moe_w4a16_dispatch(ctypes.byref(cfg), _tptr(topk_idx, i32, n, dev, w),
+                                    _tptr(x, dt, cfg.tokens * cfg.hidden, dev, w),
+                                    _tptr(expert_offsets, i32, cfg.experts + 1, dev, w),
+                                    _tptr(pair_list, i32, n, dev, w), _tptr(pair_pos, i32, n, dev, w),
+                                    _tptr(rows, dt, n * cfg.hidden, dev, w), _dptr(workspace), _nbytes(workspace),
+                                    _stream(stream)), w)
+
+
+def moe_w4a16_dispatch_backward(cfg: Rows, pair_pos, grad_rows, grad_x, stream=None) -> None:
+    w = "moe_w4a16_dispatch_backward"
+    dt, i32, _, dev = _rows_types(cfg, w)
+    n = cfg.tokens * cfg.top_k
+    _check(lib().moe_w4a16_dispatch_backward(ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev, w),
+                                             _tptr(grad_rows, dt, n * cfg.hidden, dev, w),
+                                             _tptr(grad_x, dt, cfg.tokens * cfg.hidden, dev, w), _stream(stream)), w)
+
+
+def moe_w4a16_combine_rows(cfg: Rows, pair_pos, topk_w, rows, residual, out, stream=None) -> None:
+    w = "moe_w4a16_combine_rows"
+    dt, i32, f32, dev = _rows_types(cfg, w)
+    n, m = cfg.tokens * cfg.top_k, cfg.tokens * cfg.hidden
+    _check(lib().moe_w4a16_combine_rows(ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev, w),
+                                        _tptr(topk_w, f32, n, dev, w), _tptr(rows, dt, n * cfg.hidden, dev, w),
+                                        _tptr(residual, dt, m, dev, w), _tptr(out, dt, m, dev, w),
+                                        _stream(stream)), w)
+
+
+def moe_w4a16_combine_rows_backward(cfg: Rows, topk_idx, pair_pos, topk_w, rows, grad_out, grad_rows, grad_topk_w,
+                                    grad_logits, stream=None) -> None:
+    w = "moe_w4a16_combine_rows_backward"
+    dt, i32, f32, dev = _rows_types(cfg, w)
+    n, m = cfg.tokens * cfg.top_k, cfg.tokens * cfg.hidden
+    _check(lib().moe_w4a16_combine_rows_backward(
+        ctypes.byref(cfg), _tptr(topk_idx, i32, n, dev, w), _tptr(pair_pos, i32, n, dev, w),
+        _tptr(topk_w, f32, n, dev, w), _tptr(rows, dt, n * cfg.hidden, dev, w), _tptr(grad_out, dt, m, dev, w),
+        _tptr(grad_rows, dt, n * cfg.hidden, dev, w), _tptr(grad_topk_w, f32, n, dev, w),
+        _tptr(grad_logits, f32, cfg.tokens * cfg.experts, dev, w), _stream(stream)), w)
 
 
 def moe_w4a16_read_error(workspace, stream=None) -> int:

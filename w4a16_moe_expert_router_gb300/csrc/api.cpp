@@ -81,6 +81,13 @@ moe_w4a16_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_W4A1
 
 }  // namespace
 
+moe_w4a16_status moe::current_device(int* num_sms) {
+  const DeviceState* dev = nullptr;
+  const moe_w4a16_status st = device_state(&dev);
+  if (st == MOE_W4A16_OK) *num_sms = dev->num_sms;
+  return st;
+}
+
 extern "C" {
 
 size_t moe_w4a16_workspace_bytes(const moe_w4a16_shape* shape) {

@@ -173,6 +173,26 @@ cudaError_t launch_sample(int P, int64_t V, float inv_temp, uint64_t seed, uint3
                           int noise, const float* logits, const uint8_t* revealed, int32_t* token, float* entropy, float* pmax,
                           uint8_t* accept, void* workspace, cudaStream_t st);
 
+// Token rows sorted by expert and back (rows.cu).
+constexpr int kMaxRowCols = 65536;
+struct RowDims {
+  int T, E, k, d, type;  // type: 0 fp16, 1 bf16, 2 fp32
+  int64_t pairs() const { return int64_t(T) * k; }
+  int nvec() const { return type == 2 ? d / 4 : d / 8; }  // 16-byte pieces of a row
+};
+size_t dispatch_ws_bytes(const RowDims& s);
+cudaError_t launch_dispatch(const RowDims& s, const int32_t* topk_idx, const void* x, int32_t* offsets,
+                            int32_t* pair_list, int32_t* pair_pos, void* rows, void* workspace, cudaStream_t st);
+// topk_w NULL: weights of one.
+cudaError_t launch_combine_rows(const RowDims& s, const int32_t* pair_pos, const float* topk_w, const void* rows,
+                                const void* residual, void* out, cudaStream_t st);
+cudaError_t launch_combine_rows_backward(const RowDims& s, const int32_t* topk_idx, const int32_t* pair_pos,
+                                         const float* topk_w, const void* rows, const void* dout, void* drows,
+                                         float* dtopk_w, float* dlogits, cudaStream_t st);
+
+// The current device's state: MOE_W4A16_OK with its SM count, or why it cannot be used.
+moe_w4a16_status current_device(int* num_sms);
+
 // Self-test of the expert launch's bounded waits: waits that cannot complete (an
 // mbarrier phase, then the counter *flag, which must stay 0) give up after limit_ns
 // each and record MOE_W4A16_ERR_TIMEOUT in *err.
