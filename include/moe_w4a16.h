@@ -359,8 +359,10 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_dispatch_backward(const moe_w4a16_rows*
 /* Rows back to their tokens: out[t] = residual[t] + sum_r w[t][r] rows[pair_pos[t*k+r]],
  * the sum in rank order in fp32 (fused multiply-adds from 0), then the residual, rounded
  * once.  Dropped pairs (pair_pos outside 0..T*k-1) add nothing.
- *   topk_w  fp32 [T][k]    rows  type [T*k][d]    residual  type [T][d] or NULL
- *   out     type [T][d], written; may be residual itself */
+ *   topk_w    fp32 [T][k], or NULL for weights of one (the gradient of dispatch with another
+ *             gradient of x added)
+ *   rows      type [T*k][d]    residual  type [T][d] or NULL
+ *   out       type [T][d], written; may be residual itself */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_combine_rows(const moe_w4a16_rows* cfg, const int32_t* pair_pos,
                                                       const float* topk_w, const void* rows, const void* residual,
                                                       void* out, void* stream);
@@ -380,6 +382,61 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_combine_rows_backward(const moe_w4a16_r
                                                                const void* rows, const void* grad_out,
                                                                void* grad_rows, float* grad_topk_w,
                                                                float* grad_logits, void* stream);
+
+/* Products of rows with weights.
+ *   rows        R, 0..2^22, rows of x
+ *   in          K, columns of x, a multiple of 8, 8..65536
+ *   out         N, columns of the output, a multiple of 8, 8..65536
+ *   groups      E, 1..256 weights; rows sorted by expert (see expert_offsets below)
+ *   activation  0 = GELU tanh form, 1 = GELU erf form (as moe_w4a16_shape), 2 = SiLU
+ *               z / (1 + e^-z), 3 = identity
+ *   gated       0: Nw = N, y = act(z);  1: Nw = 2N, y = act(z_gate) z_up with rows [0, N) of a
+ *               weight the gate's and [N, 2N) the up projection's
+ *   type        MOE_W4A16_FP16 or _BF16: type of x, weight, residual, out and preact */
+typedef struct {
+  int32_t rows, in, out, groups, activation, gated, type;
+} moe_w4a16_linear_cfg;
+
+/* Device workspace bytes of the calls (0 on an invalid cfg).  The workspace starts with the
+ * error word that moe_w4a16_read_error reads; initialise it once with
+ * moe_w4a16_workspace_init. */
+MOE_W4A16_API size_t moe_w4a16_linear_workspace_bytes(const moe_w4a16_linear_cfg* cfg);
+MOE_W4A16_API size_t moe_w4a16_linear_backward_workspace_bytes(const moe_w4a16_linear_cfg* cfg);
+
+/* out[r] = act(x[r] W^T + b) (or gated) + residual[r], accumulated, activated and added in
+ * fp32, rounded once.
+ *   x               type [R][K]
+ *   expert_offsets  int32 [E+1] (moe_w4a16_dispatch): rows offsets[e] .. offsets[e+1]-1 take
+ *                   weight e; non-decreasing from 0.  Rows from offsets[E] on are neither used
+ *                   nor written.  NULL with E = 1: every row takes the one weight
+ *   weight          type [E][Nw][K]     bias  fp32 [E][Nw] or NULL
+ *   residual        type [R][N] or NULL
+ *   out             type [R][N], written; may be residual itself
+ *   preact          type [R][Nw] or NULL, written: z = x W^T + b, for the gradient
+ * R = 0 is an OK no-op. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_cfg* cfg, const void* x,
+                                                const int32_t* expert_offsets, const void* weight, const float* bias,
+                                                const void* residual, void* out, void* preact, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/* The gradient of moe_w4a16_linear (that of the residual is grad_out itself), each output
+ * NULL where it is not wanted (one at least is):
+ *   preact       type [R][Nw]: z as the forward call wrote it; NULL when the activation is the
+ *                identity and there is no gate
+ *   grad_out     type [R][N]
+ *   grad_x       type [R][K]      dz W; rows from offsets[E] on are left as they were
+ *   grad_weight  type [E][Nw][K]  sum over the expert's rows of dz x^T; zeros for an expert
+ *                                 without rows
+ *   grad_bias    fp32 [E][Nw]     sum over the expert's rows of dz
+ * dz = grad_out act'(z) (gated: grad_out z_up act'(z_gate) and grad_out act(z_gate)) is rounded
+ * to the type once, as the operand of the two products; grad_bias adds the unrounded values.
+ * x is read for grad_weight only, weight for grad_x only (else they may be NULL).  With R = 0
+ * grad_weight and grad_bias are cleared. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_backward(const moe_w4a16_linear_cfg* cfg, const void* x,
+                                                         const int32_t* expert_offsets, const void* weight,
+                                                         const void* preact, const void* grad_out, void* grad_x,
+                                                         void* grad_weight, float* grad_bias, void* workspace,
+                                                         size_t workspace_bytes, void* stream);
 
 /* ---- host-side weight helpers (no GPU needed) ---------------------------- */
 

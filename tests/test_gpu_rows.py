@@ -141,9 +141,9 @@ def test_combine_and_dispatch_backward(B, T, E, k, d, typ, kind):
     idx, pos, rows, w, v = _data(T, E, k, d, typ, kind)
     cfg = B.make_rows(T, E, k, d, typ)
     res = _normal((T, d), 6, typ)
-    for weights, residual in ((w, None), (w, res), (None, None)):
+    for weights, residual in ((w, None), (w, res), (None, None), (None, res)):
         out = torch.full((T, d), float("nan"), dtype=TYPES[typ], device="cuda")
-        if weights is None:
+        if weights is None and residual is None:
             B.moe_w4a16_dispatch_backward(cfg, pos, rows, out)
         else:
             B.moe_w4a16_combine_rows(cfg, pos, weights, rows, residual, out)

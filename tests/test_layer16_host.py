@@ -58,7 +58,7 @@ def test_row_configurations_refused(bad):
     ("idx", {"dispatch"}), ("x", {"dispatch"}), ("off", {"dispatch"}), ("list", {"dispatch"}), ("ws", {"dispatch"}),
     ("pos", {"dispatch", "dispatch_backward", "combine", "combine_backward"}),
     ("rows", {"dispatch", "dispatch_backward", "combine", "combine_backward"}),
-    ("gx", {"dispatch_backward"}), ("w", {"combine", "combine_backward"}), ("out", {"combine"}),
+    ("gx", {"dispatch_backward"}), ("w", {"combine_backward"}), ("out", {"combine"}),
     ("go", {"combine_backward"}),
 ])
 def test_row_pointers_refused(name, calls):
@@ -68,7 +68,8 @@ def test_row_pointers_refused(name, calls):
 
 
 def test_row_optional_pointers():
-    assert _row_calls(_rows(), res=P + 8)["combine"]() == B.ERR_ALIGN
+    for name in ("res", "w"):
+        assert _row_calls(_rows(), **{name: P + 8})["combine"]() == B.ERR_ALIGN
     for name in ("gr", "gw", "gl"):
         assert _row_calls(_rows(), **{name: P + 8})["combine_backward"]() == B.ERR_ALIGN
     assert _row_calls(_rows(), gr=None, gw=None, gl=None)["combine_backward"]() == B.ERR_NULL
@@ -89,6 +90,66 @@ def test_no_tokens_is_a_no_op():
     assert got["dispatch_backward"]() == got["combine"]() == got["combine_backward"]() == B.OK
     assert _row_calls(_rows(tokens=0), off=None)["dispatch"]() == B.ERR_NULL  # the offsets are written all the same
     assert _row_calls(_rows(tokens=0), off=P + 4)["dispatch"]() == B.ERR_ALIGN
+
+
+LINEAR = dict(rows=16, inp=64, out=32, groups=4, activation=0, gated=0, type=0)
+
+
+def _linear(**kw):
+    return B.make_linear(**{**LINEAR, **kw})
+
+
+def _linear_calls(cfg, ws_bytes=1 << 30, **null):
+    """Both product calls on stand-in addresses; only calls that are refused are made."""
+    L, c = B.lib(), ctypes.byref(cfg)
+    a = {n: P for n in ("x", "off", "weight", "bias", "res", "out", "z", "ws", "go", "gx", "gw", "gb")}
+    a.update(null)
+    return {
+        "forward": lambda: L.moe_w4a16_linear(c, a["x"], a["off"], a["weight"], a["bias"], a["res"], a["out"], a["z"],
+                                              a["ws"], ws_bytes, None),
+        "backward": lambda: L.moe_w4a16_linear_backward(c, a["x"], a["off"], a["weight"], a["z"], a["go"], a["gx"],
+                                                        a["gw"], a["gb"], a["ws"], ws_bytes, None),
+    }
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=-1), dict(rows=(1 << 22) + 1), dict(inp=0), dict(inp=12), dict(inp=65544), dict(out=0), dict(out=20),
+    dict(out=65544), dict(groups=0), dict(groups=257), dict(activation=-1), dict(activation=4), dict(gated=2),
+    dict(gated=-1), dict(type=2), dict(type=-1),
+])
+def test_linear_configurations_refused(bad):
+    cfg = _linear(**bad)
+    assert B.moe_w4a16_linear_workspace_bytes(cfg) == B.moe_w4a16_linear_backward_workspace_bytes(cfg) == 0
+    assert {call() for call in _linear_calls(cfg).values()} == {B.ERR_SHAPE}
+
+
+@pytest.mark.parametrize("name,calls", [
+    ("x", {"forward", "backward"}), ("weight", {"forward", "backward"}), ("off", {"forward", "backward"}),
+    ("out", {"forward"}), ("ws", {"forward", "backward"}), ("z", {"backward"}), ("go", {"backward"}),
+])
+def test_linear_pointers_refused(name, calls):
+    for call in calls:
+        assert _linear_calls(_linear(), **{name: None})[call]() == B.ERR_NULL, call
+        assert _linear_calls(_linear(), **{name: P + 8})[call]() == B.ERR_ALIGN, call
+
+
+def test_linear_optional_pointers_and_workspace():
+    for name in ("bias", "res", "z"):
+        assert _linear_calls(_linear(), **{name: P + 8})["forward"]() == B.ERR_ALIGN
+    for name in ("gx", "gw", "gb"):
+        assert _linear_calls(_linear(), **{name: P + 8})["backward"]() == B.ERR_ALIGN
+    assert _linear_calls(_linear(), gx=None, gw=None, gb=None)["backward"]() == B.ERR_NULL
+    assert _linear_calls(_linear(activation=3, gated=1), z=None)["backward"]() == B.ERR_NULL
+    assert _linear_calls(_linear(), ws_bytes=255)["forward"]() == B.ERR_WORKSPACE
+    # header, dz [16][64] in 16 bits, partial sums of 1 + 4 row blocks of 64 columns
+    need = B.moe_w4a16_linear_backward_workspace_bytes(_linear(gated=1))
+    assert need == 256 + 16 * 64 * 2 + 5 * 64 * 4
+    assert _linear_calls(_linear(gated=1), ws_bytes=need - 1)["backward"]() == B.ERR_WORKSPACE
+
+
+def test_linear_without_rows_is_a_no_op():
+    none = {n: None for n in ("x", "off", "weight", "bias", "res", "out", "z", "ws")}
+    assert _linear_calls(_linear(rows=0), **none)["forward"]() == B.OK
 
 
 def test_binding_refuses_tensors_it_cannot_pass_on(monkeypatch):
@@ -114,11 +175,12 @@ def test_binding_refuses_tensors_it_cannot_pass_on(monkeypatch):
 
 
 def test_structs_match_the_header(tmp_path):
-    structs = {"moe_w4a16_rows": B.Rows}
+    structs = {"moe_w4a16_rows": B.Rows, "moe_w4a16_linear_cfg": B.Linear}
     lines = ['#include <stddef.h>', '#include <stdio.h>', '#include "moe_w4a16.h"', "int main(void) {"]
+    name = lambda f: {"inp": "in"}.get(f, f)  # a keyword in Python
     for cname, cls in structs.items():
         lines.append(f'  printf("{cname} size %zu\\n", sizeof({cname}));')
-        lines += [f'  printf("{cname} {f} %zu\\n", offsetof({cname}, {f}));' for f, _ in cls._fields_]
+        lines += [f'  printf("{cname} {f} %zu\\n", offsetof({cname}, {name(f)}));' for f, _ in cls._fields_]
     src, exe = tmp_path / "layout.c", tmp_path / "layout"
     src.write_text("\n".join(lines + ["  return 0;\n}"]))
     include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")

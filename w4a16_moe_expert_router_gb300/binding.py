@@ -29,7 +29,8 @@ EXPORTED = ("moe_w4a16_workspace_bytes", "moe_w4a16_workspace_init", "moe_w4a16_
             "moe_w4a16_selftest_wait_timeout", "moe_w4a16_sampler_workspace_bytes", "moe_w4a16_sample",
             "moe_w4a16_block_front", "moe_w4a16_block", "moe_w4a16_noalloc_read_error",
             "moe_w4a16_dispatch_workspace_bytes", "moe_w4a16_dispatch", "moe_w4a16_dispatch_backward",
-            "moe_w4a16_combine_rows", "moe_w4a16_combine_rows_backward")
+            "moe_w4a16_combine_rows", "moe_w4a16_combine_rows_backward", "moe_w4a16_linear_workspace_bytes",
+            "moe_w4a16_linear_backward_workspace_bytes", "moe_w4a16_linear", "moe_w4a16_linear_backward")
 FP16, BF16, FP32 = 0, 1, 2
 
 NOALLOC_SCRATCH_BYTES = 40 << 20  # MOE_W4A16_NOALLOC_SCRATCH_BYTES
@@ -54,6 +55,10 @@ class Sampler(ctypes.Structure):
 
 class Rows(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "experts", "top_k", "hidden", "type")]
+
+
+class Linear(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "inp", "out", "groups", "activation", "gated", "type")]
 
 
 class Weights(ctypes.Structure):
@@ -122,6 +127,12 @@ def lib() -> ctypes.CDLL:
             L.moe_w4a16_combine_rows.restype = st
             L.moe_w4a16_combine_rows_backward.argtypes = [P(Rows), vp, vp, vp, vp, vp, vp, vp, vp, vp]
             L.moe_w4a16_combine_rows_backward.restype = st
+            for fn in (L.moe_w4a16_linear_workspace_bytes, L.moe_w4a16_linear_backward_workspace_bytes):
+                fn.argtypes, fn.restype = [P(Linear)], sz
+            L.moe_w4a16_linear.argtypes = [P(Linear), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            L.moe_w4a16_linear.restype = st
+            L.moe_w4a16_linear_backward.argtypes = [P(Linear), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            L.moe_w4a16_linear_backward.restype = st
             L.moe_w4a16_read_error.argtypes = [vp, sz, vp, P(ctypes.c_int)]
             L.moe_w4a16_read_error.restype = st
             L.moe_w4a16_pack.argtypes = [vp, i64, i64, vp]
@@ -325,6 +336,12 @@ def _tptr(t, dtype, n, dev, where) -> int | None:
     return t.data_ptr()
 
 
+def _workspace(t, dev, where):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise MoeW4A16Error(ERR_DEVICE, f"{where}: a contiguous workspace on cuda:{dev} is wanted")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def make_rows(tokens, experts, top_k, hidden, type=0) -> Rows:
     return Rows(tokens, experts, top_k, hidden, type)
 
@@ -349,7 +366,7 @@ def moe_w4a16_dispatch(cfg: Rows, topk_idx, x, expert_offsets, pair_list, pair_p
                                     _tptr(x, dt, cfg.tokens * cfg.hidden, dev, w),
                                     _tptr(expert_offsets, i32, cfg.experts + 1, dev, w),
                                     _tptr(pair_list, i32, n, dev, w), _tptr(pair_pos, i32, n, dev, w),
-                                    _tptr(rows, dt, n * cfg.hidden, dev, w), _dptr(workspace), _nbytes(workspace),
+                                    _tptr(rows, dt, n * cfg.hidden, dev, w), *_workspace(workspace, dev, w),
                                     _stream(stream)), w)
 
 
@@ -382,6 +399,51 @@ def moe_w4a16_combine_rows_backward(cfg: Rows, topk_idx, pair_pos, topk_w, rows,
         _tptr(topk_w, f32, n, dev, w), _tptr(rows, dt, n * cfg.hidden, dev, w), _tptr(grad_out, dt, m, dev, w),
         _tptr(grad_rows, dt, n * cfg.hidden, dev, w), _tptr(grad_topk_w, f32, n, dev, w),
         _tptr(grad_logits, f32, cfg.tokens * cfg.experts, dev, w), _stream(stream)), w)
+
+
+def make_linear(rows, inp, out, groups=1, activation=3, gated=0, type=0) -> Linear:
+    return Linear(rows, inp, out, groups, activation, gated, type)
+
+
+def moe_w4a16_linear_workspace_bytes(cfg: Linear) -> int:
+    return int(lib().moe_w4a16_linear_workspace_bytes(ctypes.byref(cfg)))
+
+
+def moe_w4a16_linear_backward_workspace_bytes(cfg: Linear) -> int:
+    return int(lib().moe_w4a16_linear_backward_workspace_bytes(ctypes.byref(cfg)))
+
+
+def _linear_types(cfg: Linear, where: str):
+    if not 0 <= cfg.type <= 1:
+        raise MoeW4A16Error(ERR_SHAPE, where)
+    kinds, i32, f32, current = _types()
+    return kinds[cfg.type], i32, f32, current(), cfg.out * (2 if cfg.gated else 1)
+
+
+def moe_w4a16_linear(cfg: Linear, x, expert_offsets, weight, bias, residual, out, preact, workspace,
+                     stream=None) -> None:
+    w = "moe_w4a16_linear"
+    dt, i32, f32, dev, nw = _linear_types(cfg, w)
+    R, E = cfg.rows, cfg.groups
+    _check(lib().moe_w4a16_linear(ctypes.byref(cfg), _tptr(x, dt, R * cfg.inp, dev, w),
+                                  _tptr(expert_offsets, i32, E + 1, dev, w),
+                                  _tptr(weight, dt, E * nw * cfg.inp, dev, w), _tptr(bias, f32, E * nw, dev, w),
+                                  _tptr(residual, dt, R * cfg.out, dev, w), _tptr(out, dt, R * cfg.out, dev, w),
+                                  _tptr(preact, dt, R * nw, dev, w), *_workspace(workspace, dev, w),
+                                  _stream(stream)), w)
+
+
+def moe_w4a16_linear_backward(cfg: Linear, x, expert_offsets, weight, preact, grad_out, grad_x, grad_weight,
+                              grad_bias, workspace, stream=None) -> None:
+    w = "moe_w4a16_linear_backward"
+    dt, i32, f32, dev, nw = _linear_types(cfg, w)
+    R, E, K = cfg.rows, cfg.groups, cfg.inp
+    _check(lib().moe_w4a16_linear_backward(
+        ctypes.byref(cfg), _tptr(x, dt, R * K, dev, w), _tptr(expert_offsets, i32, E + 1, dev, w),
+        _tptr(weight, dt, E * nw * K, dev, w), _tptr(preact, dt, R * nw, dev, w),
+        _tptr(grad_out, dt, R * cfg.out, dev, w), _tptr(grad_x, dt, R * K, dev, w),
+        _tptr(grad_weight, dt, E * nw * K, dev, w), _tptr(grad_bias, f32, E * nw, dev, w),
+        *_workspace(workspace, dev, w), _stream(stream)), w)
 
 
 def moe_w4a16_read_error(workspace, stream=None) -> int:

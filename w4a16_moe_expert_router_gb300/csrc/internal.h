@@ -190,6 +190,26 @@ cudaError_t launch_combine_rows_backward(const RowDims& s, const int32_t* topk_i
                                          const float* topk_w, const void* rows, const void* dout, void* drows,
                                          float* dtopk_w, float* dlogits, cudaStream_t st);
 
+// Products of rows with weights and their gradients (linear.cu, linear_small.cu, linear_grad.cu).
+constexpr int kSmallRows = 8;  // forward calls up to this many rows take linear_small.cu's kernel
+struct LinearDims {
+  int R, K, N, E, act, gated, type;  // type: 0 fp16, 1 bf16
+  bool grouped;                      // rows sorted by expert (offsets given)
+  int Nw() const { return gated ? 2 * N : N; }
+};
+cudaError_t init_linear_kernels();
+cudaError_t launch_linear(const LinearDims& s, const int32_t* offsets, const void* x, const void* w, const float* bias,
+                          const void* residual, void* out, void* preact, int32_t* err, int num_sms, cudaStream_t st);
+cudaError_t launch_linear_small(const LinearDims& s, const int32_t* offsets, const void* x, const void* w,
+                                const float* bias, const void* residual, void* out, void* preact, cudaStream_t st);
+cudaError_t launch_linear_input_grad(const LinearDims& s, const int32_t* offsets, const void* w, const void* dz, void* dx,
+                                     int32_t* err, int num_sms, cudaStream_t st);
+cudaError_t launch_linear_weight_grad(const LinearDims& s, const int32_t* offsets, const void* x, const void* dz,
+                                      void* dw, int32_t* err, int num_sms, cudaStream_t st);
+int linear_row_blocks(const LinearDims& s);  // row blocks of the bias gradient's partial sums, at most
+cudaError_t launch_linear_dz(const LinearDims& s, const int32_t* offsets, const void* z, const void* dout, void* dz,
+                             float* partial, float* dbias, cudaStream_t st);
+
 // The current device's state: MOE_W4A16_OK with its SM count, or why it cannot be used.
 moe_w4a16_status current_device(int* num_sms);
 

@@ -1,0 +1,190 @@
+// linear_grad.cu -- the element-wise front of a product's gradient and its bias gradient.
+//
+//   dz = dout act'(z)                       (gated: dz_g = dout z_u act'(z_g), dz_u = dout act(z_g))
+//   db[e][n] = sum over the rows of expert e of dz[r][n]
+//
+// One pass over z and dout writes dz in the rows' type, the operand of the two products
+// that follow: a rounding of half a step per element, independent from element to
+// element, so a sum over dz is off by about what its own rounding to the type costs.
+// The bias gradient takes the fp32 values: a CTA sums up to 128 rows of one expert for
+// 256 columns (16 rows per thread, then eight threads in order) into a partial, and a
+// second launch adds an expert's partials in order: no atomics.  Bound by memory: z and
+// dout read once, dz written once.
+#include "activation.cuh"
+#include "internal.h"
+#include "row_vec.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsPerCta = 128;
+constexpr int kPieces = 32;              // 16-byte pieces (256 columns) per CTA
+constexpr int kLanes = kThreads / kPieces;  // rows at a time
+
+// The row range of block b: experts own ceil(rows / 128) blocks each, in order.
+// Whole CTA; false when there is no such block.
+__device__ __forceinline__ bool find_block(const int32_t* offsets, int E, int R, int b, int* sh, int& e, int& r0,
+                                           int& r1) {
+  if (!offsets) {
+    e = 0;
+    r0 = b * kRowsPerCta;
+    r1 = min(R, r0 + kRowsPerCta);
+    return r0 < R;
+  }
+  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  int lo = 0, hi = 0;
+  if (i < E) {
+    lo = min(max(offsets[i], 0), R);
+    hi = max(min(offsets[i + 1], R), lo);
+  }
+  const int n = (hi - lo + kRowsPerCta - 1) / kRowsPerCta;
+  int incl = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) sh[warp] = incl;
+  if (i == 0) sh[8] = -1;
+  __syncthreads();
+  int before = incl - n;
+  for (int w = 0; w < warp; ++w) before += sh[w];
+  if (n > 0 && b >= before && b < before + n) {
+    sh[8] = i;
+    sh[9] = lo + (b - before) * kRowsPerCta;
+    sh[10] = hi;
+  }
+  __syncthreads();
+  e = sh[8];
+  r0 = sh[9];
+  r1 = min(sh[10], r0 + kRowsPerCta);
+  return e >= 0;
+}
+
+// grid (column blocks of N, row blocks).  z NULL: dz is dout itself and only the bias is wanted.
+template <int kType>
+__global__ void __launch_bounds__(kThreads) linear_dz_kernel(const int32_t* offsets, const uint4* z, const uint4* dout,
+                                                             uint4* dz, float* partial, int R, int E, int N, int gated,
+                                                             int act) {
+  __shared__ int sh[12];
+  __shared__ float sum[2][kLanes][kPieces * 8];
+  grid_dependents_launch();
+  grid_dependency_wait();
+  int e, r0, r1;
+  if (!find_block(offsets, E, R, blockIdx.y, sh, e, r0, r1)) return;
+  const int piece = threadIdx.x % kPieces, rl = threadIdx.x / kPieces;
+  const int nvec = N / 8, zvec = gated ? 2 * nvec : nvec;
+  const int col = blockIdx.x * kPieces + piece;
+  float sg[8], su[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.f;
+  if (col < nvec) {
+#pragma unroll 2
+    for (int r = r0 + rl; r < r1; r += kLanes) {
+      float d[8];
+      Vec<kType>::load(dout[static_cast<size_t>(r) * nvec + col], d);
+      if (z) {
+        const size_t at = static_cast<size_t>(r) * zvec + col;
+        float g[8], o[8];
+        Vec<kType>::load(z[at], g);
+        if (gated) {
+          float u[8], ou[8];
+          Vec<kType>::load(z[at + nvec], u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float y, dy;
+            activate_grad(g[i], act, y, dy);
+            o[i] = d[i] * u[i] * dy;
+            ou[i] = d[i] * y;
+            su[i] += ou[i];
+          }
+          dz[at + nvec] = Vec<kType>::store(ou);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float y, dy;
+            activate_grad(g[i], act, y, dy);
+            o[i] = d[i] * dy;
+          }
+        }
+        dz[at] = Vec<kType>::store(o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = o[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sg[i] += d[i];
+    }
+  }
+  if (!partial) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    sum[0][rl][piece * 8 + i] = sg[i];
+    sum[1][rl][piece * 8 + i] = su[i];
+  }
+  __syncthreads();
+  const int n = blockIdx.x * kPieces * 8 + threadIdx.x;
+  if (n >= N) return;
+  const int Nw = gated ? 2 * N : N;
+  for (int h = 0; h <= gated; ++h) {
+    float s = 0.f;
+#pragma unroll
+    for (int l = 0; l < kLanes; ++l) s += sum[h][l][threadIdx.x];
+    partial[static_cast<size_t>(blockIdx.y) * Nw + h * N + n] = s;
+  }
+}
+
+// db[e][n]: the partials of expert e's blocks, in order.
+__global__ void __launch_bounds__(kThreads) linear_dbias_kernel(const int32_t* offsets, const float* partial, float* db,
+                                                                int R, int E, int Nw) {
+  __shared__ int sh[9];
+  grid_dependents_launch();
+  grid_dependency_wait();
+  const int e = blockIdx.y, i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  int first = 0, count = (R + kRowsPerCta - 1) / kRowsPerCta;
+  if (offsets) {
+    int n = 0;
+    if (i < E) {
+      const int lo = min(max(offsets[i], 0), R), hi = max(min(offsets[i + 1], R), lo);
+      n = (hi - lo + kRowsPerCta - 1) / kRowsPerCta;
+    }
+    if (i == e) sh[8] = n;
+    int before = i < e ? n : 0;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+    if (lane == 0) sh[warp] = before;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) first += sh[w];
+    count = sh[8];
+  }
+  const int n = blockIdx.x * kThreads + i;
+  if (n >= Nw) return;
+  float s = 0.f;
+  const float* p = partial + static_cast<size_t>(first) * Nw + n;
+#pragma unroll 8
+  for (int b = 0; b < count; ++b) s += p[static_cast<size_t>(b) * Nw];
+  db[static_cast<size_t>(e) * Nw + n] = s;
+}
+
+}  // namespace
+
+int linear_row_blocks(const LinearDims& s) {
+  const int blocks = (s.R + kRowsPerCta - 1) / kRowsPerCta;
+  return s.grouped ? blocks + (s.E < s.R ? s.E : s.R) : blocks;
+}
+
+cudaError_t launch_linear_dz(const LinearDims& s, const int32_t* offsets, const void* z, const void* dout, void* dz,
+                             float* partial, float* dbias, cudaStream_t st) {
+  const dim3 grid((s.N + kPieces * 8 - 1) / (kPieces * 8), linear_row_blocks(s));
+  const auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, st, offsets, static_cast<const uint4*>(z),
+                      static_cast<const uint4*>(dout), static_cast<uint4*>(dz), dbias ? partial : nullptr, s.R, s.E,
+                      s.N, s.gated, s.act);
+  };
+  const cudaError_t err = s.type == 1 ? go(linear_dz_kernel<1>) : go(linear_dz_kernel<0>);
+  if (err != cudaSuccess || !dbias) return err;
+  return launch_pdl(linear_dbias_kernel, dim3((s.Nw() + kThreads - 1) / kThreads, s.E), dim3(kThreads), 0, st, offsets,
+                    static_cast<const float*>(partial), dbias, s.R, s.E, s.Nw());
+}
+
+}  // namespace moe

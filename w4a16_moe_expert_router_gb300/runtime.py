@@ -97,3 +97,75 @@ def to_device_x(x_bits: np.ndarray, device="cuda") -> torch.Tensor:
 
 def to_device_f32(a: np.ndarray, device="cuda") -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(device)
+
+
+class Layer16:
+    """The expert layer in 16 bits with gradients: the buffers of one batch and the call
+    sequence route -> dispatch -> gate and up -> down -> combine (with the residual), and
+    back.  ``backward`` belongs to the last ``forward``; both leave their results in the
+    layer's buffers.
+
+    Rows are fp16 (type 0) or bf16 (type 1); gate_up [E][2f][d] with an fp32 bias
+    [E][2f] or None, down [E][d][f], router logits fp32 [T][E].
+    """
+
+    def __init__(self, tokens: int, hidden: int, inter: int, experts: int, top_k: int, activation: int = 0,
+                 type: int = 0, device="cuda"):
+        T, d, f, E, k = tokens, hidden, inter, experts, top_k
+        dt = (torch.float16, torch.bfloat16)[type]
+        # the routing call takes a layer shape; only its tokens, experts and top_k matter to it
+        self.shape = B.make_shape(T, 128, 64, E, k, 32, 32)
+        self.rows = B.make_rows(T, E, k, d, type)
+        self.up = B.make_linear(T * k, d, f, E, activation, 1, type)
+        self.dn = B.make_linear(T * k, f, d, E, 3, 0, type)
+
+        def new(*shape, dtype=dt):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        i32, f32 = torch.int32, torch.float32
+        self.routing = B.RoutingBuffers(new(T, k, dtype=i32), new(T, k, dtype=f32), new(E + 1, dtype=i32),
+                                        new(T * k, dtype=i32))
+        self.pair_pos = new(T, k, dtype=i32)
+        self.x_rows, self.z, self.h, self.y = new(T * k, d), new(T * k, 2 * f), new(T * k, f), new(T * k, d)
+        self.out = new(T, d)
+        self.grad_y, self.grad_h, self.grad_rows, self.grad_x = new(T * k, d), new(T * k, f), new(T * k, d), new(T, d)
+        self.grad_w, self.grad_logits = new(T, k, dtype=f32), new(T, E, dtype=f32)
+        self.grad_gate_up, self.grad_down = new(E, 2 * f, d), new(E, d, f)
+        self.grad_bias = new(E, 2 * f, dtype=f32)
+        self.ws = [new(max(n, 256), dtype=torch.uint8) for n in (
+            B.moe_w4a16_workspace_bytes(self.shape), B.moe_w4a16_dispatch_workspace_bytes(self.rows),
+            max(B.moe_w4a16_linear_workspace_bytes(self.up), B.moe_w4a16_linear_backward_workspace_bytes(self.up),
+                B.moe_w4a16_linear_backward_workspace_bytes(self.dn)))]
+        B.moe_w4a16_workspace_init(self.ws[0])
+        B.moe_w4a16_workspace_init(self.ws[2])
+
+    def forward(self, x, logits, gate_up, gate_up_bias, down, stream=None) -> torch.Tensor:
+        """out = x + sum_r w_r expert_r(x) for every token."""
+        r = self.routing
+        self.saved = (gate_up, gate_up_bias, down)
+        B.moe_w4a16_route(self.shape, logits, r, self.ws[0], stream)
+        B.moe_w4a16_dispatch(self.rows, r.topk_idx, x, r.expert_offsets, r.pair_list, self.pair_pos, self.x_rows,
+                             self.ws[1], stream)
+        B.moe_w4a16_linear(self.up, self.x_rows, r.expert_offsets, gate_up, gate_up_bias, None, self.h, self.z,
+                           self.ws[2], stream)
+        B.moe_w4a16_linear(self.dn, self.h, r.expert_offsets, down, None, None, self.y, None, self.ws[2], stream)
+        B.moe_w4a16_combine_rows(self.rows, self.pair_pos, r.topk_w, self.y, x, self.out, stream)
+        return self.out
+
+    def backward(self, grad_out, stream=None) -> dict:
+        """Gradients of the last forward: x (the residual's included), logits, gate_up,
+        gate_up_bias (where there is a bias) and down."""
+        r, (gate_up, bias, down) = self.routing, self.saved
+        B.moe_w4a16_combine_rows_backward(self.rows, r.topk_idx, self.pair_pos, r.topk_w, self.y, grad_out, self.grad_y,
+                                          self.grad_w, self.grad_logits, stream)
+        B.moe_w4a16_linear_backward(self.dn, self.h, r.expert_offsets, down, None, self.grad_y, self.grad_h,
+                                    self.grad_down, None, self.ws[2], stream)
+        B.moe_w4a16_linear_backward(self.up, self.x_rows, r.expert_offsets, gate_up, self.z, self.grad_h,
+                                    self.grad_rows, self.grad_gate_up, None if bias is None else self.grad_bias,
+                                    self.ws[2], stream)
+        # dispatch's gradient with the residual's added: the rows back with weights of one
+        B.moe_w4a16_combine_rows(self.rows, self.pair_pos, None, self.grad_rows, grad_out, self.grad_x, stream)
+        out = {"x": self.grad_x, "logits": self.grad_logits, "gate_up": self.grad_gate_up, "down": self.grad_down}
+        if bias is not None:
+            out["gate_up_bias"] = self.grad_bias
+        return out
