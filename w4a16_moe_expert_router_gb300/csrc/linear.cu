@@ -15,13 +15,14 @@
 // weights' way from memory, and a column past an expert's last row is computed from
 // its neighbour's data and not stored.
 //
-// One persistent CTA (or pair of CTAs) per SM walks a list of tiles: a warp loads
-// 64-element stages of A and B by TMA, one thread issues the matrix instructions into
-// one of two accumulators in tensor memory, and eight warps empty the other one: 32
-// columns at a time through shared memory, so that the outputs leave as 16-byte pieces
-// of contiguous rows.  Accumulation, bias, activation and residual are in fp32,
+// Persistent pairs of CTAs (two SMs on one tile of 256 outputs x kCols rows, each
+// holding its 128 outputs of A and half of B) walk a list of tiles: a thread of each
+// loads 64-element stages of A and B by TMA, one thread of the pair issues the matrix
+// instructions into one of two accumulators in tensor memory, and eight warps of each
+// empty the other one: 32 columns at a time through shared memory, so that the outputs
+// leave as 16-byte pieces of contiguous rows.  Accumulation, bias, activation and residual are in fp32,
 // rounded once.
-#include <cstring>
+#include <cstdint>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -35,12 +36,12 @@ namespace moe {
 namespace {
 
 constexpr int kForward = 0, kInputGrad = 1, kWeightGrad = 2;
-constexpr int kTileM = 128;            // lanes of tensor memory
-constexpr int kDepth = 64;             // contraction elements per stage (128 bytes)
-constexpr int kABytes = kTileM * 128;  // A per stage
+constexpr int kTileM = 128;            // lanes of tensor memory: outputs of one CTA's half of a tile
 constexpr int kEpiCols = 32;           // columns per epilogue step
-constexpr int kEpiBytes = kEpiCols * kTileM * 4;
+constexpr int kStepBytes = kEpiCols * kTileM * 2;  // 16-bit values of one step
+constexpr int kEpiBytes = 2 * kStepBytes;          // two steps per group of four epilogue warps
 constexpr int kThreads = 384;          // TMA, MMA, tail and one idle warp, then 8 epilogue warps
+constexpr int kMaxStages = 8;
 constexpr int kSmemLimit = 227 * 1024;
 
 struct Args {
@@ -50,23 +51,31 @@ struct Args {
   uint16_t* out;
   uint16_t* preact;
   int32_t* err;
-  int mode, R, E, K, N, Nw, act, gated, bf16;
+  int R, E, N, Nw, act, gated, bf16;
   int width;    // extent of m, and the row length of out
-  int tile_m;   // outputs per CTA tile (64 of a gate and their ups, or 128)
-  int tiles_m;  // tiles along m, of the CTA or pair
+  int tile_m;   // outputs per CTA and tile (64 of a gate and their ups, or 128)
+  int tiles_m;  // tiles along m
   int tiles_c;  // weight grad: tiles along c
   int depth;    // contraction length (weight grad: the expert's rows)
   uint32_t word;
 };
 
-template <int kCols, int kCtas>
+// A stage holds 64 contraction elements of the largest tile and 128 of the smaller ones: a
+// stage costs its barriers and two waiting threads about 0.24 us whatever it holds (measured:
+// tiles of 32 columns 814 -> 514 us on 8192 x 2048 x 8192, of 128 columns 219 -> 171 us),
+// which is below the matrix instructions' time at 256 columns only, and there six short
+// stages hide latency better than three long ones (141 against 146 us).
+template <int kCols>
 struct Config {
-  static constexpr int cols = kCols / kCtas;  // columns whose B rows this CTA loads
-  static constexpr int b_bytes = cols * 128;
-  static constexpr int stage = kABytes + b_bytes;
-  static constexpr int fixed = 2 * kEpiBytes + (2 * (kMaxExperts + 1) + 2) * 4 + 256;
+  static constexpr int depth = kCols == 256 ? 64 : 128;
+  static constexpr int cols = kCols / 2;  // columns whose B rows each CTA loads
+  static constexpr int a_bytes = kTileM * depth * 2;
+  static constexpr int b_bytes = cols * depth * 2;
+  static constexpr int box_bytes = depth * 128;  // 64 elements of each of a stage's contraction rows
+  static constexpr int stage = a_bytes + b_bytes;
+  static constexpr int fixed = 2 * kEpiBytes + (2 * (kMaxExperts + 1) + 2) * 4 + (4 * kMaxStages + 5) * 8 + 16;
   static constexpr int fit = (kSmemLimit - fixed) / stage;
-  static constexpr int stages = fit < 8 ? fit : 8;
+  static constexpr int stages = fit < kMaxStages ? fit : kMaxStages;
   static constexpr int smem = stages * stage + fixed;
   static constexpr uint32_t tmem = 2 * kCols;  // two accumulators
 };
@@ -75,23 +84,23 @@ struct Tile {
   int e, m0, c0, row0, row_end, first, len;  // len: contraction length, first: its first row (weight grad)
 };
 
-// The tile of index t.  start[e]: tiles before expert e; off[e]: its first row.
-__device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const int* off, int t, int& e, int cols,
-                                        int ctas, int rank) {
+// The CTA's half of the tile of index t.  start[e]: tiles before expert e; off[e]: its first row.
+template <int kMode, int kCols>
+__device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const int* off, int t, int& e, int rank) {
   while (t >= start[e + 1]) ++e;  // t only grows
   const int i = t - start[e];
-  const int m = i % a.tiles_m, c = i / a.tiles_m;
+  const int c = i / a.tiles_m, m = i - c * a.tiles_m;
   Tile r;
   r.e = e;
-  r.m0 = (m * ctas + rank) * a.tile_m;
-  if (a.mode == kWeightGrad) {
-    r.c0 = c * cols;
+  r.m0 = (m * 2 + rank) * a.tile_m;
+  if (kMode == kWeightGrad) {
+    r.c0 = c * kCols;
     r.row0 = e * a.Nw + r.c0;
     r.row_end = (e + 1) * a.Nw;
     r.first = off[e];
     r.len = off[e + 1] - off[e];
   } else {
-    r.c0 = off[e] + c * cols;
+    r.c0 = off[e] + c * kCols;
     r.row0 = r.c0;
     r.row_end = off[e + 1];
     r.first = 0;
@@ -100,20 +109,18 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const i
   return r;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8], int bf16) {
-  return bf16 ? Vec<1>::store(f) : Vec<0>::store(f);
+// Two 16-bit values, the first in the lower half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int bf16) {
+  return bf16 ? Vec<1>::pack(lo, hi) : h2_bits(__floats2half2_rn(lo, hi));
 }
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8], int bf16) {
-  if (bf16)
-    Vec<1>::load(v, f);
-  else
-    Vec<0>::load(v, f);
+__device__ __forceinline__ float2 unpack2(uint32_t v, int bf16) {
+  return bf16 ? make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)) : __half22float2(bits_h2(v));
 }
 
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // Barrier of a group of 128 threads that tells each whether `ok` held for all, so that a
-// group whose bounded wait ran out for one thread leaves together.
+// group whose bounded wait ran out for one warp leaves together.
 __device__ __forceinline__ bool group_all(int id, bool ok) {
   uint32_t r;
   asm volatile(
@@ -124,83 +131,230 @@ __device__ __forceinline__ bool group_all(int id, bool ok) {
   return r != 0;
 }
 
-// One epilogue step: rows row0 .. row0+31 (those below row_end) of the tile's outputs
-// from the accumulator step in buf [32][128].  A thread owns eight contiguous outputs
-// m0 + f .. of one row in `per` passes, with their biases in registers.
-__device__ __forceinline__ void store_step(const Args& a, const float* buf, int tid, int m0, int row0, int row_end,
-                                           const float (&b)[8], const float (&bu)[8]) {
-  const int groups = a.gated ? 8 : 16;  // threads per row
-  const int f = (tid % groups) * 8, rows = 128 / groups;
-  if (m0 + f >= a.width) return;
-  for (int c = tid / groups; c < kEpiCols; c += rows) {
-    const int row = row0 + c;
-    if (row >= row_end) break;
-    const size_t o = static_cast<size_t>(row) * a.width + m0 + f;
-    uint4 res = make_uint4(0u, 0u, 0u, 0u);
-    if (a.residual) res = *reinterpret_cast<const uint4*>(a.residual + o);
-    const float4 p = *reinterpret_cast<const float4*>(buf + c * kTileM + f);
-    const float4 q = *reinterpret_cast<const float4*>(buf + c * kTileM + f + 4);
-    float z[8] = {p.x + b[0], p.y + b[1], p.z + b[2], p.w + b[3], q.x + b[4], q.y + b[5], q.z + b[6], q.w + b[7]};
-    float y[8];
-    if (a.preact) {
-      const size_t zo = static_cast<size_t>(row) * a.Nw + m0 + f;
-      *reinterpret_cast<uint4*>(a.preact + zo) = pack8(z, a.bf16);
-    }
+template <int kCount>
+__device__ __forceinline__ void activate_all(float (&z)[kCount], int act) {
+  switch (act) {
+    case kGeluTanh:
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = activate(z[i], a.act);
-    if (a.gated) {
-      const float4 r = *reinterpret_cast<const float4*>(buf + c * kTileM + 64 + f);
-      const float4 s = *reinterpret_cast<const float4*>(buf + c * kTileM + 64 + f + 4);
-      float u[8] = {r.x + bu[0], r.y + bu[1], r.z + bu[2], r.w + bu[3],
-                    s.x + bu[4], s.y + bu[5], s.z + bu[6], s.w + bu[7]};
-      if (a.preact)
-        *reinterpret_cast<uint4*>(a.preact + static_cast<size_t>(row) * a.Nw + a.N + m0 + f) = pack8(u, a.bf16);
+      for (int i = 0; i < kCount; ++i) z[i] = activate(z[i], kGeluTanh);
+      break;
+    case kGeluErf:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= u[i];
-    }
-    if (a.residual) {
-      float g[8];
-      unpack8(res, g, a.bf16);
+      for (int i = 0; i < kCount; ++i) z[i] = activate(z[i], kGeluErf);
+      break;
+    case kSilu:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] += g[i];
-    }
-    *reinterpret_cast<uint4*>(a.out + o) = pack8(y, a.bf16);
+      for (int i = 0; i < kCount; ++i) z[i] = activate(z[i], kSilu);
+      break;
+    default:
+      break;
   }
 }
 
-template <int kCols, int kCtas>
+// ---- one epilogue step: 32 columns c of the accumulator.
+//
+// A warp holds 32 lanes x 32 columns as blocks of 8 x 8: block i of half h (16 lanes) gives
+// a thread the lanes 16 h + g and 16 h + g + 8 at columns 8 i + q and 8 i + q + 1 (g = lane
+// / 4, q = 2 (lane % 4)).  Everything between the accumulator and the rounding happens in
+// these registers; the rounded blocks go transposed to a step buffer [32 columns][outputs],
+// swizzled so that neither the blocks nor the rows meet in a bank, and leave by TMA, or,
+// where the step ends inside an expert's rows, as 16-byte pieces of the rows that are the
+// expert's.  A gated tile's lanes alternate, 8 of the gate and the 8 of the up product with
+// the same outputs, so a thread holds both.
+
+// Place of chunk `chunk` of column c in a step buffer: 64 outputs (8 chunks) of the 32 columns,
+// then the other 64, each in the 128-byte swizzle of a TMA box.
+constexpr int kHalfStep = kStepBytes / 2;
+__device__ __forceinline__ uint32_t chunk_at(int c, int chunk) {
+  return static_cast<uint32_t>((chunk >> 3) * kHalfStep + c * 128 + ((chunk ^ c) & 7) * 16);
+}
+
+// The rows of a step buffer to global memory (or back, for the residual): thread tid of 128
+// takes chunk tid % kChunks of every (128 / kChunks)-th column.  f: first column of `p` in
+// elements, valid while f < width; rows of stride `ld` from row0 on, those below row_end.
+template <int kChunks, bool kLoad, typename Ptr>
+__device__ __forceinline__ void move_rows(uint8_t* buf, Ptr* p, int tid, int f, int width, int ld, int row0,
+                                          int row_end) {
+  constexpr int rows = 128 / kChunks, passes = kEpiCols / rows;
+  const int chunk = tid % kChunks, c0 = tid / kChunks;
+  if (f >= width) return;
+  uint4 v[passes];
+#pragma unroll
+  for (int i = 0; i < passes; ++i) {
+    const int c = c0 + i * rows;
+    if (!kLoad)
+      v[i] = *reinterpret_cast<const uint4*>(buf + chunk_at(c, chunk));
+    else if (row0 + c < row_end)
+      v[i] = *reinterpret_cast<const uint4*>(p + static_cast<size_t>(row0 + c) * ld + f);
+  }
+#pragma unroll
+  for (int i = 0; i < passes; ++i) {
+    const int c = c0 + i * rows;
+    if constexpr (kLoad) {
+      if (row0 + c < row_end) *reinterpret_cast<uint4*>(buf + chunk_at(c, chunk)) = v[i];
+    } else {
+      if (row0 + c < row_end) *reinterpret_cast<uint4*>(p + static_cast<size_t>(row0 + c) * ld + f) = v[i];
+    }
+  }
+}
+
+// kForm: 0 without bias, activation, residual or saved z (the gradients' products), 1 forward,
+// 2 forward gated.  b: the biases of the thread's lanes g, g + 8, g + 16, g + 24 of its quarter.
+// buf: the group's two step buffers.  whole: the step's rows all belong to the tile (map_out
+// clips those past the end of the array); they are row0 .. of the output, y .. of plane z of
+// the map.
+template <int kForm>
+__device__ __forceinline__ void epilogue_step(const Args& a, const CUtensorMap* map_out, const CUtensorMap* map_z,
+                                              uint32_t (&v)[2][16], const float (&b)[4], uint8_t* buf, int& flip,
+                                              int group, int tid, int m0, int row0, int row_end, bool whole, int y,
+                                              int z_plane) {
+  constexpr int chunks = kForm == 2 ? 8 : 16;  // 16-byte chunks of outputs per column
+  const int lane = tid & 31, quarter = tid >> 5;
+  const int f = m0 + (tid % chunks) * 8;
+  uint8_t* const ybuf = kForm > 0 && a.preact ? buf : buf + flip * kStepBytes;
+  uint8_t* const zbuf = buf + kStepBytes;
+  flip ^= 1;
+  if (kForm > 0 && a.residual) {
+    move_rows<chunks, true>(ybuf, a.residual, tid, f, a.width, a.width, row0, row_end);
+    group_sync(1 + group);
+  }
+  const int sub = lane >> 3, j = lane & 7;  // the block and row whose address this lane gives
+  if (kForm != 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // block column i: the four blocks of 8 lanes
+      float z[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) z[k] = __uint_as_float(v[k >> 2][4 * i + (k & 3)]);
+      const uint32_t at = chunk_at(8 * i + j, quarter * 4 + sub);
+      uint32_t r[4];
+      if (kForm == 1) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z[k] += b[k >> 1];
+        if (a.preact) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = pack2(z[2 * k], z[2 * k + 1], a.bf16);
+          store_blocks_transposed(smem_addr(zbuf) + at, r);
+        }
+        activate_all(z, a.act);
+        if (a.residual) {
+          load_blocks_transposed(smem_addr(ybuf) + at, r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 g = unpack2(r[k], a.bf16);
+            z[2 * k] += g.x;
+            z[2 * k + 1] += g.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = pack2(z[2 * k], z[2 * k + 1], a.bf16);
+      store_blocks_transposed(smem_addr(ybuf) + at, r);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {  // block columns i and i + 1 of both halves
+      float z[8], u[8];               // [column][half][2]
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = 4 * (i + (k >> 2)) + (k & 1), h = (k >> 1) & 1;
+        z[k] = __uint_as_float(v[h][at]) + b[2 * h];
+        u[k] = __uint_as_float(v[h][at + 2]) + b[2 * h + 1];
+      }
+      const int c = 8 * (i + (sub >> 1)) + j, chunk = quarter * 2 + (sub & 1);
+      uint32_t r[4];
+      if (a.preact) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] = pack2(z[2 * k], z[2 * k + 1], a.bf16);
+        store_blocks_transposed(smem_addr(zbuf) + chunk_at(c, chunk), r);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] = pack2(u[2 * k], u[2 * k + 1], a.bf16);
+        store_blocks_transposed(smem_addr(zbuf) + chunk_at(c, 8 + chunk), r);
+      }
+      activate_all(z, a.act);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) z[k] *= u[k];
+      const uint32_t at = chunk_at(c, chunk);
+      if (a.residual) {
+        load_blocks_transposed(smem_addr(ybuf) + at, r);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 g = unpack2(r[k], a.bf16);
+          z[2 * k] += g.x;
+          z[2 * k + 1] += g.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = pack2(z[2 * k], z[2 * k + 1], a.bf16);
+      store_blocks_transposed(smem_addr(ybuf) + at, r);
+    }
+  }
+  // one thread stores for the group; its last store has read the other buffer by now, which
+  // the barrier tells the rest
+  const bool issuer = quarter == 0 && elect_one();
+  if (whole) fence_proxy_async();
+  if (issuer) bulk_wait_read();
+  group_sync(1 + group);
+  if (whole) {
+    if (issuer && m0 < a.width) {
+      tma_store_3d(map_out, smem_addr(ybuf), m0, y, z_plane);
+      if (kForm != 2 && m0 + 64 < a.width) tma_store_3d(map_out, smem_addr(ybuf) + kHalfStep, m0 + 64, y, z_plane);
+      if (kForm > 0 && a.preact) {  // planes of map_z: gate, up
+        tma_store_3d(map_z, smem_addr(zbuf), m0, 0, y);
+        if (kForm == 2)
+          tma_store_3d(map_z, smem_addr(zbuf) + kHalfStep, m0, 1, y);
+        else if (m0 + 64 < a.width)
+          tma_store_3d(map_z, smem_addr(zbuf) + kHalfStep, m0 + 64, 0, y);
+      }
+      bulk_commit();
+    }
+  } else {
+    move_rows<chunks, false>(ybuf, a.out, tid, f, a.width, a.width, row0, row_end);
+    if (kForm > 0 && a.preact) {
+      const int zc = tid % 16, zf = kForm == 2 ? m0 + (zc & 7) * 8 : m0 + zc * 8;
+      move_rows<16, false>(zbuf, kForm == 2 && zc >= 8 ? a.preact + a.N : a.preact, tid, zf, a.width, a.Nw, row0,
+                           row_end);
+    }
+  }
+  if (kForm > 0 && a.preact) {  // both buffers are taken: the next step waits for them
+    if (issuer) bulk_wait_read();
+    group_sync(1 + group);
+  }
+}
+
+template <int kMode, int kCols>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ Args a,
                                                              const __grid_constant__ CUtensorMap map_a,
-                                                             const __grid_constant__ CUtensorMap map_b) {
-  using C = Config<kCols, kCtas>;
+                                                             const __grid_constant__ CUtensorMap map_b,
+                                                             const __grid_constant__ CUtensorMap map_out,
+                                                             const __grid_constant__ CUtensorMap map_z) {
+  using C = Config<kCols>;
+  constexpr int kDepth = C::depth;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const epi = smem + C::stages * C::stage;
   int* const start = reinterpret_cast<int*>(epi + 2 * kEpiBytes);  // [E + 1]
   int* const off = start + kMaxExperts + 1;                        // [E + 1]
   uint64_t* const bars = reinterpret_cast<uint64_t*>(off + kMaxExperts + 1 + 2);
   const uint32_t bar0 = smem_addr(bars);
-  const auto full = [&](int s) { return bar0 + 8u * s; };
-  const auto empty = [&](int s) { return bar0 + 8u * (8 + s); };
-  const auto acc_full = [&](int s) { return bar0 + 8u * (16 + s); };
-  const auto acc_empty = [&](int s) { return bar0 + 8u * (18 + s); };
-  const uint32_t tail_ready = bar0 + 8u * 20, tail_done = bar0 + 8u * 21, drained = bar0 + 8u * 22;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
+  constexpr int S = C::stages;
+  const uint32_t full = bar0, empty = full + 8 * S, tail_full = empty + 8 * S, tail_done = tail_full + 8 * S;
+  const uint32_t acc_full = tail_done + 8 * S, acc_empty = acc_full + 16, drained = acc_empty + 16;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * S + 5);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = kCtas == 2 ? static_cast<int>(cluster_rank()) : 0;
+  const int rank = static_cast<int>(cluster_rank());
   grid_dependents_launch();
-  if (warp == 1) tmem_alloc<kCtas>(smem_addr(tmem_slot), C::tmem);
+  if (warp == 1) tmem_alloc(smem_addr(tmem_slot), C::tmem);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::stages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+      mbar_init(tail_full + 8 * s, 1);
+      mbar_init(tail_done + 8 * s, 2);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(acc_full(s), 1);
-      mbar_init(acc_empty(s), 8 * kCtas);
+      mbar_init(acc_full + 8 * s, 1);
+      mbar_init(acc_empty + 8 * s, 16);  // the epilogue warps of both CTAs
     }
-    mbar_init(tail_ready, 1);
-    mbar_init(tail_done, 1);
     mbar_init(drained, 1);
     fence_barrier_init();
   }
@@ -218,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     for (int i = 0; i < 8; ++i) {
       const int e = lane * 8 + i;
       const int rows = max(o[i + 1] - o[i], 0);
-      n[i] = e < a.E ? a.tiles_m * (a.mode == kWeightGrad ? a.tiles_c : (rows + kCols - 1) / kCols) : 0;
+      n[i] = e < a.E ? a.tiles_m * (kMode == kWeightGrad ? a.tiles_c : (rows + kCols - 1) / kCols) : 0;
       sum += n[i];
     }
     int incl = sum;
@@ -244,43 +398,59 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   }
   tcgen05_fence_before();
   __syncthreads();
-  if (kCtas == 2) cluster_sync();  // the peer's barriers are initialised
+  cluster_sync();  // the peer's barriers are initialised
   tcgen05_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int tiles = start[a.E];
-  const int first_tile = blockIdx.x / kCtas, step = gridDim.x / kCtas;
+  const int first_tile = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---- loads
-      int e = 0, s = 0;
-      uint32_t phase = 0;
+      const uint32_t lead_full = cluster_addr(full, 0), stage0 = smem_addr(smem);
+      const uint32_t own_tail = cluster_addr(tail_full, rank);
+      int e = 0, s = 0, issued = 0;
+      uint32_t phase = 0, uses = 0, tails = 0, tail_uses = 0;  // one bit per stage, see below
       bool alive = true;
-      int issued = 0;
       for (int t = first_tile; alive && t < tiles; t += step) {
-        const Tile r = tile_at(a, start, off, t, e, kCols, kCtas, rank);
+        const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
         const int bc = r.c0 + rank * C::cols;
+#pragma unroll 1
         for (int j = 0; j < r.len; j += kDepth) {
-          if (!mbar_wait(empty(s), phase ^ 1, a.err)) {
+          if (!stage_wait(empty + 8 * s, phase ^ 1, a.err)) {
             alive = false;
             break;
           }
-          const uint32_t sa = smem_addr(smem + s * C::stage), sb = sa + kABytes;
-          const uint32_t bar = kCtas == 2 ? cluster_addr(full(s), 0) : full(s);
-          if (rank == 0) mbar_arrive_expect_tx(full(s), C::stage * kCtas);
-          if (a.mode == kForward) {
-            tma_load_4d<kCtas>(sa, &map_a, j, r.m0, 0, r.e, bar);
-            tma_load_2d<kCtas>(sb, &map_b, j, bc, bar);
-          } else if (a.mode == kInputGrad) {
-            tma_load_3d<kCtas>(sa, &map_a, r.m0, j, r.e, bar);
-            tma_load_3d<kCtas>(sa + kABytes / 2, &map_a, r.m0 + 64, j, r.e, bar);
-            tma_load_2d<kCtas>(sb, &map_b, j, bc, bar);
+          const uint32_t sa = stage0 + s * C::stage, sb = sa + C::a_bytes;
+          uint32_t bar = lead_full + 8 * s;
+          if (kMode == kWeightGrad && r.len - j < kDepth) {
+            bar = own_tail + 8 * s;  // a tail is mended by its own CTA first
+            mbar_arrive_expect_tx(tail_full + 8 * s, C::stage);
+            tail_uses ^= 1u << s;
+            tails |= 1u << s;
           } else {
-            tma_load_2d<kCtas>(sa, &map_a, r.m0, r.first + j, bar);
-            tma_load_2d<kCtas>(sa + kABytes / 2, &map_a, r.m0 + 64, r.first + j, bar);
+            if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * C::stage);
+            uses ^= 1u << s;
+            tails &= ~(1u << s);
+          }
+          if (kMode == kForward) {
+            tma_load_5d(sa, &map_a, j, 0, 0, r.m0 >> 3, r.e, bar);
+            tma_load_2d(sb, &map_b, j, bc, bar);
+            if constexpr (kDepth == 128) {
+              tma_load_5d(sa + C::a_bytes / 2, &map_a, j + 64, 0, 0, r.m0 >> 3, r.e, bar);
+              tma_load_2d(sb + C::b_bytes / 2, &map_b, j + 64, bc, bar);
+            }
+          } else if (kMode == kInputGrad) {
+            tma_load_3d(sa, &map_a, r.m0, j, r.e, bar);
+            tma_load_3d(sa + C::a_bytes / 2, &map_a, r.m0 + 64, j, r.e, bar);
+            tma_load_2d(sb, &map_b, j, bc, bar);
+            if constexpr (kDepth == 128) tma_load_2d(sb + C::b_bytes / 2, &map_b, j + 64, bc, bar);
+          } else {
+            tma_load_2d(sa, &map_a, r.m0, r.first + j, bar);
+            tma_load_2d(sa + C::a_bytes / 2, &map_a, r.m0 + 64, r.first + j, bar);
 #pragma unroll
             for (int x = 0; x < C::cols / 64; ++x)
-              tma_load_2d<kCtas>(sb + x * 8192, &map_b, bc + 64 * x, r.first + j, bar);
+              tma_load_2d(sb + x * C::box_bytes, &map_b, bc + 64 * x, r.first + j, bar);
           }
           if (issued < C::stages) ++issued;
           if (++s == C::stages) {
@@ -289,152 +459,169 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           }
         }
       }
-      if (!alive && rank == 0) {
-        // a wait ran out: the copies in flight land before the CTA's shared memory goes
-        // (the first CTA of a pair sees the bytes of both)
+      if (!alive) {
+        // a wait ran out: the copies in flight land before the CTAs' shared memory goes.  A
+        // stage's last copies are counted on its tail barrier (bit in `tails`), or for both
+        // CTAs on the first one's barrier; a bit of `uses` is the number of uses, so the
+        // parity of the last phase is its complement.
         for (int i = 0; i < issued; ++i) {
-          if (--s < 0) {
-            s = C::stages - 1;
-            phase ^= 1;
-          }
-          mbar_wait(full(s), phase, a.err);
+          if (tails >> i & 1)
+            mbar_wait(tail_full + 8 * i, (tail_uses >> i & 1) ^ 1, a.err);
+          else if (rank == 0)
+            mbar_wait(full + 8 * i, (uses >> i & 1) ^ 1, a.err);
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       // ---- matrix instructions
+      constexpr bool a_strided = kMode != kForward, b_strided = kMode == kWeightGrad;
+      const uint32_t stage0 = smem_addr(smem);
       int e = 0, s = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0, tail_phase = 0;
+      uint32_t phases = 0, acc_phase = 0, tail_phases = 0;  // per stage: parity of its next use
       bool alive = true;
-      const bool a_strided = a.mode != kForward, b_strided = a.mode == kWeightGrad;
-      const uint32_t a_step = a_strided ? 2048 >> 4 : 32 >> 4, b_step = b_strided ? 2048 >> 4 : 32 >> 4;
       for (int t = first_tile; alive && t < tiles; t += step) {
-        const Tile r = tile_at(a, start, off, t, e, kCols, kCtas, rank);
+        const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
         if (r.len <= 0) continue;  // no rows: the epilogue writes zeros
-        if (!mbar_wait(acc_empty(acc), acc_phase ^ 1, a.err)) break;
+        if (!stage_wait(acc_empty + 8 * acc, acc_phase ^ 1, a.err)) {
+          alive = false;
+          break;
+        }
         tcgen05_fence_after();
         const uint32_t d = tmem + acc * kCols;
+#pragma unroll 1
         for (int j = 0; j < r.len; j += kDepth) {
-          int ks = kDepth / 16;
-          if (!mbar_wait(full(s), phase, a.err)) {
-            alive = false;
-            break;
+          if (kMode == kWeightGrad && r.len - j < kDepth) {
+            alive = stage_wait(tail_done + 8 * s, tail_phases >> s & 1, a.err);
+            tail_phases ^= 1u << s;
+          } else {
+            alive = stage_wait(full + 8 * s, phases >> s & 1, a.err);
+            phases ^= 1u << s;
           }
-          if (kCtas == 1 && a.mode == kWeightGrad && r.len - j < kDepth) {
-            ks = (r.len - j + 15) / 16;
-            mbar_arrive(tail_ready);
-            if (!mbar_wait(tail_done, tail_phase, a.err)) {
-              alive = false;
-              break;
-            }
-            tail_phase ^= 1;
-          }
+          if (!alive) break;
           tcgen05_fence_after();
-          const uint32_t sa = smem_addr(smem + s * C::stage);
-          const uint64_t da = smem_operand(sa, a_strided ? kABytes / 2 : 16);
-          const uint64_t db = smem_operand(sa + kABytes, b_strided ? 8192 : 16);
-          for (int k = 0; k < ks; ++k)
-            mma_f16<kCtas>(d, da + k * a_step, db + k * b_step, a.word, (j | k) != 0);
-          mma_commit<kCtas>(empty(s));
-          if (++s == C::stages) {
-            s = 0;
-            phase ^= 1;
+          const uint32_t sa = stage0 + s * C::stage;
+          const uint64_t da = smem_operand(sa, a_strided ? C::box_bytes : 16);
+          const uint64_t db = smem_operand(sa + C::a_bytes, b_strided ? C::box_bytes : 16);
+          const auto issue = [&](int k) {  // contraction elements 16 k .. of the stage
+            const uint64_t ka = a_strided ? k * (2048 >> 4) : (k >> 2) * (C::a_bytes >> 5) + (k & 3) * (32 >> 4);
+            const uint64_t kb = b_strided ? k * (2048 >> 4) : (k >> 2) * (C::b_bytes >> 5) + (k & 3) * (32 >> 4);
+            mma_f16(d, da + ka, db + kb, a.word, static_cast<uint32_t>(j | k));
+          };
+          if (r.len - j >= kDepth) {
+#pragma unroll
+            for (int k = 0; k < kDepth / 16; ++k) issue(k);
+          } else {
+#pragma unroll 1
+            for (int k = 0; 16 * k < r.len - j; ++k) issue(k);
           }
+          mma_commit(empty + 8 * s);
+          if (++s == C::stages) s = 0;
         }
         if (!alive) break;
-        mma_commit<kCtas>(acc_full(acc));
+        mma_commit(acc_full + 8 * acc);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
       if (!alive) {  // a wait ran out: the instructions in flight end before tensor memory is given back
-        mma_commit<1>(drained);
+        mma_commit(drained);
         mbar_wait(drained, 0, a.err);
       }
     }
   } else if (warp == 2) {
-    // ---- weight grad by experts: the last stage of an expert holds rows of the next one
-    // (or rows that nobody wrote): zeros, up to a multiple of 16 rows, before it is used.
-    // One weight for all rows needs none of this: TMA fills rows past the end with zeros.
-    if (kCtas == 1 && a.mode == kWeightGrad) {
+    // ---- weight grad: the last stage of an expert holds rows of the next one (or rows that
+    // nobody wrote): zeros, up to a multiple of 16 rows, in each CTA's operands before they are
+    // used.  Such a stage has barriers of its own, so a stage's phases stay in step with the
+    // thread that waits for them.
+    if (kMode == kWeightGrad) {
+      const uint32_t lead_done = cluster_addr(tail_done, 0);
       int e = 0, it = 0;
-      uint32_t phase = 0;
+      uint32_t phases = 0;
       for (int t = first_tile; t < tiles; t += step) {
-        const Tile r = tile_at(a, start, off, t, e, kCols, kCtas, rank);
+        const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
         if (r.len <= 0) continue;
         it += (r.len + kDepth - 1) / kDepth;
         const int rest = r.len % kDepth;
         if (rest == 0) continue;
         const int s = (it - 1) % C::stages;
-        // the stage is announced, not taken from its own barrier, whose phase repeats
-        if (!mbar_wait(tail_ready, phase, a.err)) break;
-        phase ^= 1;
+        if (!stage_wait_warp(tail_full + 8 * s, phases >> s & 1, a.err)) break;
+        phases ^= 1u << s;
         const int z0 = rest * 128, z1 = (rest + 15) / 16 * 16 * 128;
         uint8_t* const base = smem + s * C::stage;
-        for (int box = 0; box < C::stage / 8192; ++box)
+        for (int box = 0; box < C::stage / C::box_bytes; ++box)
           for (int z = z0 + lane * 16; z < z1; z += 512)
-            *reinterpret_cast<uint4*>(base + box * 8192 + z) = make_uint4(0u, 0u, 0u, 0u);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            *reinterpret_cast<uint4*>(base + box * C::box_bytes + z) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tail_done);
+        if (lane == 0) mbar_arrive_cluster(lead_done + 8 * s);
       }
     }
   } else if (warp >= 4) {
     // ---- epilogue: two groups of four warps take the 32-column steps in turn
     const int group = (warp - 4) >> 2, tid = threadIdx.x & 127, quarter = warp & 3;
-    float* const buf = reinterpret_cast<float*>(epi + group * kEpiBytes);
-    int e = 0, acc = 0;
+    uint8_t* const buf = epi + group * kEpiBytes;
+    const uint32_t lead_empty = cluster_addr(acc_empty, 0);
+    int e = 0, acc = 0, flip = 0;
     uint32_t acc_phase = 0;
     for (int t = first_tile; t < tiles; t += step) {
-      const Tile r = tile_at(a, start, off, t, e, kCols, kCtas, rank);
-      float b[8], bu[8];
-      const int f = r.m0 + (tid % (a.gated ? 8 : 16)) * 8;
+      const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
+      float b[4] = {0.f, 0.f, 0.f, 0.f};
+      if (kMode == kForward && a.bias) {
+        const float* const bp = a.bias + static_cast<size_t>(r.e) * a.Nw;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        b[i] = a.bias && f < a.width ? a.bias[static_cast<size_t>(r.e) * a.Nw + f + i] : 0.f;
-        bu[i] = a.bias && a.gated && f < a.width ? a.bias[static_cast<size_t>(r.e) * a.Nw + a.N + f + i] : 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const int g = lane >> 2;
+          const int f = a.gated ? r.m0 + quarter * 16 + (i >> 1) * 8 + g : r.m0 + quarter * 32 + i * 8 + g;
+          if (f < a.width) b[i] = bp[a.gated && (i & 1) ? a.N + f : f];
+        }
       }
       if (r.len > 0) {
-        const bool ok = mbar_wait(acc_full(acc), acc_phase, a.err);
-        __syncwarp();
+        const bool ok = stage_wait_warp(acc_full + 8 * acc, acc_phase, a.err);
         if (!group_all(1 + group, ok)) break;
         tcgen05_fence_after();
       }
+#pragma unroll 1
       for (int c = group * kEpiCols; c < kCols && r.row0 + c < r.row_end; c += 2 * kEpiCols) {
-        uint32_t v[32];
+        uint32_t v[2][16];
         if (r.len > 0) {
-          tmem_load_32(tmem + acc * kCols + c + (static_cast<uint32_t>(quarter * 32) << 16), v);
+          const uint32_t at = tmem + acc * kCols + c + (static_cast<uint32_t>(quarter * 32) << 16);
+          tmem_load_16x32(at, v[0]);
+          tmem_load_16x32(at + (16u << 16), v[1]);
           tmem_load_wait();
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0u;
+          for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0u;
         }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) buf[j * kTileM + quarter * 32 + lane] = __uint_as_float(v[j]);
-        group_sync(1 + group);
-        store_step(a, buf, tid, r.m0, r.row0 + c, r.row_end, b, bu);
-        group_sync(1 + group);
+        const int row0 = r.row0 + c;
+        const bool whole = kMode == kWeightGrad || row0 + kEpiCols <= r.row_end;
+        const int y = kMode == kWeightGrad ? r.c0 + c : row0;
+        if constexpr (kMode != kForward) {
+          epilogue_step<0>(a, &map_out, nullptr, v, b, buf, flip, group, tid, r.m0, row0, r.row_end, whole, y,
+                           kMode == kWeightGrad ? r.e : 0);
+        } else {
+          if (a.gated)
+            epilogue_step<2>(a, &map_out, &map_z, v, b, buf, flip, group, tid, r.m0, row0, r.row_end, whole, y, 0);
+          else
+            epilogue_step<1>(a, &map_out, &map_z, v, b, buf, flip, group, tid, r.m0, row0, r.row_end, whole, y, 0);
+        }
       }
       if (r.len > 0) {
         tcgen05_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (kCtas == 2)
-            mbar_arrive_cluster(cluster_addr(acc_empty(acc), 0));
-          else
-            mbar_arrive(acc_empty(acc));
-        }
+        if (lane == 0) mbar_arrive_cluster(lead_empty + 8 * acc);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
     }
+    __syncwarp();
+    if (quarter == 0 && elect_one()) bulk_wait();
   }
   __syncwarp();
   __syncthreads();
-  if (kCtas == 2) cluster_sync();  // neither CTA leaves while the other may still signal it
+  cluster_sync();  // neither CTA leaves while the other may still signal it
   if (warp == 1) {
     tcgen05_fence_after();
-    tmem_dealloc<kCtas>(tmem, C::tmem);
+    tmem_dealloc(tmem, C::tmem);
   }
 }
 
@@ -443,9 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-// Map of a row-major array of 16-bit elements: extents from the contiguous one outwards,
-// boxes 64 elements wide, 128-byte swizzle, zeros outside.
-bool make_map(CUtensorMap* map, bool bf16, const void* base, int rank, const int64_t* dims, const int* box) {
+// Map of an array of 16-bit elements: extents from the contiguous one outwards, strides (in
+// elements) from the second, boxes 64 elements wide, 128-byte swizzle, zeros outside.
+bool make_map(CUtensorMap* map, bool bf16, const void* base, int rank, const int64_t* dims, const int64_t* strides,
+              const int* box) {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -454,112 +642,140 @@ bool make_map(CUtensorMap* map, bool bf16, const void* base, int rank, const int
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   if (!g_encode) return false;
-  cuuint64_t d[4], st[3];
-  cuuint32_t b[4], es[4];
-  uint64_t bytes = 2;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5];
   for (int i = 0; i < rank; ++i) {
     d[i] = static_cast<cuuint64_t>(dims[i]);
     b[i] = static_cast<cuuint32_t>(box[i]);
     es[i] = 1;
-    bytes *= d[i];
-    if (i + 1 < rank) st[i] = bytes;
+    if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]) * 2;
   }
   return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
                   const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kCols, int kCtas>
-cudaError_t launch_tiles(const Args& a, const CUtensorMap& ma, const CUtensorMap& mb, int64_t most_tiles, int num_sms,
+template <int kMode, int kCols>
+cudaError_t launch_tiles(const Args& a, const CUtensorMap (&maps)[4], int64_t most_tiles, int num_sms,
                          cudaStream_t st) {
-  const int units = num_sms / kCtas;
-  const int grid = static_cast<int>(most_tiles < units ? most_tiles : units) * kCtas;
+  const int pairs = num_sms / 2;
+  const int grid = static_cast<int>(most_tiles < pairs ? most_tiles : pairs) * 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Config<kCols, kCtas>::smem;
+  cfg.dynamicSmemBytes = Config<kCols>::smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = kCtas == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<kCols, kCtas>, a, ma, mb);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<kMode, kCols>, a, maps[0], maps[1], maps[2], maps[3]);
 }
 
-template <int kCols, int kCtas>
+template <int kMode, int kCols>
 cudaError_t init_tiles() {
-  return cudaFuncSetAttribute(linear_kernel<kCols, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Config<kCols, kCtas>::smem);
+  return cudaFuncSetAttribute(linear_kernel<kMode, kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Config<kCols>::smem);
 }
 
-struct Shape {
-  int cols, ctas;
-};
-
-Shape choose(const LinearDims& s, int mode, int num_sms) {
-  (void)num_sms;
-  if (mode == kWeightGrad) return s.Nw() <= 64 ? Shape{64, 1} : s.Nw() <= 128 ? Shape{128, 1} : Shape{256, 1};
-  const int rows = s.grouped ? (s.R + s.E - 1) / s.E * 3 / 2 : s.R;
-  if (rows <= 32) return {32, 1};
-  if (rows <= 64) return {64, 1};
-  if (rows <= 128) return {128, 1};
-  return {256, 1};
+// Columns of a tile.  Rows by experts: the average rows of an expert with room for uneven
+// loads (a tile's unused columns cost its time, tiles of an expert beyond the first its
+// weights once more from L2).  Otherwise the fewest microseconds of: waves of tiles over the
+// pairs of SMs, times 64-element steps of the measured 0.15, 0.2 and 0.32 us for 32, 128 and
+// 256 columns, plus the last tile's epilogue.
+int choose_cols(const LinearDims& s, int mode, int tiles_m, int depth, int num_sms) {
+  if (s.grouped && mode != kWeightGrad) {
+    const int rows = (s.R + s.E - 1) / s.E;
+    return rows <= 22 ? 32 : rows <= 176 ? 128 : 256;
+  }
+  const int c = mode == kWeightGrad ? s.Nw() : s.R;
+  const int64_t groups = mode == kWeightGrad ? s.E : 1;
+  const auto cost = [&](int cols, int per_step, int last) {
+    const int64_t tiles = groups * tiles_m * ((c + cols - 1) / cols), pairs = num_sms / 2;
+    return (tiles + pairs - 1) / pairs * ((depth + 63) / 64) * per_step + last;
+  };
+  const int64_t c32 = mode == kWeightGrad ? INT64_MAX : cost(32, 15, 50), c128 = cost(128, 20, 100),
+                c256 = cost(256, 32, 200);
+  return c32 < c128 && c32 < c256 ? 32 : c128 < c256 ? 128 : 256;
 }
 
 cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, const void* x, const void* w, const void* dz,
                      Args& a, int num_sms, cudaStream_t st) {
-  const Shape sh = choose(s, mode, num_sms);
-  const int cols = sh.cols / sh.ctas;
   a.offsets = offsets;
-  a.mode = mode;
   a.R = s.R;
   a.E = s.E;
-  a.K = s.K;
   a.N = s.N;
   a.Nw = s.Nw();
   a.bf16 = s.type;
   a.width = mode == kForward ? s.N : s.K;
-  a.tile_m = a.gated ? 64 : 128;
-  a.tiles_m = (a.width + a.tile_m * sh.ctas - 1) / (a.tile_m * sh.ctas);
-  a.tiles_c = (a.Nw + sh.cols - 1) / sh.cols;
+  a.tile_m = a.gated ? 64 : kTileM;
+  a.tiles_m = (a.width + 2 * a.tile_m - 1) / (2 * a.tile_m);
   a.depth = mode == kForward ? s.K : a.Nw;
-  a.word = mma_word(s.type == 1, mode != kForward, mode == kWeightGrad, 128 * sh.ctas, sh.cols);
-  CUtensorMap ma, mb;
+  int cols = choose_cols(s, mode, a.tiles_m, mode == kWeightGrad ? (s.R + s.E - 1) / s.E : a.depth, num_sms);
+  const int depth = cols == 256 ? Config<256>::depth : Config<128>::depth;
+  a.tiles_c = (a.Nw + cols - 1) / cols;
+  a.word = mma_word(s.type == 1, mode != kForward, mode == kWeightGrad, 2 * kTileM, cols);
+  CUtensorMap maps[4] = {};  // A, B, output, saved z
   bool ok;
+  const bool bf16 = s.type == 1;
   const int64_t K = s.K, R = s.R, E = s.E, Nw = a.Nw;
   if (mode == kForward) {
-    const int64_t da[4] = {K, s.N, s.gated ? 2 : 1, E}, db[2] = {K, R};
-    const int ba[4] = {kDepth, a.tile_m, s.gated ? 2 : 1, 1}, bb[2] = {kDepth, cols};
-    ok = make_map(&ma, s.type == 1, w, 4, da, ba) && make_map(&mb, s.type == 1, x, 2, db, bb);
+    // rows in blocks of 8, a gated weight's gate and up blocks in turn
+    const int64_t da[5] = {K, 8, s.gated ? 2 : 1, s.N / 8, E}, sa[4] = {K, s.N * K, 8 * K, Nw * K};
+    const int ba[5] = {64, 8, s.gated ? 2 : 1, a.tile_m / 8, 1};
+    const int64_t db[2] = {K, R}, sb[1] = {K};
+    const int bb[2] = {64, cols / 2};
+    ok = make_map(&maps[0], bf16, w, 5, da, sa, ba) && make_map(&maps[1], bf16, x, 2, db, sb, bb);
   } else if (mode == kInputGrad) {
-    const int64_t da[3] = {K, Nw, E}, db[2] = {Nw, R};
-    const int ba[3] = {64, kDepth, 1}, bb[2] = {kDepth, cols};
-    ok = make_map(&ma, s.type == 1, w, 3, da, ba) && make_map(&mb, s.type == 1, dz, 2, db, bb);
+    const int64_t da[3] = {K, Nw, E}, sa[2] = {K, Nw * K}, db[2] = {Nw, R}, sb[1] = {Nw};
+    const int ba[3] = {64, depth, 1}, bb[2] = {64, cols / 2};
+    ok = make_map(&maps[0], bf16, w, 3, da, sa, ba) && make_map(&maps[1], bf16, dz, 2, db, sb, bb);
   } else {
-    const int64_t da[2] = {K, R}, db[2] = {Nw, R};
-    const int bx[2] = {64, kDepth};
-    ok = make_map(&ma, s.type == 1, x, 2, da, bx) && make_map(&mb, s.type == 1, dz, 2, db, bx);
+    const int64_t da[2] = {K, R}, sa[1] = {K}, db[2] = {Nw, R}, sb[1] = {Nw};
+    const int box[2] = {64, depth};
+    ok = make_map(&maps[0], bf16, x, 2, da, sa, box) && make_map(&maps[1], bf16, dz, 2, db, sb, box);
+  }
+  const int64_t width = a.width, planes = mode == kWeightGrad ? E : 1, lines = mode == kWeightGrad ? Nw : R;
+  const int64_t dout[3] = {width, lines, planes}, sout[2] = {width, width * lines};
+  const int bout[3] = {64, kEpiCols, 1};
+  ok = ok && make_map(&maps[2], bf16, a.out, 3, dout, sout, bout);
+  if (a.preact) {
+    const int64_t dzm[3] = {width, s.gated ? 2 : 1, R}, szm[2] = {width, Nw};
+    const int bzm[3] = {64, 1, kEpiCols};
+    ok = ok && make_map(&maps[3], bf16, a.preact, 3, dzm, szm, bzm);
   }
   if (!ok) return cudaErrorInvalidValue;
   const int64_t most = mode == kWeightGrad ? E * a.tiles_m * a.tiles_c
-                                           : int64_t(a.tiles_m) * ((R + sh.cols - 1) / sh.cols + (offsets ? E : 0));
-  if (sh.cols == 32) return launch_tiles<32, 1>(a, ma, mb, most, num_sms, st);
-  if (sh.cols == 64) return launch_tiles<64, 1>(a, ma, mb, most, num_sms, st);
-  if (sh.cols == 128) return launch_tiles<128, 1>(a, ma, mb, most, num_sms, st);
-  return launch_tiles<256, 1>(a, ma, mb, most, num_sms, st);
+                                           : int64_t(a.tiles_m) * ((R + cols - 1) / cols + (offsets ? E : 0));
+  if (mode == kForward) {
+    if (cols == 32) return launch_tiles<kForward, 32>(a, maps, most, num_sms, st);
+    if (cols == 128) return launch_tiles<kForward, 128>(a, maps, most, num_sms, st);
+    return launch_tiles<kForward, 256>(a, maps, most, num_sms, st);
+  }
+  if (mode == kInputGrad) {
+    if (cols == 32) return launch_tiles<kInputGrad, 32>(a, maps, most, num_sms, st);
+    if (cols == 128) return launch_tiles<kInputGrad, 128>(a, maps, most, num_sms, st);
+    return launch_tiles<kInputGrad, 256>(a, maps, most, num_sms, st);
+  }
+  if (cols == 128) return launch_tiles<kWeightGrad, 128>(a, maps, most, num_sms, st);
+  return launch_tiles<kWeightGrad, 256>(a, maps, most, num_sms, st);
 }
 
 }  // namespace
 
 cudaError_t init_linear_kernels() {
-  cudaError_t err = init_tiles<32, 1>();
-  if (err == cudaSuccess) err = init_tiles<64, 1>();
-  if (err == cudaSuccess) err = init_tiles<128, 1>();
-  if (err == cudaSuccess) err = init_tiles<256, 1>();
+  cudaError_t err = init_tiles<kForward, 32>();
+  if (err == cudaSuccess) err = init_tiles<kForward, 128>();
+  if (err == cudaSuccess) err = init_tiles<kForward, 256>();
+  if (err == cudaSuccess) err = init_tiles<kInputGrad, 32>();
+  if (err == cudaSuccess) err = init_tiles<kInputGrad, 128>();
+  if (err == cudaSuccess) err = init_tiles<kInputGrad, 256>();
+  if (err == cudaSuccess) err = init_tiles<kWeightGrad, 128>();
+  if (err == cudaSuccess) err = init_tiles<kWeightGrad, 256>();
   return err;
 }
 
