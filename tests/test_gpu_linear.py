@@ -209,7 +209,7 @@ class Grad:
             self.dx[i:j], self.dw[e], self.db[e] = z @ w, z.T @ x, z.sum(0)
             self.e_dx[i:j] = ez @ w.abs() + (c.Nw + 2) * T23 * a
             self.e_dw[e] = ez.T @ x.abs() + (j - i + 2) * T23 * b
-            # 16 rows a thread, eight threads, then up to 1 + rows / 128 partial sums
+            # at most 16 rows a thread, eight threads, then up to 1 + rows / 128 partial sums in a row
             self.e_db[e] = e_dz[i:j].sum(0) + (26 + (j - i) / 128) * T23 * z.abs().sum(0) + 1e-12
             s_dx, s_dw = s_dx + float(a.norm()) ** 2, s_dw + float(b.norm()) ** 2
         self.e_dx = (1 + u) * self.e_dx + u * self.dx.abs() + SMALL[c.typ]

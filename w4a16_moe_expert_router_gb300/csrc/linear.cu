@@ -17,7 +17,7 @@
 //
 // Persistent pairs of CTAs (two SMs on one tile of 256 outputs x kCols rows, each
 // holding its 128 outputs of A and half of B) walk a list of tiles: a thread of each
-// loads 64-element stages of A and B by TMA, one thread of the pair issues the matrix
+// loads stages of A and B by TMA, one thread of the pair issues the matrix
 // instructions into one of two accumulators in tensor memory, and eight warps of each
 // empty the other one: 32 columns at a time through shared memory, so that the outputs
 // leave as 16-byte pieces of contiguous rows.  Accumulation, bias, activation and residual are in fp32,
@@ -37,9 +37,12 @@ namespace {
 
 constexpr int kForward = 0, kInputGrad = 1, kWeightGrad = 2;
 constexpr int kTileM = 128;            // lanes of tensor memory: outputs of one CTA's half of a tile
-constexpr int kEpiCols = 32;           // columns per epilogue step
-constexpr int kStepBytes = kEpiCols * kTileM * 2;  // 16-bit values of one step
-constexpr int kEpiBytes = 2 * kStepBytes;          // two steps per group of four epilogue warps
+// Columns per epilogue step: 64 for the weight gradient, whose tiles are a few stages long by
+// experts, so that the epilogue's fences, barriers and stores bound it (16384 rows over 128 experts, 2048 x 1408: 161 -> 149 us).
+template <int kMode>
+constexpr int step_cols = kMode == kWeightGrad ? 64 : 32;
+template <int kMode>
+constexpr int step_bytes = step_cols<kMode> * kTileM * 2;
 constexpr int kThreads = 384;          // TMA, MMA, tail and one idle warp, then 8 epilogue warps
 constexpr int kMaxStages = 8;
 constexpr int kSmemLimit = 227 * 1024;
@@ -55,9 +58,11 @@ struct Args {
   int width;    // extent of m, and the row length of out
   int tile_m;   // outputs per CTA and tile (64 of a gate and their ups, or 128)
   int tiles_m;  // tiles along m
+  uint64_t per_m;  // ceil(2^40 / tiles_m): i / tiles_m = i per_m >> 40 for i < 2^30 (tiles_m <= 1024)
   int tiles_c;  // weight grad: tiles along c
   int depth;    // contraction length (weight grad: the expert's rows)
   uint32_t word;
+  int one_store;  // the output's map takes a step in one store (see run_mode)
 };
 
 // A stage holds 64 contraction elements of the largest tile and 128 of the smaller ones: a
@@ -65,7 +70,7 @@ struct Args {
 // tiles of 32 columns 814 -> 514 us on 8192 x 2048 x 8192, of 128 columns 219 -> 171 us),
 // which is below the matrix instructions' time at 256 columns only, and there six short
 // stages hide latency better than three long ones (141 against 146 us).
-template <int kCols>
+template <int kMode, int kCols>
 struct Config {
   static constexpr int depth = kCols == 256 ? 64 : 128;
   static constexpr int cols = kCols / 2;  // columns whose B rows each CTA loads
@@ -73,7 +78,8 @@ struct Config {
   static constexpr int b_bytes = cols * depth * 2;
   static constexpr int box_bytes = depth * 128;  // 64 elements of each of a stage's contraction rows
   static constexpr int stage = a_bytes + b_bytes;
-  static constexpr int fixed = 2 * kEpiBytes + (2 * (kMaxExperts + 1) + 2) * 4 + (4 * kMaxStages + 5) * 8 + 16;
+  static constexpr int epi_bytes = 2 * step_bytes<kMode>;  // two steps per group of four epilogue warps
+  static constexpr int fixed = 2 * epi_bytes + (2 * (kMaxExperts + 1) + 2) * 4 + (4 * kMaxStages + 5) * 8 + 16;
   static constexpr int fit = (kSmemLimit - fixed) / stage;
   static constexpr int stages = fit < kMaxStages ? fit : kMaxStages;
   static constexpr int smem = stages * stage + fixed;
@@ -89,7 +95,7 @@ template <int kMode, int kCols>
 __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const int* off, int t, int& e, int rank) {
   while (t >= start[e + 1]) ++e;  // t only grows
   const int i = t - start[e];
-  const int c = i / a.tiles_m, m = i - c * a.tiles_m;
+  const int c = static_cast<int>(i * a.per_m >> 40), m = i - c * a.tiles_m;
   Tile r;
   r.e = e;
   r.m0 = (m * 2 + rank) * a.tile_m;
@@ -162,20 +168,20 @@ __device__ __forceinline__ void activate_all(float (&z)[kCount], int act) {
 // expert's.  A gated tile's lanes alternate, 8 of the gate and the 8 of the up product with
 // the same outputs, so a thread holds both.
 
-// Place of chunk `chunk` of column c in a step buffer: 64 outputs (8 chunks) of the 32 columns,
-// then the other 64, each in the 128-byte swizzle of a TMA box.
-constexpr int kHalfStep = kStepBytes / 2;
+// Place of chunk `chunk` of column c in a step buffer: 64 outputs (8 chunks) of the step's
+// columns, then the other 64, each in the 128-byte swizzle of a TMA box.
+template <int kStep>
 __device__ __forceinline__ uint32_t chunk_at(int c, int chunk) {
-  return static_cast<uint32_t>((chunk >> 3) * kHalfStep + c * 128 + ((chunk ^ c) & 7) * 16);
+  return static_cast<uint32_t>((chunk >> 3) * (kStep * 128) + c * 128 + ((chunk ^ c) & 7) * 16);
 }
 
-// The rows of a step buffer to global memory (or back, for the residual): thread tid of 128
-// takes chunk tid % kChunks of every (128 / kChunks)-th column.  f: first column of `p` in
-// elements, valid while f < width; rows of stride `ld` from row0 on, those below row_end.
+// The rows of a 32-column step buffer to global memory (or back, for the residual): thread tid
+// of 128 takes chunk tid % kChunks of every (128 / kChunks)-th column.  f: first column of `p`
+// in elements, valid while f < width; rows of stride `ld` from row0 on, those below row_end.
 template <int kChunks, bool kLoad, typename Ptr>
 __device__ __forceinline__ void move_rows(uint8_t* buf, Ptr* p, int tid, int f, int width, int ld, int row0,
                                           int row_end) {
-  constexpr int rows = 128 / kChunks, passes = kEpiCols / rows;
+  constexpr int rows = 128 / kChunks, passes = 32 / rows;
   const int chunk = tid % kChunks, c0 = tid / kChunks;
   if (f >= width) return;
   uint4 v[passes];
@@ -183,7 +189,7 @@ __device__ __forceinline__ void move_rows(uint8_t* buf, Ptr* p, int tid, int f, 
   for (int i = 0; i < passes; ++i) {
     const int c = c0 + i * rows;
     if (!kLoad)
-      v[i] = *reinterpret_cast<const uint4*>(buf + chunk_at(c, chunk));
+      v[i] = *reinterpret_cast<const uint4*>(buf + chunk_at<32>(c, chunk));
     else if (row0 + c < row_end)
       v[i] = *reinterpret_cast<const uint4*>(p + static_cast<size_t>(row0 + c) * ld + f);
   }
@@ -191,134 +197,172 @@ __device__ __forceinline__ void move_rows(uint8_t* buf, Ptr* p, int tid, int f, 
   for (int i = 0; i < passes; ++i) {
     const int c = c0 + i * rows;
     if constexpr (kLoad) {
-      if (row0 + c < row_end) *reinterpret_cast<uint4*>(buf + chunk_at(c, chunk)) = v[i];
+      if (row0 + c < row_end) *reinterpret_cast<uint4*>(buf + chunk_at<32>(c, chunk)) = v[i];
     } else {
       if (row0 + c < row_end) *reinterpret_cast<uint4*>(p + static_cast<size_t>(row0 + c) * ld + f) = v[i];
     }
   }
 }
 
-// kForm: 0 without bias, activation, residual or saved z (the gradients' products), 1 forward,
-// 2 forward gated.  b: the biases of the thread's lanes g, g + 8, g + 16, g + 24 of its quarter.
-// buf: the group's two step buffers.  whole: the step's rows all belong to the tile (map_out
-// clips those past the end of the array); they are row0 .. of the output, y .. of plane z of
-// the map.
-template <int kForm>
-__device__ __forceinline__ void epilogue_step(const Args& a, const CUtensorMap* map_out, const CUtensorMap* map_z,
-                                              uint32_t (&v)[2][16], const float (&b)[4], uint8_t* buf, int& flip,
-                                              int group, int tid, int m0, int row0, int row_end, bool whole, int y,
-                                              int z_plane) {
-  constexpr int chunks = kForm == 2 ? 8 : 16;  // 16-byte chunks of outputs per column
-  const int lane = tid & 31, quarter = tid >> 5;
-  const int f = m0 + (tid % chunks) * 8;
-  uint8_t* const ybuf = kForm > 0 && a.preact ? buf : buf + flip * kStepBytes;
-  uint8_t* const zbuf = buf + kStepBytes;
-  flip ^= 1;
-  if (kForm > 0 && a.residual) {
-    move_rows<chunks, true>(ybuf, a.residual, tid, f, a.width, a.width, row0, row_end);
-    group_sync(1 + group);
-  }
-  const int sub = lane >> 3, j = lane & 7;  // the block and row whose address this lane gives
-  if (kForm != 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // block column i: the four blocks of 8 lanes
-      float z[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) z[k] = __uint_as_float(v[k >> 2][4 * i + (k & 3)]);
-      const uint32_t at = chunk_at(8 * i + j, quarter * 4 + sub);
-      uint32_t r[4];
-      if (kForm == 1) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) z[k] += b[k >> 1];
-        if (a.preact) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) r[k] = pack2(z[2 * k], z[2 * k + 1], a.bf16);
-          store_blocks_transposed(smem_addr(zbuf) + at, r);
-        }
-        activate_all(z, a.act);
-        if (a.residual) {
-          load_blocks_transposed(smem_addr(ybuf) + at, r);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 g = unpack2(r[k], a.bf16);
-            z[2 * k] += g.x;
-            z[2 * k + 1] += g.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) r[k] = pack2(z[2 * k], z[2 * k + 1], a.bf16);
-      store_blocks_transposed(smem_addr(ybuf) + at, r);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {  // block columns i and i + 1 of both halves
-      float z[8], u[8];               // [column][half][2]
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int at = 4 * (i + (k >> 2)) + (k & 1), h = (k >> 1) & 1;
-        z[k] = __uint_as_float(v[h][at]) + b[2 * h];
-        u[k] = __uint_as_float(v[h][at + 2]) + b[2 * h + 1];
-      }
-      const int c = 8 * (i + (sub >> 1)) + j, chunk = quarter * 2 + (sub & 1);
-      uint32_t r[4];
-      if (a.preact) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] = pack2(z[2 * k], z[2 * k + 1], a.bf16);
-        store_blocks_transposed(smem_addr(zbuf) + chunk_at(c, chunk), r);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] = pack2(u[2 * k], u[2 * k + 1], a.bf16);
-        store_blocks_transposed(smem_addr(zbuf) + chunk_at(c, 8 + chunk), r);
-      }
-      activate_all(z, a.act);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) z[k] *= u[k];
-      const uint32_t at = chunk_at(c, chunk);
-      if (a.residual) {
-        load_blocks_transposed(smem_addr(ybuf) + at, r);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 g = unpack2(r[k], a.bf16);
-          z[2 * k] += g.x;
-          z[2 * k + 1] += g.y;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) r[k] = pack2(z[2 * k], z[2 * k + 1], a.bf16);
-      store_blocks_transposed(smem_addr(ybuf) + at, r);
-    }
-  }
-  // one thread stores for the group; its last store has read the other buffer by now, which
-  // the barrier tells the rest
-  const bool issuer = quarter == 0 && elect_one();
-  if (whole) fence_proxy_async();
+// Where the rows of an epilogue step go.
+struct StepRows {
+  int m0, row0, row_end;
+  bool whole;  // the rows all belong to the tile (the maps clip those past the end of the array)
+  int y, z;    // the rows in the output's map: row y of plane z
+};
+
+// The group's step buffer `buf`, all blocks stored, to the output (kSaved: to the saved z).
+// One thread stores for the group; the store before has read the other buffer by now, which
+// the barrier tells the rest, so that the two buffers may be taken in turn.
+template <int kForm, int kStep, bool kSaved>
+__device__ __forceinline__ void send_step(const Args& a, const CUtensorMap* map, uint8_t* buf, int group, int tid,
+                                          const StepRows& r) {
+  const bool issuer = (tid >> 5) == 0 && elect_one();
+  if (r.whole) fence_proxy_async();
   if (issuer) bulk_wait_read();
   group_sync(1 + group);
-  if (whole) {
-    if (issuer && m0 < a.width) {
-      tma_store_3d(map_out, smem_addr(ybuf), m0, y, z_plane);
-      if (kForm != 2 && m0 + 64 < a.width) tma_store_3d(map_out, smem_addr(ybuf) + kHalfStep, m0 + 64, y, z_plane);
-      if (kForm > 0 && a.preact) {  // planes of map_z: gate, up
-        tma_store_3d(map_z, smem_addr(zbuf), m0, 0, y);
-        if (kForm == 2)
-          tma_store_3d(map_z, smem_addr(zbuf) + kHalfStep, m0, 1, y);
-        else if (m0 + 64 < a.width)
-          tma_store_3d(map_z, smem_addr(zbuf) + kHalfStep, m0 + 64, 0, y);
+  if (r.whole) {
+    if (issuer && r.m0 < a.width) {
+      const uint32_t src = smem_addr(buf);
+      constexpr int half = kStep * 128;
+      if (!kSaved) {
+        if (a.one_store) {
+          tma_store_4d(map, src, 0, r.y, r.m0 >> 6, r.z);
+        } else {
+          tma_store_4d(map, src, r.m0, r.y, 0, r.z);
+          if (kForm != 2 && r.m0 + 64 < a.width) tma_store_4d(map, src + half, r.m0 + 64, r.y, 0, r.z);
+        }
+      } else if (kForm == 2) {  // planes: gate, up
+        tma_store_3d(map, src, r.m0, 0, r.y);
+        tma_store_3d(map, src + half, r.m0, 1, r.y);
+      } else {
+        tma_store_3d(map, src, r.m0, 0, r.y);
+        if (r.m0 + 64 < a.width) tma_store_3d(map, src + half, r.m0 + 64, 0, r.y);
       }
       bulk_commit();
     }
-  } else {
-    move_rows<chunks, false>(ybuf, a.out, tid, f, a.width, a.width, row0, row_end);
-    if (kForm > 0 && a.preact) {
-      const int zc = tid % 16, zf = kForm == 2 ? m0 + (zc & 7) * 8 : m0 + zc * 8;
-      move_rows<16, false>(zbuf, kForm == 2 && zc >= 8 ? a.preact + a.N : a.preact, tid, zf, a.width, a.Nw, row0,
-                           row_end);
+  } else if constexpr (kStep == 32) {
+    if (kSaved) {
+      const int chunk = tid % 16;
+      move_rows<16, false>(buf, kForm == 2 && chunk >= 8 ? a.preact + a.N : a.preact, tid,
+                           r.m0 + (kForm == 2 ? chunk & 7 : chunk) * 8, a.width, a.Nw, r.row0, r.row_end);
+    } else {
+      constexpr int chunks = kForm == 2 ? 8 : 16;
+      move_rows<chunks, false>(buf, a.out, tid, r.m0 + tid % chunks * 8, a.width, a.width, r.row0, r.row_end);
     }
   }
-  if (kForm > 0 && a.preact) {  // both buffers are taken: the next step waits for them
-    if (issuer) bulk_wait_read();
+}
+
+// A step of the gradients' products: kStep columns from `tmem` on (zeros where the tile has no
+// contraction), rounded.  buf: the group's two step buffers, the next one to take is `flip`.
+template <int kStep>
+__device__ __forceinline__ void gradient_step(const Args& a, const CUtensorMap* map_out, uint32_t tmem, bool any,
+                                              uint8_t* buf, int& flip, int group, int tid, const StepRows& rows) {
+  const int lane = tid & 31, quarter = tid >> 5;
+  const int sub = lane >> 3, j = lane & 7;  // the block and row whose address this lane gives
+  uint32_t v[kStep / 32][2][16];
+  if (any) {
+#pragma unroll
+    for (int h = 0; h < kStep / 32; ++h) {
+      tmem_load_16x32(tmem + 32 * h, v[h][0]);
+      tmem_load_16x32(tmem + 32 * h + (16u << 16), v[h][1]);
+    }
+    tmem_load_wait();
+  } else {
+#pragma unroll
+    for (int h = 0; h < kStep / 32; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[h][0][i] = v[h][1][i] = 0u;
+  }
+  uint8_t* const ybuf = buf + flip * (kStep * kTileM * 2);
+  flip ^= 1;
+#pragma unroll
+  for (int i = 0; i < kStep / 8; ++i) {  // block column i: the four blocks of 8 lanes
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t* const p = &v[i >> 2][k >> 1][4 * (i & 3) + 2 * (k & 1)];
+      r[k] = pack2(__uint_as_float(p[0]), __uint_as_float(p[1]), a.bf16);
+    }
+    store_blocks_transposed(smem_addr(ybuf) + chunk_at<kStep>(8 * i + j, quarter * 4 + sub), r);
+  }
+  send_step<0, kStep, false>(a, map_out, ybuf, group, tid, rows);
+}
+
+// A forward step of 32 columns.  kForm: 1 plain, 2 gated.  b: the biases of the thread's lanes
+// g, g + 8, g + 16, g + 24 of its quarter.
+template <int kForm>
+__device__ __forceinline__ void forward_step(const Args& a, const CUtensorMap* map_out, const CUtensorMap* map_z,
+                                             uint32_t tmem, const float (&b)[4], uint8_t* buf, int& flip, int group,
+                                             int tid, const StepRows& rows) {
+  constexpr int chunks = kForm == 2 ? 8 : 16;  // 16-byte chunks of outputs per column
+  const int lane = tid & 31, quarter = tid >> 5;
+  const int sub = lane >> 3, j = lane & 7;
+  uint32_t v[2][16];
+  tmem_load_16x32(tmem, v[0]);
+  tmem_load_16x32(tmem + (16u << 16), v[1]);
+  tmem_load_wait();
+  float z[2][16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[h][i] = __uint_as_float(v[h][i]) + b[2 * h + (i >> 1 & 1)];
+  if (a.preact) {
+    uint8_t* const zbuf = buf + flip * step_bytes<kForward>;
+    flip ^= 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // gated: chunks 0 .. 7 of the gate, 8 .. 15 of the up product
+      uint32_t r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = pack2(z[k >> 1][4 * i + 2 * (k & 1)], z[k >> 1][4 * i + 2 * (k & 1) + 1], a.bf16);
+      const int chunk = kForm == 2 ? (sub & 1) * 8 + quarter * 2 + (sub >> 1) : quarter * 4 + sub;
+      store_blocks_transposed(smem_addr(zbuf) + chunk_at<32>(8 * i + j, chunk), r);
+    }
+    send_step<kForm, 32, true>(a, map_z, zbuf, group, tid, rows);
+  }
+  uint8_t* const ybuf = buf + flip * step_bytes<kForward>;
+  flip ^= 1;
+  if (a.residual) {
+    move_rows<chunks, true>(ybuf, a.residual, tid, rows.m0 + tid % chunks * 8, a.width, a.width, rows.row0,
+                            rows.row_end);
     group_sync(1 + group);
   }
+#pragma unroll
+  for (int i = 0; i < 4; i += (kForm == 2 ? 2 : 1)) {  // block column i (gated: i and i + 1)
+    float y[8];                                        // [block][2]
+    if (kForm == 2) {
+      float u[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = 4 * (i + (k >> 2)) + (k & 1), h = k >> 1 & 1;
+        y[k] = z[h][at];
+        u[k] = z[h][at + 2];
+      }
+      activate_all(y, a.act);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] *= u[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = z[k >> 2][4 * i + (k & 3)];
+      activate_all(y, a.act);
+    }
+    const uint32_t at = smem_addr(ybuf) + (kForm == 2 ? chunk_at<32>(8 * (i + (sub >> 1)) + j, quarter * 2 + (sub & 1))
+                                                      : chunk_at<32>(8 * i + j, quarter * 4 + sub));
+    uint32_t r[4];
+    if (a.residual) {
+      load_blocks_transposed(at, r);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 g = unpack2(r[k], a.bf16);
+        y[2 * k] += g.x;
+        y[2 * k + 1] += g.y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = pack2(y[2 * k], y[2 * k + 1], a.bf16);
+    store_blocks_transposed(at, r);
+  }
+  send_step<kForm, 32, false>(a, map_out, ybuf, group, tid, rows);
 }
 
 template <int kMode, int kCols>
@@ -327,11 +371,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                                                              const __grid_constant__ CUtensorMap map_b,
                                                              const __grid_constant__ CUtensorMap map_out,
                                                              const __grid_constant__ CUtensorMap map_z) {
-  using C = Config<kCols>;
+  using C = Config<kMode, kCols>;
   constexpr int kDepth = C::depth;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const epi = smem + C::stages * C::stage;
-  int* const start = reinterpret_cast<int*>(epi + 2 * kEpiBytes);  // [E + 1]
+  int* const start = reinterpret_cast<int*>(epi + 2 * C::epi_bytes);  // [E + 1]
   int* const off = start + kMaxExperts + 1;                        // [E + 1]
   uint64_t* const bars = reinterpret_cast<uint64_t*>(off + kMaxExperts + 1 + 2);
   const uint32_t bar0 = smem_addr(bars);
@@ -559,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   } else if (warp >= 4) {
     // ---- epilogue: two groups of four warps take the 32-column steps in turn
     const int group = (warp - 4) >> 2, tid = threadIdx.x & 127, quarter = warp & 3;
-    uint8_t* const buf = epi + group * kEpiBytes;
+    uint8_t* const buf = epi + group * C::epi_bytes;
     const uint32_t lead_empty = cluster_addr(acc_empty, 0);
     int e = 0, acc = 0, flip = 0;
     uint32_t acc_phase = 0;
@@ -580,29 +624,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         if (!group_all(1 + group, ok)) break;
         tcgen05_fence_after();
       }
+      constexpr int kStep = step_cols<kMode>;
 #pragma unroll 1
-      for (int c = group * kEpiCols; c < kCols && r.row0 + c < r.row_end; c += 2 * kEpiCols) {
-        uint32_t v[2][16];
-        if (r.len > 0) {
-          const uint32_t at = tmem + acc * kCols + c + (static_cast<uint32_t>(quarter * 32) << 16);
-          tmem_load_16x32(at, v[0]);
-          tmem_load_16x32(at + (16u << 16), v[1]);
-          tmem_load_wait();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0u;
-        }
+      for (int c = group * kStep; c < kCols && r.row0 + c < r.row_end; c += 2 * kStep) {
+        const uint32_t at = tmem + acc * kCols + c + (static_cast<uint32_t>(quarter * 32) << 16);
         const int row0 = r.row0 + c;
-        const bool whole = kMode == kWeightGrad || row0 + kEpiCols <= r.row_end;
-        const int y = kMode == kWeightGrad ? r.c0 + c : row0;
+        const StepRows rows{r.m0, row0, r.row_end, kMode == kWeightGrad || row0 + kStep <= r.row_end,
+                            kMode == kWeightGrad ? r.c0 + c : row0, kMode == kWeightGrad ? r.e : 0};
         if constexpr (kMode != kForward) {
-          epilogue_step<0>(a, &map_out, nullptr, v, b, buf, flip, group, tid, r.m0, row0, r.row_end, whole, y,
-                           kMode == kWeightGrad ? r.e : 0);
+          gradient_step<kStep>(a, &map_out, at, r.len > 0, buf, flip, group, tid, rows);
         } else {
           if (a.gated)
-            epilogue_step<2>(a, &map_out, &map_z, v, b, buf, flip, group, tid, r.m0, row0, r.row_end, whole, y, 0);
+            forward_step<2>(a, &map_out, &map_z, at, b, buf, flip, group, tid, rows);
           else
-            epilogue_step<1>(a, &map_out, &map_z, v, b, buf, flip, group, tid, r.m0, row0, r.row_end, whole, y, 0);
+            forward_step<1>(a, &map_out, &map_z, at, b, buf, flip, group, tid, rows);
         }
       }
       if (r.len > 0) {
@@ -669,7 +704,7 @@ cudaError_t launch_tiles(const Args& a, const CUtensorMap (&maps)[4], int64_t mo
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Config<kCols>::smem;
+  cfg.dynamicSmemBytes = Config<kMode, kCols>::smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -679,7 +714,7 @@ cudaError_t launch_tiles(const Args& a, const CUtensorMap (&maps)[4], int64_t mo
 template <int kMode, int kCols>
 cudaError_t init_tiles() {
   return cudaFuncSetAttribute(linear_kernel<kMode, kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Config<kCols>::smem);
+                              Config<kMode, kCols>::smem);
 }
 
 // Columns of a tile.  Rows by experts: the average rows of an expert with room for uneven
@@ -714,9 +749,10 @@ cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, cons
   a.width = mode == kForward ? s.N : s.K;
   a.tile_m = a.gated ? 64 : kTileM;
   a.tiles_m = (a.width + 2 * a.tile_m - 1) / (2 * a.tile_m);
+  a.per_m = ((uint64_t(1) << 40) + a.tiles_m - 1) / a.tiles_m;
   a.depth = mode == kForward ? s.K : a.Nw;
   int cols = choose_cols(s, mode, a.tiles_m, mode == kWeightGrad ? (s.R + s.E - 1) / s.E : a.depth, num_sms);
-  const int depth = cols == 256 ? Config<256>::depth : Config<128>::depth;
+  const int depth = cols == 256 ? Config<kForward, 256>::depth : Config<kForward, 128>::depth;
   a.tiles_c = (a.Nw + cols - 1) / cols;
   a.word = mma_word(s.type == 1, mode != kForward, mode == kWeightGrad, 2 * kTileM, cols);
   CUtensorMap maps[4] = {};  // A, B, output, saved z
@@ -740,12 +776,22 @@ cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, cons
     ok = make_map(&maps[0], bf16, x, 2, da, sa, box) && make_map(&maps[1], bf16, dz, 2, db, sb, box);
   }
   const int64_t width = a.width, planes = mode == kWeightGrad ? E : 1, lines = mode == kWeightGrad ? Nw : R;
-  const int64_t dout[3] = {width, lines, planes}, sout[2] = {width, width * lines};
-  const int bout[3] = {64, kEpiCols, 1};
-  ok = ok && make_map(&maps[2], bf16, a.out, 3, dout, sout, bout);
+  // the output: rows of `width` in planes; where the width is a multiple of 64, columns of 64 as
+  // an extent of their own, so that one box takes both halves of a step
+  const int rows = mode == kWeightGrad ? step_cols<kWeightGrad> : step_cols<kForward>;
+  a.one_store = width % 64 == 0;
+  if (a.one_store) {
+    const int64_t d[4] = {64, lines, width / 64, planes}, st4[3] = {width, 64, width * lines};
+    const int box[4] = {64, rows, a.gated ? 1 : 2, 1};
+    ok = ok && make_map(&maps[2], bf16, a.out, 4, d, st4, box);
+  } else {
+    const int64_t d[4] = {width, lines, 1, planes}, st4[3] = {width, width * lines, width * lines};
+    const int box[4] = {64, rows, 1, 1};
+    ok = ok && make_map(&maps[2], bf16, a.out, 4, d, st4, box);
+  }
   if (a.preact) {
     const int64_t dzm[3] = {width, s.gated ? 2 : 1, R}, szm[2] = {width, Nw};
-    const int bzm[3] = {64, 1, kEpiCols};
+    const int bzm[3] = {64, 1, rows};
     ok = ok && make_map(&maps[3], bf16, a.preact, 3, dzm, szm, bzm);
   }
   if (!ok) return cudaErrorInvalidValue;

@@ -6,10 +6,11 @@
 // One pass over z and dout writes dz in the rows' type, the operand of the two products
 // that follow: a rounding of half a step per element, independent from element to
 // element, so a sum over dz is off by about what its own rounding to the type costs.
-// The bias gradient takes the fp32 values: a CTA sums up to 128 rows of one expert for
-// 256 columns (16 rows per thread, then eight threads in order) into a partial, and a
-// second launch adds an expert's partials in order: no atomics.  Bound by memory: z and
-// dout read once, dz written once.
+// The bias gradient takes the fp32 values: a CTA sums up to 32 rows of one expert for 256
+// columns (four rows per thread, then eight threads in order) into a partial, and a second
+// launch adds an expert's partials, eight threads per column, in order: no atomics.  Bound
+// by memory: z and dout read once, dz written once; each thread requests its four rows
+// before it uses the first.
 #include "activation.cuh"
 #include "internal.h"
 #include "row_vec.cuh"
@@ -18,18 +19,21 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerCta = 128;
-constexpr int kPieces = 32;              // 16-byte pieces (256 columns) per CTA
-constexpr int kLanes = kThreads / kPieces;  // rows at a time
+constexpr int kPieces = 32;                 // 16-byte pieces (256 columns) per CTA
+constexpr int kLanes = kThreads / kPieces;  // threads per column
+constexpr int kBatch = 4;                   // rows per thread at a time
+// Rows per CTA; four times as many where the blocks would be more than a grid's y extent holds.
+__host__ __device__ __forceinline__ int rows_per_cta(int R) { return R <= (1 << 20) ? kLanes * kBatch : 4 * kLanes * kBatch; }
 
-// The row range of block b: experts own ceil(rows / 128) blocks each, in order.
+// The row range of block b: experts own ceil(rows / rows_per_cta) blocks each, in order.
 // Whole CTA; false when there is no such block.
 __device__ __forceinline__ bool find_block(const int32_t* offsets, int E, int R, int b, int* sh, int& e, int& r0,
                                            int& r1) {
+  const int per = rows_per_cta(R);
   if (!offsets) {
     e = 0;
-    r0 = b * kRowsPerCta;
-    r1 = min(R, r0 + kRowsPerCta);
+    r0 = b * per;
+    r1 = min(R, r0 + per);
     return r0 < R;
   }
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
@@ -38,7 +42,7 @@ __device__ __forceinline__ bool find_block(const int32_t* offsets, int E, int R,
     lo = min(max(offsets[i], 0), R);
     hi = max(min(offsets[i + 1], R), lo);
   }
-  const int n = (hi - lo + kRowsPerCta - 1) / kRowsPerCta;
+  const int n = (hi - lo + per - 1) / per;
   int incl = n;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -52,101 +56,129 @@ __device__ __forceinline__ bool find_block(const int32_t* offsets, int E, int R,
   for (int w = 0; w < warp; ++w) before += sh[w];
   if (n > 0 && b >= before && b < before + n) {
     sh[8] = i;
-    sh[9] = lo + (b - before) * kRowsPerCta;
+    sh[9] = lo + (b - before) * per;
     sh[10] = hi;
   }
   __syncthreads();
   e = sh[8];
   r0 = sh[9];
-  r1 = min(sh[10], r0 + kRowsPerCta);
+  r1 = min(sh[10], r0 + per);
   return e >= 0;
 }
 
+// g becomes act(g), o its derivative.
+__device__ __forceinline__ void derivatives(float (&g)[8], int act, float (&o)[8]) {
+  const auto all = [&](int kind) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float y;
+      activate_grad(g[i], kind, y, o[i]);
+      g[i] = y;
+    }
+  };
+  switch (act) {  // outside of the loop over the elements
+    case kGeluTanh: all(kGeluTanh); break;
+    case kGeluErf: all(kGeluErf); break;
+    case kSilu: all(kSilu); break;
+    default: all(kIdentity); break;
+  }
+}
+
 // grid (column blocks of N, row blocks).  z NULL: dz is dout itself and only the bias is wanted.
-template <int kType>
+template <int kType, bool kGated>
 __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const int32_t* offsets, const uint4* z, const uint4* dout,
-                                                             uint4* dz, float* partial, int R, int E, int N, int gated,
-                                                             int act) {
+                                                             uint4* dz, float* partial, int R, int E, int N, int act) {
   __shared__ int sh[12];
-  __shared__ float sum[2][kLanes][kPieces * 8];
+  __shared__ float sum[kGated ? 2 : 1][kLanes][kPieces * 8];
   grid_dependents_launch();
   grid_dependency_wait();
   int e, r0, r1;
   if (!find_block(offsets, E, R, blockIdx.y, sh, e, r0, r1)) return;
   const int piece = threadIdx.x % kPieces, rl = threadIdx.x / kPieces;
-  const int nvec = N / 8, zvec = gated ? 2 * nvec : nvec;
+  const int nvec = N / 8, zvec = kGated ? 2 * nvec : nvec;
   const int col = blockIdx.x * kPieces + piece;
   float sg[8], su[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.f;
   if (col < nvec) {
-#pragma unroll 2
-    for (int r = r0 + rl; r < r1; r += kLanes) {
-      float d[8];
-      Vec<kType>::load(dout[static_cast<size_t>(r) * nvec + col], d);
-      if (z) {
-        const size_t at = static_cast<size_t>(r) * zvec + col;
-        float g[8], o[8];
-        Vec<kType>::load(z[at], g);
-        if (gated) {
-          float u[8], ou[8];
-          Vec<kType>::load(z[at + nvec], u);
+    for (int base = r0 + rl; base < r1; base += kLanes * kBatch) {
+      uint4 vd[kBatch], vg[kBatch], vu[kBatch];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float y, dy;
-            activate_grad(g[i], act, y, dy);
-            o[i] = d[i] * u[i] * dy;
-            ou[i] = d[i] * y;
-            su[i] += ou[i];
-          }
-          dz[at + nvec] = Vec<kType>::store(ou);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float y, dy;
-            activate_grad(g[i], act, y, dy);
-            o[i] = d[i] * dy;
+      for (int k = 0; k < kBatch; ++k) {
+        const int r = base + k * kLanes;
+        if (r < r1) {
+          vd[k] = dout[static_cast<size_t>(r) * nvec + col];
+          if (z) {
+            const size_t at = static_cast<size_t>(r) * zvec + col;
+            vg[k] = z[at];
+            if (kGated) vu[k] = z[at + nvec];
           }
         }
-        dz[at] = Vec<kType>::store(o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = o[i];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sg[i] += d[i];
+      for (int k = 0; k < kBatch; ++k) {
+        const int r = base + k * kLanes;
+        if (r >= r1) break;
+        float d[8];
+        Vec<kType>::load(vd[k], d);
+        if (z) {
+          const size_t at = static_cast<size_t>(r) * zvec + col;
+          float g[8];
+          Vec<kType>::load(vg[k], g);
+          float u[8], o[8];
+          if (kGated) Vec<kType>::load(vu[k], u);
+          derivatives(g, act, o);  // g becomes act(g), o its derivative
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float ou = d[i] * g[i];
+            d[i] = kGated ? d[i] * u[i] * o[i] : d[i] * o[i];
+            if (kGated) {
+              u[i] = ou;
+              su[i] += ou;
+            }
+          }
+          dz[at] = Vec<kType>::store(d);
+          if (kGated) dz[at + nvec] = Vec<kType>::store(u);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sg[i] += d[i];
+      }
     }
   }
   if (!partial) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     sum[0][rl][piece * 8 + i] = sg[i];
-    sum[1][rl][piece * 8 + i] = su[i];
+    if (kGated) sum[kGated ? 1 : 0][rl][piece * 8 + i] = su[i];
   }
   __syncthreads();
   const int n = blockIdx.x * kPieces * 8 + threadIdx.x;
   if (n >= N) return;
-  const int Nw = gated ? 2 * N : N;
-  for (int h = 0; h <= gated; ++h) {
+  constexpr int halves = kGated ? 2 : 1;
+#pragma unroll
+  for (int h = 0; h < halves; ++h) {
     float s = 0.f;
 #pragma unroll
     for (int l = 0; l < kLanes; ++l) s += sum[h][l][threadIdx.x];
-    partial[static_cast<size_t>(blockIdx.y) * Nw + h * N + n] = s;
+    partial[static_cast<size_t>(blockIdx.y) * halves * N + h * N + n] = s;
   }
 }
 
-// db[e][n]: the partials of expert e's blocks, in order.
+// db[e][n]: the partials of expert e's blocks; grid (column blocks of 32, experts), warp l
+// takes every eighth partial.
 __global__ void __launch_bounds__(kThreads) linear_dbias_kernel(const int32_t* offsets, const float* partial, float* db,
                                                                 int R, int E, int Nw) {
   __shared__ int sh[9];
+  __shared__ float sum[8][32];
   grid_dependents_launch();
   grid_dependency_wait();
-  const int e = blockIdx.y, i = threadIdx.x, lane = i & 31, warp = i >> 5;
-  int first = 0, count = (R + kRowsPerCta - 1) / kRowsPerCta;
+  const int e = blockIdx.y, i = threadIdx.x, lane = i & 31, warp = i >> 5, per = rows_per_cta(R);
+  int first = 0, count = (R + per - 1) / per;
   if (offsets) {
     int n = 0;
     if (i < E) {
       const int lo = min(max(offsets[i], 0), R), hi = max(min(offsets[i + 1], R), lo);
-      n = (hi - lo + kRowsPerCta - 1) / kRowsPerCta;
+      n = (hi - lo + per - 1) / per;
     }
     if (i == e) sh[8] = n;
     int before = i < e ? n : 0;
@@ -157,19 +189,27 @@ __global__ void __launch_bounds__(kThreads) linear_dbias_kernel(const int32_t* o
     for (int w = 0; w < kThreads / 32; ++w) first += sh[w];
     count = sh[8];
   }
-  const int n = blockIdx.x * kThreads + i;
-  if (n >= Nw) return;
+  const int n = blockIdx.x * 32 + lane;
   float s = 0.f;
-  const float* p = partial + static_cast<size_t>(first) * Nw + n;
-#pragma unroll 8
-  for (int b = 0; b < count; ++b) s += p[static_cast<size_t>(b) * Nw];
-  db[static_cast<size_t>(e) * Nw + n] = s;
+  if (n < Nw) {
+    const float* p = partial + static_cast<size_t>(first) * Nw + n;
+#pragma unroll 4
+    for (int b = warp; b < count; b += 8) s += p[static_cast<size_t>(b) * Nw];
+  }
+  sum[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && n < Nw) {
+    s = 0.f;
+#pragma unroll
+    for (int l = 0; l < 8; ++l) s += sum[l][lane];
+    db[static_cast<size_t>(e) * Nw + n] = s;
+  }
 }
 
 }  // namespace
 
 int linear_row_blocks(const LinearDims& s) {
-  const int blocks = (s.R + kRowsPerCta - 1) / kRowsPerCta;
+  const int per = rows_per_cta(s.R), blocks = (s.R + per - 1) / per;
   return s.grouped ? blocks + (s.E < s.R ? s.E : s.R) : blocks;
 }
 
@@ -179,11 +219,12 @@ cudaError_t launch_linear_dz(const LinearDims& s, const int32_t* offsets, const 
   const auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, dim3(kThreads), 0, st, offsets, static_cast<const uint4*>(z),
                       static_cast<const uint4*>(dout), static_cast<uint4*>(dz), dbias ? partial : nullptr, s.R, s.E,
-                      s.N, s.gated, s.act);
+                      s.N, s.act);
   };
-  const cudaError_t err = s.type == 1 ? go(linear_dz_kernel<1>) : go(linear_dz_kernel<0>);
+  const cudaError_t err = s.type == 1 ? (s.gated ? go(linear_dz_kernel<1, true>) : go(linear_dz_kernel<1, false>))
+                                      : (s.gated ? go(linear_dz_kernel<0, true>) : go(linear_dz_kernel<0, false>));
   if (err != cudaSuccess || !dbias) return err;
-  return launch_pdl(linear_dbias_kernel, dim3((s.Nw() + kThreads - 1) / kThreads, s.E), dim3(kThreads), 0, st, offsets,
+  return launch_pdl(linear_dbias_kernel, dim3((s.Nw() + 31) / 32, s.E), dim3(kThreads), 0, st, offsets,
                     static_cast<const float*>(partial), dbias, s.R, s.E, s.Nw());
 }
 
