@@ -6,8 +6,8 @@ fp32) and v = 2^-24: the integers and the copied rows are equal.  A combined ele
 is a chain of k fused multiply-adds and one addition in fp32, each off by at most v
 of a partial sum, all of which are at most S = sum |w row| + |res| (1 + k v): at most
 (k + 1) v S (1 + 2^-20); the one rounding to the type adds u |out|, or half of fp16's
-smallest step, 2^-25.  A weight's gradient adds n fused products in a thread and at
-most 5 + 8 partial sums: (n + 13) v sum |dout row|.  A logit's gradient
+smallest step, 2^-25.  A weight's gradient adds at most n fused products in a thread, a
+32nd of the row's, and at most 5 + 8 partial sums: (n + 13) v sum |dout row|.  A logit's gradient
 w_r (dw_r - m), m the k-fold chain over w dw, takes w_r (e_r + e_m) from those errors
 with e_m = sum_j w_j e_j + (k + 1) v sum_j |w_j dw_j|, and three roundings of its own,
 for each time the token chose the expert.
@@ -189,9 +189,7 @@ def test_combine_backward(B, T, E, k, d, typ, kind):
     there = pos >= 0
     prod = v * D[:, None, :]
     dw, per = prod.sum(2), 4 if typ == 2 else 8
-    nvec = d // per
-    group = min(256, max(32, 1 << (nvec - 1).bit_length()))
-    e_dw = (-(-nvec // group) * per + 13) * V * prod.abs().sum(2) * 1.01
+    e_dw = (-(-d // per // 32) * per + 13) * V * prod.abs().sum(2) * 1.01
     _within(gw, dw, e_dw)
     want = (W[:, :, None] * D[:, None, :])
     tol = (HALF[typ] + V) * want.abs() * 1.01 + SMALL[typ]

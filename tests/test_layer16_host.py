@@ -78,7 +78,7 @@ def test_row_optional_pointers():
 
 def test_dispatch_workspace():
     assert B.moe_w4a16_dispatch_workspace_bytes(_rows(tokens=2048)) == 16           # 4096 pairs: one chunk
-    big = _rows(tokens=2049)                                                        # 4098 pairs, chunks of 512
+    big = _rows(tokens=2049)                                                        # 4098 pairs in chunks of 512
     assert B.moe_w4a16_dispatch_workspace_bytes(big) == (9 + 1) * 8 * 4
     assert B.moe_w4a16_dispatch_workspace_bytes(_rows(tokens=1000, top_k=7)) == (14 + 1) * 8 * 4  # chunks of 504
     assert _row_calls(big, ws_bytes=(9 + 1) * 8 * 4 - 1)["dispatch"]() == B.ERR_WORKSPACE

@@ -12,6 +12,8 @@
 // A token's pairs are handled together, so x and dout are read once, not k times,
 // and the k rows of a token are summed in registers in rank order: no atomics, the
 // same bits in every run.
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "row_vec.cuh"
@@ -37,9 +39,23 @@ __device__ __forceinline__ int expert_of(int id, int E) {
 // (prefix), and every CTA of the copy counts only the ids of its chunk before its
 // own pairs.
 constexpr int kOneChunkPairs = 4096;
-constexpr int kCtaPairs = 64;   // pairs per CTA of the copy, at most
-constexpr int kChunkCtas = 8;   // CTAs of the copy per chunk (chunks of about 512 pairs)
-inline int chunk_pairs(int k) { return kChunkCtas * (kCtaPairs / k) * k; }  // whole CTAs of whole tokens
+constexpr int kChunkPairs = 512;  // pairs per chunk above that, about
+constexpr int kCtaPairs = 64;     // pairs per CTA of the copy, at most: two warps place them
+constexpr int kCopyLoads = 4;     // pieces a thread has in flight
+
+// Tokens per CTA of the copy: about 64 KB of rows.  A CTA spends some microseconds on its
+// pairs' places first, so many small ones hide each other's (16384 tokens top-8 of 4 KB rows:
+// 108 us with 64 pairs per CTA, 98 us with 16), but below that the placing shows (1 KB rows:
+// 33 us with 64 pairs, 40 us with 16).
+inline int copy_tokens(const RowDims& s) {
+  int pairs = 65536 / (s.nvec() * 16);
+  pairs = pairs < 16 ? 16 : pairs > kCtaPairs ? kCtaPairs : pairs;
+  return pairs / s.k;
+}
+inline int chunk_pairs(const RowDims& s) {  // whole CTAs of whole tokens
+  const int cta = copy_tokens(s) * s.k;
+  return kChunkPairs / cta * cta;
+}
 
 __global__ void __launch_bounds__(kThreads) dispatch_count_kernel(const int32_t* ids, int P, int E,
                                                                   int chunk, int32_t* hist) {
@@ -85,7 +101,7 @@ __global__ void __launch_bounds__(1024) dispatch_prefix_kernel(int32_t* hist, in
   }
 }
 
-// One CTA places the pairs of `tpc` tokens (tpc * k <= 64) and copies their rows: each
+// One CTA places the pairs of `tpc` tokens (tpc * k <= kCtaPairs) and copies their rows: each
 // 16-byte piece of a token is read once and written to the token's k rows.
 // hist/tot are NULL when all pairs are one chunk.
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const int32_t* ids, int T, int k, int E,
@@ -166,15 +182,24 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const int32_t* ids, 
   // pair_list behind the kept pairs
   for (int p = kept + blockIdx.x * kThreads + tid; p < P; p += gridDim.x * kThreads) pair_list[p] = -1;
   const uint4* src = x + static_cast<size_t>(t0) * nvec;
-  for (int j = tid; j < nt * nvec; j += kThreads) {
-    const uint4 piece = src[j];
-    const int t = j / nvec, col = j - t * nvec;
+  const int total_pieces = nt * nvec;
+  for (int j0 = tid; j0 < total_pieces; j0 += kThreads * kCopyLoads) {
+    uint4 piece[kCopyLoads];
 #pragma unroll
-    for (int r = 0; r < kMaxTopK; ++r)
-      if (r < k) {
-        const int row = row_of[t * k + r];
-        if (row >= 0) rows[static_cast<size_t>(row) * nvec + col] = piece;
-      }
+    for (int u = 0; u < kCopyLoads; ++u)
+      if (j0 + u * kThreads < total_pieces) piece[u] = src[j0 + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < kCopyLoads; ++u) {
+      const int j = j0 + u * kThreads;
+      if (j >= total_pieces) break;
+      const int t = j / nvec, col = j - t * nvec;
+#pragma unroll
+      for (int r = 0; r < kMaxTopK; ++r)
+        if (r < k) {
+          const int row = row_of[t * k + r];
+          if (row >= 0) rows[static_cast<size_t>(row) * nvec + col] = piece[u];
+        }
+    }
   }
 }
 
@@ -183,65 +208,81 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const int32_t* ids, 
 // One thread per 16-byte piece of a token's row; the pieces of the k rows are all
 // requested before the first is used.  With topk_w NULL every weight is one (the
 // gradient of dispatch).
-template <int kType>
-__global__ void __launch_bounds__(kThreads) combine_rows_kernel(const int32_t* pair_pos,
-                                                                const float* topk_w,
+// With few choices a thread takes several tokens' pieces at once, 8 / kChoices of them, so that
+// eight loads are in flight whatever k is.
+template <int kType, int kChoices>
+__global__ void __launch_bounds__(kThreads) combine_rows_kernel(const int32_t* pair_pos, const float* topk_w,
                                                                 const uint4* rows,
                                                                 const uint4* residual,  // may equal out
                                                                 uint4* out, int T, int k, int nvec, int tpc) {
+  constexpr int kPieces = kMaxTopK / kChoices, N = Vec<kType>::n;
   grid_dependents_launch();
   grid_dependency_wait();
   const int P = T * k;
-  const int t0 = blockIdx.x * tpc, nt = min(tpc, T - t0);
-  for (int j = threadIdx.x; j < nt * nvec; j += kThreads) {
-    const int tl = j / nvec, col = j - tl * nvec;
-    const int t = t0 + tl;
-    int pos[kMaxTopK];
-    float w[kMaxTopK];
-    uint4 v[kMaxTopK];
+  const int t0 = blockIdx.x * tpc, n = min(tpc, T - t0) * nvec;
+  for (int j0 = threadIdx.x; j0 < n; j0 += kThreads * kPieces) {
+    int pos[kPieces][kChoices];
+    float w[kPieces][kChoices];
+    uint4 v[kPieces][kChoices], res[kPieces];
+    size_t at[kPieces];
 #pragma unroll
-    for (int r = 0; r < kMaxTopK; ++r) {
-      pos[r] = r < k ? pair_pos[t * k + r] : -1;
-      w[r] = r < k && topk_w ? topk_w[t * k + r] : 1.f;
-    }
+    for (int u = 0; u < kPieces; ++u) {
+      const int j = j0 + u * kThreads;
+      const int tl = j / nvec, t = t0 + tl;
+      at[u] = static_cast<size_t>(t0) * nvec + j;
 #pragma unroll
-    for (int r = 0; r < kMaxTopK; ++r)
-      if (static_cast<unsigned>(pos[r]) < static_cast<unsigned>(P))
-        v[r] = rows[static_cast<size_t>(pos[r]) * nvec + col];
-    float acc[Vec<kType>::n];
-#pragma unroll
-    for (int i = 0; i < Vec<kType>::n; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int r = 0; r < kMaxTopK; ++r)
-      if (static_cast<unsigned>(pos[r]) < static_cast<unsigned>(P)) {
-        float f[Vec<kType>::n];
-        Vec<kType>::load(v[r], f);
-#pragma unroll
-        for (int i = 0; i < Vec<kType>::n; ++i) acc[i] = fmaf(w[r], f[i], acc[i]);
+      for (int r = 0; r < kChoices; ++r) {
+        const bool on = j < n && r < k;
+        pos[u][r] = on ? pair_pos[t * k + r] : -1;
+        w[u][r] = on && topk_w ? topk_w[t * k + r] : 1.f;
       }
-    const size_t o = static_cast<size_t>(t) * nvec + col;
-    if (residual) {
-      float f[Vec<kType>::n];
-      Vec<kType>::load(residual[o], f);
-#pragma unroll
-      for (int i = 0; i < Vec<kType>::n; ++i) acc[i] += f[i];
     }
-    out[o] = Vec<kType>::store(acc);
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int j = j0 + u * kThreads, col = j % nvec;
+#pragma unroll
+      for (int r = 0; r < kChoices; ++r)
+        if (static_cast<unsigned>(pos[u][r]) < static_cast<unsigned>(P))
+          v[u][r] = rows[static_cast<size_t>(pos[u][r]) * nvec + col];
+      if (residual && j < n) res[u] = residual[at[u]];
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      if (j0 + u * kThreads >= n) break;
+      float acc[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int r = 0; r < kChoices; ++r)
+        if (static_cast<unsigned>(pos[u][r]) < static_cast<unsigned>(P)) {
+          float f[N];
+          Vec<kType>::load(v[u][r], f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[i] = fmaf(w[u][r], f[i], acc[i]);
+        }
+      if (residual) {
+        float f[N];
+        Vec<kType>::load(res[u], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += f[i];
+      }
+      out[at[u]] = Vec<kType>::store(acc);
+    }
   }
 }
 
 // -------------------------------------------------------- combine backward
 //
 // kGroup threads per token, 256 / kGroup tokens per CTA.  Each thread keeps the k
-// partial products <dout, row_r> of its pieces; they meet in a fixed tree (a
-// butterfly that halves the values at each of its first three steps, then the warps
-// of the group in order).
-template <int kType, int kGroup>
+// partial products <dout, row_r> of its pieces, 8 / kChoices pieces at a time so that eight
+// rows' loads are in flight whatever k is; they meet in a fixed tree (a butterfly that halves
+// the values at each of its first three steps, then the warps of the group in order).
+template <int kType, int kGroup, int kChoices>
 __global__ void __launch_bounds__(kThreads) combine_rows_backward_kernel(
-    const int32_t* topk_idx, const int32_t* pair_pos, const float* topk_w,
-    const uint4* rows, const uint4* dout, uint4* drows,
-    float* dtopk_w, float* dlogits, int T, int k, int E, int nvec) {
+    const int32_t* topk_idx, const int32_t* pair_pos, const float* topk_w, const uint4* rows, const uint4* dout,
+    uint4* drows, float* dtopk_w, float* dlogits, int T, int k, int E, int nvec) {
   constexpr int kTokens = kThreads / kGroup, kWarps = kGroup / 32, N = Vec<kType>::n;
+  constexpr int kPieces = kMaxTopK / kChoices;
   __shared__ float part[kThreads / 32][kMaxTopK];
   grid_dependents_launch();
   grid_dependency_wait();
@@ -253,32 +294,43 @@ __global__ void __launch_bounds__(kThreads) combine_rows_backward_kernel(
   float w[kMaxTopK], dot[kMaxTopK];
 #pragma unroll
   for (int r = 0; r < kMaxTopK; ++r) {
-    pos[r] = on && r < k ? pair_pos[t * k + r] : -1;
-    w[r] = on && r < k ? topk_w[t * k + r] : 0.f;
+    pos[r] = on && r < kChoices && r < k ? pair_pos[t * k + r] : -1;
+    w[r] = on && r < kChoices && r < k ? topk_w[t * k + r] : 0.f;
     dot[r] = 0.f;
   }
   if (on) {
-    for (int col = g; col < nvec; col += kGroup) {
-      uint4 v[kMaxTopK];
-      const uint4 dv = dout[static_cast<size_t>(t) * nvec + col];
+    for (int col0 = g; col0 < nvec; col0 += kGroup * kPieces) {
+      uint4 v[kPieces][kChoices], dv[kPieces];
 #pragma unroll
-      for (int r = 0; r < kMaxTopK; ++r)
-        if (static_cast<unsigned>(pos[r]) < static_cast<unsigned>(P))
-          v[r] = rows[static_cast<size_t>(pos[r]) * nvec + col];
-      float d[N];
-      Vec<kType>::load(dv, d);
+      for (int u = 0; u < kPieces; ++u) {
+        const int col = col0 + u * kGroup;
+        if (col < nvec) {
+          dv[u] = dout[static_cast<size_t>(t) * nvec + col];
 #pragma unroll
-      for (int r = 0; r < kMaxTopK; ++r)
-        if (static_cast<unsigned>(pos[r]) < static_cast<unsigned>(P)) {
-          float f[N], o[N];
-          Vec<kType>::load(v[r], f);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            dot[r] = fmaf(d[i], f[i], dot[r]);
-            o[i] = w[r] * d[i];
-          }
-          if (drows) drows[static_cast<size_t>(pos[r]) * nvec + col] = Vec<kType>::store(o);
+          for (int r = 0; r < kChoices; ++r)
+            if (static_cast<unsigned>(pos[r]) < static_cast<unsigned>(P))
+              v[u][r] = rows[static_cast<size_t>(pos[r]) * nvec + col];
         }
+      }
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        const int col = col0 + u * kGroup;
+        if (col >= nvec) break;
+        float d[N];
+        Vec<kType>::load(dv[u], d);
+#pragma unroll
+        for (int r = 0; r < kChoices; ++r)
+          if (static_cast<unsigned>(pos[r]) < static_cast<unsigned>(P)) {
+            float f[N], o[N];
+            Vec<kType>::load(v[u][r], f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              dot[r] = fmaf(d[i], f[i], dot[r]);
+              o[i] = w[r] * d[i];
+            }
+            if (drows) drows[static_cast<size_t>(pos[r]) * nvec + col] = Vec<kType>::store(o);
+          }
+      }
     }
   }
   // lane l ends with the warp's sum for r = l & 7: each step exchanges the half of the
@@ -333,12 +385,6 @@ __global__ void __launch_bounds__(kThreads) combine_rows_backward_kernel(
   }
 }
 
-int tokens_per_cta(int nvec, int most) {
-  int n = kThreads / nvec;
-  if (n < 1) n = 1;
-  return n < most ? n : most;
-}
-
 template <int kType>
 cudaError_t launch_backward(const RowDims& s, const int32_t* topk_idx, const int32_t* pair_pos, const float* topk_w,
                             const uint4* rows, const uint4* dout, uint4* drows, float* dtopk_w, float* dlogits,
@@ -349,10 +395,21 @@ cudaError_t launch_backward(const RowDims& s, const int32_t* topk_idx, const int
     return launch_pdl(kernel, dim3((s.T + per - 1) / per), dim3(kThreads), 0, st, topk_idx, pair_pos, topk_w, rows,
                       dout, drows, dtopk_w, dlogits, s.T, s.k, s.E, nvec);
   };
-  if (nvec <= 32) return go(combine_rows_backward_kernel<kType, 32>, 32);
-  if (nvec <= 64) return go(combine_rows_backward_kernel<kType, 64>, 64);
-  if (nvec <= 128) return go(combine_rows_backward_kernel<kType, 128>, 128);
-  return go(combine_rows_backward_kernel<kType, 256>, 256);
+  // threads per token: one round of its pieces, at most
+  if (s.k == 1) return go(combine_rows_backward_kernel<kType, 32, 1>, 32);
+  if (s.k == 2) {
+    if (nvec <= 128) return go(combine_rows_backward_kernel<kType, 32, 2>, 32);
+    return go(combine_rows_backward_kernel<kType, 64, 2>, 64);
+  }
+  if (s.k <= 4) {
+    if (nvec <= 64) return go(combine_rows_backward_kernel<kType, 32, 4>, 32);
+    if (nvec <= 128) return go(combine_rows_backward_kernel<kType, 64, 4>, 64);
+    return go(combine_rows_backward_kernel<kType, 128, 4>, 128);
+  }
+  if (nvec <= 32) return go(combine_rows_backward_kernel<kType, 32, 8>, 32);
+  if (nvec <= 64) return go(combine_rows_backward_kernel<kType, 64, 8>, 64);
+  if (nvec <= 128) return go(combine_rows_backward_kernel<kType, 128, 8>, 128);
+  return go(combine_rows_backward_kernel<kType, 256, 8>, 256);
 }
 
 }  // namespace
@@ -360,7 +417,7 @@ cudaError_t launch_backward(const RowDims& s, const int32_t* topk_idx, const int
 size_t dispatch_ws_bytes(const RowDims& s) {
   const int64_t P = s.pairs();
   if (P <= kOneChunkPairs) return 16;
-  const int chunk = chunk_pairs(s.k);
+  const int chunk = chunk_pairs(s);
   return (size_t((P + chunk - 1) / chunk) + 1) * s.E * 4;
 }
 
@@ -376,7 +433,7 @@ cudaError_t launch_dispatch(const RowDims& s, const int32_t* topk_idx, const voi
                       tpc, P, static_cast<const int32_t*>(nullptr), static_cast<const int32_t*>(nullptr), xv, nvec,
                       offsets, pair_list, pair_pos, rv);
   }
-  const int tpc = kCtaPairs / s.k, chunk = chunk_pairs(s.k), nchunks = (P + chunk - 1) / chunk;
+  const int tpc = copy_tokens(s), chunk = chunk_pairs(s), nchunks = (P + chunk - 1) / chunk;
   auto* hist = static_cast<int32_t*>(workspace);
   int32_t* tot = hist + static_cast<size_t>(nchunks) * s.E;
   cudaError_t err =
@@ -391,15 +448,25 @@ cudaError_t launch_dispatch(const RowDims& s, const int32_t* topk_idx, const voi
 
 cudaError_t launch_combine_rows(const RowDims& s, const int32_t* pair_pos, const float* topk_w, const void* rows,
                                 const void* residual, void* out, cudaStream_t st) {
-  const int nvec = s.nvec(), tpc = tokens_per_cta(nvec, kThreads);
-  const auto go = [&](auto kernel) {
+  const int nvec = s.nvec();
+  const auto go = [&](auto kernel, int choices) {
+    int tpc = kThreads * (kMaxTopK / choices) / nvec;  // one round of a CTA, whole tokens
+    if (tpc < 1) tpc = 1;
+    while (tpc > 1 && (s.T + tpc - 1) / tpc < 608) tpc = (tpc + 1) / 2;  // four CTAs per SM at least
     return launch_pdl(kernel, dim3((s.T + tpc - 1) / tpc), dim3(kThreads), 0, st, pair_pos, topk_w,
                       static_cast<const uint4*>(rows), static_cast<const uint4*>(residual), static_cast<uint4*>(out),
                       s.T, s.k, nvec, tpc);
   };
-  if (s.type == 0) return go(combine_rows_kernel<0>);
-  if (s.type == 1) return go(combine_rows_kernel<1>);
-  return go(combine_rows_kernel<2>);
+  const auto by_k = [&](auto type) {
+    constexpr int t = decltype(type)::value;
+    if (s.k == 1) return go(combine_rows_kernel<t, 1>, 1);
+    if (s.k == 2) return go(combine_rows_kernel<t, 2>, 2);
+    if (s.k <= 4) return go(combine_rows_kernel<t, 4>, 4);
+    return go(combine_rows_kernel<t, 8>, 8);
+  };
+  if (s.type == 0) return by_k(std::integral_constant<int, 0>{});
+  if (s.type == 1) return by_k(std::integral_constant<int, 1>{});
+  return by_k(std::integral_constant<int, 2>{});
 }
 
 cudaError_t launch_combine_rows_backward(const RowDims& s, const int32_t* topk_idx, const int32_t* pair_pos,
