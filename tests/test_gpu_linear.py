@@ -143,14 +143,17 @@ def _check_forward(B, c):
 
 # R, K, N, E (0: dense), activation, gated, type, bias, residual, rows of no expert
 FORWARD = [
-    # up to eight rows: the kernel for single tokens
+    # up to 32 rows: the kernel for single tokens and small batches
     (1, 8, 8, 0, 3, 0, 0, False, False, 0), (1, 2048, 136, 0, 0, 0, 0, True, True, 0), (2, 264, 72, 0, 1, 1, 1, True, True, 0),
     (3, 1000, 16, 0, 2, 0, 1, True, False, 0), (5, 72, 200, 0, 0, 1, 0, False, True, 0), (8, 2056, 40, 0, 3, 0, 1, True, True, 0),
     (1, 64, 64, 5, 0, 1, 0, True, False, 0), (8, 704, 72, 128, 0, 1, 1, False, True, 0), (8, 136, 8, 256, 3, 0, 0, True, False, 3),
     (7, 200, 24, 3, 2, 0, 0, True, True, 2), (8, 64, 32, 1, 1, 0, 0, False, False, 0),
-    # tiles of 32 columns
     (9, 8, 8, 0, 3, 0, 0, False, False, 0), (16, 64, 128, 0, 3, 0, 0, False, False, 0), (31, 72, 136, 0, 0, 0, 1, True, True, 0),
     (32, 1000, 264, 0, 2, 1, 0, True, True, 0), (9, 65536, 8, 0, 3, 0, 1, True, False, 0),
+    (17, 40, 24, 0, 1, 1, 1, True, True, 0), (32, 200, 72, 5, 0, 1, 0, True, True, 2), (24, 2056, 40, 2, 2, 0, 1, False, False, 0),
+    (32, 64, 16, 256, 3, 0, 0, True, True, 0), (16, 72, 8, 3, 0, 1, 0, True, False, 16),
+    # tiles
+    (33, 65536, 8, 0, 3, 0, 1, True, False, 0), (48, 8, 8, 0, 0, 1, 0, True, True, 0),
     # 64, 128, 256 columns and their edges
     (33, 136, 72, 0, 1, 0, 0, True, False, 0), (64, 520, 200, 0, 0, 1, 1, False, True, 0), (65, 64, 1032, 0, 3, 0, 0, True, True, 0),
     (127, 200, 136, 0, 2, 0, 1, True, True, 0), (128, 256, 128, 0, 0, 1, 0, True, False, 0), (129, 72, 264, 0, 0, 0, 0, True, True, 0),

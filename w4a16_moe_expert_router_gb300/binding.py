@@ -176,25 +176,25 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
-_current_stream = None
+_raw_stream = None
 
 
-def _find_current_stream():
-    """torch's current stream as a raw handle: its raw getter where there is one (0.1 us a call
-    on a Grace CPU; building a torch.cuda.Stream to ask it takes 3 us)."""
+def _find_raw_stream():
+    """The getter of a device's current stream as a raw handle: torch's own where it has one (0.1 us
+    a call on a Grace CPU; building a torch.cuda.Stream to ask it takes 3 us)."""
+    global _raw_stream
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return lambda: torch.cuda.current_stream().cuda_stream
-    return lambda: raw(torch.cuda.current_device())
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return _raw_stream
 
 
-def _stream(stream) -> int | None:
-    global _current_stream
-    if stream is None and _current_stream is None:
-        _current_stream = _find_current_stream()
+def _stream(stream, dev=None) -> int | None:
     if stream is None:
-        return _current_stream()
+        if dev is None:
+            import torch
+            dev = torch.cuda.current_device()
+        return (_raw_stream or _find_raw_stream())(dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -334,11 +334,12 @@ _TORCH_TYPES = None
 
 
 def _types():
+    """torch's types by code, int32, fp32, and the getter of the current device."""
     global _TORCH_TYPES
     if _TORCH_TYPES is None:
         import torch
-        _TORCH_TYPES = ((torch.float16, torch.bfloat16, torch.float32), torch.int32, torch.float32,
-                        torch.cuda.current_device)
+        _TORCH_TYPES = ({FP16: torch.float16, BF16: torch.bfloat16, FP32: torch.float32}, torch.int32,
+                        torch.float32, torch.cuda.current_device)
     return _TORCH_TYPES
 
 
@@ -367,55 +368,53 @@ def moe_w4a16_dispatch_workspace_bytes(cfg: Rows) -> int:
     return int(lib().moe_w4a16_dispatch_workspace_bytes(ctypes.byref(cfg)))
 
 
-def _rows_types(cfg: Rows, where: str):
-    if not 0 <= cfg.type <= 2:
-        raise MoeW4A16Error(ERR_SHAPE, where)
-    kinds, i32, f32, current = _types()
-    return kinds[cfg.type], i32, f32, current()
+def _rows_types(cfg: Rows):
+    kinds, i32, f32, current = _TORCH_TYPES or _types()
+    return kinds.get(cfg.type), i32, f32, current()
 
 
 def moe_w4a16_dispatch(cfg: Rows, topk_idx, x, expert_offsets, pair_list, pair_pos, rows, workspace,
                        stream=None) -> None:
     w = "moe_w4a16_dispatch"
-    dt, i32, _, dev = _rows_types(cfg, w)
+    dt, i32, _, dev = _rows_types(cfg)
     n = cfg.tokens * cfg.top_k
-    _check(lib().moe_w4a16_dispatch(ctypes.byref(cfg), _tptr(topk_idx, i32, n, dev, w),
+    _check((_lib or lib()).moe_w4a16_dispatch(ctypes.byref(cfg), _tptr(topk_idx, i32, n, dev, w),
                                     _tptr(x, dt, cfg.tokens * cfg.hidden, dev, w),
                                     _tptr(expert_offsets, i32, cfg.experts + 1, dev, w),
                                     _tptr(pair_list, i32, n, dev, w), _tptr(pair_pos, i32, n, dev, w),
                                     _tptr(rows, dt, n * cfg.hidden, dev, w), *_workspace(workspace, dev, w),
-                                    _stream(stream)), w)
+                                    _stream(stream, dev)), w)
 
 
 def moe_w4a16_dispatch_backward(cfg: Rows, pair_pos, grad_rows, grad_x, stream=None) -> None:
     w = "moe_w4a16_dispatch_backward"
-    dt, i32, _, dev = _rows_types(cfg, w)
+    dt, i32, _, dev = _rows_types(cfg)
     n = cfg.tokens * cfg.top_k
-    _check(lib().moe_w4a16_dispatch_backward(ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev, w),
+    _check((_lib or lib()).moe_w4a16_dispatch_backward(ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev, w),
                                              _tptr(grad_rows, dt, n * cfg.hidden, dev, w),
-                                             _tptr(grad_x, dt, cfg.tokens * cfg.hidden, dev, w), _stream(stream)), w)
+                                             _tptr(grad_x, dt, cfg.tokens * cfg.hidden, dev, w), _stream(stream, dev)), w)
 
 
 def moe_w4a16_combine_rows(cfg: Rows, pair_pos, topk_w, rows, residual, out, stream=None) -> None:
     w = "moe_w4a16_combine_rows"
-    dt, i32, f32, dev = _rows_types(cfg, w)
+    dt, i32, f32, dev = _rows_types(cfg)
     n, m = cfg.tokens * cfg.top_k, cfg.tokens * cfg.hidden
-    _check(lib().moe_w4a16_combine_rows(ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev, w),
+    _check((_lib or lib()).moe_w4a16_combine_rows(ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev, w),
                                         _tptr(topk_w, f32, n, dev, w), _tptr(rows, dt, n * cfg.hidden, dev, w),
                                         _tptr(residual, dt, m, dev, w), _tptr(out, dt, m, dev, w),
-                                        _stream(stream)), w)
+                                        _stream(stream, dev)), w)
 
 
 def moe_w4a16_combine_rows_backward(cfg: Rows, topk_idx, pair_pos, topk_w, rows, grad_out, grad_rows, grad_topk_w,
                                     grad_logits, stream=None) -> None:
     w = "moe_w4a16_combine_rows_backward"
-    dt, i32, f32, dev = _rows_types(cfg, w)
+    dt, i32, f32, dev = _rows_types(cfg)
     n, m = cfg.tokens * cfg.top_k, cfg.tokens * cfg.hidden
-    _check(lib().moe_w4a16_combine_rows_backward(
+    _check((_lib or lib()).moe_w4a16_combine_rows_backward(
         ctypes.byref(cfg), _tptr(topk_idx, i32, n, dev, w), _tptr(pair_pos, i32, n, dev, w),
         _tptr(topk_w, f32, n, dev, w), _tptr(rows, dt, n * cfg.hidden, dev, w), _tptr(grad_out, dt, m, dev, w),
         _tptr(grad_rows, dt, n * cfg.hidden, dev, w), _tptr(grad_topk_w, f32, n, dev, w),
-        _tptr(grad_logits, f32, cfg.tokens * cfg.experts, dev, w), _stream(stream)), w)
+        _tptr(grad_logits, f32, cfg.tokens * cfg.experts, dev, w), _stream(stream, dev)), w)
 
 
 def make_linear(rows, inp, out, groups=1, activation=3, gated=0, type=0) -> Linear:
@@ -423,44 +422,42 @@ def make_linear(rows, inp, out, groups=1, activation=3, gated=0, type=0) -> Line
 
 
 def moe_w4a16_linear_workspace_bytes(cfg: Linear) -> int:
-    return int(lib().moe_w4a16_linear_workspace_bytes(ctypes.byref(cfg)))
+    return int((_lib or lib()).moe_w4a16_linear_workspace_bytes(ctypes.byref(cfg)))
 
 
 def moe_w4a16_linear_backward_workspace_bytes(cfg: Linear) -> int:
-    return int(lib().moe_w4a16_linear_backward_workspace_bytes(ctypes.byref(cfg)))
+    return int((_lib or lib()).moe_w4a16_linear_backward_workspace_bytes(ctypes.byref(cfg)))
 
 
-def _linear_types(cfg: Linear, where: str):
-    if not 0 <= cfg.type <= 1:
-        raise MoeW4A16Error(ERR_SHAPE, where)
-    kinds, i32, f32, current = _types()
-    return kinds[cfg.type], i32, f32, current(), cfg.out * (2 if cfg.gated else 1)
+def _linear_types(cfg: Linear):
+    kinds, i32, f32, current = _TORCH_TYPES or _types()
+    return kinds.get(cfg.type), i32, f32, current(), cfg.out * (2 if cfg.gated else 1)
 
 
 def moe_w4a16_linear(cfg: Linear, x, expert_offsets, weight, bias, residual, out, preact, workspace,
                      stream=None) -> None:
     w = "moe_w4a16_linear"
-    dt, i32, f32, dev, nw = _linear_types(cfg, w)
+    dt, i32, f32, dev, nw = _linear_types(cfg)
     R, E = cfg.rows, cfg.groups
-    _check(lib().moe_w4a16_linear(ctypes.byref(cfg), _tptr(x, dt, R * cfg.inp, dev, w),
+    _check((_lib or lib()).moe_w4a16_linear(ctypes.byref(cfg), _tptr(x, dt, R * cfg.inp, dev, w),
                                   _tptr(expert_offsets, i32, E + 1, dev, w),
                                   _tptr(weight, dt, E * nw * cfg.inp, dev, w), _tptr(bias, f32, E * nw, dev, w),
                                   _tptr(residual, dt, R * cfg.out, dev, w), _tptr(out, dt, R * cfg.out, dev, w),
                                   _tptr(preact, dt, R * nw, dev, w), *_workspace(workspace, dev, w),
-                                  _stream(stream)), w)
+                                  _stream(stream, dev)), w)
 
 
 def moe_w4a16_linear_backward(cfg: Linear, x, expert_offsets, weight, preact, grad_out, grad_x, grad_weight,
                               grad_bias, workspace, stream=None) -> None:
     w = "moe_w4a16_linear_backward"
-    dt, i32, f32, dev, nw = _linear_types(cfg, w)
+    dt, i32, f32, dev, nw = _linear_types(cfg)
     R, E, K = cfg.rows, cfg.groups, cfg.inp
-    _check(lib().moe_w4a16_linear_backward(
+    _check((_lib or lib()).moe_w4a16_linear_backward(
         ctypes.byref(cfg), _tptr(x, dt, R * K, dev, w), _tptr(expert_offsets, i32, E + 1, dev, w),
         _tptr(weight, dt, E * nw * K, dev, w), _tptr(preact, dt, R * nw, dev, w),
         _tptr(grad_out, dt, R * cfg.out, dev, w), _tptr(grad_x, dt, R * K, dev, w),
         _tptr(grad_weight, dt, E * nw * K, dev, w), _tptr(grad_bias, f32, E * nw, dev, w),
-        *_workspace(workspace, dev, w), _stream(stream)), w)
+        *_workspace(workspace, dev, w), _stream(stream, dev)), w)
 
 
 def moe_w4a16_read_error(workspace, stream=None) -> int:

@@ -34,6 +34,35 @@
 
 namespace moe {
 namespace {
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+}  // namespace
+
+bool make_map(CUtensorMap* map, bool bf16, const void* base, int rank, const int64_t* dims, const int64_t* strides,
+              const int* box, bool swizzled) {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    es[i] = 1;
+    if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]) * 2;
+  }
+  return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                  const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
 
 constexpr int kForward = 0, kInputGrad = 1, kWeightGrad = 2;
 constexpr int kTileM = 128;            // lanes of tensor memory: outputs of one CTA's half of a tile
@@ -175,33 +204,29 @@ __device__ __forceinline__ uint32_t chunk_at(int c, int chunk) {
   return static_cast<uint32_t>((chunk >> 3) * (kStep * 128) + c * 128 + ((chunk ^ c) & 7) * 16);
 }
 
-// The rows of a 32-column step buffer to global memory (or back, for the residual): thread tid
-// of 128 takes chunk tid % kChunks of every (128 / kChunks)-th column.  f: first column of `p`
-// in elements, valid while f < width; rows of stride `ld` from row0 on, those below row_end.
-template <int kChunks, bool kLoad, typename Ptr>
-__device__ __forceinline__ void move_rows(uint8_t* buf, Ptr* p, int tid, int f, int width, int ld, int row0,
-                                          int row_end) {
+// The rows of a 32-column step between a step buffer and global memory: thread tid of 128 takes
+// chunk tid % kChunks of every (128 / kChunks)-th column, four at most.  f: the chunk's first
+// column in elements, valid while f < width; rows of stride `ld` from row0 on, those below
+// row_end.
+template <int kChunks, typename Do>
+__device__ __forceinline__ void for_rows(int tid, int f, int width, int row0, int row_end, Do&& act) {
   constexpr int rows = 128 / kChunks, passes = 32 / rows;
-  const int chunk = tid % kChunks, c0 = tid / kChunks;
+  const int c0 = tid / kChunks;
   if (f >= width) return;
-  uint4 v[passes];
 #pragma unroll
-  for (int i = 0; i < passes; ++i) {
-    const int c = c0 + i * rows;
-    if (!kLoad)
-      v[i] = *reinterpret_cast<const uint4*>(buf + chunk_at<32>(c, chunk));
-    else if (row0 + c < row_end)
-      v[i] = *reinterpret_cast<const uint4*>(p + static_cast<size_t>(row0 + c) * ld + f);
-  }
-#pragma unroll
-  for (int i = 0; i < passes; ++i) {
-    const int c = c0 + i * rows;
-    if constexpr (kLoad) {
-      if (row0 + c < row_end) *reinterpret_cast<uint4*>(buf + chunk_at<32>(c, chunk)) = v[i];
-    } else {
-      if (row0 + c < row_end) *reinterpret_cast<uint4*>(p + static_cast<size_t>(row0 + c) * ld + f) = v[i];
-    }
-  }
+  for (int i = 0; i < passes; ++i)
+    if (row0 + c0 + i * rows < row_end) act(i, c0 + i * rows);
+}
+template <int kChunks>
+__device__ __forceinline__ void store_rows(const uint8_t* buf, uint16_t* p, int tid, int f, int width, int ld, int row0,
+                                           int row_end) {
+  uint4 v[4];
+  for_rows<kChunks>(tid, f, width, row0, row_end, [&](int i, int c) {
+    v[i] = *reinterpret_cast<const uint4*>(buf + chunk_at<32>(c, tid % kChunks));
+  });
+  for_rows<kChunks>(tid, f, width, row0, row_end, [&](int i, int c) {
+    *reinterpret_cast<uint4*>(p + static_cast<size_t>(row0 + c) * ld + f) = v[i];
+  });
 }
 
 // Where the rows of an epilogue step go.
@@ -244,11 +269,11 @@ __device__ __forceinline__ void send_step(const Args& a, const CUtensorMap* map,
   } else if constexpr (kStep == 32) {
     if (kSaved) {
       const int chunk = tid % 16;
-      move_rows<16, false>(buf, kForm == 2 && chunk >= 8 ? a.preact + a.N : a.preact, tid,
-                           r.m0 + (kForm == 2 ? chunk & 7 : chunk) * 8, a.width, a.Nw, r.row0, r.row_end);
+      store_rows<16>(buf, kForm == 2 && chunk >= 8 ? a.preact + a.N : a.preact, tid,
+                     r.m0 + (kForm == 2 ? chunk & 7 : chunk) * 8, a.width, a.Nw, r.row0, r.row_end);
     } else {
       constexpr int chunks = kForm == 2 ? 8 : 16;
-      move_rows<chunks, false>(buf, a.out, tid, r.m0 + tid % chunks * 8, a.width, a.width, r.row0, r.row_end);
+      store_rows<chunks>(buf, a.out, tid, r.m0 + tid % chunks * 8, a.width, a.width, r.row0, r.row_end);
     }
   }
 }
@@ -289,12 +314,23 @@ __device__ __forceinline__ void gradient_step(const Args& a, const CUtensorMap* 
   send_step<0, kStep, false>(a, map_out, ybuf, group, tid, rows);
 }
 
+// The residual's pieces of a step, requested a step ahead of their use.
+template <int kForm>
+__device__ __forceinline__ void request_residual(const Args& a, uint4 (&res)[4], int tid, int m0, int row0,
+                                                 int row_end) {
+  constexpr int chunks = kForm == 2 ? 8 : 16;
+  const int f = m0 + tid % chunks * 8;
+  for_rows<chunks>(tid, f, a.width, row0, row_end, [&](int i, int c) {
+    res[i] = *reinterpret_cast<const uint4*>(a.residual + static_cast<size_t>(row0 + c) * a.width + f);
+  });
+}
+
 // A forward step of 32 columns.  kForm: 1 plain, 2 gated.  b: the biases of the thread's lanes
-// g, g + 8, g + 16, g + 24 of its quarter.
+// g, g + 8, g + 16, g + 24 of its quarter.  res: the step's residual, then the one's at `next`.
 template <int kForm>
 __device__ __forceinline__ void forward_step(const Args& a, const CUtensorMap* map_out, const CUtensorMap* map_z,
-                                             uint32_t tmem, const float (&b)[4], uint8_t* buf, int& flip, int group,
-                                             int tid, const StepRows& rows) {
+                                             uint32_t tmem, const float (&b)[4], uint4 (&res)[4], int next,
+                                             uint8_t* buf, int& flip, int group, int tid, const StepRows& rows) {
   constexpr int chunks = kForm == 2 ? 8 : 16;  // 16-byte chunks of outputs per column
   const int lane = tid & 31, quarter = tid >> 5;
   const int sub = lane >> 3, j = lane & 7;
@@ -323,9 +359,11 @@ __device__ __forceinline__ void forward_step(const Args& a, const CUtensorMap* m
   uint8_t* const ybuf = buf + flip * step_bytes<kForward>;
   flip ^= 1;
   if (a.residual) {
-    move_rows<chunks, true>(ybuf, a.residual, tid, rows.m0 + tid % chunks * 8, a.width, a.width, rows.row0,
-                            rows.row_end);
+    for_rows<chunks>(tid, rows.m0 + tid % chunks * 8, a.width, rows.row0, rows.row_end, [&](int i, int c) {
+      *reinterpret_cast<uint4*>(ybuf + chunk_at<32>(c, tid % chunks)) = res[i];
+    });
     group_sync(1 + group);
+    request_residual<kForm>(a, res, tid, rows.m0, next, rows.row_end);
   }
 #pragma unroll
   for (int i = 0; i < 4; i += (kForm == 2 ? 2 : 1)) {  // block column i (gated: i and i + 1)
@@ -401,16 +439,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
     mbar_init(drained, 1);
     fence_barrier_init();
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+    prefetch_map(&map_out);
   }
+  // the set-up overlaps the launch before; what it may still write is read after the wait
+  tcgen05_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised
+  tcgen05_fence_after();
   grid_dependency_wait();
-  if (warp == 2) {
+  if (!a.offsets) {
+    if (threadIdx.x == 0) {
+      start[0] = off[0] = 0;
+      start[1] = a.tiles_m * (kMode == kWeightGrad ? a.tiles_c : (a.R + kCols - 1) / kCols);
+      off[1] = a.R;
+    }
+  } else if (warp == 2) {
     // first rows of the experts (clamped to the rows there are) and their tiles: eight
     // experts per lane, then a scan over the lanes
     int o[9], n[8], sum = 0;
 #pragma unroll
     for (int i = 0; i < 9; ++i) {
       const int e = lane * 8 + i;
-      o[i] = a.offsets ? (e <= a.E ? min(max(a.offsets[e], 0), a.R) : a.R) : (e == 0 ? 0 : a.R);
+      o[i] = e <= a.E ? min(max(a.offsets[e], 0), a.R) : a.R;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -440,10 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       }
     }
   }
-  tcgen05_fence_before();
   __syncthreads();
-  cluster_sync();  // the peer's barriers are initialised
-  tcgen05_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int tiles = start[a.E];
   const int first_tile = blockIdx.x >> 1, step = gridDim.x >> 1;
@@ -619,6 +668,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           if (f < a.width) b[i] = bp[a.gated && (i & 1) ? a.N + f : f];
         }
       }
+      uint4 res[4];
+      if (kMode == kForward && a.residual) {
+        const int row0 = r.row0 + group * step_cols<kMode>;
+        if (a.gated)
+          request_residual<2>(a, res, tid, r.m0, row0, r.row_end);
+        else
+          request_residual<1>(a, res, tid, r.m0, row0, r.row_end);
+      }
       if (r.len > 0) {
         const bool ok = stage_wait_warp(acc_full + 8 * acc, acc_phase, a.err);
         if (!group_all(1 + group, ok)) break;
@@ -635,9 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           gradient_step<kStep>(a, &map_out, at, r.len > 0, buf, flip, group, tid, rows);
         } else {
           if (a.gated)
-            forward_step<2>(a, &map_out, &map_z, at, b, buf, flip, group, tid, rows);
+            forward_step<2>(a, &map_out, &map_z, at, b, res, row0 + 2 * kStep, buf, flip, group, tid, rows);
           else
-            forward_step<1>(a, &map_out, &map_z, at, b, buf, flip, group, tid, rows);
+            forward_step<1>(a, &map_out, &map_z, at, b, res, row0 + 2 * kStep, buf, flip, group, tid, rows);
         }
       }
       if (r.len > 0) {
@@ -661,34 +718,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------------- host
-
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-// Map of an array of 16-bit elements: extents from the contiguous one outwards, strides (in
-// elements) from the second, boxes 64 elements wide, 128-byte swizzle, zeros outside.
-bool make_map(CUtensorMap* map, bool bf16, const void* base, int rank, const int64_t* dims, const int64_t* strides,
-              const int* box) {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  if (!g_encode) return false;
-  cuuint64_t d[5], st[4];
-  cuuint32_t b[5], es[5];
-  for (int i = 0; i < rank; ++i) {
-    d[i] = static_cast<cuuint64_t>(dims[i]);
-    b[i] = static_cast<cuuint32_t>(box[i]);
-    es[i] = 1;
-    if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]) * 2;
-  }
-  return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
-                  const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int kMode, int kCols>
 cudaError_t launch_tiles(const Args& a, const CUtensorMap (&maps)[4], int64_t most_tiles, int num_sms,
@@ -765,15 +794,15 @@ cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, cons
     const int ba[5] = {64, 8, s.gated ? 2 : 1, a.tile_m / 8, 1};
     const int64_t db[2] = {K, R}, sb[1] = {K};
     const int bb[2] = {64, cols / 2};
-    ok = make_map(&maps[0], bf16, w, 5, da, sa, ba) && make_map(&maps[1], bf16, x, 2, db, sb, bb);
+    ok = make_map(&maps[0], bf16, w, 5, da, sa, ba, true) && make_map(&maps[1], bf16, x, 2, db, sb, bb, true);
   } else if (mode == kInputGrad) {
     const int64_t da[3] = {K, Nw, E}, sa[2] = {K, Nw * K}, db[2] = {Nw, R}, sb[1] = {Nw};
     const int ba[3] = {64, depth, 1}, bb[2] = {64, cols / 2};
-    ok = make_map(&maps[0], bf16, w, 3, da, sa, ba) && make_map(&maps[1], bf16, dz, 2, db, sb, bb);
+    ok = make_map(&maps[0], bf16, w, 3, da, sa, ba, true) && make_map(&maps[1], bf16, dz, 2, db, sb, bb, true);
   } else {
     const int64_t da[2] = {K, R}, sa[1] = {K}, db[2] = {Nw, R}, sb[1] = {Nw};
     const int box[2] = {64, depth};
-    ok = make_map(&maps[0], bf16, x, 2, da, sa, box) && make_map(&maps[1], bf16, dz, 2, db, sb, box);
+    ok = make_map(&maps[0], bf16, x, 2, da, sa, box, true) && make_map(&maps[1], bf16, dz, 2, db, sb, box, true);
   }
   const int64_t width = a.width, planes = mode == kWeightGrad ? E : 1, lines = mode == kWeightGrad ? Nw : R;
   // the output: rows of `width` in planes; where the width is a multiple of 64, columns of 64 as
@@ -783,16 +812,16 @@ cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, cons
   if (a.one_store) {
     const int64_t d[4] = {64, lines, width / 64, planes}, st4[3] = {width, 64, width * lines};
     const int box[4] = {64, rows, a.gated ? 1 : 2, 1};
-    ok = ok && make_map(&maps[2], bf16, a.out, 4, d, st4, box);
+    ok = ok && make_map(&maps[2], bf16, a.out, 4, d, st4, box, true);
   } else {
     const int64_t d[4] = {width, lines, 1, planes}, st4[3] = {width, width * lines, width * lines};
     const int box[4] = {64, rows, 1, 1};
-    ok = ok && make_map(&maps[2], bf16, a.out, 4, d, st4, box);
+    ok = ok && make_map(&maps[2], bf16, a.out, 4, d, st4, box, true);
   }
   if (a.preact) {
     const int64_t dzm[3] = {width, s.gated ? 2 : 1, R}, szm[2] = {width, Nw};
     const int bzm[3] = {64, 1, rows};
-    ok = ok && make_map(&maps[3], bf16, a.preact, 3, dzm, szm, bzm);
+    ok = ok && make_map(&maps[3], bf16, a.preact, 3, dzm, szm, bzm, true);
   }
   if (!ok) return cudaErrorInvalidValue;
   const int64_t most = mode == kWeightGrad ? E * a.tiles_m * a.tiles_c
