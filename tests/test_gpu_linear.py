@@ -403,6 +403,47 @@ def test_in_place_residual_and_infinities(B):
     assert [bool(v) for v in finite] == [i != e for i in range(c.E)]
 
 
+@pytest.mark.parametrize("E", [0, 3])
+def test_outputs_beyond_32_bits(B, E):
+    """2^21 rows of 1032 outputs: elements past 2^31, bytes past 2^32, in the output, the saved z,
+    the residual and dz; checked at the first, middle and last rows."""
+    R, K, N = (1 << 21) + 5, 16, 1032
+    dt, u = torch.bfloat16, HALF[1]
+    x, w = _normal((R, K), 1, dt), _normal((max(E, 1), N, K), 2, dt, K ** -0.5)
+    off = torch.tensor([0, 7, R - 100, R], dtype=torch.int32, device="cuda") if E else None
+    res = torch.randn(R, N, device="cuda", dtype=dt)
+    out, z = torch.empty_like(res), torch.empty_like(res)
+    cfg = B.make_linear(R, K, N, max(E, 1), 2, 0, 1)
+    ws = torch.empty(B.moe_w4a16_linear_backward_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    B.moe_w4a16_workspace_init(ws)
+    B.moe_w4a16_linear(cfg, x, off, w, None, res, out, z, ws)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    B.moe_w4a16_linear_backward(cfg, x, off, w, z, res, dx, dw, None, ws)
+    torch.cuda.synchronize()
+    assert B.moe_w4a16_read_error(ws) == B.OK
+    for r, e in ((0, 0), (6, 0), (7, 1), (R // 2, 1), (R - 101, 1), (R - 100, 2), (R - 1, 2)):
+        we = w[e if E else 0].double()
+        S = x[r].double().abs() @ we.abs().T
+        zz = x[r].double() @ we.T
+        e_z = (K + 2) * T23 * S
+        _check(z[r], zz, (1 + u) * e_z + u * zz.abs(), 1)
+        y = _act(zz, 2) + res[r].double()
+        _check(out[r], y, (1 + u) * (1.13 * e_z + ACT * zz.abs() + 1e-9) + (u + T23) * y.abs(), 1)
+        g = z[r].double()
+        dz = res[r].double() * _act_grad(g, 2)
+        e_dz = (1 + u) * res[r].double().abs() * 2 * ACT + u * dz.abs()
+        want = dz @ we
+        tol = (1 + u) * (e_dz @ we.abs() + (N + 2) * T23 * (dz.abs() @ we.abs())) + u * want.abs()
+        _check(dx[r], want, tol, 1)
+    if E:  # the expert of the last hundred rows
+        g, xs = z[R - 100:].double(), x[R - 100:].double()
+        d = res[R - 100:].double()
+        dz = d * _act_grad(g, 2)
+        e_dz = (1 + u) * d.abs() * 2 * ACT + u * dz.abs()
+        want = dz.T @ xs
+        _check(dw[2], want, (1 + u) * (e_dz.T @ xs.abs() + 102 * T23 * (dz.abs().T @ xs.abs())) + u * want.abs(), 1)
+
+
 def test_no_rows(B):
     cfg = B.make_linear(0, 64, 32, 3, 0, 0, 0)
     dw = torch.full((3, 32, 64), 7, dtype=torch.float16, device="cuda")

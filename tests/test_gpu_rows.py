@@ -291,6 +291,35 @@ def test_two_streams_and_a_captured_graph(B):
     assert all(torch.equal(bufs[n], replayed[n]) for n in bufs)
 
 
+def test_rows_beyond_32_bits(B):
+    """2^17 tokens top-8 of 2056 columns: the rows' last elements lie past 2^31, their bytes past 2^32."""
+    T, E, k, d, typ = (1 << 17) + 3, 16, 8, 2056, 1
+    cfg = B.make_rows(T, E, k, d, typ)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    idx = torch.argsort(torch.rand(T, E, generator=g, device="cuda"), dim=1)[:, :k].int().contiguous()
+    x = torch.randn(T, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    got = _dispatch(B, cfg, idx, x)
+    torch.cuda.synchronize()
+    order = torch.sort(idx.reshape(-1).long(), stable=True).indices
+    assert torch.equal(got["lst"].long(), order)
+    for part in torch.arange(T * k, device="cuda").split(1 << 17):
+        assert torch.equal(got["rows"][part], x[order[part] // k])
+    w = torch.rand(T, k, generator=g, device="cuda")
+    out, gw = torch.empty_like(x), torch.empty_like(w)
+    B.moe_w4a16_combine_rows(cfg, got["pos"], w, got["rows"], None, out)
+    gr = torch.empty_like(got["rows"])
+    B.moe_w4a16_combine_rows_backward(cfg, None, got["pos"], w, got["rows"], x, gr, gw, None)
+    torch.cuda.synchronize()
+    t = torch.tensor([0, T // 2, T - 1], device="cuda")
+    want = x[t].double() * w[t].double().sum(1, keepdim=True)
+    _within(out[t], want, (HALF[typ] + 9 * V) * want.abs() * 1.01)
+    for r in range(k):
+        want = w[t, r, None].double() * x[t].double()
+        _within(gr[got["pos"][t, r].long()], want, (HALF[typ] + V) * want.abs() * 1.01)
+        dw = (x[t].double() ** 2).sum(1)
+        _within(gw[t, r], dw, (-(-d // 8 // 32) * 8 + 13) * V * dw * 1.01)
+
+
 def test_no_tokens(B):
     cfg = B.make_rows(0, 5, 2, 64, 0)
     off = torch.full((6,), 3, dtype=torch.int32, device="cuda")

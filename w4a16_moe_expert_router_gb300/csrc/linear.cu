@@ -669,12 +669,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         }
       }
       uint4 res[4];
+      const int tile_end = min(r.row_end, r.row0 + kCols);  // the next tile's rows may be written meanwhile
       if (kMode == kForward && a.residual) {
         const int row0 = r.row0 + group * step_cols<kMode>;
         if (a.gated)
-          request_residual<2>(a, res, tid, r.m0, row0, r.row_end);
+          request_residual<2>(a, res, tid, r.m0, row0, tile_end);
         else
-          request_residual<1>(a, res, tid, r.m0, row0, r.row_end);
+          request_residual<1>(a, res, tid, r.m0, row0, tile_end);
       }
       if (r.len > 0) {
         const bool ok = stage_wait_warp(acc_full + 8 * acc, acc_phase, a.err);
@@ -683,10 +684,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       }
       constexpr int kStep = step_cols<kMode>;
 #pragma unroll 1
-      for (int c = group * kStep; c < kCols && r.row0 + c < r.row_end; c += 2 * kStep) {
+      for (int c = group * kStep; r.row0 + c < tile_end; c += 2 * kStep) {
         const uint32_t at = tmem + acc * kCols + c + (static_cast<uint32_t>(quarter * 32) << 16);
         const int row0 = r.row0 + c;
-        const StepRows rows{r.m0, row0, r.row_end, kMode == kWeightGrad || row0 + kStep <= r.row_end,
+        const StepRows rows{r.m0, row0, tile_end, kMode == kWeightGrad || row0 + kStep <= tile_end,
                             kMode == kWeightGrad ? r.c0 + c : row0, kMode == kWeightGrad ? r.e : 0};
         if constexpr (kMode != kForward) {
           gradient_step<kStep>(a, &map_out, at, r.len > 0, buf, flip, group, tid, rows);
