@@ -22,7 +22,9 @@
  *               RMSNorm).
  * Beside the layer, moe_w4a16_sample runs the per-step sampler of the
  * denoising loop (entropy, Gumbel-max token, acceptance of positions) in one
- * streaming pass over the vocabulary logits (see its section below).
+ * streaming pass over the vocabulary logits (see its section below), and the calls
+ * of the section "the layer in 16 bits, with gradients" run the layer's steps on
+ * fp16 or bf16 weights, forwards and backwards.
  * The weight format follows the model card's "requirements" paragraph
  * (dg-w4a16-v1: two nibbles per byte; gate_up_proj grouped along the
  * contraction dim; down_proj grouped at 64 because its contraction dim, 704, is
