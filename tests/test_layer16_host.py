@@ -154,7 +154,7 @@ def test_linear_without_rows_is_a_no_op():
 
 def test_binding_refuses_tensors_it_cannot_pass_on(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(B, "_TORCH_TYPES", None)
+    monkeypatch.setattr(B, "_CONTEXT", None)
     cfg = _rows()
     good = dict(pos=torch.zeros(16, 2, dtype=torch.int32), w=torch.zeros(16, 2),
                 rows=torch.zeros(32, 64, dtype=torch.float16), out=torch.zeros(16, 64, dtype=torch.float16))
@@ -171,7 +171,7 @@ def test_binding_refuses_tensors_it_cannot_pass_on(monkeypatch):
     assert call(pos=torch.zeros(2, 16, dtype=torch.int32).t()) == B.ERR_SHAPE    # strided
     assert call(pos=P, w=torch.zeros(16, 2, dtype=torch.float16)) == B.ERR_SHAPE
     assert call(pos=P, w=P, rows=torch.zeros(32, 64)) == B.ERR_SHAPE
-    monkeypatch.setattr(B, "_TORCH_TYPES", None)
+    monkeypatch.setattr(B, "_CONTEXT", None)
 
 
 def test_structs_match_the_header(tmp_path):

@@ -189,12 +189,10 @@ def _find_raw_stream():
     return _raw_stream
 
 
-def _stream(stream, dev=None) -> int | None:
+def _stream(stream) -> int | None:
     if stream is None:
-        if dev is None:
-            import torch
-            dev = torch.cuda.current_device()
-        return (_raw_stream or _find_raw_stream())(dev)
+        import torch
+        return (_raw_stream or _find_raw_stream())(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -328,36 +326,41 @@ def moe_w4a16_sample(cfg: Sampler, logits, revealed, token, entropy, pmax, accep
 #
 # These calls take tensors of several types, so a tensor is checked before its
 # address is passed on: type, number of elements, contiguity, and that it lives on
-# the current CUDA device (raw addresses are passed on as they are).
+# the current CUDA device (raw addresses are passed on as they are).  The checks are
+# most of a small call's time, so they are kept short.
 
-_TORCH_TYPES = None
+_CONTEXT = None
 
 
-def _types():
-    """torch's types by code, int32, fp32, and the getter of the current device."""
-    global _TORCH_TYPES
-    if _TORCH_TYPES is None:
+def _context():
+    """torch's types by code, int32, fp32, and the getters of the current device and of a
+    device's current stream."""
+    global _CONTEXT
+    if _CONTEXT is None:
         import torch
-        _TORCH_TYPES = ({FP16: torch.float16, BF16: torch.bfloat16, FP32: torch.float32}, torch.int32,
-                        torch.float32, torch.cuda.current_device)
-    return _TORCH_TYPES
+        _CONTEXT = ({FP16: torch.float16, BF16: torch.bfloat16, FP32: torch.float32}, torch.int32, torch.float32,
+                    torch.cuda.current_device, _raw_stream or _find_raw_stream())
+    return _CONTEXT
 
 
-def _tptr(t, dtype, n, dev, where) -> int | None:
-    if t is None or type(t) is int:
-        return t
-    if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
+def _tptr(t, dtype, n, dev) -> int | None:
+    try:
+        if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # no tensor
+        if t is None or isinstance(t, int):
+            return t
+        raise
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
-        raise MoeW4A16Error(ERR_SHAPE, f"{where}: a contiguous {dtype} tensor of {n} elements is wanted, got "
-                                       f"{t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}")
-    raise MoeW4A16Error(ERR_DEVICE, f"{where}: a tensor lives on {t.device}, the call runs on cuda:{dev}")
+        raise MoeW4A16Error(ERR_SHAPE, f"a contiguous {dtype} tensor of {n} elements is wanted, got {t.dtype} "
+                                       f"{tuple(t.shape)}, strides {tuple(t.stride())}")
+    raise MoeW4A16Error(ERR_DEVICE, f"a tensor lives on {t.device}, the call runs on cuda:{dev}")
 
 
-def _workspace(t, dev, where):
+def _wptr(t, dev):
     if t.get_device() != dev or not t.is_contiguous():
-        raise MoeW4A16Error(ERR_DEVICE, f"{where}: a contiguous workspace on cuda:{dev} is wanted")
-    return t.data_ptr(), t.numel() * t.element_size()
+        raise MoeW4A16Error(ERR_DEVICE, f"a contiguous workspace on cuda:{dev} is wanted, got one on {t.device}")
+    return t.data_ptr()
 
 
 def make_rows(tokens, experts, top_k, hidden, type=0) -> Rows:
@@ -368,53 +371,57 @@ def moe_w4a16_dispatch_workspace_bytes(cfg: Rows) -> int:
     return int(lib().moe_w4a16_dispatch_workspace_bytes(ctypes.byref(cfg)))
 
 
-def _rows_types(cfg: Rows):
-    kinds, i32, f32, current = _TORCH_TYPES or _types()
-    return kinds.get(cfg.type), i32, f32, current()
-
-
 def moe_w4a16_dispatch(cfg: Rows, topk_idx, x, expert_offsets, pair_list, pair_pos, rows, workspace,
                        stream=None) -> None:
-    w = "moe_w4a16_dispatch"
-    dt, i32, _, dev = _rows_types(cfg)
-    n = cfg.tokens * cfg.top_k
-    _check((_lib or lib()).moe_w4a16_dispatch(ctypes.byref(cfg), _tptr(topk_idx, i32, n, dev, w),
-                                    _tptr(x, dt, cfg.tokens * cfg.hidden, dev, w),
-                                    _tptr(expert_offsets, i32, cfg.experts + 1, dev, w),
-                                    _tptr(pair_list, i32, n, dev, w), _tptr(pair_pos, i32, n, dev, w),
-                                    _tptr(rows, dt, n * cfg.hidden, dev, w), *_workspace(workspace, dev, w),
-                                    _stream(stream, dev)), w)
+    types, i32, _, device, current = _CONTEXT or _context()
+    dev, dt, T, d = device(), types.get(cfg.type), cfg.tokens, cfg.hidden
+    n = T * cfg.top_k
+    st = lib().moe_w4a16_dispatch(
+        ctypes.byref(cfg), _tptr(topk_idx, i32, n, dev), _tptr(x, dt, T * d, dev),
+        _tptr(expert_offsets, i32, cfg.experts + 1, dev), _tptr(pair_list, i32, n, dev), _tptr(pair_pos, i32, n, dev),
+        _tptr(rows, dt, n * d, dev), _wptr(workspace, dev), _nbytes(workspace),
+        current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_dispatch")
 
 
 def moe_w4a16_dispatch_backward(cfg: Rows, pair_pos, grad_rows, grad_x, stream=None) -> None:
-    w = "moe_w4a16_dispatch_backward"
-    dt, i32, _, dev = _rows_types(cfg)
-    n = cfg.tokens * cfg.top_k
-    _check((_lib or lib()).moe_w4a16_dispatch_backward(ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev, w),
-                                             _tptr(grad_rows, dt, n * cfg.hidden, dev, w),
-                                             _tptr(grad_x, dt, cfg.tokens * cfg.hidden, dev, w), _stream(stream, dev)), w)
+    types, i32, _, device, current = _CONTEXT or _context()
+    dev, dt, T, d = device(), types.get(cfg.type), cfg.tokens, cfg.hidden
+    n = T * cfg.top_k
+    st = lib().moe_w4a16_dispatch_backward(
+        ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev), _tptr(grad_rows, dt, n * d, dev),
+        _tptr(grad_x, dt, T * d, dev), current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_dispatch_backward")
 
 
 def moe_w4a16_combine_rows(cfg: Rows, pair_pos, topk_w, rows, residual, out, stream=None) -> None:
-    w = "moe_w4a16_combine_rows"
-    dt, i32, f32, dev = _rows_types(cfg)
-    n, m = cfg.tokens * cfg.top_k, cfg.tokens * cfg.hidden
-    _check((_lib or lib()).moe_w4a16_combine_rows(ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev, w),
-                                        _tptr(topk_w, f32, n, dev, w), _tptr(rows, dt, n * cfg.hidden, dev, w),
-                                        _tptr(residual, dt, m, dev, w), _tptr(out, dt, m, dev, w),
-                                        _stream(stream, dev)), w)
+    types, i32, f32, device, current = _CONTEXT or _context()
+    dev, dt, T, d = device(), types.get(cfg.type), cfg.tokens, cfg.hidden
+    n, m = T * cfg.top_k, T * d
+    st = lib().moe_w4a16_combine_rows(
+        ctypes.byref(cfg), _tptr(pair_pos, i32, n, dev), topk_w if topk_w is None else _tptr(topk_w, f32, n, dev),
+        _tptr(rows, dt, n * d, dev), residual if residual is None else _tptr(residual, dt, m, dev),
+        _tptr(out, dt, m, dev), current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_combine_rows")
 
 
 def moe_w4a16_combine_rows_backward(cfg: Rows, topk_idx, pair_pos, topk_w, rows, grad_out, grad_rows, grad_topk_w,
                                     grad_logits, stream=None) -> None:
-    w = "moe_w4a16_combine_rows_backward"
-    dt, i32, f32, dev = _rows_types(cfg)
-    n, m = cfg.tokens * cfg.top_k, cfg.tokens * cfg.hidden
-    _check((_lib or lib()).moe_w4a16_combine_rows_backward(
-        ctypes.byref(cfg), _tptr(topk_idx, i32, n, dev, w), _tptr(pair_pos, i32, n, dev, w),
-        _tptr(topk_w, f32, n, dev, w), _tptr(rows, dt, n * cfg.hidden, dev, w), _tptr(grad_out, dt, m, dev, w),
-        _tptr(grad_rows, dt, n * cfg.hidden, dev, w), _tptr(grad_topk_w, f32, n, dev, w),
-        _tptr(grad_logits, f32, cfg.tokens * cfg.experts, dev, w), _stream(stream, dev)), w)
+    types, i32, f32, device, current = _CONTEXT or _context()
+    dev, dt, T, d = device(), types.get(cfg.type), cfg.tokens, cfg.hidden
+    n, m = T * cfg.top_k, T * d
+    st = lib().moe_w4a16_combine_rows_backward(
+        ctypes.byref(cfg), topk_idx if topk_idx is None else _tptr(topk_idx, i32, n, dev),
+        _tptr(pair_pos, i32, n, dev), _tptr(topk_w, f32, n, dev), _tptr(rows, dt, n * d, dev),
+        _tptr(grad_out, dt, m, dev), grad_rows if grad_rows is None else _tptr(grad_rows, dt, n * d, dev),
+        grad_topk_w if grad_topk_w is None else _tptr(grad_topk_w, f32, n, dev),
+        grad_logits if grad_logits is None else _tptr(grad_logits, f32, T * cfg.experts, dev),
+        current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_combine_rows_backward")
 
 
 def make_linear(rows, inp, out, groups=1, activation=3, gated=0, type=0) -> Linear:
@@ -422,42 +429,45 @@ def make_linear(rows, inp, out, groups=1, activation=3, gated=0, type=0) -> Line
 
 
 def moe_w4a16_linear_workspace_bytes(cfg: Linear) -> int:
-    return int((_lib or lib()).moe_w4a16_linear_workspace_bytes(ctypes.byref(cfg)))
+    return int(lib().moe_w4a16_linear_workspace_bytes(ctypes.byref(cfg)))
 
 
 def moe_w4a16_linear_backward_workspace_bytes(cfg: Linear) -> int:
-    return int((_lib or lib()).moe_w4a16_linear_backward_workspace_bytes(ctypes.byref(cfg)))
-
-
-def _linear_types(cfg: Linear):
-    kinds, i32, f32, current = _TORCH_TYPES or _types()
-    return kinds.get(cfg.type), i32, f32, current(), cfg.out * (2 if cfg.gated else 1)
+    return int(lib().moe_w4a16_linear_backward_workspace_bytes(ctypes.byref(cfg)))
 
 
 def moe_w4a16_linear(cfg: Linear, x, expert_offsets, weight, bias, residual, out, preact, workspace,
                      stream=None) -> None:
-    w = "moe_w4a16_linear"
-    dt, i32, f32, dev, nw = _linear_types(cfg)
-    R, E = cfg.rows, cfg.groups
-    _check((_lib or lib()).moe_w4a16_linear(ctypes.byref(cfg), _tptr(x, dt, R * cfg.inp, dev, w),
-                                  _tptr(expert_offsets, i32, E + 1, dev, w),
-                                  _tptr(weight, dt, E * nw * cfg.inp, dev, w), _tptr(bias, f32, E * nw, dev, w),
-                                  _tptr(residual, dt, R * cfg.out, dev, w), _tptr(out, dt, R * cfg.out, dev, w),
-                                  _tptr(preact, dt, R * nw, dev, w), *_workspace(workspace, dev, w),
-                                  _stream(stream, dev)), w)
+    types, i32, f32, device, current = _CONTEXT or _context()
+    dev, dt, R, K, N, E = device(), types.get(cfg.type), cfg.rows, cfg.inp, cfg.out, cfg.groups
+    Nw = 2 * N if cfg.gated else N
+    st = lib().moe_w4a16_linear(
+        ctypes.byref(cfg), _tptr(x, dt, R * K, dev),
+        expert_offsets if expert_offsets is None else _tptr(expert_offsets, i32, E + 1, dev),
+        _tptr(weight, dt, E * Nw * K, dev), bias if bias is None else _tptr(bias, f32, E * Nw, dev),
+        residual if residual is None else _tptr(residual, dt, R * N, dev), _tptr(out, dt, R * N, dev),
+        preact if preact is None else _tptr(preact, dt, R * Nw, dev), _wptr(workspace, dev), _nbytes(workspace),
+        current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_linear")
 
 
 def moe_w4a16_linear_backward(cfg: Linear, x, expert_offsets, weight, preact, grad_out, grad_x, grad_weight,
                               grad_bias, workspace, stream=None) -> None:
-    w = "moe_w4a16_linear_backward"
-    dt, i32, f32, dev, nw = _linear_types(cfg)
-    R, E, K = cfg.rows, cfg.groups, cfg.inp
-    _check((_lib or lib()).moe_w4a16_linear_backward(
-        ctypes.byref(cfg), _tptr(x, dt, R * K, dev, w), _tptr(expert_offsets, i32, E + 1, dev, w),
-        _tptr(weight, dt, E * nw * K, dev, w), _tptr(preact, dt, R * nw, dev, w),
-        _tptr(grad_out, dt, R * cfg.out, dev, w), _tptr(grad_x, dt, R * K, dev, w),
-        _tptr(grad_weight, dt, E * nw * K, dev, w), _tptr(grad_bias, f32, E * nw, dev, w),
-        *_workspace(workspace, dev, w), _stream(stream, dev)), w)
+    types, i32, f32, device, current = _CONTEXT or _context()
+    dev, dt, R, K, N, E = device(), types.get(cfg.type), cfg.rows, cfg.inp, cfg.out, cfg.groups
+    Nw = 2 * N if cfg.gated else N
+    st = lib().moe_w4a16_linear_backward(
+        ctypes.byref(cfg), x if x is None else _tptr(x, dt, R * K, dev),
+        expert_offsets if expert_offsets is None else _tptr(expert_offsets, i32, E + 1, dev),
+        weight if weight is None else _tptr(weight, dt, E * Nw * K, dev),
+        preact if preact is None else _tptr(preact, dt, R * Nw, dev), _tptr(grad_out, dt, R * N, dev),
+        grad_x if grad_x is None else _tptr(grad_x, dt, R * K, dev),
+        grad_weight if grad_weight is None else _tptr(grad_weight, dt, E * Nw * K, dev),
+        grad_bias if grad_bias is None else _tptr(grad_bias, f32, E * Nw, dev), _wptr(workspace, dev),
+        _nbytes(workspace), current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_linear_backward")
 
 
 def moe_w4a16_read_error(workspace, stream=None) -> int:

@@ -202,16 +202,19 @@ moe_w4a16_status moe_w4a16_linear_backward(const moe_w4a16_linear_cfg* cfg, cons
   auto* base = static_cast<uint8_t*>(workspace);
   int32_t* err = &static_cast<moe::WsHeader*>(workspace)->error;
   const void* dz = needs_z ? base + w.dz : grad_out;
-  if (needs_z || grad_bias) {
-    if (moe::launch_linear_dz(s, expert_offsets, needs_z ? preact : nullptr, grad_out, base + w.dz,
-                              reinterpret_cast<float*>(base + w.partial), grad_bias, cs) != cudaSuccess)
-      return MOE_W4A16_ERR_CUDA;
-  }
+  auto* const partial = grad_bias ? reinterpret_cast<float*>(base + w.partial) : nullptr;
+  if ((needs_z || grad_bias) &&
+      moe::launch_linear_dz(s, expert_offsets, needs_z ? preact : nullptr, grad_out, base + w.dz, partial, cs) !=
+          cudaSuccess)
+    return MOE_W4A16_ERR_CUDA;
   if (grad_x &&
       moe::launch_linear_input_grad(s, expert_offsets, weight, dz, grad_x, err, sms, cs) != cudaSuccess)
     return MOE_W4A16_ERR_CUDA;
-  if (grad_weight &&
-      moe::launch_linear_weight_grad(s, expert_offsets, x, dz, grad_weight, err, sms, cs) != cudaSuccess)
+  if (grad_weight && moe::launch_linear_weight_grad(s, expert_offsets, x, dz, grad_weight, partial, grad_bias, err, sms,
+                                                    cs) != cudaSuccess)
+    return MOE_W4A16_ERR_CUDA;
+  if (grad_bias && !grad_weight &&
+      moe::launch_linear_dbias(s, expert_offsets, partial, grad_bias, cs) != cudaSuccess)
     return MOE_W4A16_ERR_CUDA;
   return MOE_W4A16_OK;
 }

@@ -7,8 +7,9 @@
 // that follow: a rounding of half a step per element, independent from element to
 // element, so a sum over dz is off by about what its own rounding to the type costs.
 // The bias gradient takes the fp32 values: a CTA sums up to 64 rows of one expert for 256
-// columns (eight rows per thread, then eight threads in order) into a partial, and a second
-// launch adds an expert's partials, eight threads per column, in order: no atomics.  Bound
+// columns (eight rows per thread, then eight threads in order) into a partial, and an
+// expert's partials are added, eight strided sums per column in order, by an idle warp of
+// the weight gradient that follows or, without one, by a launch of its own: no atomics.  Bound
 // by memory: z and dout read once, dz written once; each thread requests two rows
 // before it uses the first.
 #include "activation.cuh"
@@ -21,16 +22,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPieces = 32;                 // 16-byte pieces (256 columns) per CTA
 constexpr int kLanes = kThreads / kPieces;  // threads per column
-constexpr int kBatch = 2;                   // rows per thread at a time (four hold too many registers: 79 against 70 us at 8192 x 8192)
-// Rows per CTA (64: 16384 gated rows over 128 experts take 34 us, 39 with 32 and 35 with 128);
-// more where the blocks would be more than a grid's y extent holds.
-__host__ __device__ __forceinline__ int rows_per_cta(int R) { return R <= (1 << 21) ? 64 : 256; }
+constexpr int kBatch = 2;  // rows per thread at a time (four: too many registers, 79 against 70 us at 8192 x 8192)
 
-// The row range of block b: experts own ceil(rows / rows_per_cta) blocks each, in order.
+// The row range of block b: experts own ceil(rows / per) blocks each, in order.
 // Whole CTA; false when there is no such block.
-__device__ __forceinline__ bool find_block(const int32_t* offsets, int E, int R, int b, int* sh, int& e, int& r0,
-                                           int& r1) {
-  const int per = rows_per_cta(R);
+__device__ __forceinline__ bool find_block(const int32_t* offsets, int E, int R, int per, int b, int* sh, int& e,
+                                           int& r0, int& r1) {
   if (!offsets) {
     e = 0;
     r0 = b * per;
@@ -88,13 +85,14 @@ __device__ __forceinline__ void derivatives(float (&g)[8], int act, float (&o)[8
 // grid (column blocks of N, row blocks).  z NULL: dz is dout itself and only the bias is wanted.
 template <int kType, bool kGated>
 __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const int32_t* offsets, const uint4* z, const uint4* dout,
-                                                             uint4* dz, float* partial, int R, int E, int N, int act) {
+                                                             uint4* dz, float* partial, int R, int E, int N, int act,
+                                                             int per) {
   __shared__ int sh[12];
   __shared__ float sum[kGated ? 2 : 1][kLanes][kPieces * 8];
   grid_dependents_launch();
   grid_dependency_wait();
   int e, r0, r1;
-  if (!find_block(offsets, E, R, blockIdx.y, sh, e, r0, r1)) return;
+  if (!find_block(offsets, E, R, per, blockIdx.y, sh, e, r0, r1)) return;
   const int piece = threadIdx.x % kPieces, rl = threadIdx.x / kPieces;
   const int nvec = N / 8, zvec = kGated ? 2 * nvec : nvec;
   const int col = blockIdx.x * kPieces + piece;
@@ -166,14 +164,14 @@ __global__ void __launch_bounds__(kThreads) linear_dz_kernel(const int32_t* offs
 }
 
 // db[e][n]: the partials of expert e's blocks; grid (column blocks of 32, experts), warp l
-// takes every eighth partial.
+// takes every eighth partial (the order in which the weight gradient's warp adds them too).
 __global__ void __launch_bounds__(kThreads) linear_dbias_kernel(const int32_t* offsets, const float* partial, float* db,
-                                                                int R, int E, int Nw) {
+                                                                int R, int E, int Nw, int per) {
   __shared__ int sh[9];
   __shared__ float sum[8][32];
   grid_dependents_launch();
   grid_dependency_wait();
-  const int e = blockIdx.y, i = threadIdx.x, lane = i & 31, warp = i >> 5, per = rows_per_cta(R);
+  const int e = blockIdx.y, i = threadIdx.x, lane = i & 31, warp = i >> 5;
   int first = 0, count = (R + per - 1) / per;
   if (offsets) {
     int n = 0;
@@ -210,23 +208,26 @@ __global__ void __launch_bounds__(kThreads) linear_dbias_kernel(const int32_t* o
 }  // namespace
 
 int linear_row_blocks(const LinearDims& s) {
-  const int per = rows_per_cta(s.R), blocks = (s.R + per - 1) / per;
+  const int per = linear_block_rows(s.R), blocks = (s.R + per - 1) / per;
   return s.grouped ? blocks + (s.E < s.R ? s.E : s.R) : blocks;
 }
 
 cudaError_t launch_linear_dz(const LinearDims& s, const int32_t* offsets, const void* z, const void* dout, void* dz,
-                             float* partial, float* dbias, cudaStream_t st) {
+                             float* partial, cudaStream_t st) {
   const dim3 grid((s.N + kPieces * 8 - 1) / (kPieces * 8), linear_row_blocks(s));
   const auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, dim3(kThreads), 0, st, offsets, static_cast<const uint4*>(z),
-                      static_cast<const uint4*>(dout), static_cast<uint4*>(dz), dbias ? partial : nullptr, s.R, s.E,
-                      s.N, s.act);
+                      static_cast<const uint4*>(dout), static_cast<uint4*>(dz), partial, s.R, s.E, s.N, s.act,
+                      linear_block_rows(s.R));
   };
-  const cudaError_t err = s.type == 1 ? (s.gated ? go(linear_dz_kernel<1, true>) : go(linear_dz_kernel<1, false>))
-                                      : (s.gated ? go(linear_dz_kernel<0, true>) : go(linear_dz_kernel<0, false>));
-  if (err != cudaSuccess || !dbias) return err;
-  return launch_pdl(linear_dbias_kernel, dim3((s.Nw() + 31) / 32, s.E), dim3(kThreads), 0, st, offsets,
-                    static_cast<const float*>(partial), dbias, s.R, s.E, s.Nw());
+  if (s.type == 1) return s.gated ? go(linear_dz_kernel<1, true>) : go(linear_dz_kernel<1, false>);
+  return s.gated ? go(linear_dz_kernel<0, true>) : go(linear_dz_kernel<0, false>);
+}
+
+cudaError_t launch_linear_dbias(const LinearDims& s, const int32_t* offsets, const float* partial, float* dbias,
+                                cudaStream_t st) {
+  return launch_pdl(linear_dbias_kernel, dim3((s.Nw() + 31) / 32, s.E), dim3(kThreads), 0, st, offsets, partial, dbias,
+                    s.R, s.E, s.Nw(), linear_block_rows(s.R));
 }
 
 }  // namespace moe

@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     if (!__syncthreads_and(ok)) {  // (the chunk is read)
       // a wait ran out and is recorded: the other copies in flight land, and the outputs are invalid
       if (fetcher)
-        for (int k = i + 1; k < chunks && k < i + kStages; ++k) mbar_wait(full + 8 * (k % kStages), (k / kStages) & 1, err);
+        for (int k = i + 1; k < chunks && k < i + kStages; ++k)
+          mbar_wait(full + 8 * (k % kStages), (k / kStages) & 1, err);
       return false;
     }
     if (fetcher && i + kStages < chunks) fetch(i + kStages);
@@ -194,7 +195,8 @@ cudaError_t launch_type(const LinearDims& s, const int32_t* offsets, const void*
   CUtensorMap map;
   if (!make_map(&map, kType == 1, w, 5, dims, strides, box, false)) return cudaErrorInvalidValue;
   const auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(kThreads), kSmem, st, map, offsets, static_cast<const uint4*>(x), bias, static_cast<const uint16_t*>(residual),
+    return launch_pdl(kernel, grid, dim3(kThreads), kSmem, st, map, offsets, static_cast<const uint4*>(x), bias,
+                      static_cast<const uint16_t*>(residual),
                       static_cast<uint16_t*>(out), static_cast<uint16_t*>(preact), err, s.R, s.E, s.K, s.N, s.gated,
                       s.act);
   };
