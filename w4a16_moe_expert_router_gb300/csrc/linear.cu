@@ -659,33 +659,49 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       }
     }
   } else if (kMode == kWeightGrad && warp == 3) {
-    // ---- weight grad: the bias gradient, for the columns of each first tile along m.  Four
-    // columns at a time, eight strided sums over the expert's row blocks, added in order.
+    // ---- weight grad: the bias gradient, for the columns of one tile along m (not always the
+    // same one, so that the pairs share the work: a load takes microseconds while the tiles
+    // stream).  Eight strided sums over the expert's row blocks, added in order.
     if (a.dbias && rank == 0) {
       int e = 0, counted = 0, before = 0;  // row blocks of the experts before `counted`
       for (int t = first_tile; t < tiles; t += step) {
         const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
-        if (r.m0 != 0) continue;
+        if (r.m0 / (2 * kTileM) != (r.c0 / kCols + r.e) % a.tiles_m) continue;
         const auto blocks = [&](int i) { return (max(off[i + 1] - off[i], 0) + a.block_rows - 1) / a.block_rows; };
         for (; counted < r.e; ++counted) before += blocks(counted);
         const int count = blocks(r.e);
-        for (int c = r.c0 + lane * 4; c < min(r.c0 + kCols, a.Nw); c += 128) {
-          const float* const p = a.partial + static_cast<size_t>(before) * a.Nw + c;
-          float4 s[8];
+        constexpr int kParts = kCols > 128 ? kCols / 128 : 1;  // columns c0 + 128 i + 4 lane ..
+        const float* const p = a.partial + static_cast<size_t>(before) * a.Nw + r.c0 + 4 * lane;
+        float4 s[kParts][8];
 #pragma unroll
-          for (int l = 0; l < 8; ++l) s[l] = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int b = 0; b < count; b += 8) {
+        for (int i = 0; i < kParts; ++i)
+#pragma unroll
+          for (int l = 0; l < 8; ++l) s[i][l] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b = 0; b < count; b += 8) {
+          float4 v[kParts][8];
+#pragma unroll
+          for (int i = 0; i < kParts; ++i)
+#pragma unroll
+            for (int l = 0; l < 8; ++l) {
+              v[i][l] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (b + l < count && r.c0 + 128 * i + 4 * lane < a.Nw)
+                v[i][l] = *reinterpret_cast<const float4*>(p + static_cast<size_t>(b + l) * a.Nw + 128 * i);
+            }
+#pragma unroll
+          for (int i = 0; i < kParts; ++i)
 #pragma unroll
             for (int l = 0; l < 8; ++l)
-              if (b + l < count) {
-                const float4 v = *reinterpret_cast<const float4*>(p + static_cast<size_t>(b + l) * a.Nw);
-                s[l] = make_float4(s[l].x + v.x, s[l].y + v.y, s[l].z + v.z, s[l].w + v.w);
-              }
-          }
+              s[i][l] = make_float4(s[i][l].x + v[i][l].x, s[i][l].y + v[i][l].y, s[i][l].z + v[i][l].z,
+                                    s[i][l].w + v[i][l].w);
+        }
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
           float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int l = 0; l < 8; ++l) d = make_float4(d.x + s[l].x, d.y + s[l].y, d.z + s[l].z, d.w + s[l].w);
-          *reinterpret_cast<float4*>(a.dbias + static_cast<size_t>(r.e) * a.Nw + c) = d;
+          for (int l = 0; l < 8; ++l)
+            d = make_float4(d.x + s[i][l].x, d.y + s[i][l].y, d.z + s[i][l].z, d.w + s[i][l].w);
+          const int c = r.c0 + 128 * i + 4 * lane;
+          if (c < a.Nw) *reinterpret_cast<float4*>(a.dbias + static_cast<size_t>(r.e) * a.Nw + c) = d;
         }
       }
     }
