@@ -162,18 +162,6 @@ __device__ __forceinline__ float2 unpack2(uint32_t v, int bf16) {
 
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
-// Barrier of a group of 128 threads that tells each whether `ok` held for all, so that a
-// group whose bounded wait ran out for one warp leaves together.
-__device__ __forceinline__ bool group_all(int id, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(ok)), "r"(id)
-      : "memory");
-  return r != 0;
-}
-
 template <int kCount>
 __device__ __forceinline__ void activate_all(float (&z)[kCount], int act) {
   switch (act) {
@@ -712,6 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     const uint32_t lead_empty = cluster_addr(acc_empty, 0);
     int e = 0, acc = 0, flip = 0;
     uint32_t acc_phase = 0;
+    bool alive = true;
     for (int t = first_tile; t < tiles; t += step) {
       const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
       float b[4] = {0.f, 0.f, 0.f, 0.f};
@@ -734,8 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           request_residual<1>(a, res, tid, r.m0, row0, tile_end);
       }
       if (r.len > 0) {
-        const bool ok = stage_wait_warp(acc_full + 8 * acc, acc_phase, a.err);
-        if (!group_all(1 + group, ok)) break;
+        // a warp whose wait ran out goes on without waiting: the group's barriers stay matched, and
+        // the outputs are invalid as recorded
+        alive = alive && stage_wait_warp(acc_full + 8 * acc, acc_phase, a.err);
         tcgen05_fence_after();
       }
       constexpr int kStep = step_cols<kMode>;
