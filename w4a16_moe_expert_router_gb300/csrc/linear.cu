@@ -95,7 +95,7 @@ struct Args {
   uint64_t per_m;  // ceil(2^40 / tiles_m): i / tiles_m = i per_m >> 40 for i < 2^30 (tiles_m <= 1024)
   int tiles_c;  // weight grad: tiles along c
   int depth;    // contraction length (weight grad: the expert's rows)
-  uint32_t word;
+  uint32_t word;  // instruction word without its N
   int one_store;  // the output's map takes a step in one store (see run_mode)
   const float* partial;  // weight grad: the bias gradient's sums over row blocks, and where it goes (or NULL)
   float* dbias;
@@ -123,8 +123,12 @@ struct Config {
   static constexpr uint32_t tmem = 2 * kCols;  // two accumulators
 };
 
+// cols: the columns that are multiplied, as many as the tile has rounded up to what the
+// instructions take (a pair's N in steps of 32; 64 strided columns to a box of each CTA), so
+// that an expert's last tile costs what it holds.  len: contraction length, first: its first
+// row (weight grad).
 struct Tile {
-  int e, m0, c0, row0, row_end, first, len;  // len: contraction length, first: its first row (weight grad)
+  int e, m0, c0, cols, row0, row_end, first, len;
 };
 
 // The CTA's half of the tile of index t.  start[e]: tiles before expert e; off[e]: its first row.
@@ -140,12 +144,14 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const i
     r.c0 = c * kCols;
     r.row0 = e * a.Nw + r.c0;
     r.row_end = (e + 1) * a.Nw;
+    r.cols = min(kCols, (a.Nw - r.c0 + 127) & ~127);
     r.first = off[e];
     r.len = off[e + 1] - off[e];
   } else {
     r.c0 = off[e] + c * kCols;
     r.row0 = r.c0;
     r.row_end = off[e + 1];
+    r.cols = min(kCols, (r.row_end - r.c0 + 31) & ~31);
     r.first = 0;
     r.len = a.depth;
   }
@@ -504,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       bool alive = true;
       for (int t = first_tile; alive && t < tiles; t += step) {
         const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
-        const int bc = r.c0 + rank * C::cols;
+        const int bc = r.c0 + rank * (r.cols >> 1);
 #pragma unroll 1
         for (int j = 0; j < r.len; j += kDepth) {
           if (!stage_wait(empty + 8 * s, phase ^ 1, a.err)) {
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           break;
         }
         tcgen05_fence_after();
-        const uint32_t d = tmem + acc * kCols;
+        const uint32_t d = tmem + acc * kCols, word = a.word | static_cast<uint32_t>(r.cols >> 3) << 17;
 #pragma unroll 1
         for (int j = 0; j < r.len; j += kDepth) {
           if (kMode == kWeightGrad && r.len - j < kDepth) {
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           const auto issue = [&](int k) {  // contraction elements 16 k .. of the stage
             const uint64_t ka = a_strided ? k * (2048 >> 4) : (k >> 2) * (C::a_bytes >> 5) + (k & 3) * (32 >> 4);
             const uint64_t kb = b_strided ? k * (2048 >> 4) : (k >> 2) * (C::b_bytes >> 5) + (k & 3) * (32 >> 4);
-            mma_f16(d, da + ka, db + kb, a.word, static_cast<uint32_t>(j | k));
+            mma_f16(d, da + ka, db + kb, word, static_cast<uint32_t>(j | k));
           };
           if (r.len - j >= kDepth) {
 #pragma unroll
@@ -793,15 +799,18 @@ cudaError_t init_tiles() {
                               Config<kMode, kCols>::smem);
 }
 
-// Columns of a tile.  Rows by experts: the average rows of an expert with room for uneven
-// loads (a tile's unused columns cost its time, tiles of an expert beyond the first its
-// weights once more from L2).  Otherwise the fewest microseconds of: waves of tiles over the
-// pairs of SMs, times 64-element steps of the measured 0.15, 0.2 and 0.32 us for 32, 128 and
-// 256 columns, plus the last tile's epilogue.
+// Columns of a tile.  Rows by experts, from an expert's average rows: 32 columns where they hold
+// it with room for uneven loads (16 rows, gate and up of 128 experts: 111 us, 116 with 128
+// columns), then 128, and 256 where most experts would otherwise take a second tile and their
+// weights come twice (128 rows: input gradient 126 us, 131 with 128 columns; the forward
+// product's epilogue prefers 128 columns there, 135 against 139 us; 256 rows: 93 against 105).
+// Otherwise the fewest microseconds of: waves of tiles over the pairs of SMs, times 64-element
+// steps of the measured 0.15, 0.2 and 0.32 us for 32, 128 and 256 columns, plus the last tile's
+// epilogue.
 int choose_cols(const LinearDims& s, int mode, int tiles_m, int depth, int num_sms) {
   if (s.grouped && mode != kWeightGrad) {
     const int rows = (s.R + s.E - 1) / s.E;
-    return rows <= 22 ? 32 : rows <= 176 ? 128 : 256;
+    return rows <= 22 ? 32 : rows <= (mode == kInputGrad ? 96 : 176) ? 128 : 256;
   }
   const int c = mode == kWeightGrad ? s.Nw() : s.R;
   const int64_t groups = mode == kWeightGrad ? s.E : 1;
@@ -830,7 +839,7 @@ cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, cons
   int cols = choose_cols(s, mode, a.tiles_m, mode == kWeightGrad ? (s.R + s.E - 1) / s.E : a.depth, num_sms);
   const int depth = cols == 256 ? Config<kForward, 256>::depth : Config<kForward, 128>::depth;
   a.tiles_c = (a.Nw + cols - 1) / cols;
-  a.word = mma_word(s.type == 1, mode != kForward, mode == kWeightGrad, 2 * kTileM, cols);
+  a.word = mma_word(s.type == 1, mode != kForward, mode == kWeightGrad, 2 * kTileM);
   CUtensorMap maps[4] = {};  // A, B, output, saved z
   bool ok;
   const bool bf16 = s.type == 1;

@@ -91,10 +91,10 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t box_byt
 }
 
 // Instruction word of kind::f16: fp32 accumulators, both operands fp16 or both bf16,
-// *_strided where the operand's contraction index is the strided one.
-inline uint32_t mma_word(bool bf16, bool a_strided, bool b_strided, int m, int n) {
+// *_strided where the operand's contraction index is the strided one; N / 8 goes to bit 17.
+inline uint32_t mma_word(bool bf16, bool a_strided, bool b_strided, int m) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_strided ? 1u << 15 : 0u) | (b_strided ? 1u << 16 : 0u) |
-         (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+         (uint32_t(m >> 4) << 24);
 }
 
 // D (+)= A B over 16 contraction elements, by one thread of the pair's first CTA: each CTA holds
