@@ -15,7 +15,7 @@
 // weights' way from memory, and a column past an expert's last row is computed from
 // its neighbour's data and not stored.
 //
-// Persistent pairs of CTAs (two SMs on one tile of 256 outputs x kCols rows, each
+// Persistent pairs of CTAs (two SMs on one tile of 256 outputs x up to kCols rows, each
 // holding its 128 outputs of A and half of B) walk a list of tiles: a thread of each
 // loads stages of A and B by TMA, one thread of the pair issues the matrix
 // instructions into one of two accumulators in tensor memory, and eight warps of each
@@ -93,7 +93,9 @@ struct Args {
   int tile_m;   // outputs per CTA and tile (64 of a gate and their ups, or 128)
   int tiles_m;  // tiles along m
   uint64_t per_m;  // ceil(2^40 / tiles_m): i / tiles_m = i per_m >> 40 for i < 2^30 (tiles_m <= 1024)
+  int tile_c;   // columns of a tile, kCols at most
   int tiles_c;  // weight grad: tiles along c
+  int stage_bytes;  // what a CTA loads for a stage
   int depth;    // contraction length (weight grad: the expert's rows)
   uint32_t word;  // instruction word without its N
   int one_store;  // the output's map takes a step in one store (see run_mode)
@@ -132,7 +134,7 @@ struct Tile {
 };
 
 // The CTA's half of the tile of index t.  start[e]: tiles before expert e; off[e]: its first row.
-template <int kMode, int kCols>
+template <int kMode>
 __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const int* off, int t, int& e, int rank) {
   while (t >= start[e + 1]) ++e;  // t only grows
   const int i = t - start[e];
@@ -141,17 +143,17 @@ __device__ __forceinline__ Tile tile_at(const Args& a, const int* start, const i
   r.e = e;
   r.m0 = (m * 2 + rank) * a.tile_m;
   if (kMode == kWeightGrad) {
-    r.c0 = c * kCols;
+    r.c0 = c * a.tile_c;
     r.row0 = e * a.Nw + r.c0;
     r.row_end = (e + 1) * a.Nw;
-    r.cols = min(kCols, (a.Nw - r.c0 + 127) & ~127);
+    r.cols = min(a.tile_c, (a.Nw - r.c0 + 127) & ~127);
     r.first = off[e];
     r.len = off[e + 1] - off[e];
   } else {
-    r.c0 = off[e] + c * kCols;
+    r.c0 = off[e] + c * a.tile_c;
     r.row0 = r.c0;
     r.row_end = off[e + 1];
-    r.cols = min(kCols, (r.row_end - r.c0 + 31) & ~31);
+    r.cols = min(a.tile_c, (r.row_end - r.c0 + 31) & ~31);
     r.first = 0;
     r.len = a.depth;
   }
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   if (!a.offsets) {
     if (threadIdx.x == 0) {
       start[0] = off[0] = 0;
-      start[1] = a.tiles_m * (kMode == kWeightGrad ? a.tiles_c : (a.R + kCols - 1) / kCols);
+      start[1] = a.tiles_m * (kMode == kWeightGrad ? a.tiles_c : (a.R + a.tile_c - 1) / a.tile_c);
       off[1] = a.R;
     }
   } else if (warp == 2) {
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     for (int i = 0; i < 8; ++i) {
       const int e = lane * 8 + i;
       const int rows = max(o[i + 1] - o[i], 0);
-      n[i] = e < a.E ? a.tiles_m * (kMode == kWeightGrad ? a.tiles_c : (rows + kCols - 1) / kCols) : 0;
+      n[i] = e < a.E ? a.tiles_m * (kMode == kWeightGrad ? a.tiles_c : (rows + a.tile_c - 1) / a.tile_c) : 0;
       sum += n[i];
     }
     int incl = sum;
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       uint32_t phase = 0, uses = 0, tails = 0, tail_uses = 0;  // one bit per stage, see below
       bool alive = true;
       for (int t = first_tile; alive && t < tiles; t += step) {
-        const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
+        const Tile r = tile_at<kMode>(a, start, off, t, e, rank);
         const int bc = r.c0 + rank * (r.cols >> 1);
 #pragma unroll 1
         for (int j = 0; j < r.len; j += kDepth) {
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             tail_uses ^= 1u << s;
             tails |= 1u << s;
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * C::stage);
+            if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * a.stage_bytes);
             uses ^= 1u << s;
             tails &= ~(1u << s);
           }
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       uint32_t phases = 0, acc_phase = 0, tail_phases = 0;  // per stage: parity of its next use
       bool alive = true;
       for (int t = first_tile; alive && t < tiles; t += step) {
-        const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
+        const Tile r = tile_at<kMode>(a, start, off, t, e, rank);
         if (r.len <= 0) continue;  // no rows: the epilogue writes zeros
         if (!stage_wait(acc_empty + 8 * acc, acc_phase ^ 1, a.err)) {
           alive = false;
@@ -634,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       int e = 0, it = 0;
       uint32_t phases = 0;
       for (int t = first_tile; t < tiles; t += step) {
-        const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
+        const Tile r = tile_at<kMode>(a, start, off, t, e, rank);
         if (r.len <= 0) continue;
         it += (r.len + kDepth - 1) / kDepth;
         const int rest = r.len % kDepth;
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     if (a.dbias && rank == 0) {
       int e = 0, counted = 0, before = 0;  // row blocks of the experts before `counted`
       for (int t = first_tile; t < tiles; t += step) {
-        const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
+        const Tile r = tile_at<kMode>(a, start, off, t, e, rank);
         if (r.m0 / (2 * kTileM) != (r.c0 / kCols + r.e) % a.tiles_m) continue;
         const auto blocks = [&](int i) { return (max(off[i + 1] - off[i], 0) + a.block_rows - 1) / a.block_rows; };
         for (; counted < r.e; ++counted) before += blocks(counted);
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     uint32_t acc_phase = 0;
     bool alive = true;
     for (int t = first_tile; t < tiles; t += step) {
-      const Tile r = tile_at<kMode, kCols>(a, start, off, t, e, rank);
+      const Tile r = tile_at<kMode>(a, start, off, t, e, rank);
       float b[4] = {0.f, 0.f, 0.f, 0.f};
       if (kMode == kForward && a.bias) {
         const float* const bp = a.bias + static_cast<size_t>(r.e) * a.Nw;
@@ -720,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         }
       }
       uint4 res[4];
-      const int tile_end = min(r.row_end, r.row0 + kCols);  // the next tile's rows may be written meanwhile
+      const int tile_end = min(r.row_end, r.row0 + a.tile_c);  // the next tile's rows may be written meanwhile
       if (kMode == kForward && a.residual) {
         const int row0 = r.row0 + group * step_cols<kMode>;
         if (a.gated)
@@ -799,28 +801,34 @@ cudaError_t init_tiles() {
                               Config<kMode, kCols>::smem);
 }
 
-// Columns of a tile.  Rows by experts, from an expert's average rows: 32 columns where they hold
-// it with room for uneven loads (16 rows, gate and up of 128 experts: 111 us, 116 with 128
-// columns), then 128, and 256 where most experts would otherwise take a second tile and their
-// weights come twice (128 rows: input gradient 126 us, 131 with 128 columns; the forward
-// product's epilogue prefers 128 columns there, 135 against 139 us; 256 rows: 93 against 105).
-// Otherwise the fewest microseconds of: waves of tiles over the pairs of SMs, times 64-element
-// steps of the measured 0.15, 0.2 and 0.32 us for 32, 128 and 256 columns, plus the last tile's
-// epilogue.
+// Columns of a tile, in steps of 32 (of 128 for the weight gradient).  Rows by experts, from an
+// expert's average rows: 32 columns where they hold it with room for uneven loads (16 rows, gate
+// and up of 128 experts: 111 us, 116 with 128 columns), then 128, and 256 where most experts would
+// otherwise take a second tile and their weights come twice (128 rows: input gradient 126 us, 131
+// with 128 columns; the forward product's epilogue prefers 128 columns there, 135 against 139 us;
+// 256 rows: 93 against 105).  Otherwise the least time of: waves of tiles over the pairs of SMs,
+// times 64-element steps (measured: 0.15 us with 32 columns, 0.2 with 128, 0.32 with 256, 0.24 at
+// least in the kernel of 256), plus the last tile's epilogue.
 int choose_cols(const LinearDims& s, int mode, int tiles_m, int depth, int num_sms) {
   if (s.grouped && mode != kWeightGrad) {
     const int rows = (s.R + s.E - 1) / s.E;
     return rows <= 22 ? 32 : rows <= (mode == kInputGrad ? 96 : 176) ? 128 : 256;
   }
-  const int c = mode == kWeightGrad ? s.Nw() : s.R;
-  const int64_t groups = mode == kWeightGrad ? s.E : 1;
-  const auto cost = [&](int cols, int per_step, int last) {
-    const int64_t tiles = groups * tiles_m * ((c + cols - 1) / cols), pairs = num_sms / 2;
-    return (tiles + pairs - 1) / pairs * ((depth + 63) / 64) * per_step + last;
-  };
-  const int64_t c32 = mode == kWeightGrad ? INT64_MAX : cost(32, 15, 50), c128 = cost(128, 20, 100),
-                c256 = cost(256, 32, 200);
-  return c32 < c128 && c32 < c256 ? 32 : c128 < c256 ? 128 : 256;
+  const int64_t c = mode == kWeightGrad ? s.Nw() : s.R, groups = mode == kWeightGrad ? s.E : 1;
+  const int64_t pairs = num_sms / 2, steps = (depth + 63) / 64;
+  const int by = mode == kWeightGrad ? 128 : 32;
+  int best = 256;
+  int64_t least = INT64_MAX;
+  for (int cols = 256; cols >= by; cols -= by) {
+    const int64_t tiles = groups * tiles_m * ((c + cols - 1) / cols);
+    const int64_t step = cols > 192 ? cols : cols > 128 ? 192 : 108 + cols * 52 / 128;  // in 1.25 ns
+    const int64_t cost = (tiles + pairs - 1) / pairs * steps * step + 6 * cols;
+    if (cost < least) {
+      least = cost;
+      best = cols;
+    }
+  }
+  return best;
 }
 
 cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, const void* x, const void* w, const void* dz,
@@ -836,9 +844,11 @@ cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, cons
   a.tiles_m = (a.width + 2 * a.tile_m - 1) / (2 * a.tile_m);
   a.per_m = ((uint64_t(1) << 40) + a.tiles_m - 1) / a.tiles_m;
   a.depth = mode == kForward ? s.K : a.Nw;
-  int cols = choose_cols(s, mode, a.tiles_m, mode == kWeightGrad ? (s.R + s.E - 1) / s.E : a.depth, num_sms);
+  a.tile_c = choose_cols(s, mode, a.tiles_m, mode == kWeightGrad ? (s.R + s.E - 1) / s.E : a.depth, num_sms);
+  const int cols = a.tile_c <= 32 ? 32 : a.tile_c <= 128 ? 128 : 256;  // the kernel's
   const int depth = cols == 256 ? Config<kForward, 256>::depth : Config<kForward, 128>::depth;
-  a.tiles_c = (a.Nw + cols - 1) / cols;
+  a.tiles_c = (a.Nw + a.tile_c - 1) / a.tile_c;
+  a.stage_bytes = (kTileM + a.tile_c / 2) * depth * 2;
   a.word = mma_word(s.type == 1, mode != kForward, mode == kWeightGrad, 2 * kTileM);
   CUtensorMap maps[4] = {};  // A, B, output, saved z
   bool ok;
@@ -849,11 +859,11 @@ cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, cons
     const int64_t da[5] = {K, 8, s.gated ? 2 : 1, s.N / 8, E}, sa[4] = {K, s.N * K, 8 * K, Nw * K};
     const int ba[5] = {64, 8, s.gated ? 2 : 1, a.tile_m / 8, 1};
     const int64_t db[2] = {K, R}, sb[1] = {K};
-    const int bb[2] = {64, cols / 2};
+    const int bb[2] = {64, a.tile_c / 2};
     ok = make_map(&maps[0], bf16, w, 5, da, sa, ba, true) && make_map(&maps[1], bf16, x, 2, db, sb, bb, true);
   } else if (mode == kInputGrad) {
     const int64_t da[3] = {K, Nw, E}, sa[2] = {K, Nw * K}, db[2] = {Nw, R}, sb[1] = {Nw};
-    const int ba[3] = {64, depth, 1}, bb[2] = {64, cols / 2};
+    const int ba[3] = {64, depth, 1}, bb[2] = {64, a.tile_c / 2};
     ok = make_map(&maps[0], bf16, w, 3, da, sa, ba, true) && make_map(&maps[1], bf16, dz, 2, db, sb, bb, true);
   } else {
     const int64_t da[2] = {K, R}, sa[1] = {K}, db[2] = {Nw, R}, sb[1] = {Nw};
@@ -881,7 +891,7 @@ cudaError_t run_mode(const LinearDims& s, int mode, const int32_t* offsets, cons
   }
   if (!ok) return cudaErrorInvalidValue;
   const int64_t most = mode == kWeightGrad ? E * a.tiles_m * a.tiles_c
-                                           : int64_t(a.tiles_m) * ((R + cols - 1) / cols + (offsets ? E : 0));
+                                           : int64_t(a.tiles_m) * ((R + a.tile_c - 1) / a.tile_c + (offsets ? E : 0));
   if (mode == kForward) {
     if (cols == 32) return launch_tiles<kForward, 32>(a, maps, most, num_sms, st);
     if (cols == 128) return launch_tiles<kForward, 128>(a, maps, most, num_sms, st);
