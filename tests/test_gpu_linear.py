@@ -167,6 +167,24 @@ FORWARD = [
 ]
 
 
+# few tiles with a long contraction, which two, three and four pairs of CTAs share: the same columns
+SHARED = [
+    (40, 4096, 264, 0, 0, 0, 0, True, True, 0), (33, 2056, 1032, 0, 2, 1, 1, True, True, 0), (100, 4000, 520, 0, 1, 0, 1, False, True, 0),
+    (300, 8200, 136, 0, 3, 0, 0, True, False, 0), (128, 2048, 72, 0, 0, 1, 0, True, True, 0), (64, 4096, 4096, 0, 2, 0, 1, True, True, 0),
+    (100, 2056, 6000, 0, 3, 0, 0, False, True, 0), (1000, 4104, 600, 0, 0, 1, 0, True, False, 0),
+]
+# the gradients' long contractions: outputs (input gradient) and rows (weight gradient)
+SHARED_BACKWARD = [
+    (40, 264, 4096, 0, 0, 0, 0, 0), (129, 1000, 2056, 0, 2, 1, 1, 0), (5001, 264, 136, 0, 3, 0, 1, 0), (4097, 72, 8, 0, 0, 1, 0, 0),
+    (3000, 2048, 256, 0, 1, 0, 0, 0), (2500, 2056, 520, 0, 3, 0, 1, 0), (1152, 136, 1032, 0, 2, 0, 0, 0),
+]
+
+
+@pytest.mark.parametrize("R,K,N,E,act,gated,typ,bias,res,spare", SHARED, ids=["-".join(map(str, c)) for c in SHARED])
+def test_forward_of_shared_tiles(B, R, K, N, E, act, gated, typ, bias, res, spare):
+    _check_forward(B, Case(R, K, N, E, act, gated, typ, bias, res, R + K, spare))
+
+
 @pytest.mark.parametrize("R,K,N,E,act,gated,typ,bias,res,spare", FORWARD, ids=["-".join(map(str, c)) for c in FORWARD])
 def test_forward(B, R, K, N, E, act, gated, typ, bias, res, spare):
     _check_forward(B, Case(R, K, N, E, act, gated, typ, bias, res, R + K, spare))
@@ -260,6 +278,11 @@ def test_backward(B, R, K, N, E, act, gated, typ, spare):
     for n in range(3):  # each output alone gives the same bits
         alone = _run_backward(B, c, g, tuple(i == n for i in range(3)))
         assert torch.equal(alone[n], (dx, dw, db)[n])
+
+
+@pytest.mark.parametrize("R,K,N,E,act,gated,typ,spare", SHARED_BACKWARD, ids=["-".join(map(str, c)) for c in SHARED_BACKWARD])
+def test_backward_of_shared_tiles(B, R, K, N, E, act, gated, typ, spare):
+    test_backward(B, R, K, N, E, act, gated, typ, spare)
 
 
 def test_gradient_against_differences(B):

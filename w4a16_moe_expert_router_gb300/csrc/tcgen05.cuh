@@ -36,6 +36,17 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// The registers of a thread, changed by all warps of a warpgroup.  What some take must be no more
+// than the others of the block release.
+template <int kCount>
+__device__ __forceinline__ void registers_release() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+template <int kCount>
+__device__ __forceinline__ void registers_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+
 // ------------------------------------------------------------ tensor memory
 
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {  // a whole warp of each CTA
@@ -64,12 +75,12 @@ __device__ __forceinline__ void tcgen05_fence_after() { asm volatile("tcgen05.fe
 // Four 8 x 8 blocks of 16-bit values, transposed on the way: element (g, q) of a thread's pair
 // (g = lane / 4, q = 2 (lane % 4)) lies at place g of memory row q.  Lane 8 b + j gives the
 // address of row j of block b.
-__device__ __forceinline__ void store_blocks_transposed(uint32_t addr, const uint32_t (&r)[4]) {
+__device__ __forceinline__ void store_blocks_transposed(uint32_t addr, const uint32_t* r) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3])
                : "memory");
 }
-__device__ __forceinline__ void load_blocks_transposed(uint32_t addr, uint32_t (&r)[4]) {
+__device__ __forceinline__ void load_blocks_transposed(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
@@ -107,11 +118,12 @@ __device__ __forceinline__ void mma_f16(uint32_t tmem_d, uint64_t a, uint64_t b,
       : "memory");
 }
 
-// Arrives on the barrier in both CTAs when the thread's matrix instructions so far are done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+// Arrives on the barrier in the cluster's CTAs of the mask when the thread's matrix instructions so
+// far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t ctas) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(ctas))
       : "memory");
 }
 
@@ -185,11 +197,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without an order of memory accesses.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // The address in the cluster's shared window of `addr` in CTA `rank`.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+// 16 bytes to another CTA's shared memory, counted on a barrier there (both cluster addresses).
+__device__ __forceinline__ void store_async_16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+               : "memory");
 }
 // Arrives on a barrier of either CTA (a cluster address).  Ordered after the thread's shared-memory
 // accesses and fences, not after its global stores: a release for the whole cluster waits for
