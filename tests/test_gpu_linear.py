@@ -172,6 +172,11 @@ SHARED = [
     (40, 4096, 264, 0, 0, 0, 0, True, True, 0), (33, 2056, 1032, 0, 2, 1, 1, True, True, 0), (100, 4000, 520, 0, 1, 0, 1, False, True, 0),
     (300, 8200, 136, 0, 3, 0, 0, True, False, 0), (128, 2048, 72, 0, 0, 1, 0, True, True, 0), (64, 4096, 4096, 0, 2, 0, 1, True, True, 0),
     (100, 2056, 6000, 0, 3, 0, 0, False, True, 0), (1000, 4104, 600, 0, 0, 1, 0, True, False, 0),
+    # single tokens and small batches: long rows shared by up to eight CTAs, and CTAs with several items
+    (1, 4096, 128, 0, 0, 0, 0, True, True, 0), (16, 8200, 72, 0, 2, 1, 1, True, True, 0), (9, 1032, 2048, 0, 3, 0, 0, False, True, 0),
+    (7, 65536, 24, 0, 1, 0, 1, True, False, 0), (5, 3080, 264, 3, 0, 1, 0, True, True, 2), (1, 72, 6000, 0, 3, 0, 1, True, True, 0),
+    (16, 1032, 2056, 5, 2, 1, 0, True, True, 1), (16, 264, 4104, 40, 0, 0, 1, False, True, 0),
+    (16, 4096, 4096, 0, 1, 0, 0, True, True, 0), (3, 2048, 22000, 0, 3, 0, 0, True, False, 0),
 ]
 # the gradients' long contractions: outputs (input gradient) and rows (weight gradient)
 SHARED_BACKWARD = [

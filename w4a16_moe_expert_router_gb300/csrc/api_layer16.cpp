@@ -164,8 +164,9 @@ moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_cfg* cfg, const void* x
   if ((st = moe::current_device(&sms)) != MOE_W4A16_OK) return st;
   const auto cs = static_cast<cudaStream_t>(stream);
   int32_t* const err = &static_cast<moe::WsHeader*>(workspace)->error;
-  if (s.R <= moe::kSmallRows)
-    return cuda_status(moe::launch_linear_small(s, expert_offsets, x, weight, bias, residual, out, preact, err, cs));
+  if (moe::is_small_linear(s))
+    return cuda_status(
+        moe::launch_linear_small(s, expert_offsets, x, weight, bias, residual, out, preact, err, sms, cs));
   return cuda_status(moe::launch_linear(s, expert_offsets, x, weight, bias, residual, out, preact, err, sms, cs));
 }
 

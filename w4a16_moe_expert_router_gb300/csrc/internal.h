@@ -191,7 +191,7 @@ cudaError_t launch_combine_rows_backward(const RowDims& s, const int32_t* topk_i
                                          float* dtopk_w, float* dlogits, cudaStream_t st);
 
 // Products of rows with weights and their gradients (linear.cu, linear_small.cu, linear_grad.cu).
-constexpr int kSmallRows = 16;  // forward calls up to this many rows take linear_small.cu's kernel
+constexpr int kSmallRows = 16;  // rows at most in linear_small.cu's kernel
 struct LinearDims {
   int R, K, N, E, act, gated, type;  // type: 0 fp16, 1 bf16
   bool grouped;                      // rows sorted by expert (offsets given)
@@ -205,9 +205,10 @@ bool make_map(CUtensorMap* map, bool bf16, const void* base, int rank, const int
 cudaError_t init_linear_kernels();
 cudaError_t launch_linear(const LinearDims& s, const int32_t* offsets, const void* x, const void* w, const float* bias,
                           const void* residual, void* out, void* preact, int32_t* err, int num_sms, cudaStream_t st);
+bool is_small_linear(const LinearDims& s);  // a forward call of linear_small.cu's
 cudaError_t launch_linear_small(const LinearDims& s, const int32_t* offsets, const void* x, const void* w,
                                 const float* bias, const void* residual, void* out, void* preact, int32_t* err,
-                                cudaStream_t st);
+                                int num_sms, cudaStream_t st);
 cudaError_t init_linear_small_kernels();
 cudaError_t launch_linear_input_grad(const LinearDims& s, const int32_t* offsets, const void* w, const void* dz, void* dx,
                                      int32_t* err, int num_sms, cudaStream_t st);

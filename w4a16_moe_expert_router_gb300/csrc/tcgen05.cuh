@@ -213,6 +213,11 @@ __device__ __forceinline__ void store_async_16(uint32_t addr, uint32_t x, uint32
                "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
                : "memory");
 }
+__device__ __forceinline__ void store_async_4(uint32_t addr, float x, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+               "r"(__float_as_uint(x)), "r"(bar)
+               : "memory");
+}
 // Arrives on a barrier of either CTA (a cluster address).  Ordered after the thread's shared-memory
 // accesses and fences, not after its global stores: a release for the whole cluster waits for
 // those too, 1,500 to 3,000 cycles when measured here.
