@@ -992,14 +992,15 @@ cudaError_t init_tiles() {
 // and up of 128 experts: 111 us, 116 with 128 columns), then 128, and 256 where most experts would
 // otherwise take a second tile and their weights come twice (128 rows: input gradient 126 us, 131
 // with 128 columns; the forward product's epilogue prefers 128 columns there, 135 against 139 us;
-// 256 rows: 93 against 105).  Otherwise the least time, in ns, of waves of tiles over the pairs of
-// SMs, times 64-element steps (a step takes an SM's 0.13 us for what it loads, or what all pairs
-// load at the 18.5 TB/s of L2; with 256 columns the matrix instructions' 0.32, 0.24 at least in
-// that kernel), plus the last tile's epilogue.  Where few tiles leave most SMs without one and
-// their contraction is long, two to four pairs share each (as many as run at a time) for the time
-// of the exchange, 0.15 us per further pair and 0.045 per pair in all: 128 x 4096 x 1024 12.4 ->
-// 8.2 us, 300 x 8192 x 1024 21.8 -> 12.1, 64 x 2048 x 4096 8.1 -> 7.2, the weight gradient of
-// 16384 x 2048 x 128 60 -> 19.5; 512 x 1024 x 2048 takes 6.4 without, 7.6 with.
+// 256 rows: 93 against 105).  Otherwise the least time, in ns, of: waves of tiles over the pairs of
+// SMs, times 64-element steps (0.13 us for what an SM loads, or what all pairs load at the 18.5 TB/s
+// of L2; above 128 columns 0.25 to 0.32, where the matrix instructions bound a step), plus the last
+// tile's epilogue (8192 x 2048 x 8192: 256 columns 181 us, 224 189; 4096 x 2048 x 2048: 23.5 each,
+// 128 columns 28).  Where few tiles leave most SMs without one and their contraction is long, two
+// to four pairs share each (as many as run at a time) for the time of the exchange, 0.15 us per
+// further pair and 0.045 per pair in all: 128 x 4096 x 1024 12.4 -> 8.2 us, 300 x 8192 x 1024 21.8 ->
+// 12.1, 64 x 2048 x 4096 8.1 -> 7.2, the weight gradient of 16384 x 2048 x 128 60 -> 19.5; 512 x 1024 x
+// 2048 takes 6.4 without, 7.6 with.
 int choose_tiles(const LinearDims& s, int mode, int tiles_m, int depth, int num_sms, int* split) {
   *split = 1;
   if (s.grouped && mode != kWeightGrad) {
@@ -1014,7 +1015,7 @@ int choose_tiles(const LinearDims& s, int mode, int tiles_m, int depth, int num_
   for (int cols = 256; cols >= by; cols -= by) {
     const int64_t tiles = groups * tiles_m * ((c + cols - 1) / cols);
     const auto step = [&](int64_t busy) {
-      if (cols > 128) return static_cast<int64_t>(cols > 192 ? cols * 5 / 4 : 240);
+      if (cols > 128) return static_cast<int64_t>(128 + cols * 3 / 4);
       return std::max<int64_t>({122, 45 + cols * 2 / 3, std::min(busy, pairs) * (256 + cols) / 145});
     };
     const int64_t cost = (tiles + pairs - 1) / pairs * steps * step(tiles) + std::max(600, cols * 15 / 2);
