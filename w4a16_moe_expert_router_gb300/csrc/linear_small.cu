@@ -15,7 +15,7 @@
 // sums meet in shared memory in order.  With experts an item's rows are one expert's.
 //
 // Two CTAs per SM walk the items, the next item's chunks on their way while one ends (1 row,
-// 4096 x 8192: 15.3 -> 13.5 us; 16 rows of 128 experts, 2048 x 704 gated: 21.9 -> 18.1, each
+// 4096 x 8192: 15.3 -> 13.5 us; 16 rows of 128 experts, 2048 x 704 gated: 21.9 -> 19.4, each
 // an item of its own before).  Fewer items with long rows are shared by the CTAs of a cluster,
 // a part of the columns each, whose sums go to the first one and are added in order (1 row,
 // 4096 x 128: 3.9 -> 2.5 us; 8192 x 2048: 10.3 -> 8.7).
@@ -48,7 +48,7 @@ struct Tail {
   float parts[kMaxSplit - 1][values];             // the other CTAs' of a cluster
   float total[values];
   uint64_t full[kStages], got;
-  int expert[kSmallRows], first[kSmallRows], end[kSmallRows], count;  // experts with rows
+  int expert[kSmallRows], first[kSmallRows], end[kSmallRows], counts[kWarps];  // experts with rows
 };
 template <int kTiles>
 constexpr int kSmem = kStages * kChunkBytes + static_cast<int>(sizeof(Tail<kTiles>));  // two CTAs per SM
@@ -86,7 +86,6 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(full + 8 * s, 1);
     mbar_init(got, 1);
-    sm.count = 0;
     if (split > 1) mbar_arrive_expect_tx(got, (split - 1) * sizeof(sm.total));
     fence_barrier_init();
   }
@@ -102,21 +101,28 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
   __syncthreads();
   if (split > 1) cluster_sync();  // the first CTA's barrier is initialised
   grid_dependency_wait();
+  int experts = 0;
   if (offsets) {
-    if (tid < E) {
-      const int lo = offsets[tid], hi = min(offsets[tid + 1], R);
-      if (lo >= 0 && lo < hi) {
-        const int k = atomicAdd(&sm.count, 1);  // (in any order: an item's result is its own)
-        if (k < kSmallRows) {
-          sm.expert[k] = tid;
-          sm.first[k] = lo;
-          sm.end[k] = hi;
-        }
-      }
+    // the same list in every CTA, in the order of the experts
+    const int lo = tid < E ? offsets[tid] : 0, hi = tid < E ? min(offsets[tid + 1], R) : 0;
+    const bool some = lo >= 0 && lo < hi;
+    const unsigned those = __ballot_sync(0xffffffffu, some);
+    if (lane == 0) sm.counts[warp] = __popc(those);
+    __syncthreads();
+    int k = __popc(those & ((1u << lane) - 1u));
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) k += sm.counts[w];
+      experts += sm.counts[w];
     }
+    if (some && k < kSmallRows) {
+      sm.expert[k] = tid;
+      sm.first[k] = lo;
+      sm.end[k] = hi;
+    }
+    experts = min(experts, kSmallRows);
     __syncthreads();
   }
-  const int items = offsets ? min(sm.count, kSmallRows) * blocks : blocks;
+  const int items = offsets ? experts * blocks : blocks;
   // the next chunk to fetch, by one thread; zeros past the last column and row
   int fetch_item = item, fetch_chunk = 0, fetched = 0;
   const auto fetch = [&] {
