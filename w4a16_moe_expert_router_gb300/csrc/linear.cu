@@ -23,10 +23,10 @@
 // empty the other one: 32 columns at a time through shared memory, so that the outputs
 // leave by TMA.  Accumulation, bias, activation and residual are in fp32, rounded once.
 //
-// Measured: 8192 x 2048 x 8192 bf16 in 145 us (1.89 PFLOP/s, cuBLAS 138) in short bursts, below
-// that under the power cap; gate and up products of 128 experts on 2048 rows in 111 us (6.7 TB/s);
-// the gradient's products of 128 experts on 16384 rows, 2048 x 1408, in 131 us (input, 6.5 TB/s)
-// and 148 us (weights, 5.7 TB/s).
+// Measured: 8192 x 2048 x 8192 bf16 in 146 us (1.88 PFLOP/s, cuBLAS 142) in short bursts, 164 (158)
+// under the power cap; gate and up products of 128 experts on 2048 rows in 111 us (6.7 TB/s); the
+// gradient's products of 128 experts on 16384 rows, 2048 x 1408, in 127 us (input, 6.7 TB/s) and
+// 148 us (weights: 738 MB of them leave at 5 TB/s, a fill's rate is 4).
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
