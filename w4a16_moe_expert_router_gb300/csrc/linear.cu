@@ -403,26 +403,21 @@ __device__ __forceinline__ void load_bias(const Args& a, float (&b)[4], const Ti
   }
 }
 
-// A forward step of 32 columns (any: not of zeros).  kForm: 1 plain, 2 gated.  b: the biases of the thread's lanes
+// A forward step of 32 columns.  kForm: 1 plain, 2 gated.  b: the biases of the thread's lanes
 // g, g + 8, g + 16, g + 24 of its quarter.  res: the step's residual, then the one's at `next`.
 template <int kForm>
 __device__ __forceinline__ void forward_step(const Args& a, const CUtensorMap* map_out, const CUtensorMap* map_z,
-                                             uint32_t tmem, bool any, const Partials& others, const float (&b)[4],
+                                             uint32_t tmem, const Partials& others, const float (&b)[4],
                                              uint4 (&res)[4], int next, uint8_t* buf, int& flip, int group, int tid,
                                              const StepRows& rows) {
   constexpr int chunks = kForm == 2 ? 8 : 16;  // 16-byte chunks of outputs per column
   const int lane = tid & 31, quarter = tid >> 5;
   const int sub = lane >> 3, j = lane & 7;
   uint32_t v[2][16];
-  if (any) {
-    tmem_load_16x32(tmem, v[0]);
-    tmem_load_16x32(tmem + (16u << 16), v[1]);
-    tmem_load_wait();
-    add_partials(v, others, tid);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0u;
-  }
+  tmem_load_16x32(tmem, v[0]);
+  tmem_load_16x32(tmem + (16u << 16), v[1]);
+  tmem_load_wait();
+  add_partials(v, others, tid);
   float z[2][16];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -453,7 +448,7 @@ __device__ __forceinline__ void forward_step(const Args& a, const CUtensorMap* m
     request_residual<kForm>(a, res, tid, rows.m0, next, rows.row_end);
   }
   // 16 values at a time, so that activation and type are asked for once or twice (for every 4 it
-  // costs a step 400 cycles); r[4 i ..] are the blocks that one instruction stores, of block column
+  // costs a step 200 cycles of 1,600); r[4 i ..] are the blocks that one instruction stores, of block column
   // 2 p + i (gated: 2 i and 2 i + 1)
 #pragma unroll
   for (int p = 0; p < (kForm == 2 ? 1 : 2); ++p) {
@@ -505,9 +500,9 @@ __device__ __forceinline__ void step_of(const Args& a, const CUtensorMap* map_ou
   if constexpr (kMode != kForward)
     gradient_step<kStep>(a, map_out, tmem, any, others, buf, flip, group, tid, rows);
   else if (a.gated)
-    forward_step<2>(a, map_out, map_z, tmem, any, others, b, res, next, buf, flip, group, tid, rows);
+    forward_step<2>(a, map_out, map_z, tmem, others, b, res, next, buf, flip, group, tid, rows);
   else
-    forward_step<1>(a, map_out, map_z, tmem, any, others, b, res, next, buf, flip, group, tid, rows);
+    forward_step<1>(a, map_out, map_z, tmem, others, b, res, next, buf, flip, group, tid, rows);
 }
 
 // kSplit: a cluster of a.split pairs on one tile, each with a share of the contraction.
@@ -983,6 +978,12 @@ cudaError_t launch_tiles(const Args& a, const CUtensorMap (&maps)[4], int64_t mo
 
 template <int kMode, int kCols, bool kSplit = false>
 cudaError_t init_tiles() {
+  if (kMode == kForward) {  // the epilogue would wait for registers that nobody has
+    cudaFuncAttributes f;
+    const cudaError_t err = cudaFuncGetAttributes(&f, linear_kernel<kMode, kCols, kSplit>);
+    if (err != cudaSuccess) return err;
+    if (f.numRegs * 3 < kFewRegisters + 2 * kManyRegisters) return cudaErrorInvalidConfiguration;
+  }
   return cudaFuncSetAttribute(linear_kernel<kMode, kCols, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Config<kMode, kCols, kSplit>::smem);
 }
