@@ -408,6 +408,47 @@ def test_streams_and_a_captured_graph(B):
     assert all(torch.equal(x, y) for x, y in zip(bufs[0][:5], bufs[1][:5]))  # not the workspaces
 
 
+@pytest.mark.parametrize("R,K,N,E", [(40, 4096, 264, 0), (300, 2056, 1032, 0), (1, 4096, 128, 0), (16, 264, 4104, 40)])
+def test_clusters_in_a_graph_beside_another_stream(B, R, K, N, E):
+    """CTAs that share a tile or an item, in replayed graphs while another stream runs the same:
+    the same bits every time."""
+    c = Case(R, K, N, E, 0, 1, 1, True, True, R + 3)
+    g = Grad(c, 4)
+    want = _run_forward(B, c) + _run_backward(B, c, g)
+    cfg = B.make_linear(R, K, N, max(E, 1), 0, 1, 1)
+    streams, sets = [torch.cuda.Stream(), torch.cuda.Stream()], []
+
+    def call(b):
+        B.moe_w4a16_linear(cfg, c.x, c.offd, c.w, c.b, c.res, b[0], b[1], b[5])
+        B.moe_w4a16_linear_backward(cfg, c.x, c.offd, c.w, g.z, g.dout, b[2], b[3], b[4], b[6])
+
+    for _ in streams:
+        b = [t.clone() for t in want] + [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (
+            B.moe_w4a16_linear_workspace_bytes(cfg), B.moe_w4a16_linear_backward_workspace_bytes(cfg))]
+        B.moe_w4a16_workspace_init(b[5])
+        B.moe_w4a16_workspace_init(b[6])
+        sets.append(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(sets[0])
+        call(sets[0])
+    for _ in range(3):
+        for b in sets:
+            for t in b[:5]:
+                t.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        with torch.cuda.stream(streams[1]):
+            call(sets[1])
+            call(sets[1])
+        torch.cuda.synchronize()
+        for b in sets:
+            assert all(torch.equal(t, w) for t, w in zip(b, want))
+            assert B.moe_w4a16_read_error(b[5]) == B.OK and B.moe_w4a16_read_error(b[6]) == B.OK
+
+
 def test_in_place_residual_and_infinities(B):
     """out may be the residual; an infinite row reaches its own outputs only, and an expert's
     weight gradient only from its own rows."""
