@@ -376,8 +376,11 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_combine_rows(const moe_w4a16_rows* cfg,
  *   grad_topk_w  fp32 [T][k]    <grad_out[t], rows[pair_pos[p]]>, 0 for a dropped pair
  *   grad_logits  fp32 [T][E]    the gradient of the router logits when topk_w is the softmax
  *                               over the selected k (moe_w4a16_route): w_r (dw_r - sum_j w_j dw_j)
- *                               at expert topk_idx[t][r] of a kept pair (summed where a token
- *                               chose an expert twice), 0 elsewhere
+ *                               at expert topk_idx[t][r] (summed where a token chose an expert
+ *                               twice), 0 elsewhere.  A pair that pair_pos drops has dw_r = 0, and
+ *                               its logit still counts through the softmax's sum: a caller whose
+ *                               full experts drop pairs passes their true ids here.  An id outside
+ *                               0..E-1 (as dispatch drops a pair) names no logit to write to
  *   topk_idx     int32 [T][k], read for grad_logits only (may be NULL without it) */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_combine_rows_backward(const moe_w4a16_rows* cfg, const int32_t* topk_idx,
                                                                const int32_t* pair_pos, const float* topk_w,

@@ -329,3 +329,39 @@ def test_no_tokens(B):
                          torch.empty(16, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert bool((off == 0).all())
+
+
+@pytest.mark.parametrize("T,E,k,d,typ,twice", [(5, 6, 3, 64, 2, False), (700, 32, 8, 200, 1, False), (33, 256, 8, 2056, 0, False),
+                                               (260, 5, 2, 520, 2, False), (91, 9, 4, 72, 0, True), (64, 16, 1, 136, 1, False)])
+def test_logit_gradients_of_dropped_choices(B, T, E, k, d, typ, twice):
+    """Choices that full experts dropped, their ids still the router's: the kept weights are a
+    softmax over all k chosen logits, so a dropped one has a gradient too.  Against autograd
+    through softmax in 64 bits.  The kernel's weights are rounded to fp32, which adds v w
+    (|dw| + 2 sum_j w_j |dw_j|) to the error of the formula in the heading."""
+    idx = _ids(T, E, k, T, "twice" if twice else "plain")
+    gone = np.random.default_rng(d).random((T, k)) < 0.3
+    gone[0], gone[T - 1] = np.arange(k) == 0, True
+    off, _, pos = _places(np.where(gone, -1, idx), E)
+    pos[gone & (np.arange(k) % 2 == 1)] = T * k + 3  # any place outside the rows drops a pair
+    rows, dout = _normal((T * k, d), 4, typ), _normal((T, d), 8, typ)
+    rows[int(off[E]):] = float("nan")
+    di, dp, kept = torch.from_numpy(idx).cuda(), torch.from_numpy(pos).cuda(), torch.from_numpy(~gone).cuda()
+    logits = torch.randn(T, E, generator=torch.Generator().manual_seed(9), dtype=torch.float64).cuda().requires_grad_()
+    w = torch.softmax(logits.gather(1, di.long()), 1)
+    at = torch.where(kept, dp, torch.zeros_like(dp)).long()
+    v = torch.where(kept[:, :, None], rows[at].double(), torch.zeros((), dtype=torch.float64, device="cuda"))
+    prod = v * dout.double()[:, None, :]
+    (w[:, :, None] * prod).sum().backward()
+    gw, gl = torch.full((T, k), float("nan"), device="cuda"), torch.full((T, E), float("nan"), device="cuda")
+    B.moe_w4a16_combine_rows_backward(B.make_rows(T, E, k, d, typ), di, dp, w.detach().float(), rows, dout, None, gw, gl)
+    torch.cuda.synchronize()
+    W, dw, per = w.detach(), prod.sum(2).abs(), 4 if typ == 2 else 8
+    e_dw = (-(-d // per // 32) * per + 13) * V * prod.abs().sum(2)
+    m = (W * dw).sum(1, keepdim=True)
+    e_m = (W * e_dw).sum(1, keepdim=True) + (k + 1) * V * m
+    tol = torch.zeros_like(logits).scatter_add_(1, di.long(), W * (e_dw + e_m) + (5 + (k if twice else 0)) * V * W * (dw + m))
+    _within(gw, prod.sum(2), e_dw * 1.01)
+    _within(gl, logits.grad, tol * 1.01)
+    assert bool((gl[T - 1] == 0).all())  # all of a token's choices dropped
+    if k > 1:
+        assert float(gl[0, idx[0, 0]]) != 0  # one dropped, the others kept

@@ -371,10 +371,10 @@ __global__ void __launch_bounds__(kThreads) combine_rows_backward_kernel(
   }
   if (dtopk_w && g < k) dtopk_w[t * k + g] = h1;  // lane g of the group's first warp: r = g
   if (dlogits) {
+    // a dropped choice too: its logit is in the softmax's sum, whatever became of its row
     int id[kMaxTopK];
 #pragma unroll
-    for (int r = 0; r < kMaxTopK; ++r)
-      id[r] = r < k && static_cast<unsigned>(pos[r]) < static_cast<unsigned>(P) ? topk_idx[t * k + r] : -1;
+    for (int r = 0; r < kMaxTopK; ++r) id[r] = r < k ? topk_idx[t * k + r] : -1;
     for (int e = g; e < E; e += kGroup) {
       float s = 0.f;
 #pragma unroll
