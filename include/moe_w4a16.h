@@ -380,7 +380,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_combine_rows(const moe_w4a16_rows* cfg,
  *                               twice), 0 elsewhere.  A pair that pair_pos drops has dw_r = 0, and
  *                               its logit still counts through the softmax's sum: a caller whose
  *                               full experts drop pairs passes their true ids here.  An id outside
- *                               0..E-1 (as dispatch drops a pair) names no logit to write to
+ *                               0..E-1 (as dispatch drops a pair) names no logit to write to,
+ *                               and its weight is not used
  *   topk_idx     int32 [T][k], read for grad_logits only (may be NULL without it) */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_combine_rows_backward(const moe_w4a16_rows* cfg, const int32_t* topk_idx,
                                                                const int32_t* pair_pos, const float* topk_w,

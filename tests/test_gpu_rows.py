@@ -365,3 +365,25 @@ def test_logit_gradients_of_dropped_choices(B, T, E, k, d, typ, twice):
     assert bool((gl[T - 1] == 0).all())  # all of a token's choices dropped
     if k > 1:
         assert float(gl[0, idx[0, 0]]) != 0  # one dropped, the others kept
+
+
+def test_weights_of_dropped_choices_are_not_used(B):
+    """Whatever lies in topk_w at a pair without an expert (padding that nobody wrote, infinities):
+    the same bits as with zeros there, forwards and backwards."""
+    T, E, k, d, typ = 70, 12, 4, 136, 1
+    cfg = B.make_rows(T, E, k, d, typ)
+    idx, pos, rows, w, _ = _data(T, E, k, d, typ, "drop")
+    di, dout = torch.from_numpy(idx).cuda(), _normal((T, d), 8, typ)
+    assert bool(((pos < 0).any(1) & (pos >= 0).any(1)).any())
+
+    def go(w):
+        out, gr = torch.empty_like(dout), torch.zeros_like(rows)
+        gw, gl = torch.empty_like(w), torch.empty(T, E, device="cuda")
+        B.moe_w4a16_combine_rows(cfg, pos, w, rows, None, out)
+        B.moe_w4a16_combine_rows_backward(cfg, di, pos, w, rows, dout, gr, gw, gl)
+        torch.cuda.synchronize()
+        return out, gr, gw, gl
+
+    want = go(torch.where(pos < 0, 0.0, w))
+    for junk in (float("nan"), float("inf"), -1e30):
+        assert all(torch.equal(a, b) for a, b in zip(go(torch.where(pos < 0, junk, w)), want))

@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(kThreads) combine_rows_backward_kernel(
 #pragma unroll
   for (int r = 0; r < kMaxTopK; ++r) {
     dw[r] = __shfl_sync(0xffffffffu, h1, r);
-    if (r < k) mean = fmaf(w[r], dw[r], mean);  // a dropped pair has dw = 0
+    // (a dropped pair has dw = 0, and its weight may be anything)
+    if (static_cast<unsigned>(pos[r]) < static_cast<unsigned>(P)) mean = fmaf(w[r], dw[r], mean);
   }
   if (dtopk_w && g < k) dtopk_w[t * k + g] = h1;  // lane g of the group's first warp: r = g
   if (dlogits) {
