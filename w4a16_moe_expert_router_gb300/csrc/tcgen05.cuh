@@ -21,9 +21,11 @@ __device__ __forceinline__ bool stage_wait(uint32_t bar, uint32_t parity, int32_
   return mbar_wait(bar, parity, err);
 }
 __device__ __forceinline__ bool stage_wait_warp(uint32_t bar, uint32_t parity, int32_t* err) {
-  // one lane polls for a converged warp
+  // one lane polls for a converged warp; the warp's barrier orders the others' accesses after what
+  // that lane has seen (a shuffle alone orders no memory)
   int ok = 0;
   if ((threadIdx.x & 31) == 0) ok = stage_wait(bar, parity, err);
+  __syncwarp();
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
