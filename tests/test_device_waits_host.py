@@ -29,3 +29,20 @@ def test_a_wait_by_one_lane_orders_the_warps_accesses():
     passes the result on but orders no memory."""
     body = _block(_source("tcgen05.cuh"), _source("tcgen05.cuh").index("bool stage_wait_warp("))
     assert re.search(r"stage_wait\w*(<\w+>)?\(bar, parity, err\);.*__syncwarp\(\);.*return", body)
+
+
+def test_waits_for_another_ctas_signals_have_cluster_scope():
+    """What another CTA of a cluster did before it signalled a barrier is ordered by a wait of cluster scope only (the
+    default is the own CTA's), and by an arrival of that scope: all barriers but the one that a CTA's own copies of
+    a tail complete."""
+    waits = re.findall(r"\bstage_wait\w*(<true>)?\((\w+)", _source("linear.cu"))
+    assert {bar for _, bar in waits} == {"full", "empty", "tail_full", "tail_done", "acc_full", "acc_empty", "vacant",
+                                         "summed"}
+    assert all(scope or bar == "tail_full" for scope, bar in waits)
+    assert len(re.findall(r"mbar_wait<true>\(got,", _source("linear_small.cu"))) == 2
+    arrivals = re.findall(r"mbarrier\.arrive[\w.:]*shared::cluster", _source("tcgen05.cuh"))
+    assert arrivals and all(".cluster.shared::cluster" in a for a in arrivals)
+    release = _block(_source("tcgen05.cuh"), _source("tcgen05.cuh").index("void mbar_arrive_cluster_shared("))
+    assert release.index("fence.release") < release.index("mbar_arrive_cluster_relaxed(")
+    assert re.search(r"fence_proxy_async\(\); __syncwarp\(\); if \(lane == 0\) mbar_arrive_cluster_shared\(lead_done",
+                     _source("linear.cu"))

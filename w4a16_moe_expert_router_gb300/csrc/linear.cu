@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           const int bc = r.c0 + (rank & 1) * (r.cols >> 1);
 #pragma unroll 1
           for (int j = 0, f = r.first; j < r.len; j += kDepth, f += kDepth) {
-            if (!stage_wait(empty + 8 * s, phase ^ 1, a.err)) {
+            if (!stage_wait<true>(empty + 8 * s, phase ^ 1, a.err)) {
               alive = false;
               break;
             }
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         }
         // the peer's instructions have told this CTA of every stage before it leaves
         for (int i = 0; alive && i < C::stages; ++i) {
-          alive = stage_wait(empty + 8 * s, phase ^ 1, a.err);
+          alive = stage_wait<true>(empty + 8 * s, phase ^ 1, a.err);
           if (++s == C::stages) {
             s = 0;
             phase ^= 1;
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         for (int t = first_tile; alive && t < tiles; t += step) {
           const Tile r = tile_at<kMode, kSplit>(a, start, off, t, e, rank);
           if (r.len <= 0) continue;  // no rows: the epilogue writes zeros
-          if (!stage_wait(acc_empty + 8 * acc, acc_phase ^ 1, a.err)) {
+          if (!stage_wait<true>(acc_empty + 8 * acc, acc_phase ^ 1, a.err)) {
             alive = false;
             break;
           }
@@ -715,10 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll 1
           for (int j = 0; j < r.len; j += kDepth) {
             if (kMode == kWeightGrad && r.len - j < kDepth) {
-              alive = stage_wait(tail_done + 8 * s, tail_phases >> s & 1, a.err);
+              alive = stage_wait<true>(tail_done + 8 * s, tail_phases >> s & 1, a.err);
               tail_phases ^= 1u << s;
             } else {
-              alive = stage_wait(full + 8 * s, phases >> s & 1, a.err);
+              alive = stage_wait<true>(full + 8 * s, phases >> s & 1, a.err);
               phases ^= 1u << s;
             }
             if (!alive) break;
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           if (acc == 0) acc_phase ^= 1;
         }
         for (int i = 0; !kSplit && alive && i < 2; ++i) {  // and the peer's epilogue has told this one of its tiles
-          alive = stage_wait(acc_empty + 8 * acc, acc_phase ^ 1, a.err);
+          alive = stage_wait<true>(acc_empty + 8 * acc, acc_phase ^ 1, a.err);
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
         }
@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
               *reinterpret_cast<uint4*>(base + box * C::box_bytes + z) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_done + 8 * s);
+          if (lane == 0) mbar_arrive_cluster_shared(lead_done + 8 * s);
         }
       }
     } else if (kMode == kWeightGrad && warp == 3) {
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       if (r.len > 0) {
         // a warp whose wait ran out goes on without waiting: the group's barriers stay matched, and
         // the outputs are invalid as recorded
-        alive = alive && stage_wait_warp(acc_full + 8 * acc, acc_phase, a.err);
+        alive = alive && stage_wait_warp<true>(acc_full + 8 * acc, acc_phase, a.err);
         tcgen05_fence_after();
       }
 #pragma unroll 1
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       if (r.len > 0) {
         tcgen05_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_empty + 8 * acc);
+        if (lane == 0) mbar_arrive_cluster_relaxed(lead_empty + 8 * acc);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
@@ -907,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           request_residual<1>(a, res, tid, r.m0, row0, tile_end);
       }
     }
-    failed = !stage_wait_warp(acc_full, 0, a.err) || !stage_wait_warp(vacant, 0, a.err);
+    failed = !stage_wait_warp<true>(acc_full, 0, a.err) || !stage_wait_warp<true>(vacant, 0, a.err);
     tcgen05_fence_after();
     for (int i = group; !failed && r.row0 + i * 32 < tile_end; i += 2) {
       const int owner = i % a.split, to = owner * 2 + (rank & 1);
@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     cluster_addr(summed + 8 * (i / a.split), to), tid);
     }
     if (row0 < tile_end) {
-      late = !stage_wait_warp(summed + 8 * group, 0, a.err);
+      late = !stage_wait_warp<true>(summed + 8 * group, 0, a.err);
       const StepRows rows{r.m0, row0, tile_end, kMode == kWeightGrad || row0 + 32 <= tile_end, row0, 0};
       step_of<kMode, 32>(a, &map_out, &map_z, at + mine * 32, true,
                          Partials{reinterpret_cast<const float4*>(smem + group * others * kBlockBytes), others}, b, res,

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
           store_async_4(cluster_addr(smem_addr(&sm.parts[part - 1][tid]), 0), v, cluster_addr(got, 0));
         } else {
           // a wait that ran out is recorded; sums that are still on their way land before the CTA goes
-          if (!mbar_wait(got, 0, err)) mbar_wait(got, 0, err);
+          if (!mbar_wait<true>(got, 0, err)) mbar_wait<true>(got, 0, err);
           for (int k = 0; k < split - 1; ++k) v += sm.parts[k][tid];
           sm.total[tid] = v;
         }
