@@ -46,3 +46,19 @@ def test_waits_for_another_ctas_signals_have_cluster_scope():
     assert release.index("fence.release") < release.index("mbar_arrive_cluster_relaxed(")
     assert re.search(r"fence_proxy_async\(\); __syncwarp\(\); if \(lane == 0\) mbar_arrive_cluster_shared\(lead_done",
                      _source("linear.cu"))
+
+
+def test_every_role_waits_for_the_launch_before_first():
+    """A bounded wait of the products' kernel for a stage, an accumulator or a sum starts behind the wait for the
+    launch before, whose rest would count against the limit.  (The loading thread's first waits are for stages that
+    are still empty and return at once.)"""
+    text = _source("linear.cu")
+    kernel = _block(text, text.index("linear_kernel(const __grid_constant__ Args a,"))
+    roles = kernel[kernel.index("if (warp < 4)"):]
+    starts = [roles.index(m) for m in ("else if (warp == 1)", "else if (warp == 2)", "else if (kMode == kWeightGrad && warp == 3)",
+                                       "else if (!kSplit)")]
+    starts.append(roles.index("else {", starts[-1]))
+    for at in starts:
+        role = _block(roles, at)
+        wait = re.search(r"(stage_wait\w*|mbar_wait)(<\w+>)?\(", role)
+        assert 0 < role.find("grid_dependency_wait()") < (wait.start() if wait else len(role)), role[:60]

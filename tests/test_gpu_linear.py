@@ -523,3 +523,25 @@ def test_no_rows(B):
     B.moe_w4a16_linear_backward(cfg, none, off, dw.clone(), none, none, None, dw, db, ws)
     torch.cuda.synchronize()
     assert bool((dw == 0).all()) and bool((db == 0).all())
+
+
+@pytest.mark.parametrize("R,K,N", [(300, 256, 520), (300, 8200, 136), (3000, 256, 264), (5, 264, 72)])
+def test_a_launch_before_that_outlasts_a_waits_limit(B, R, K, N):
+    """Behind a launch of 2.4 s that lets the next one start at once (each wait in these kernels may last 2 s),
+    the products' waits have not run out."""
+    c = Case(R, K, N, 0, 3, 0, 1, True, True, R + 9)
+    g = Grad(c, 4)
+    want, (_, dw, _) = _run_forward(B, c), _run_backward(B, c, g, (False, True, False))
+    cfg = B.make_linear(R, K, N, 1, 3, 0, 1)
+    ws = [torch.empty(max(n, 256), dtype=torch.uint8, device="cuda") for n in (
+        0, B.moe_w4a16_linear_workspace_bytes(cfg), B.moe_w4a16_linear_backward_workspace_bytes(cfg))]
+    for w in ws:
+        B.moe_w4a16_workspace_init(w)
+    out, z, got = torch.zeros_like(want[0]), torch.zeros_like(want[1]), torch.zeros_like(dw)
+    B.moe_w4a16_selftest_wait_timeout(ws[0], 1_200_000_000)
+    B.moe_w4a16_linear(cfg, c.x, None, c.w, c.b, c.res, out, z, ws[1])
+    B.moe_w4a16_selftest_wait_timeout(ws[0], 1_200_000_000)
+    B.moe_w4a16_linear_backward(cfg, c.x, None, None, None, g.dout, None, got, None, ws[2])
+    torch.cuda.synchronize()
+    assert [B.moe_w4a16_read_error(w) for w in ws] == [B.ERR_TIMEOUT, B.OK, B.OK]
+    assert torch.equal(out, want[0]) and torch.equal(z, want[1]) and torch.equal(got, dw)

@@ -678,10 +678,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 // Self-test of the bounded waits above: one warp waits, with the given bound, on
 // an mbarrier phase that nothing completes and then on a counter that nothing
 // raises (flag, left at 0); each wait gives up, records MOE_W4A16_ERR_TIMEOUT in
-// *err and the kernel returns.  Nothing is in flight when it returns.
+// *err and the kernel returns.  Nothing is in flight when it returns.  The next launch may start
+// meanwhile, as behind every kernel here: a launch before that lasts longer than a wait may.
 __global__ void __launch_bounds__(32) wait_selftest_kernel(int32_t* err, const int32_t* flag, uint64_t limit_ns) {
   __shared__ uint64_t bar;
   __shared__ int abort;
+  grid_dependents_launch();
   if (threadIdx.x == 0) {
     mbar_init(smem_addr(&bar), 1);  // one arrival that never comes
     abort = 0;

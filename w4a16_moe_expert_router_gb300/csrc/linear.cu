@@ -703,6 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         int e = 0, s = 0, acc = 0;
         uint32_t phases = 0, acc_phase = 0, tail_phases = 0;  // per stage: parity of its next use
         bool alive = true;
+        grid_dependency_wait();  // the limit of a wait for a stage does not run while the launch before does
         for (int t = first_tile; alive && t < tiles; t += step) {
           const Tile r = tile_at<kMode, kSplit>(a, start, off, t, e, rank);
           if (r.len <= 0) continue;  // no rows: the epilogue writes zeros
@@ -766,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const uint32_t lead_done = cluster_addr(tail_done, lead);
         int e = 0, it = 0;
         uint32_t phases = 0;
+        grid_dependency_wait();  // as the thread above
         for (int t = first_tile; t < tiles; t += step) {
           const Tile r = tile_at<kMode, kSplit>(a, start, off, t, e, rank);
           if (r.len <= 0) continue;

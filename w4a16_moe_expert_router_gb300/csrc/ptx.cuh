@@ -10,7 +10,7 @@ namespace moe {
 
 // A device-side wait gives up after this long, records MOE_W4A16_ERR_TIMEOUT in
 // the workspace error word and lets the kernel return.  Legitimate waits in
-// these kernels last microseconds.
+// these kernels last microseconds, and none begins before the launch before has ended.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int32_t kStatusTimeout = 7;              // MOE_W4A16_ERR_TIMEOUT
 
