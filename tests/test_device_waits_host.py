@@ -62,3 +62,13 @@ def test_every_role_waits_for_the_launch_before_first():
         role = _block(roles, at)
         wait = re.search(r"(stage_wait\w*|mbar_wait)(<\w+>)?\(", role)
         assert 0 < role.find("grid_dependency_wait()") < (wait.start() if wait else len(role)), role[:60]
+
+
+def test_copies_in_flight_land_after_a_wait_ran_out():
+    """The kernel for few rows counts a chunk before it waits for it, so the copies that may still be in flight when
+    that wait runs out begin with the last chunk counted, not behind it."""
+    body = _source("linear_small.cu")
+    chunk = _block(body, body.index("const auto chunk = "))
+    assert chunk.index("stage_wait_warp(") < chunk.index("++used;") < chunk.index("__syncthreads_and(")
+    drain = re.search(r"for \(int k = (used[^;]*); k < fetched; \+\+k\) mbar_wait\(full", chunk)
+    assert drain and drain.group(1) == "used - 1"

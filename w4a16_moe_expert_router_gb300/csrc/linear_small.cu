@@ -176,9 +176,10 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
       }
     }
     if (!__syncthreads_and(ok)) {  // (the chunk is read)
-      // a wait ran out and is recorded: the other copies in flight land, and the outputs are invalid
+      // a wait ran out and is recorded: the copies in flight land, that chunk's among them, and the
+      // outputs are invalid
       if (fetcher)
-        for (int k = used; k < fetched; ++k) mbar_wait(full + 8 * (k % kStages), (k / kStages) & 1, err);
+        for (int k = used - 1; k < fetched; ++k) mbar_wait(full + 8 * (k % kStages), (k / kStages) & 1, err);
       if (split > 1 && part == 0) mbar_wait(got, 0, err);
       return false;
     }
