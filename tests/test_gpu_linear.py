@@ -545,3 +545,83 @@ def test_a_launch_before_that_outlasts_a_waits_limit(B, R, K, N):
     torch.cuda.synchronize()
     assert [B.moe_w4a16_read_error(w) for w in ws] == [B.ERR_TIMEOUT, B.OK, B.OK]
     assert torch.equal(out, want[0]) and torch.equal(z, want[1]) and torch.equal(got, dw)
+
+
+@pytest.mark.parametrize("gated,act", [(0, 0), (1, 2), (0, 1), (1, 0)])
+def test_gradient_against_differences_along_itself(B, gated, act):
+    """Central differences of sum(g out) along the sign of each gradient, where the quotient is the sum of the
+    gradient's magnitudes and not lost in the outputs' roundings.  It may differ from the gradient's product with the
+    step by the roundings of the two calls' outputs (5 u |g out| each, over 2), by the quotient's own distance from the
+    derivative, taken from the same quotient in 64 bits, and by the roundings of z, dz and the gradient: 8 u of the sum
+    of magnitudes.  All of that is at most 3 % of the quotient."""
+    R, K, N, u = 96, 64, 40, HALF[0]
+    c = Case(R, K, N, 0, act, gated, 0, True, False, 11)
+    g = _normal((R, N), 3, torch.float16)
+    leaves = {n: getattr(c, n).double().requires_grad_() for n in ("x", "w", "b")}
+    zz = leaves["x"] @ leaves["w"][0].T + leaves["b"]
+    y = _act(zz[:, :N], act)
+    ((y * zz[:, N:] if gated else y) * g.double()).sum().backward()
+
+    class G:
+        z, dout = _run_forward(B, c)[1], g
+
+    def f():
+        out, exact = _run_forward(B, c, save=False)[0].double() * g.double(), c.forward()[0] * g.double()
+        return float(out.sum()), float(out.norm()), float(exact.sum())
+
+    for name, grad in zip(("x", "w", "b"), _run_backward(B, c, G)):
+        keep = getattr(c, name)
+        step = torch.sign(leaves[name].grad).reshape(keep.shape) * (2.0 ** -7 if name == "x" else 2.0 ** -9 if name == "w" else 2.0 ** -5)
+        up, down = (keep.double() + step).to(keep.dtype), (keep.double() - step).to(keep.dtype)
+        moved = (up.double() - down.double()) / 2  # what the rounded steps are
+        want, true = (float((t.double().reshape(moved.shape) * moved).sum()) for t in (grad, leaves[name].grad))
+        setattr(c, name, up)
+        a, na, a64 = f()
+        setattr(c, name, down)
+        b, nb, b64 = f()
+        setattr(c, name, keep)
+        tol = 5 * u * (na + nb) / 2 + abs((a64 - b64) / 2 - true) + 8 * u * float((grad.double().reshape(moved.shape) * moved).abs().sum())
+        assert tol <= 0.03 * abs(want), (name, tol, want)
+        assert abs((a - b) / 2 - want) <= tol, (name, (a - b) / 2, want, tol)
+
+
+@pytest.mark.parametrize("E", [0, 3])
+@pytest.mark.parametrize("gated", [0, 1])
+def test_bias_gradient_of_more_than_two_million_rows(B, E, gated):
+    """Above 2^21 rows the bias gradient's partial sums cover 256 rows each.  Whole numbers, whose sums stay below
+    2^24, so that every addition in fp32 is exact: the sums are equal to those in 64 bits, the weight gradient to its
+    one rounding, with and without the other outputs.  An expert without rows gets zeros, rows of none add nothing."""
+    R, K, N = (1 << 21) + 300, 8, 24
+    gen = torch.Generator(device="cuda").manual_seed(E + gated)
+
+    def whole(most, *shape):
+        return torch.randint(-most, most + 1, shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+    Nw = 2 * N if gated else N
+    off = [0, 700001, 700001, R - 37] if E else [0, R]
+    x, dout, z = whole(1, R, K), whole(4, R, N), whole(1, R, Nw) if gated else None
+    for t in (x, dout) + ((z,) if gated else ()):
+        t[off[-1]:] = float("nan")
+    cfg = B.make_linear(R, K, N, max(E, 1), 3, gated, 1)
+    offd = torch.tensor(off, dtype=torch.int32, device="cuda") if E else None
+    ws = torch.full((B.moe_w4a16_linear_backward_workspace_bytes(cfg),), 255, dtype=torch.uint8, device="cuda")
+    B.moe_w4a16_workspace_init(ws)
+
+    def go(with_weight):
+        dw = torch.full((max(E, 1), Nw, K), 7, dtype=torch.bfloat16, device="cuda") if with_weight else None
+        db = torch.full((max(E, 1), Nw), 7, dtype=torch.float32, device="cuda")
+        B.moe_w4a16_linear_backward(cfg, x if with_weight else None, offd, None, z, dout, None, dw, db, ws)
+        torch.cuda.synchronize()
+        assert B.moe_w4a16_read_error(ws) == B.OK
+        return dw, db
+
+    (dw, db), (_, alone) = go(True), go(False)
+    assert torch.equal(db, alone)
+    for e in range(len(off) - 1):
+        d, rows = dout[off[e]:off[e + 1]].double(), x[off[e]:off[e + 1]].double()
+        if gated:
+            zz = z[off[e]:off[e + 1]].double()
+            d = torch.cat([d * zz[:, N:], d * zz[:, :N]], 1)
+        assert float(d.abs().sum(0).max() if len(d) else 0) < 2 ** 24
+        assert torch.equal(db[e].double(), d.sum(0))
+        assert torch.equal(dw[e], (d.T @ rows).to(torch.bfloat16))
