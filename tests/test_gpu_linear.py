@@ -625,3 +625,35 @@ def test_bias_gradient_of_more_than_two_million_rows(B, E, gated):
         assert float(d.abs().sum(0).max() if len(d) else 0) < 2 ** 24
         assert torch.equal(db[e].double(), d.sum(0))
         assert torch.equal(dw[e], (d.T @ rows).to(torch.bfloat16))
+
+
+def test_a_layer_on_another_stream_than_its_constructors(B):
+    """A layer whose buffers take over memory that the constructor's stream still writes, used on another stream."""
+    from w4a16_moe_expert_router_gb300 import runtime
+    T, d, f, E, k, dt = 200, 264, 72, 8, 2, torch.bfloat16
+    x, lg = _normal((T, d), 1, dt), _normal((T, E), 2, torch.float32)
+    gu, dn, dout = _normal((E, 2 * f, d), 3, dt, d ** -0.5), _normal((E, d, f), 4, dt, f ** -0.5), _normal((T, d), 6, dt)
+    out, grads = _layer(B, x, lg, gu, None, dn, E, k, f, 1, dout)
+    want = [out] + [grads[n].clone() for n in sorted(grads)]
+    torch.cuda.synchronize()
+    busy = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (1 << 20, 1 << 20, 1 << 24)]
+    torch.cuda._sleep(100_000_000)
+    for t in busy:
+        t.fill_(255)
+    del busy, t
+    layer, other = runtime.Layer16(T, d, f, E, k, type=1), torch.cuda.Stream()
+    out = layer.forward(x, lg, gu, None, dn, stream=other)
+    grads = layer.backward(dout, stream=other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip([out] + [grads[n] for n in sorted(grads)], want))
+    assert all(B.moe_w4a16_read_error(layer.ws[i]) == B.OK for i in (0, 2))
+
+
+def test_a_layer_without_tokens(B):
+    from w4a16_moe_expert_router_gb300 import runtime
+    none, gu, dn = (torch.ones(s, dtype=torch.float16, device="cuda") for s in ((0, 64), (4, 128, 64), (4, 64, 64)))
+    layer = runtime.Layer16(0, 64, 64, 4, 2)
+    out = layer.forward(none, torch.zeros(0, 4, device="cuda"), gu, None, dn)
+    grads = layer.backward(none)
+    torch.cuda.synchronize()
+    assert out.shape == (0, 64) and bool((grads["gate_up"] == 0).all()) and bool((grads["down"] == 0).all())

@@ -192,3 +192,21 @@ def test_structs_match_the_header(tmp_path):
     for cname, cls in structs.items():
         assert got[(cname, "size")] == ctypes.sizeof(cls)
         assert all(got[(cname, f)] == getattr(cls, f).offset for f, _ in cls._fields_)
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_a_layers_buffers_are_ready_for_any_stream(monkeypatch, capturing):
+    """The constructor ends when its stream has: what it took over and cleared is done before a call on another
+    stream.  A stream that is being captured cannot be waited for."""
+    from w4a16_moe_expert_router_gb300 import runtime
+    seen = []
+
+    class Stream:
+        def synchronize(self):
+            seen.append("synchronize")
+
+    monkeypatch.setattr(B, "moe_w4a16_workspace_init", lambda ws, stream=None: seen.append("init"))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    runtime.Layer16(4, 64, 64, 4, 2, device="cpu")
+    assert seen == ["init", "init"] + ([] if capturing else ["synchronize"])

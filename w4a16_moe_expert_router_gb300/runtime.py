@@ -103,7 +103,8 @@ class Layer16:
     """The expert layer in 16 bits with gradients: the buffers of one batch and the call
     sequence route -> dispatch -> gate and up -> down -> combine (with the residual), and
     back.  ``backward`` belongs to the last ``forward``; both leave their results in the
-    layer's buffers.
+    layer's buffers.  The calls take any stream, one after the other: their order over several
+    streams is the caller's.  Nothing is recorded by autograd.
 
     Rows are fp16 (type 0) or bf16 (type 1); gate_up [E][2f][d] with an fp32 bias
     [E][2f] or None, down [E][d][f], router logits fp32 [T][E].
@@ -138,6 +139,10 @@ class Layer16:
                 B.moe_w4a16_linear_backward_workspace_bytes(self.dn)))]
         B.moe_w4a16_workspace_init(self.ws[0])
         B.moe_w4a16_workspace_init(self.ws[2])
+        # memory that the buffers took over may still be in use on this stream, and the workspaces' start is
+        # cleared on it: done before another stream gets a call (a captured constructor keeps to its graph)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
 
     def forward(self, x, logits, gate_up, gate_up_bias, down, stream=None) -> torch.Tensor:
         """out = x + sum_r w_r expert_r(x) for every token."""
