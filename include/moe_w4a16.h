@@ -435,7 +435,8 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_linear(const moe_w4a16_linear_cfg* cfg,
  *                                 without rows
  *   grad_bias    fp32 [E][Nw]     sum over the expert's rows of dz
  * dz = grad_out act'(z) (gated: grad_out z_up act'(z_gate) and grad_out act(z_gate)) is rounded
- * to the type once, as the operand of the two products; grad_bias adds the unrounded values.
+ * to the type once, as the operand of the two products; grad_bias adds the unrounded values, whose
+ * activation and derivative are good to about 2^-17 of their terms (fast exponential and divide).
  * x is read for grad_weight only, weight for grad_x only (else they may be NULL).  With R = 0
  * grad_weight and grad_bias are cleared. */
 MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_backward(const moe_w4a16_linear_cfg* cfg, const void* x,

@@ -143,7 +143,7 @@ def _check_forward(B, c):
 
 # R, K, N, E (0: dense), activation, gated, type, bias, residual, rows of no expert
 FORWARD = [
-    # up to 32 rows: the kernel for single tokens and small batches
+    # up to 32 rows: the kernel for single tokens and small batches (16 at most), and tiles of 32 columns
     (1, 8, 8, 0, 3, 0, 0, False, False, 0), (1, 2048, 136, 0, 0, 0, 0, True, True, 0), (2, 264, 72, 0, 1, 1, 1, True, True, 0),
     (3, 1000, 16, 0, 2, 0, 1, True, False, 0), (5, 72, 200, 0, 0, 1, 0, False, True, 0), (8, 2056, 40, 0, 3, 0, 1, True, True, 0),
     (1, 64, 64, 5, 0, 1, 0, True, False, 0), (8, 704, 72, 128, 0, 1, 1, False, True, 0), (8, 136, 8, 256, 3, 0, 0, True, False, 3),
@@ -154,7 +154,7 @@ FORWARD = [
     (32, 64, 16, 256, 3, 0, 0, True, True, 0), (16, 72, 8, 3, 0, 1, 0, True, False, 16),
     # tiles
     (33, 65536, 8, 0, 3, 0, 1, True, False, 0), (48, 8, 8, 0, 0, 1, 0, True, True, 0),
-    # 64, 128, 256 columns and their edges
+    # tiles of 32 to 256 columns, in steps of 32, and their edges
     (33, 136, 72, 0, 1, 0, 0, True, False, 0), (64, 520, 200, 0, 0, 1, 1, False, True, 0), (65, 64, 1032, 0, 3, 0, 0, True, True, 0),
     (127, 200, 136, 0, 2, 0, 1, True, True, 0), (128, 256, 128, 0, 0, 1, 0, True, False, 0), (129, 72, 264, 0, 0, 0, 0, True, True, 0),
     (257, 264, 136, 0, 1, 1, 1, True, True, 0), (777, 1000, 520, 0, 2, 0, 0, True, True, 0), (300, 16, 8, 0, 3, 0, 1, False, True, 0),
@@ -235,7 +235,8 @@ class Grad:
             self.dx[i:j], self.dw[e], self.db[e] = z @ w, z.T @ x, z.sum(0)
             self.e_dx[i:j] = ez @ w.abs() + (c.Nw + 2) * T23 * a
             self.e_dw[e] = ez.T @ x.abs() + (j - i + 2) * T23 * b
-            # at most 16 rows a thread, eight threads, then up to 1 + rows / 128 partial sums in a row
+            # 8 rows a thread (blocks of 64), eight threads, then every eighth of up to 1 + rows / 64 partial sums and
+            # those eight: fewer than 26 + rows / 128 additions in a row
             self.e_db[e] = e_dz[i:j].sum(0) + (26 + (j - i) / 128) * T23 * z.abs().sum(0) + 1e-12
             s_dx, s_dw = s_dx + float(a.norm()) ** 2, s_dw + float(b.norm()) ** 2
         self.e_dx = (1 + u) * self.e_dx + u * self.dx.abs() + SMALL[c.typ]

@@ -1,8 +1,8 @@
 """Thin ctypes binding of the C ABI in ``include/moe_w4a16.h``.
 
 Functions keep the C names and only marshal arguments: device buffers are any
-object with ``data_ptr()`` (torch tensors) or raw integer addresses, host
-buffers are numpy arrays, and a stream is a ``torch.cuda.Stream``, a raw
+object with ``data_ptr()`` (torch tensors) or raw integer addresses (but for a
+workspace, whose size is read from it: a tensor), host buffers are numpy arrays, and a stream is a ``torch.cuda.Stream``, a raw
 ``cudaStream_t`` integer, or ``None`` for torch's current stream.  Every step of
 the layer runs in the library's CUDA kernels; if the shared library has not been
 built, loading it raises (there is no fallback path).
@@ -327,7 +327,8 @@ def moe_w4a16_sample(cfg: Sampler, logits, revealed, token, entropy, pmax, accep
 # These calls take tensors of several types, so a tensor is checked before its
 # address is passed on: type, number of elements, contiguity, and that it lives on
 # the current CUDA device (raw addresses are passed on as they are).  The checks are
-# most of a small call's time, so they are kept short.
+# most of a small call's time, so they are kept short.  Nothing is recorded by autograd:
+# the ``_backward`` calls are the gradients, and a tensor's ``requires_grad`` has no effect.
 
 _CONTEXT = None
 

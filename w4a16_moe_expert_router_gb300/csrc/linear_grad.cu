@@ -6,12 +6,12 @@
 // One pass over z and dout writes dz in the rows' type, the operand of the two products
 // that follow: a rounding of half a step per element, independent from element to
 // element, so a sum over dz is off by about what its own rounding to the type costs.
-// The bias gradient takes the fp32 values: a CTA sums up to 64 rows of one expert for 256
-// columns (eight rows per thread, then eight threads in order) into a partial, and an
-// expert's partials are added, eight strided sums per column in order, by an idle warp of
-// the weight gradient that follows or, without one, by a launch of its own: no atomics.  Bound
-// by memory: z and dout read once, dz written once; each thread requests two rows
-// before it uses the first.
+// The bias gradient takes the fp32 values: a CTA sums up to linear_block_rows rows of one
+// expert (64, or 256 of more than 2^21) for 256 columns (an eighth of the rows per thread,
+// then eight threads in order) into a partial, and an expert's partials are added, eight
+// strided sums per column in order, by an idle warp of the weight gradient that follows or,
+// without one, by a launch of its own: no atomics.  Bound by memory: z and dout read once,
+// dz written once; each thread requests two rows before it uses the first.
 #include "activation.cuh"
 #include "internal.h"
 #include "row_vec.cuh"
