@@ -111,7 +111,7 @@ def draw(rng):
                   flat=flat)
     else:
         dtype = rng.choice(["fp16", "bf16", "bf16", "fp32"])
-        hidden = 8 * _log_int(rng, 8, 2048)
+        hidden = 8 * _log_int(rng, 8, 1024)
         rows = max(1, min(_log_int(rng, 1, 16384), (1 << 26) // (hidden * BYTES[dtype])))
         form = rng.choice(["pre", "post", "both", "both"])
         gate_rows = 0 if form == "pre" else rng.choice([0, rows, rng.randint(1, rows), 1])
