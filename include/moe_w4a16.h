@@ -24,7 +24,9 @@
  * denoising loop (entropy, Gumbel-max token, acceptance of positions) in one
  * streaming pass over the vocabulary logits (see its section below), and the calls
  * of the section "the layer in 16 bits, with gradients" run the layer's steps on
- * fp16 or bf16 weights, forwards and backwards.
+ * fp16 or bf16 weights, forwards and backwards.  moe_w4a16_few is the whole layer for
+ * a few tokens, moe_w4a16_norm what stands between two blocks, with its gradient, and
+ * moe_w4a16_clip the gradients' norm and clipping.
  * The weight format follows the model card's "requirements" paragraph
  * (dg-w4a16-v1: two nibbles per byte; gate_up_proj grouped along the
  * contraction dim; down_proj grouped at 64 because its contraction dim, 704, is
@@ -444,6 +446,113 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_backward(const moe_w4a16_linear_
                                                          const void* preact, const void* grad_out, void* grad_x,
                                                          void* grad_weight, float* grad_bias, void* workspace,
                                                          size_t workspace_bytes, void* stream);
+
+/* ---- the whole layer for a few tokens ------------------------------------------
+ * The W4A16 layer of moe_w4a16_route + moe_w4a16_forward for at most
+ * MOE_W4A16_FEW_TOKENS tokens (a generation loop, a few requests decoded together),
+ * from the router's logits to the output in two launches, on fp16 or bf16 tokens:
+ *   out[t] = residual[t] + sum over the k chosen experts of w[t][r] Wd gelu(Wg x) (Wu x)
+ * with the choice and the weights of moe_w4a16_route (bit for bit).  The codes are multiplied
+ * as they are and a group's scale and second value applied to its fp32 sum, h is kept in two
+ * values of the type (22 bits for fp16, 16 for bf16; its range is the type's), everything else in
+ * fp32, rounded once.  A token's output does not depend on the other tokens.
+ *   shape       as for the layer, tokens 0..MOE_W4A16_FEW_TOKENS (ERR_SHAPE above); `reduction`
+ *               has no effect
+ *   type        MOE_W4A16_FP16 or _BF16: type of x, residual and out
+ *   x           type [T][d]     logits  fp32 [T][E], finite as for moe_w4a16_route
+ *   weights     prepared weights of the layer, the same as moe_w4a16_forward's
+ *   residual    type [T][d] or NULL
+ *   topk_idx    int32 [T][k], topk_w fp32 [T][k]: written, each NULL where it is not wanted
+ *   out         type [T][d], written; may be residual itself; must not overlap x
+ *   workspace   moe_w4a16_few_workspace_bytes(shape) bytes; scratch, no state
+ * T = 0 is an OK no-op. */
+#define MOE_W4A16_FEW_TOKENS 32
+MOE_W4A16_API size_t moe_w4a16_few_workspace_bytes(const moe_w4a16_shape* shape);
+MOE_W4A16_API moe_w4a16_status moe_w4a16_few(const moe_w4a16_shape* shape, int32_t type, const void* x,
+                                             const float* logits, const moe_w4a16_weights* weights,
+                                             const void* residual, int32_t* topk_idx, float* topk_w, void* out,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the norms around a block, with gradients --------------------------------------
+ * What stands between two blocks of a model, in one launch: the RMS norm after a block,
+ * its gate and the residual, and the RMS norm before the next one.
+ *   v   = gamma_post y / sqrt(mean(y^2) + eps)          (gamma_post NULL: v = y)
+ *   out = residual_scale x + gate v                     (gate NULL: ones; x NULL: no residual)
+ *   u   = gamma_pre out / sqrt(mean(out^2) + eps)
+ * in fp32 from load to store (u is the norm of out before its rounding).
+ *   rows            R, 0..2^22
+ *   hidden          d, a multiple of 8, 8..8192
+ *   type            MOE_W4A16_FP16, _BF16 or _FP32: type of the rows
+ *   gate_rows       rows that share a row of the gate (row r takes gate row r / gate_rows): R or more for
+ *                   one gate per column, a sequence's length for one per sequence, 1 for one per
+ *                   row; 0..2^22, 0 only without a gate (ERR_SHAPE)
+ *   residual_scale  finite;  eps  finite, >= 0 (ERR_VALUE; with 0 a row of zeros has no norm) */
+typedef struct {
+  int32_t rows, hidden, type, gate_rows;
+  float residual_scale, eps;
+} moe_w4a16_norm_cfg;
+
+/* Forward.  The norm before a block alone takes x and gives u; the one after it takes y
+ * (and x) and gives out; both together give out and u.
+ *   x, y        type [R][d], each NULL where it does not take part (one at least does)
+ *   gamma_post  fp32 [d] or NULL     gate  fp32 [ceil(R / gate_rows)][d] or NULL     (both NULL without y)
+ *   gamma_pre   fp32 [d], given exactly where u is wanted
+ *   out, u      type [R][d], written, each NULL where it is not wanted (one at least is); either may be
+ *               x or y itself
+ * R = 0 is an OK no-op. */
+MOE_W4A16_API moe_w4a16_status moe_w4a16_norm(const moe_w4a16_norm_cfg* cfg, const void* x, const void* y,
+                                              const float* gamma_post, const float* gate, const float* gamma_pre,
+                                              void* out, void* u, void* stream);
+
+/* Its gradient, each output NULL where it is not wanted (one at least is):
+ *   y, gamma_post, gate, gamma_pre   as in the forward call (y is read for grad_gamma_post, grad_gate and,
+ *                    with gamma_post, grad_y)
+ *   out              type [R][d]: what the forward call wrote (residual_scale x where it had no y),
+ *                    read with grad_u only
+ *   grad_out, grad_u type [R][d]: the gradients that arrive at out and u, each NULL where none does (one
+ *                    at least does)
+ *   grad_x, grad_y   type [R][d]; each may be grad_out or grad_u itself
+ *   grad_gamma_post, grad_gamma_pre  fp32 [d] (grad_gamma_pre with grad_u only)
+ *   grad_gate        fp32, as gate: the sum over the rows that share a row of it
+ *   workspace        moe_w4a16_norm_backward_workspace_bytes(cfg) bytes, for the three sums (NULL
+ *                    without them); scratch, no state
+ * Sums are fp32 in a fixed order.  With R = 0 the gammas' gradients are cleared. */
+MOE_W4A16_API size_t moe_w4a16_norm_backward_workspace_bytes(const moe_w4a16_norm_cfg* cfg);
+MOE_W4A16_API moe_w4a16_status moe_w4a16_norm_backward(const moe_w4a16_norm_cfg* cfg, const void* y,
+                                                       const float* gamma_post, const float* gate, const void* out,
+                                                       const float* gamma_pre, const void* grad_out,
+                                                       const void* grad_u, void* grad_x, void* grad_y,
+                                                       float* grad_gamma_post, float* grad_gate,
+                                                       float* grad_gamma_pre, void* workspace,
+                                                       size_t workspace_bytes, void* stream);
+
+/* ---- the norm of many gradients, and clipping ---------------------------------------
+ * norm = sqrt(sum over all tensors of g^2), and every tensor scaled by max_norm / norm where the
+ * norm is larger than max_norm:
+ *   out = g min(1, max_norm / norm), rounded once
+ * A norm that is infinite or not a number scales nothing (the caller sees it in *norm and leaves the
+ * step out).  Squares are summed in fp32 over at most 64 elements and in fp64 from there, in a fixed order;
+ * values whose squares leave fp32's range are summed in fp64 throughout.
+ *   tensors   host array of `count` (0..65536) tensors, read during the call only:
+ *             data   device, `count` elements of the type, contiguous, aligned to an element
+ *             out    device, where the scaled values go, aligned to an element: data itself (in place; left
+ *                    untouched where nothing is scaled), other memory (written always), or NULL (the
+ *                    tensor counts for the norm and is not scaled)
+ *             count  0..2^34     type  MOE_W4A16_FP16, _BF16 or _FP32
+ *             Outputs overlap neither other tensors nor each other.
+ *   max_norm  >= 0, infinity for the norm alone (ERR_VALUE for less, or not a number)
+ *   norm      device fp32, written
+ *   workspace moe_w4a16_clip_workspace_bytes(count) bytes (0 on an invalid count); scratch, no state
+ * A call captured into a graph keeps the addresses that it was captured with. */
+typedef struct {
+  const void* data;
+  void* out;
+  int64_t count;
+  int32_t type;
+} moe_w4a16_tensor;
+MOE_W4A16_API size_t moe_w4a16_clip_workspace_bytes(int32_t count);
+MOE_W4A16_API moe_w4a16_status moe_w4a16_clip(const moe_w4a16_tensor* tensors, int32_t count, double max_norm,
+                                              float* norm, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- host-side weight helpers (no GPU needed) ---------------------------- */
 

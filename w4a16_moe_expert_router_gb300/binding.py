@@ -30,9 +30,13 @@ EXPORTED = ("moe_w4a16_workspace_bytes", "moe_w4a16_workspace_init", "moe_w4a16_
             "moe_w4a16_block_front", "moe_w4a16_block", "moe_w4a16_noalloc_read_error",
             "moe_w4a16_dispatch_workspace_bytes", "moe_w4a16_dispatch", "moe_w4a16_dispatch_backward",
             "moe_w4a16_combine_rows", "moe_w4a16_combine_rows_backward", "moe_w4a16_linear_workspace_bytes",
-            "moe_w4a16_linear_backward_workspace_bytes", "moe_w4a16_linear", "moe_w4a16_linear_backward")
+            "moe_w4a16_linear_backward_workspace_bytes", "moe_w4a16_linear", "moe_w4a16_linear_backward",
+            "moe_w4a16_few_workspace_bytes", "moe_w4a16_few", "moe_w4a16_norm",
+            "moe_w4a16_norm_backward_workspace_bytes", "moe_w4a16_norm_backward", "moe_w4a16_clip_workspace_bytes",
+            "moe_w4a16_clip")
 FP16, BF16, FP32 = 0, 1, 2
 
+FEW_TOKENS = 32  # MOE_W4A16_FEW_TOKENS
 NOALLOC_SCRATCH_BYTES = 40 << 20  # MOE_W4A16_NOALLOC_SCRATCH_BYTES
 
 
@@ -59,6 +63,16 @@ class Rows(ctypes.Structure):
 
 class Linear(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("rows", "inp", "out", "groups", "activation", "gated", "type")]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "hidden", "type", "gate_rows")] + [
+        ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("type", ctypes.c_int32)]
 
 
 class Weights(ctypes.Structure):
@@ -135,6 +149,20 @@ def lib() -> ctypes.CDLL:
             L.moe_w4a16_linear.restype = st
             L.moe_w4a16_linear_backward.argtypes = [P(Linear), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
             L.moe_w4a16_linear_backward.restype = st
+            L.moe_w4a16_few_workspace_bytes.argtypes = [P(Shape)]
+            L.moe_w4a16_few_workspace_bytes.restype = sz
+            L.moe_w4a16_few.argtypes = [P(Shape), i32, vp, vp, P(Weights), vp, vp, vp, vp, vp, sz, vp]
+            L.moe_w4a16_few.restype = st
+            L.moe_w4a16_norm.argtypes = [P(Norm), vp, vp, vp, vp, vp, vp, vp, vp]
+            L.moe_w4a16_norm.restype = st
+            L.moe_w4a16_norm_backward_workspace_bytes.argtypes = [P(Norm)]
+            L.moe_w4a16_norm_backward_workspace_bytes.restype = sz
+            L.moe_w4a16_norm_backward.argtypes = [P(Norm)] + 13 * [vp] + [sz, vp]
+            L.moe_w4a16_norm_backward.restype = st
+            L.moe_w4a16_clip_workspace_bytes.argtypes = [i32]
+            L.moe_w4a16_clip_workspace_bytes.restype = sz
+            L.moe_w4a16_clip.argtypes = [vp, i32, ctypes.c_double, vp, vp, sz, vp]
+            L.moe_w4a16_clip.restype = st
             L.moe_w4a16_read_error.argtypes = [vp, sz, vp, P(ctypes.c_int)]
             L.moe_w4a16_read_error.restype = st
             L.moe_w4a16_pack.argtypes = [vp, i64, i64, vp]
@@ -469,6 +497,134 @@ def moe_w4a16_linear_backward(cfg: Linear, x, expert_offsets, weight, preact, gr
         _nbytes(workspace), current(dev) if stream is None else _stream(stream))
     if st:
         _check(st, "moe_w4a16_linear_backward")
+
+
+# ------------------------------- the whole layer for a few tokens, norms, clipping
+#
+# Tensors are checked as above.
+
+def moe_w4a16_few_workspace_bytes(shape: Shape) -> int:
+    return int(lib().moe_w4a16_few_workspace_bytes(ctypes.byref(shape)))
+
+
+def moe_w4a16_few(shape: Shape, type: int, x, logits, gate_up, down, residual, topk_idx, topk_w, out, workspace,
+                  stream=None) -> None:
+    """The whole layer for at most FEW_TOKENS tokens, from the router's logits; type: FP16 or BF16, of x, residual
+    and out.  gate_up, down: the prepared weights of the layer."""
+    types, i32, f32, device, current = _CONTEXT or _context()
+    dev, dt, T, k = device(), types.get(type), shape.tokens, shape.top_k
+    n = T * shape.hidden
+    w = Weights(_wptr(gate_up, dev), _wptr(down, dev))
+    if _nbytes(gate_up) != moe_w4a16_prepared_bytes(shape, GATE_UP) or \
+            _nbytes(down) != moe_w4a16_prepared_bytes(shape, DOWN):
+        raise MoeW4A16Error(ERR_SHAPE, "moe_w4a16_few: the prepared weights' sizes do not match the shape")
+    st = lib().moe_w4a16_few(
+        ctypes.byref(shape), type, _tptr(x, dt, n, dev), _tptr(logits, f32, T * shape.experts, dev), ctypes.byref(w),
+        residual if residual is None else _tptr(residual, dt, n, dev),
+        topk_idx if topk_idx is None else _tptr(topk_idx, i32, T * k, dev),
+        topk_w if topk_w is None else _tptr(topk_w, f32, T * k, dev), _tptr(out, dt, n, dev), _wptr(workspace, dev),
+        _nbytes(workspace), current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_few")
+
+
+def make_norm(rows, hidden, type=0, gate_rows=0, residual_scale=1.0, eps=1e-6) -> Norm:
+    return Norm(rows, hidden, type, gate_rows, residual_scale, eps)
+
+
+def moe_w4a16_norm(cfg: Norm, x, y, gamma_post, gate, gamma_pre, out, u, stream=None) -> None:
+    types, _, f32, device, current = _CONTEXT or _context()
+    dev, dt, d = device(), types.get(cfg.type), cfg.hidden
+    n = cfg.rows * d
+    st = lib().moe_w4a16_norm(
+        ctypes.byref(cfg), x if x is None else _tptr(x, dt, n, dev), y if y is None else _tptr(y, dt, n, dev),
+        gamma_post if gamma_post is None else _tptr(gamma_post, f32, d, dev),
+        gate if gate is None else _tptr(gate, f32, _gate_elements(cfg), dev),
+        gamma_pre if gamma_pre is None else _tptr(gamma_pre, f32, d, dev),
+        out if out is None else _tptr(out, dt, n, dev), u if u is None else _tptr(u, dt, n, dev),
+        current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_norm")
+
+
+def _gate_elements(cfg: Norm) -> int:
+    return -(-cfg.rows // max(cfg.gate_rows, 1)) * cfg.hidden
+
+
+def moe_w4a16_norm_backward_workspace_bytes(cfg: Norm) -> int:
+    return int(lib().moe_w4a16_norm_backward_workspace_bytes(ctypes.byref(cfg)))
+
+
+def moe_w4a16_norm_backward(cfg: Norm, y, gamma_post, gate, out, gamma_pre, grad_out, grad_u, grad_x, grad_y,
+                            grad_gamma_post, grad_gate, grad_gamma_pre, workspace, stream=None) -> None:
+    types, _, f32, device, current = _CONTEXT or _context()
+    dev, dt, d = device(), types.get(cfg.type), cfg.hidden
+    n, g = cfg.rows * d, _gate_elements(cfg)
+
+    def rows(t):
+        return t if t is None else _tptr(t, dt, n, dev)
+
+    def vec(t, count=d):
+        return t if t is None else _tptr(t, f32, count, dev)
+
+    st = lib().moe_w4a16_norm_backward(
+        ctypes.byref(cfg), rows(y), vec(gamma_post), vec(gate, g), rows(out), vec(gamma_pre), rows(grad_out),
+        rows(grad_u), rows(grad_x), rows(grad_y), vec(grad_gamma_post), vec(grad_gate, g), vec(grad_gamma_pre),
+        workspace if workspace is None else _wptr(workspace, dev), 0 if workspace is None else _nbytes(workspace),
+        current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_norm_backward")
+
+
+class TensorList:
+    """A list of gradients and where their scaled values go, checked once and held for the calls that take it
+    (make_tensors).  It keeps the tensors: their storage must not be replaced (``set_``, ``resize_``) while
+    it is used."""
+
+    def __init__(self, tensors, outs):
+        types = {t: code for code, t in _context()[0].items()}
+        tensors = list(tensors)
+        outs = tensors if outs is None else list(outs)
+        if len(outs) != len(tensors):
+            raise MoeW4A16Error(ERR_SHAPE, f"{len(tensors)} tensors and {len(outs)} outputs")
+        self.tensors, self.outs, self.device = tensors, outs, None
+        self.array = (Tensor * max(len(tensors), 1))()
+        for slot, t, o in zip(self.array, tensors, outs):
+            if t.dtype not in types:
+                raise MoeW4A16Error(ERR_SHAPE, f"fp16, bf16 or fp32 gradients are wanted, got {t.dtype}")
+            if self.device is None:
+                self.device = t.get_device()
+            n = t.numel()
+            slot.data, slot.count, slot.type = _tptr(t, t.dtype, n, self.device) if n else None, n, types[t.dtype]
+            slot.out = _tptr(o, t.dtype, n, self.device) if o is not None and n else None
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def make_tensors(tensors, outs=None) -> TensorList:
+    """outs: where the scaled values go (None: in place; an entry None: the tensor is not scaled)."""
+    return TensorList(tensors, outs)
+
+
+def moe_w4a16_clip_workspace_bytes(tensors) -> int:
+    """Of a list of tensors (any with a length), or of as many tensors."""
+    return int(lib().moe_w4a16_clip_workspace_bytes(tensors if isinstance(tensors, int) else len(tensors)))
+
+
+def moe_w4a16_clip(tensors, max_norm: float, norm, workspace, stream=None) -> None:
+    """tensors: a TensorList, or tensors to be scaled in place.  max_norm may be math.inf: the norm alone."""
+    if not isinstance(tensors, TensorList):
+        tensors = TensorList(tensors, None)
+    _, _, f32, device, current = _CONTEXT or _context()
+    dev = device()
+    if tensors.device is not None and tensors.device != dev:
+        raise MoeW4A16Error(ERR_DEVICE, f"the tensors live on cuda:{tensors.device}, the call runs on cuda:{dev}")
+    st = lib().moe_w4a16_clip(ctypes.addressof(tensors.array), len(tensors), max_norm, _tptr(norm, f32, 1, dev),
+                              _wptr(workspace, dev), _nbytes(workspace),
+                              current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st, "moe_w4a16_clip")
 
 
 def moe_w4a16_read_error(workspace, stream=None) -> int:

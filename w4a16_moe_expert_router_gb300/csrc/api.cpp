@@ -68,7 +68,8 @@ moe_w4a16_status device_state(const DeviceState** out) {
     } else {
       st.num_sms = sms;
       st.status = (moe::init_gemm_kernels() == cudaSuccess && moe::init_block_kernels() == cudaSuccess &&
-                   moe::init_linear_kernels() == cudaSuccess && moe::init_linear_small_kernels() == cudaSuccess)
+                   moe::init_linear_kernels() == cudaSuccess && moe::init_linear_small_kernels() == cudaSuccess &&
+                   moe::init_few_kernels() == cudaSuccess)
                       ? MOE_W4A16_OK
                       : MOE_W4A16_ERR_CUDA;
     }

@@ -1,0 +1,301 @@
+// clip.cu -- the norm over a list of tensors (fp16, bf16, fp32, of any length and alignment), and
+// the tensors scaled down to a bound on it.
+//
+//   norm = sqrt(sum over all tensors of g^2),   out = g min(1, max_norm / norm)
+//
+// Two passes over the data, each bound by memory: the sum of the squares, and the scaling, which is
+// left out where it would change nothing. The tensors are cut into chunks that persistent CTAs
+// take in turn; a launch carries its tensors' addresses as kernel parameters (up to kLarge of
+// them), so nothing is kept on the device from call to call and a captured graph holds its own.
+//
+// Squares are summed in fp32 over the 64 to 128 bytes that a thread takes of a chunk, in fp64 from
+// there on: an fp64 addition per element would be the bound (its rate is a hundredth of fp32's), one
+// per chunk is not seen. Where such a sum leaves the range in which fp32 squares keep their digits,
+// it is taken again in fp64. All orders are fixed: the same bits in every run.
+#include <climits>
+#include <cmath>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "row_vec.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLoads = 8;                              // 16-byte pieces of a chunk per thread
+constexpr int kChunkBytes = kThreads * kLoads * 16;    // 32 KB
+// Tensors per launch: 23 KB of parameters, or 2.3 KB for short lists (the parameters are copied a few
+// times on their way to the device).
+constexpr int kLarge = 640, kSmall = 64;
+constexpr int kCtas = 608;                             // four on each of 152 SMs
+
+struct Entry {
+  const void* data;
+  void* out;       // NULL: the tensor is not scaled
+  int64_t count;   // elements
+  int32_t type;
+  int32_t shift;   // elements between the 16-byte boundary below `data` and `data`
+};
+template <int kTable>
+struct Table {
+  Entry e[kTable];
+  int32_t first[kTable + 1];  // chunks before an entry
+  int32_t n;
+};
+static_assert(sizeof(Table<kLarge>) <= 32000, "kernel parameters");
+// the chunks of a full table fit an int32
+static_assert(kClipMaxCount * 4 / kChunkBytes * kLarge + kLarge < INT32_MAX, "chunk numbers");
+
+template <int kTable>
+__device__ __forceinline__ int find(const Table<kTable>& t, int chunk) {
+  int lo = 0, hi = t.n - 1;  // the last entry with first <= chunk
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= chunk)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Element i of 16 bytes (eight of 16 bits, four of 32).
+template <int kType>
+__device__ __forceinline__ float value(const void* p, int64_t i) {
+  if constexpr (kType == 2) return static_cast<const float*>(p)[i];
+  else return from16<kType>(static_cast<const uint16_t*>(p)[i]);
+}
+template <int kType>
+__device__ __forceinline__ void put(void* p, int64_t i, float v) {
+  if constexpr (kType == 2) static_cast<float*>(p)[i] = v;
+  else static_cast<uint16_t*>(p)[i] = to16<kType>(v);
+}
+
+// Sum of the squares of a thread's share of a chunk: pieces v, v + kThreads, .. counted from the
+// 16-byte boundary below the tensor; the pieces that the tensor fills in part are read by elements.
+template <int kType>
+__device__ double chunk_square(const Entry& e, int chunk) {
+  constexpr int N = Vec<kType>::n;
+  const int64_t v0 = static_cast<int64_t>(chunk) * (kThreads * kLoads) + threadIdx.x;
+  const int64_t end = e.shift + e.count;  // virtual elements: e.shift .. end - 1
+  const auto* aligned = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(e.data) & ~uintptr_t(15));
+  uint4 x[kLoads];
+#pragma unroll
+  for (int l = 0; l < kLoads; ++l) {
+    const int64_t v = v0 + l * kThreads;
+    x[l] = make_uint4(0u, 0u, 0u, 0u);
+    if (v * N >= e.shift && (v + 1) * N <= end) x[l] = aligned[v];
+  }
+  float s = 0.f;
+  uint32_t any = 0u;
+#pragma unroll
+  for (int l = 0; l < kLoads; ++l) {
+    const int64_t v = v0 + l * kThreads;
+    float f[N];
+    if (v * N < end && (v * N < e.shift || (v + 1) * N > end)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int64_t at = v * N + i;
+        f[i] = at >= e.shift && at < end ? value<kType>(e.data, at - e.shift) : 0.f;
+        any |= __float_as_uint(f[i]);
+      }
+    } else {
+      Vec<kType>::load(x[l], f);
+      any |= (x[l].x | x[l].y) | (x[l].z | x[l].w);
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) q = fmaf(f[i], f[i], q);
+    s += q;
+  }
+  // squares below 2^-100 may have lost digits to fp32's smallest step, those above its range are
+  // infinite: an fp64 sum (`any` of signs alone is no reason)
+  if (s >= 0x1p-100f && s <= 0x1p127f) return s;
+  if ((any & (kType == 2 ? 0x7fffffffu : 0x7fff7fffu)) == 0u) return 0.0;
+  double d = 0.0;
+  for (int l = 0; l < kLoads; ++l)
+    for (int i = 0; i < N; ++i) {
+      const int64_t at = (v0 + l * kThreads) * N + i;
+      if (at >= e.shift && at < end) {
+        const double f = value<kType>(e.data, at - e.shift);
+        d = fma(f, f, d);
+      }
+    }
+  return d;
+}
+
+__device__ __forceinline__ double cta_sum(double v) {
+  __shared__ double part[kThreads / 32];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) s += part[w];
+  return s;
+}
+
+template <int kTable>
+__global__ void __launch_bounds__(kThreads)
+    clip_square_kernel(const __grid_constant__ Table<kTable> t, double* partial) {
+  grid_dependents_launch();
+  grid_dependency_wait();
+  double s = 0.0;
+  const int chunks = t.first[t.n];
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = find(t, c);
+    const Entry& e = t.e[i];
+    const int k = c - t.first[i];
+    s += e.type == 0 ? chunk_square<0>(e, k) : e.type == 1 ? chunk_square<1>(e, k) : chunk_square<2>(e, k);
+  }
+  s = cta_sum(s);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// Partial sums of several launches into the first place.
+__global__ void __launch_bounds__(kThreads) clip_total_kernel(double* partial, int n) {
+  grid_dependents_launch();
+  grid_dependency_wait();
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) s += partial[i];
+  s = cta_sum(s);  // its barrier: all have read before the first place is written
+  if (threadIdx.x == 0) partial[0] = s;
+}
+
+template <int kType>
+__device__ void scale_chunk(const Entry& e, int chunk, float factor) {
+  constexpr int N = Vec<kType>::n;
+  const int64_t v0 = static_cast<int64_t>(chunk) * (kThreads * kLoads) + threadIdx.x;
+  const int64_t end = e.shift + e.count;
+  const auto* src = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(e.data) & ~uintptr_t(15));
+  auto* dst = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(e.out) & ~uintptr_t(15));
+  // the output's pieces lie as the input's do, or it is written by elements
+  const bool alike = ((reinterpret_cast<uintptr_t>(e.data) ^ reinterpret_cast<uintptr_t>(e.out)) & 15u) == 0;
+  uint4 x[kLoads];
+#pragma unroll
+  for (int l = 0; l < kLoads; ++l) {
+    const int64_t v = v0 + l * kThreads;
+    if (v * N >= e.shift && (v + 1) * N <= end) x[l] = src[v];
+  }
+#pragma unroll
+  for (int l = 0; l < kLoads; ++l) {
+    const int64_t v = v0 + l * kThreads;
+    if (v * N >= end) continue;
+    if (v * N >= e.shift && (v + 1) * N <= end) {
+      float f[N];
+      Vec<kType>::load(x[l], f);
+      if (factor != 1.f) {  // else the bits are copied, a NaN's too
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] *= factor;
+        x[l] = Vec<kType>::store(f);
+      }
+      if (alike) {
+        dst[v] = x[l];
+      } else {
+        if (factor == 1.f) Vec<kType>::load(x[l], f);
+        for (int i = 0; i < N; ++i) put<kType>(e.out, v * N + i - e.shift, f[i]);
+      }
+    } else {
+      for (int i = 0; i < N; ++i) {
+        const int64_t at = v * N + i;
+        if (at >= e.shift && at < end) put<kType>(e.out, at - e.shift, value<kType>(e.data, at - e.shift) * factor);
+      }
+    }
+  }
+}
+
+// Every CTA adds up the partial sums itself, in the same order. Chunks are taken from the last one
+// back: what the pass before read last is still in L2.
+template <int kTable>
+__global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ Table<kTable> t,
+                                                              const double* partial, int n_partial, double max_norm,
+                                                              float* norm) {
+  grid_dependents_launch();
+  grid_dependency_wait();
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n_partial; i += kThreads) s += partial[i];
+  s = sqrt(cta_sum(s));
+  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(s);
+  // a norm that is no number, or infinite, leaves the values as they are
+  const float factor = s > max_norm && s < INFINITY ? static_cast<float>(max_norm / s) : 1.f;
+  for (int c = t.first[t.n] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+    const int i = find(t, c);
+    const Entry& e = t.e[i];
+    if (!e.out || (factor == 1.f && e.out == e.data)) continue;
+    const int k = c - t.first[i];
+    if (e.type == 0)
+      scale_chunk<0>(e, k, factor);
+    else if (e.type == 1)
+      scale_chunk<1>(e, k, factor);
+    else
+      scale_chunk<2>(e, k, factor);
+  }
+}
+
+// The next tensors of a list, up to kTable; returns how many it took.
+template <int kTable>
+int fill(Table<kTable>& t, const moe_w4a16_tensor* tensors, int n) {
+  int taken = 0;
+  t.n = 0;
+  t.first[0] = 0;
+  for (; taken < n && t.n < kTable; ++taken) {
+    const moe_w4a16_tensor& in = tensors[taken];
+    if (in.count == 0) continue;
+    const int size = in.type == 2 ? 4 : 2;
+    const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(in.data) & 15u) / size);
+    const int64_t per = kChunkBytes / size;
+    t.e[t.n] = Entry{in.data, in.out, in.count, in.type, shift};
+    t.first[t.n + 1] = t.first[t.n] + static_cast<int32_t>((in.count + shift + per - 1) / per);
+    ++t.n;
+  }
+  return taken;
+}
+
+int ctas_of(int chunks) { return chunks < 1 ? 1 : chunks < kCtas ? chunks : kCtas; }
+
+template <int kTable>
+cudaError_t run(const moe_w4a16_tensor* tensors, int n, double max_norm, float* norm, double* partial, cudaStream_t st) {
+  static thread_local Table<kTable> t;
+  cudaError_t err = cudaSuccess;
+  int sums = 0, launches = 0;
+  for (int at = 0; at < n || launches == 0; ++launches) {
+    at += fill(t, tensors + at, n - at);
+    const int ctas = ctas_of(t.first[t.n]);
+    if ((err = launch_pdl(clip_square_kernel<kTable>, dim3(ctas), dim3(kThreads), 0, st, t, partial + sums)) !=
+        cudaSuccess)
+      return err;
+    sums += ctas;
+  }
+  if (launches > 1) {
+    if ((err = launch_pdl(clip_total_kernel, dim3(1), dim3(kThreads), 0, st, partial, sums)) != cudaSuccess) return err;
+    sums = 1;
+  }
+  for (int at = 0, i = 0; i < launches; ++i) {
+    if (launches > 1) at += fill(t, tensors + at, n - at);
+    bool scaled = false;  // whether a value may have to be written
+    for (int j = 0; j < t.n; ++j) scaled |= t.e[j].out && (max_norm < INFINITY || t.e[j].out != t.e[j].data);
+    if (i > 0 && !scaled) continue;
+    if ((err = launch_pdl(clip_scale_kernel<kTable>, dim3(scaled ? ctas_of(t.first[t.n]) : 1), dim3(kThreads), 0, st, t,
+                          static_cast<const double*>(partial), sums, max_norm, i == 0 ? norm : nullptr)) != cudaSuccess)
+      return err;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t clip_ws_bytes(int n) {
+  const size_t launches = n <= kLarge ? 1 : (n + kLarge - 1) / kLarge;
+  return launches * kCtas * sizeof(double);
+}
+
+cudaError_t launch_clip(const moe_w4a16_tensor* tensors, int n, double max_norm, float* norm, void* workspace,
+                        cudaStream_t st) {
+  auto* const partial = static_cast<double*>(workspace);
+  return n <= kSmall ? run<kSmall>(tensors, n, max_norm, norm, partial, st)
+                     : run<kLarge>(tensors, n, max_norm, norm, partial, st);
+}
+
+}  // namespace moe

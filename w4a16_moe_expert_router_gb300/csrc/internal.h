@@ -227,6 +227,36 @@ cudaError_t launch_linear_dz(const LinearDims& s, const int32_t* offsets, const 
 cudaError_t launch_linear_dbias(const LinearDims& s, const int32_t* offsets, const float* partial, float* dbias,
                                 cudaStream_t st);
 
+// The norms around a block and their gradient (norm.cu).
+constexpr int kNormCtas = 304;  // CTAs of the gradient at most: two on each of 152 SMs
+struct NormDims {
+  int R, d, type, gate_rows;  // type: 0 fp16, 1 bf16, 2 fp32
+  float scale, eps;
+  int nvec() const { return type == 2 ? d / 4 : d / 8; }
+};
+cudaError_t launch_norm(const NormDims& s, const void* x, const void* y, const float* gamma_post, const float* gate,
+                        const float* gamma_pre, void* out, void* u, cudaStream_t st);
+size_t norm_backward_ws_bytes(const NormDims& s);
+cudaError_t launch_norm_backward(const NormDims& s, const void* y, const float* gamma_post, const float* gate,
+                                 const void* out, const float* gamma_pre, const void* dout, const void* du, void* dx,
+                                 void* dy, float* dgamma_post, float* dgate, float* dgamma_pre, void* workspace,
+                                 cudaStream_t st);
+
+// The norm of a list of tensors and their scaling to a bound (clip.cu).
+constexpr int kClipMaxTensors = 1 << 16;
+constexpr int64_t kClipMaxCount = int64_t(1) << 34;  // elements of one tensor
+size_t clip_ws_bytes(int n);
+cudaError_t launch_clip(const moe_w4a16_tensor* tensors, int n, double max_norm, float* norm, void* workspace,
+                        cudaStream_t st);
+
+// The whole layer for a few tokens (few.cu).
+constexpr int kFewTokens = 32;
+size_t few_ws_bytes(const Dims& s);
+cudaError_t init_few_kernels();
+cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logits, const uint8_t* w_gate_up,
+                       const uint8_t* w_down, const void* residual, int32_t* topk_idx, float* topk_w, void* out,
+                       void* workspace, int num_sms, cudaStream_t st);
+
 // The current device's state: MOE_W4A16_OK with its SM count, or why it cannot be used.
 moe_w4a16_status current_device(int* num_sms);
 
