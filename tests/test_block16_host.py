@@ -52,7 +52,9 @@ def test_few_arguments_refused():
     for n in ("x", "logits", "gate_up", "down", "res", "idx", "w", "out", "ws"):
         assert _few(**{n: P + 8}) == B.ERR_ALIGN, n
     need = B.moe_w4a16_few_workspace_bytes(B.make_shape(**FEW))
-    assert need == 4 * 2 * 2 * 128 * 2  # pairs x (hi, lo) x f, 16 bits each
+    pair = 2 * 128 * 2 + 128 // 8 * 4  # (hi, lo) x f in 16 bits, sums of eight columns
+    more = B.moe_w4a16_few_workspace_bytes(B.make_shape(**{**FEW, "tokens": 5}))
+    assert more - need == 2 * pair and need > 4 * 2 * pair  # and the lists
     assert _few(ws_bytes=need - 1) == B.ERR_WORKSPACE
     none = {n: None for n in ("x", "logits", "gate_up", "down", "res", "idx", "w", "out", "ws")}
     assert _few(cfg=dict(tokens=0), **none) == B.OK

@@ -515,8 +515,10 @@ def moe_w4a16_few(shape: Shape, type: int, x, logits, gate_up, down, residual, t
     dev, dt, T, k = device(), types.get(type), shape.tokens, shape.top_k
     n = T * shape.hidden
     w = Weights(_wptr(gate_up, dev), _wptr(down, dev))
-    if _nbytes(gate_up) != moe_w4a16_prepared_bytes(shape, GATE_UP) or \
-            _nbytes(down) != moe_w4a16_prepared_bytes(shape, DOWN):
+    cells = shape.experts * shape.hidden * shape.inter  # codes of half a byte, 4 bytes per group of them
+    if shape.group_gate_up <= 0 or shape.group_down <= 0 or \
+            _nbytes(gate_up) != cells + 8 * (cells // shape.group_gate_up) or \
+            _nbytes(down) != cells // 2 + 4 * (cells // shape.group_down):
         raise MoeW4A16Error(ERR_SHAPE, "moe_w4a16_few: the prepared weights' sizes do not match the shape")
     st = lib().moe_w4a16_few(
         ctypes.byref(shape), type, _tptr(x, dt, n, dev), _tptr(logits, f32, T * shape.experts, dev), ctypes.byref(w),

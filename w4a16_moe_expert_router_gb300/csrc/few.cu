@@ -9,35 +9,37 @@
 //  - every CTA forms the routing itself (a warp per token), instead of a launch for it;
 //  - the down launch starts while the gate_up launch runs, forms the routing too and requests its
 //    first weights before it waits for h;
-//  - work is cut finely: 16 (8 gate and 8 up, twice) rows of weights by one CTA, whose warps share
-//    the contraction; each warp streams its own stages with cp.async, several ahead, also across
-//    work items, and needs no other warp until the item's sums meet in shared memory.
+//  - the contraction is shared by the warps of a CTA (gate_up) or by the CTAs of a cluster (down);
+//    each warp streams its own stages with cp.async, several ahead, also across work items.
 //
 // The weights stay integers: a group's codes are multiplied as they are (exact products in the fp32
 // accumulators), then scale and zero-point are applied to the group's sum,
-//   sum_k w_k x_k = s sum_k q_k x_k + c sum_k x_k,   c = -s z (affine: the bias),
-// the sum of x coming from one more matrix instruction with ones. h is kept as two 16-bit values, h =
-// hi + lo, which take two columns of one instruction (four tokens per instruction, not eight): 22 bits
-// of h for fp16, 16 for bf16. A warp multiplies its stages in ascending order, the warps' sums
-// meet in their order, and a token's experts are added in ascending order within each half of them
-// (even and odd numbers): the result does not depend on the other tokens and is the same in every run.
+//   sum_k w_k x_k = s sum_k q_k x_k + c sum_k x_k,   c = -s z (affine: the bias).
+// The sums of x come from one more matrix instruction with ones for two or four strips, the sums of h
+// from the gate_up launch. h is kept as two 16-bit values, h = hi + lo, which take two columns of
+// one instruction (four tokens per instruction, not eight): 22 bits of h for fp16, 16 for bf16. Every
+// sum has an order of its own (stages, then warps or CTAs in their order; a token's experts
+// ascending by their number modulo four), so the result does not depend on the other
+// tokens and is the same in every run.
+#include <algorithm>
+
 #include "activation.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "row_vec.cuh"
+#include "tcgen05.cuh"
 #include "topk.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxPairs16 = kFewTokens * kMaxTopK;  // pairs at most, and items
-static_assert(kMaxPairs16 <= kThreads && kMaxExperts <= kThreads, "a thread per pair and per expert");
-constexpr int kUpTokens = 8, kDownTokens = 4;       // tokens of an item
-constexpr int kDepth = 4;                           // pieces of a warp in flight
-constexpr int kXRow = kStageCols * 2 + 16;          // bytes of a token's stage in shared memory: rows shifted by a bank group
-constexpr int kHBytes = 2048;                       // a stage's h fragments: 4 tokens x (hi, lo) x 128 columns
-constexpr int kRedStride = 33;
+constexpr int kMaxItems = kFewTokens * kMaxTopK;  // as many as pairs
+constexpr int kItemTokens = 4;                    // tokens of an item
+constexpr int kUpThreads = 512, kUpWarps = kUpThreads / 32;
+constexpr int kSets = 4;                          // down: warps per pair of strips, each for every fourth expert
+constexpr int kDownMaxPairs = 4;                  // down: pairs of strips of a CTA
+constexpr int kPairBytes = 512;                   // a pair's h of one stage: (hi, lo) x 128 columns
+constexpr int kAccRow = 33;                       // down: a token's 32 sums of a warp, and one word between tokens
 
 struct Args {
   const void* x;
@@ -48,72 +50,158 @@ struct Args {
   float* topk_w;
   void* out;
   uint16_t* h;            // [pairs][2][f], in the order of the down launch's fragments
+  float* hsum;            // [pairs][f / 8]: sums of eight columns of h, in the partial sums' units
+  void* routing;          // the lists, for a down launch that does not form them
+  int listed;
   int T, d, f, E, k, act, affine;
   int K;                  // contraction: d or f
-  int64_t expert_bytes, block_bytes;
-  int stage_warps;        // warps that share an item's contraction
-  int slot_bytes;         // a piece in shared memory
+  uint32_t expert16;      // 16-byte pieces of an expert's weights
+  uint32_t block16;       // and of a block of 128 rows
+  int stage_warps;        // gate_up: warps that share an item's contraction
+  int per_item;           // gate_up: units of an item
+  float per_item_inv;
+  int step_items, step_rest;  // and how far gridDim.x units are
+  int strips, cluster;    // down: strips of a CTA, CTAs that share the contraction
+  int depth;              // pieces of a warp in its ring
 };
 
-// Routing and items, formed by every CTA.
-template <int kTokens>
-struct Routing {
-  int32_t sel[kMaxPairs16];
-  int32_t spare[kMaxPairs16];
-  float w[kMaxPairs16];
-  uint32_t mask[kMaxExperts];          // tokens of an expert
-  int32_t base[kMaxExperts];           // first item of an expert
-  int32_t expert[kMaxPairs16];         // expert of an item
-  int16_t pair[kMaxPairs16][kTokens];  // pairs of an item, -1 behind them
-  int32_t warp_tot[kWarps];
-  int32_t items, half;                 // items; those of even experts (split lists)
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Routing and items, formed by every CTA. One token needs little time for anything but this, and code
+// that runs once waits for its instructions: the loops here and below are kept rolled on purpose (the choice
+// of one token took 3.0 us unrolled over its eight rounds).
+struct alignas(16) Routing {
+  int32_t sel[kMaxItems];
+  float w[kMaxItems];                     // a pair's value, then its weight
+  uint32_t mask[kMaxExperts];             // tokens of an expert
+  int32_t base[kMaxExperts];              // first item of an expert
+  int16_t pair[kMaxItems][kItemTokens];   // pairs of an item and their tokens; pair and token 0 behind them
+  uint8_t token[kMaxItems][kItemTokens];
+  uint8_t expert[kMaxItems];              // expert of an item
+  uint8_t count[kMaxItems];               // its tokens
+  int32_t first[kSets + 1];               // first item of a set of experts, and the end
 };
 
-// Lists the items by expert ascending; kSplit: those of the even experts first.
-template <int kTokens, bool kSplit>
-__device__ __forceinline__ void form_routing(Routing<kTokens>& r, const Args& a) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  r.mask[tid] = 0u;
-  for (int i = tid; i < kMaxPairs16 * kTokens; i += kThreads) (&r.pair[0][0])[i] = -1;
-  for (int t = warp; t < a.T; t += kWarps) {
-    const float* row = a.logits + static_cast<size_t>(t) * a.E;
+// The choice of one token by one warp, as topk_softmax_warp makes it: the largest logits, ties to the
+// lower expert, and their softmax summed in rank order. Lane l holds experts l + 32 j.
+template <int NS>
+__device__ __forceinline__ void choose(const float* row, int E, int k, int lane, int32_t* sel, float* w) {
+  uint32_t key[NS];
+#pragma unroll
+  for (int j = 0; j < NS; ++j) key[j] = lane + 32 * j < E ? order_key(__ldcg(row + lane + 32 * j)) : 0u;
+#pragma unroll 1
+  for (int r = 0; r < k; ++r) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int j = 1; j < NS; ++j) best = max(best, key[j]);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const unsigned tied = __ballot_sync(0xffffffffu, best == top);
+    int first = 0;  // the lane's first expert of that key
+#pragma unroll
+    for (int j = NS - 1; j >= 0; --j)
+      if (key[j] == top) first = j;
+    const int e = lane + 32 * first;
+    int winner = __ffs(tied) - 1;
+    if (tied & (tied - 1u))
+      winner = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(e) : ~0u) & 31u);
+    if (lane == winner) {
+      sel[r] = e;
+      w[r] = __uint_as_float((top & 0x80000000u) ? top ^ 0x80000000u : ~top);
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+        if (j == first) key[j] = 0u;
+    }
+  }
+  __syncwarp();
+  const float v = lane < k ? expf(w[lane] - w[0]) : 0.f;
+  __syncwarp();
+  if (lane < k) w[lane] = v;
+  __syncwarp();
+  float den = 0.f;
+#pragma unroll
+  for (int r = 0; r < kMaxTopK; ++r)
+    if (r < k) den += w[r];
+  __syncwarp();
+  if (lane < k) w[lane] = v / den;
+}
+
+// Lists the items by expert modulo kSets, then by expert ascending. Ends with a barrier.
+__device__ __forceinline__ void form_routing(Routing& r, const Args& a) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x, pairs = a.T * a.k;
+#pragma unroll 1
+  for (int i = tid; i < kMaxExperts; i += n) r.mask[i] = 0u;
+#pragma unroll 1
+  for (int i = tid; i < pairs; i += n) {
+    reinterpret_cast<uint2*>(r.pair)[i] = make_uint2(0u, 0u);
+    reinterpret_cast<uint32_t*>(r.token)[i] = 0u;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int t = warp; t < a.T; t += n >> 5) {
+    const float* const row = a.logits + static_cast<size_t>(t) * a.E;
     if (a.E <= 128)
-      topk_softmax_warp<4>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k, r.spare + t * a.k);
+      choose<4>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k);
     else
-      topk_softmax_warp<8>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k, r.spare + t * a.k);
+      choose<8>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k);
+    if (lane < a.k) atomicOr(&r.mask[r.sel[t * a.k + lane]], 1u << t);
   }
   __syncthreads();
-  const int t = tid / a.k, e = tid < a.T * a.k ? r.sel[tid] : 0;
-  if (tid < a.T * a.k) atomicOr(&r.mask[e], 1u << t);
-  __syncthreads();
-  // thread i takes expert i, or with kSplit the i-th of the evens followed by the odds
-  const int evens = (a.E + 1) / 2;
-  const int mine = !kSplit ? tid : tid < evens ? 2 * tid : 2 * (tid - evens) + 1;
-  const int n = tid < a.E ? (__popc(r.mask[mine]) + kTokens - 1) / kTokens : 0;
-  int incl = n;
+  // every warp forms the same list. Lane l takes the experts 4 l + s of set s, and 128 on; the counts of two
+  // sets at a time go through the scan in the halves of a word
+  static_assert(kSets == 4, "two words of two sets");
+  const int rounds = a.E > 128 ? 2 : 1;
+  int own[2][kSets], before[2][kSets], total[kSets] = {};
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += o;
-  }
-  if (lane == 31) r.warp_tot[warp] = incl;
-  __syncthreads();
-  int before = 0, total = 0;
+  for (int half = 0; half < 2; ++half) {
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    before += w < warp ? r.warp_tot[w] : 0;
-    total += r.warp_tot[w];
+    for (int s = 0; s < kSets; ++s) {
+      const int e = 128 * half + 4 * lane + s;
+      own[half][s] = e < a.E ? (__popc(r.mask[e]) + kItemTokens - 1) / kItemTokens : 0;
+    }
+    if (half < rounds) {
+      uint32_t v[2] = {static_cast<uint32_t>(own[half][0] | own[half][1] << 16),
+                       static_cast<uint32_t>(own[half][2] | own[half][3] << 16)};
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, v[i], off);
+          if (lane >= off) v[i] += o;
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t sum = __shfl_sync(0xffffffffu, v[i], 31);
+        before[half][2 * i] = total[2 * i] + static_cast<int>(v[i] & 0xffffu) - own[half][2 * i];
+        before[half][2 * i + 1] = total[2 * i + 1] + static_cast<int>(v[i] >> 16) - own[half][2 * i + 1];
+        total[2 * i] += sum & 0xffffu;
+        total[2 * i + 1] += sum >> 16;
+      }
+    }
   }
-  if (tid < a.E) {
-    r.base[mine] = before + incl - n;
-    if (tid == evens - 1) r.half = before + incl;
+  int first = 0;
+#pragma unroll
+  for (int s = 0; s < kSets; ++s) {
+    if (lane == 0) r.first[s] = first;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int e = 128 * half + 4 * lane + s;
+      if (half < rounds && e < a.E) r.base[e] = first + before[half][s];
+    }
+    first += total[s];
   }
-  if (tid == 0) r.items = total;
-  __syncthreads();
-  if (tid < a.T * a.k) {
-    const int nth = __popc(r.mask[e] & ((1u << t) - 1u)), item = r.base[e] + nth / kTokens;
-    r.pair[item][nth % kTokens] = static_cast<int16_t>(tid);
-    if (nth % kTokens == 0) r.expert[item] = e;
+  if (lane == 0) r.first[kSets] = first;
+  __syncwarp();
+#pragma unroll 1
+  for (int p = tid; p < pairs; p += n) {
+    const int t = p / a.k, e = r.sel[p];
+    const uint32_t m = r.mask[e];
+    const int nth = __popc(m & ((1u << t) - 1u)), item = r.base[e] + nth / kItemTokens;
+    r.pair[item][nth % kItemTokens] = static_cast<int16_t>(p);
+    r.token[item][nth % kItemTokens] = static_cast<uint8_t>(t);
+    if (nth % kItemTokens == 0) {
+      r.expert[item] = static_cast<uint8_t>(e);
+      r.count[item] = static_cast<uint8_t>(min(__popc(m) - nth, kItemTokens));
+    }
   }
   __syncthreads();
 }
@@ -147,20 +235,23 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
   else
     mma_f16_16816(d, a, b0, b1);
 }
+// Totals and the sums of x and h are kept in the units of rows g's partial sums.
 template <bool kBf16>
-constexpr uint32_t kOnes = kBf16 ? 0x3f803f80u : 0x3c003c00u;
+constexpr float kUnit = kBf16 ? 1.f : 0x1p-24f;
+template <bool kBf16>
+constexpr uint32_t kOne = kBf16 ? 0x3f803f80u : 0x00010001u;  // two of them
 
 // A group's sums into the totals: tot += s part + c sum, for rows g (first two) and g + 8.
 template <bool kBf16>
-__device__ __forceinline__ void apply_group(float (&tot)[4], const float (&part)[4], const float (&sum)[4], uint2 sz,
+__device__ __forceinline__ void apply_group(float (&tot)[4], const float (&part)[4], float sum0, float sum1, uint2 sz,
                                             int affine) {
   const float2 lo = __half22float2(bits_h2(sz.x)), hi = __half22float2(bits_h2(sz.y));
-  const float s_lo = kBf16 ? lo.x : lo.x * 0x1p24f, s_hi = kBf16 ? hi.x : hi.x * 0x1p20f;
+  const float s_hi = kBf16 ? hi.x : hi.x * 0.0625f;
   const float c_lo = affine ? lo.y : -lo.x * lo.y, c_hi = affine ? hi.y : -hi.x * hi.y;
-  tot[0] = fmaf(s_lo, part[0], fmaf(c_lo, sum[0], tot[0]));
-  tot[1] = fmaf(s_lo, part[1], fmaf(c_lo, sum[1], tot[1]));
-  tot[2] = fmaf(s_hi, part[2], fmaf(c_hi, sum[2], tot[2]));
-  tot[3] = fmaf(s_hi, part[3], fmaf(c_hi, sum[3], tot[3]));
+  tot[0] = fmaf(lo.x, part[0], fmaf(c_lo, sum0, tot[0]));
+  tot[1] = fmaf(lo.x, part[1], fmaf(c_lo, sum1, tot[1]));
+  tot[2] = fmaf(s_hi, part[2], fmaf(c_hi, sum0, tot[2]));
+  tot[3] = fmaf(s_hi, part[3], fmaf(c_hi, sum1, tot[3]));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -173,10 +264,48 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
 
-// The warp copies `bytes` (a multiple of 16) to its slot.
-__device__ __forceinline__ void copy_warp(uint32_t dst, const uint8_t* src, int bytes, int lane) {
-  for (int i = lane * 16; i < bytes; i += 512) cp_async_16(dst + i, src + i);
+// The warp copies kBytes (a multiple of 16) to its slot.
+template <int kBytes>
+__device__ __forceinline__ void copy_warp(uint32_t dst, const uint8_t* src, int lane) {
+#pragma unroll
+  for (int i = 0; i < kBytes; i += 512)
+    if (i + 512 <= kBytes || lane * 16 < kBytes - i) cp_async_16(dst + i + lane * 16, src + i + lane * 16);
+}
+// Waits until at most depth - 1 of the thread's groups of copies are pending: the oldest piece is there.
+constexpr int kMaxDepth = 4;
+__device__ __forceinline__ void wait_piece(int depth) {
+  if (depth == 4)
+    cp_async_wait<3>();
+  else if (depth == 3)
+    cp_async_wait<2>();
+  else
+    cp_async_wait<1>();
+}
+
+// A stage of KK steps of one strip: b holds the other operand's fragments.
+template <bool kBf16, int G, int KK>
+__device__ __forceinline__ void strip_stage(float (&tot)[4], uint32_t at, const uint32_t (&b)[KK][2],
+                                            const float (&sum)[KK * 16 / G][2], int lane, int affine) {
+  constexpr int NG = KK * 16 / G, kSteps = KK / NG;
+  uint4 word[KK / 4];
+#pragma unroll
+  for (int v = 0; v < KK / 4; ++v) word[v] = lds128(at + 64 * NG + v * 512 + lane * 16);
+#pragma unroll
+  for (int j = 0; j < NG; ++j) {
+    float part[4] = {};
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int kk = j * kSteps + q;
+      uint32_t af[4];
+      codes<kBf16>(word_of(word[kk / 4], kk % 4), af);
+      mma<kBf16>(part, af, b[kk][0], b[kk][1]);
+    }
+    apply_group<kBf16>(tot, part, sum[j][0], sum[j][1], lds64(at + (lane >> 2) * (8 * NG) + j * 8), affine);
+  }
 }
 
 // The place of column c (0..63 of 64) in h's fragment order: [tq][step][value], value
@@ -188,252 +317,358 @@ __device__ __forceinline__ int h_place(int c) {
 
 // ------------------------------------------------------------------ gate_up
 //
-// A unit is an item and kWarps / stage_warps pairs of strips; warp w takes pair w / stage_warps
-// and the stages w % stage_warps, + stage_warps, ..
-template <bool kBf16, int G>
-__global__ void __launch_bounds__(kThreads) few_gate_up_kernel(const Args a) {
-  constexpr int NG = kStageCols / G, kSteps = G / 16, kStripBytes = 1024 + 64 * NG;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Routing<kUpTokens> r;
-  __shared__ float red[2][kWarps][2][4][kRedStride];
+// A unit is an item and kPairs x kUpWarps / stage_warps pairs of strips (16 gate and 16 up rows each);
+// warp w takes kPairs pairs, w / stage_warps of them, and the stages w % stage_warps, + stage_warps, ..
+// The fragments of x come from L1.
+template <bool kBf16, int G, int kPairs>
+__global__ void __launch_bounds__(kUpThreads) few_gate_up_kernel(const Args a) {
+  constexpr int NG = kStageCols / G, kStripBytes = 1024 + 64 * NG, kSlot = 2 * kPairs * kStripBytes;
+  constexpr int kType = kBf16 ? 1 : 0, kStrips = 2 * kPairs;
+  // words of a warp's sums: [strip][value][token / 2][row], shifted by eight banks from warp to warp
+  constexpr int kRedWarp = kStrips * 4 * 16 + 8;
+  extern __shared__ __align__(16) uint8_t smem[];  // rings
+  __shared__ Routing r;
+  __shared__ float red[kUpWarps * kRedWarp];
+  // the way to the logits and x (their pages' addresses) is found while the launch before runs
+  for (int i = threadIdx.x; i * 32 < a.T * a.E; i += kUpThreads) prefetch_l2(a.logits + i * 32);
+  for (int i = threadIdx.x; i * 64 < a.T * a.d; i += kUpThreads) prefetch_l2(static_cast<const uint16_t*>(a.x) + i * 64);
   grid_dependency_wait();    // the logits, x, and h, which the call before may still read
   grid_dependents_launch();  // only now: the down launch reads logits and weights before it waits
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  form_routing<kUpTokens, false>(r, a);
-  if (blockIdx.x == 0)
-    for (int i = tid; i < a.T * a.k; i += kThreads) {
-      if (a.topk_idx) a.topk_idx[i] = r.sel[i];
-      if (a.topk_w) a.topk_w[i] = r.w[i];
-    }
-  const int W = a.stage_warps, P = kWarps / W, my_pair = warp / W, my_stage = warp % W;
-  const int S = a.K / kStageCols, per_item = a.f / 16 / P, units = r.items * per_item;
-  const uint32_t ring = smem_addr(smem) + warp * kDepth * a.slot_bytes;
-  const int xrows = min(a.T, kUpTokens);
+  const int S = a.K / kStageCols;
+  const uint32_t ring = smem_addr(smem) + warp * a.depth * kSlot;
+  const auto* const x = static_cast<const uint32_t*>(a.x);
+  form_routing(r, a);
+  const int items = r.first[kSets], W = a.stage_warps, my_pair = warp / W, my_stage = warp & (W - 1);
 
-  int pu = blockIdx.x, ps = my_stage, pslot = 0;  // the piece to request next
-  const auto request = [&] {
-    if (pu < units && ps < S) {
-      const int item = pu / per_item, pr = (pu - item * per_item) * P + my_pair;
-      const uint32_t dst = ring + pslot * a.slot_bytes;
-      const uint8_t* src = a.w + r.expert[item] * a.expert_bytes + (pr >> 2) * a.block_bytes +
-                           static_cast<int64_t>(ps) * (8 * kStripBytes) + (pr & 3) * (2 * kStripBytes);
-      copy_warp(dst, src, 2 * kStripBytes, lane);
-      for (int i = lane; i < xrows * 16; i += 32) {
-        const int p = r.pair[item][i >> 4];
-        if (p >= 0)
-          cp_async_16(dst + 2 * kStripBytes + (i >> 4) * kXRow + (i & 15) * 16,
-                      static_cast<const uint8_t*>(a.x) +
-                          (static_cast<size_t>(p / a.k) * a.d + ps * kStageCols) * 2 + (i & 15) * 16);
-      }
+  // the piece to request next
+  int pi = static_cast<int>((blockIdx.x + 0.5f) * a.per_item_inv), pg = blockIdx.x - pi * a.per_item;  // exact: below 2^12
+  int ps = my_stage, pslot = 0;
+  int item = pi, group = pg, slot = 0, ahead = a.depth - 1;
+  const uint32_t warp_pair = my_pair * kPairs, unit_pairs = kPairs * (kUpWarps / W);
+  float tot[kStrips][4];
+#pragma unroll
+  for (int h = 0; h < kStrips; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tot[h][i] = 0.f;
+  int s = my_stage;
+  bool first_piece = true;
+#pragma unroll 1
+  while (true) {
+    if (pi < items && ps < S) {
+      const uint32_t pair = pg * unit_pairs + warp_pair;
+      const uint32_t off = r.expert[pi] * a.expert16 + (pair >> 2) * a.block16 +
+                           static_cast<uint32_t>(ps) * (8 * kStripBytes / 16) + (pair & 3) * (2 * kStripBytes / 16);
+      copy_warp<kSlot>(ring + pslot * kSlot, a.w + static_cast<size_t>(off) * 16, lane);
       ps += W;
       if (ps >= S) {
         ps = my_stage;
-        pu += gridDim.x;
+        pi += a.step_items;
+        pg += a.step_rest;
+        if (pg >= a.per_item) {
+          pg -= a.per_item;
+          ++pi;
+        }
       }
-      if (++pslot == kDepth) pslot = 0;
+      if (++pslot == a.depth) pslot = 0;
     }
     cp_async_commit();
-  };
-  for (int i = 0; i < kDepth - 1; ++i) request();
-  // fragment of step kk: rows of eight tokens (those behind the last one repeat it; their columns are not used)
-  const uint32_t xoff = 2 * kStripBytes + min(lane & 7, xrows - 1) * kXRow + (lane >> 3) * 16;
-  int slot = 0, buf = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    float tot[2][4] = {};
-    for (int s = my_stage; s < S; s += W) {
-      cp_async_wait<kDepth - 2>();
-      __syncwarp();
-      request();
-      const uint32_t at = ring + slot * a.slot_bytes;
+    if (ahead > 0) {
+      --ahead;
+      continue;
+    }
+    if (first_piece) {  // what others want of the routing, while the first pieces arrive
+      first_piece = false;
+      if (blockIdx.x == 0)
+#pragma unroll 1
+        for (int i = tid; i < a.T * a.k; i += kUpThreads) {
+          if (a.topk_idx) a.topk_idx[i] = r.sel[i];
+          if (a.topk_w) a.topk_w[i] = r.w[i];
+        }
+      if (a.listed && blockIdx.x == gridDim.x - 1)
+#pragma unroll 1
+        for (int i = tid; i < static_cast<int>(sizeof(Routing) / 16); i += kUpThreads)
+          reinterpret_cast<uint4*>(a.routing)[i] = reinterpret_cast<const uint4*>(&r)[i];
+    }
+    if (item >= items) break;
+    if (s < S) {  // (a warp without a stage takes part in the sums alone)
+      uint32_t b[8][2];
+      const bool on = (lane >> 2) < r.count[item];  // columns behind the item's tokens are not used
+      const uint32_t* const row =
+          x + static_cast<size_t>(r.token[item][(lane >> 2) & 3]) * (a.d / 2) + s * 64 + (lane & 3);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) b[kk][v] = on ? row[kk * 8 + v * 4] : 0u;
+      // the sums of x over the groups: a product with ones (in the units of the codes)
+      const uint32_t ones[4] = {kOne<kBf16>, kOne<kBf16>, kOne<kBf16>, kOne<kBf16>};
+      float sum[NG][2];
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
-        float part[2][4] = {}, sum[4] = {};
+        float part[4] = {};
 #pragma unroll
-        for (int q = 0; q < kSteps; q += 2) {
-          const int kk = j * kSteps + q;  // even
-          uint32_t b[4];
-          ldmatrix_x4(at + xoff + kk * 32, b[0], b[1], b[2], b[3]);
-          uint2 word[2];
+        for (int q = 0; q < 8 / NG; ++q) mma<kBf16>(part, ones, b[j * (8 / NG) + q][0], b[j * (8 / NG) + q][1]);
+        sum[j][0] = part[0];
+        sum[j][1] = part[1];
+      }
+      wait_piece(a.depth);
+      __syncwarp();
+      const uint32_t at = ring + slot * kSlot;
+#pragma unroll kPairs == 1 ? 1 : kStrips
+      for (int h = 0; h < kStrips; ++h) {
+        float t[4] = {};
+        strip_stage<kBf16, G, 8>(t, at + h * kStripBytes, b, sum, lane, a.affine);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            word[h] = lds64(at + h * kStripBytes + 64 * NG + (kk / 4) * 512 + lane * 16 + (kk % 4) * 4);
+        for (int g = 0; g < kStrips; ++g)
+          if (g == h)
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const uint32_t ones[4] = {kOnes<kBf16>, kOnes<kBf16>, kOnes<kBf16>, kOnes<kBf16>};
-            mma<kBf16>(sum, ones, b[2 * v], b[2 * v + 1]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t af[4];
-              codes<kBf16>(v ? word[h].y : word[h].x, af);
-              mma<kBf16>(part[h], af, b[2 * v], b[2 * v + 1]);
-            }
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          apply_group<kBf16>(tot[h], part[h], sum, lds64(at + h * kStripBytes + (lane >> 2) * (8 * NG) + j * 8),
-                             a.affine);
+            for (int i = 0; i < 4; ++i) tot[g][i] += t[i];
       }
       __syncwarp();  // the slot is read before it is requested again
-      if (++slot == kDepth) slot = 0;
+      if (++slot == a.depth) slot = 0;
+      s += W;
+      if (s < S) continue;
     }
+    __syncthreads();  // the unit before has been finished
+    if ((lane & 3) < 2)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kStrips; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[buf][warp][h][i][lane] = tot[h][i];
+        for (int i = 0; i < 4; ++i)
+          red[warp * kRedWarp + (h * 4 + i) * 16 + (lane & 3) * 8 + (lane >> 2)] = tot[h][i];
     __syncthreads();
-    // h of strip row j (8 of a strip) and token n: the warps' sums of its gate and up row in order
-    const int item = u / per_item, pr0 = (u - item * per_item) * P;
-    for (int o = tid; o < P * 128; o += kThreads) {
-      const int n = o & 7, j = (o >> 3) & 7, h = (o >> 6) & 1, pr = o >> 7;
-      const int p = r.pair[item][n];
-      if (p < 0) continue;
-      float gate = 0.f, up = 0.f;
-      for (int w = pr * W; w < (pr + 1) * W; ++w) {
-        gate += red[buf][w][h][n & 1][j * 4 + (n >> 1)];
-        up += red[buf][w][h][2 + (n & 1)][j * 4 + (n >> 1)];
+    // h of token n and column c: four threads add the sums of every fourth warp
+    constexpr int kToken = 64 * kPairs;  // threads of a token
+    const int n = tid / kToken, c = (tid % kToken) >> 2, q = tid & 3;
+    if (n < r.count[item])  // whole warps (and n < 4)
+#pragma unroll 1
+      for (int m = 0; m < kUpWarps / W; ++m) {
+        float gate = 0.f, up = 0.f;
+#pragma unroll 1
+        for (int w = m * W + q; w < (m + 1) * W; w += 4) {
+          const float* const p = red + w * kRedWarp + ((c >> 3) * 4 + (n & 1)) * 16 + (n >> 1) * 8 + (c & 7);
+          gate += p[0];
+          up += p[32];
+        }
+#pragma unroll
+        for (int off = 1; off < 4; off <<= 1) {
+          gate += __shfl_xor_sync(0xffffffffu, gate, off);
+          up += __shfl_xor_sync(0xffffffffu, up, off);
+        }
+        constexpr float kBack = 1.f / kUnit<kBf16>;
+        const float v = activate(gate * kBack, a.act) * (up * kBack);
+        const uint16_t hi = to16<kType>(v), lo = to16<kType>(v - from16<kType>(hi));
+        float sum = from16<kType>(hi) + from16<kType>(lo);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const size_t p = r.pair[item][n];
+        const int col = 16 * static_cast<int>(group * unit_pairs + m * kPairs) + c;
+        uint16_t* const dst = a.h + p * 2 * a.f + (col & ~63) + h_place(col & 63);
+        if (q == 0) dst[0] = hi;
+        if (q == 1) dst[a.f] = lo;
+        if (lane == 0) a.hsum[p * (a.f / 8) + col / 8] = sum * kUnit<kBf16>;
       }
-      const float v = activate(gate, a.act) * up;
-      const int c = 16 * (pr0 + pr) + 8 * h + j;
-      constexpr int kType = kBf16 ? 1 : 0;
-      const uint16_t hi = to16<kType>(v), lo = to16<kType>(v - from16<kType>(hi));
-      uint16_t* dst = a.h + static_cast<size_t>(p) * 2 * a.f + (c & ~63) + h_place(c & 63);
-      dst[0] = hi;
-      dst[a.f] = lo;
+#pragma unroll
+    for (int h = 0; h < kStrips; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tot[h][i] = 0.f;
+    s = my_stage;
+    item += a.step_items;
+    group += a.step_rest;
+    if (group >= a.per_item) {
+      group -= a.per_item;
+      ++item;
     }
-    buf ^= 1;
   }
   cp_async_wait<0>();
 }
 
 // --------------------------------------------------------------------- down
 //
-// A CTA takes one strip of 16 rows of every item. Its warps are two sets, for the even and the odd
-// experts; warp w of a set takes the stages w, w + stage_warps, .. of the set's items.
+// A CTA takes up to 2 kDownMaxPairs strips of 16 rows and one stage of 128 columns of every item (the
+// stages rank, + cluster, .. of its cluster), kSets warps per pair of strips, each for the items of the
+// experts of its own number modulo kSets. h of the stage is held for all pairs. At the end the
+// cluster's CTAs add up their sums, each for a part of the outputs.
 template <bool kBf16, int G>
-__global__ void __launch_bounds__(kThreads) few_down_kernel(const Args a) {
-  constexpr int kMaxNg = kStageCols / G;
+__global__ void __launch_bounds__(kDownMaxPairs * kSets * 32) few_down_kernel(const Args a) {
+  constexpr int kMaxNg = kStageCols / G, kStrip = 1024 + 64 * kMaxNg, kSlot = 2 * kStrip, kType = kBf16 ? 1 : 0;
+  constexpr int kHalfNg = G < 64 ? 2 : 1, kHalfStrip = 512 + 64 * kHalfNg;  // a last stage of 64 columns
+  // h [pairs][512] | rings | sums of h [pairs][groups of a stage] | acc [warps][T][33]
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Routing<kDownTokens> r;
+  __shared__ Routing r;
   grid_dependents_launch();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  form_routing<kDownTokens, true>(r, a);
-  const int W = a.stage_warps, sets = 2, set = warp / W, my_stage = warp - set * W;
-  const int S = (a.K + kStageCols - 1) / kStageCols;
-  const int i0 = set == 0 ? 0 : r.half, i1 = set >= sets ? i0 : set == 0 ? r.half : r.items;
-  const int strip = blockIdx.x;
-  const uint32_t ring = smem_addr(smem) + warp * kDepth * a.slot_bytes;
-  float* const acc = reinterpret_cast<float*>(smem + kWarps * kDepth * a.slot_bytes) + warp * a.T * 17;
-  for (int i = lane; i < a.T * 17; i += 32) acc[i] = 0.f;
-  const int steps_of_last = (a.K % kStageCols) ? 4 : 8;
-
-  const auto request_weights = [&](int item, int s, int slot) {
-    const int kk = s == S - 1 ? steps_of_last : 8, strip_bytes = kk * 128 + 64 * (kk * 16 / min(G, kk * 16));
-    const uint8_t* src = a.w + r.expert[item] * a.expert_bytes + (strip >> 3) * a.block_bytes +
-                         static_cast<int64_t>(s) * (8 * (1024 + 64 * kMaxNg)) + (strip & 7) * strip_bytes;
-    copy_warp(ring + slot * a.slot_bytes + kHBytes, src, strip_bytes, lane);
-  };
-  const auto request_h = [&](int item, int s, int slot) {  // every lane copies what it will read
-    const int p = r.pair[item][lane >> 3], part = (lane >> 2) & 1, chunks = s == S - 1 ? steps_of_last / 4 : 2;
-    if (p < 0) return;
-    const uint16_t* src = a.h + (static_cast<size_t>(p) * 2 + part) * a.f + s * kStageCols + (lane & 3) * 16;
-    for (int c = 0; c < chunks; ++c)
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
+  const int C = a.cluster, rank = static_cast<int>(cluster_rank()), tile = static_cast<int>(blockIdx.x) / C;
+  const int S = (a.K + kStageCols - 1) / kStageCols, pairs = a.T * a.k;
+  const int set = warp & (kSets - 1), strip = tile * a.strips + (warp / kSets) * 2;
+  const uint32_t hs = smem_addr(smem), ring = hs + pairs * kPairBytes + warp * a.depth * kSlot;
+  float* const hsum = reinterpret_cast<float*>(smem + pairs * kPairBytes + warps * a.depth * kSlot);
+  float* const all = hsum + pairs * kMaxNg;
+  float* const acc = all + warp * a.T * kAccRow;
+#pragma unroll 1
+  for (int i = lane; i < a.T * kAccRow; i += 32) acc[i] = 0.f;
+  if (a.listed) {  // it could not start beside the gate_up launch: the lists are there
+    grid_dependency_wait();
+#pragma unroll 1
+    for (int i = tid; i < static_cast<int>(sizeof(Routing) / 16); i += threads)
+      reinterpret_cast<uint4*>(&r)[i] = __ldcg(reinterpret_cast<const uint4*>(a.routing) + i);
+    __syncthreads();
+  } else {
+    form_routing(r, a);
+  }
+  const int i0 = r.first[set], i1 = strip * 16 >= a.d ? i0 : r.first[set + 1];  // no items for strips behind the last one
+#pragma unroll 1
+  for (int s = rank; s < S; s += C) {
+    const bool whole = (s + 1) * kStageCols <= a.K;
+    const uint8_t* const src = a.w + (static_cast<size_t>(strip >> 3) * a.block16 + s * (8 * kStrip / 16) +
+                                      (strip & 7) * ((whole ? kStrip : kHalfStrip) / 16)) * 16;
+    int pi = i0, pslot = 0, slot = 0, item = i0, ahead = a.depth - 1;
+#pragma unroll 1
+    while (true) {
+      if (pi < i1) {
+        const uint8_t* const from = src + static_cast<size_t>(r.expert[pi] * a.expert16) * 16;
+        if (whole)
+          copy_warp<kSlot>(ring + pslot * kSlot, from, lane);
+        else
+          copy_warp<2 * kHalfStrip>(ring + pslot * kSlot, from, lane);
+        ++pi;
+        if (++pslot == a.depth) pslot = 0;
+      }
+      cp_async_commit();
+      if (ahead > 0) {
+        if (--ahead > 0) continue;
+        if (s == rank)
+          grid_dependency_wait();  // h
+        else
+          __syncthreads();  // h of the stage before has been read
+        const int per = whole ? 32 : 16;  // 16-byte pieces of a pair: [hi, lo][chunk][tq][half]
+#pragma unroll 1
+        for (int i = tid; i < pairs * per; i += threads) {
+          const int p = whole ? i >> 5 : i >> 4, j = i & (per - 1), part = j >= per / 2, rest = j & (per / 2 - 1);
+          // the two halves change places in lo's rows, which would meet hi's banks
+          cp_async_16(hs + p * kPairBytes + part * 256 + ((rest ^ part) * 16),
+                      a.h + (static_cast<size_t>(p) * 2 + part) * a.f + s * kStageCols + rest * 8);
+        }
+        cp_async_commit();
+        const int ng = whole ? kMaxNg : kHalfNg, eights = (whole ? kStageCols / kMaxNg : 64 / kHalfNg) / 8;
+#pragma unroll 1
+        for (int i = tid; i < pairs * ng; i += threads) {
+          const int p = i / ng, j = i - p * ng;
+          const float* const part = a.hsum + p * (a.f / 8) + s * 16 + j * eights;
+          float v = 0.f;
+#pragma unroll 8
+          for (int q = 0; q < eights; ++q) v += __ldcg(part + q);
+          hsum[p * kMaxNg + j] = v;
+        }
+        cp_async_wait<0>();
+        __syncthreads();
+        continue;
+      }
+      if (item >= i1) break;
+      const int mine = r.pair[item][lane >> 3], p = r.pair[item][lane & 3];
+      const uint32_t hat = hs + mine * kPairBytes + ((lane >> 2) & 1) * 256 + (lane & 3) * 32;
+      uint32_t b[8][2];
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
-        cp_async_16(ring + slot * a.slot_bytes + (2 * c + v) * 512 + lane * 16, src + c * 64 + v * 8);
-  };
-  const auto advance = [&](int& item, int& s, int& slot) {
-    s += W;
-    if (s >= S) {
-      s = my_stage;
+      for (int kk = 0; kk < 8; kk += 2) {
+        const uint4 v = lds128(hat + (kk / 4) * 128 + ((((kk / 2) & 1) ^ ((lane >> 2) & 1)) << 4));
+        b[kk][0] = v.x;
+        b[kk][1] = v.y;
+        b[kk + 1][0] = v.z;
+        b[kk + 1][1] = v.w;
+      }
+      wait_piece(a.depth);
+      __syncwarp();
+      const uint32_t at = ring + slot * kSlot;
+      const bool on = (lane & 3) < r.count[item];
+      const float weight = r.w[p];
+      float sum[kMaxNg][2];
+#pragma unroll
+      for (int j = 0; j < kMaxNg; ++j) {
+        sum[j][0] = hsum[p * kMaxNg + j];
+        sum[j][1] = 0.f;
+      }
+      float* const dst = acc + r.token[item][lane & 3] * kAccRow + (lane >> 2);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        // columns 2 n and 2 n + 1 are token n's hi and lo: their sum counts, and the sum of h once
+        float t[4] = {};
+        if (whole) {
+          strip_stage<kBf16, G, 8>(t, at + h * kStrip, b, sum, lane, a.affine);
+        } else if constexpr (G <= 64) {
+          const uint32_t half[4][2] = {{b[0][0], b[0][1]}, {b[1][0], b[1][1]}, {b[2][0], b[2][1]}, {b[3][0], b[3][1]}};
+          float part[64 / G][2];
+#pragma unroll
+          for (int j = 0; j < 64 / G; ++j) {
+            part[j][0] = sum[j][0];
+            part[j][1] = 0.f;
+          }
+          strip_stage<kBf16, G, 4>(t, at + h * kHalfStrip, half, part, lane, a.affine);
+        }
+        if (on) {
+          dst[16 * h] = fmaf(weight, t[0] + t[1], dst[16 * h]);
+          dst[16 * h + 8] = fmaf(weight, t[2] + t[3], dst[16 * h + 8]);
+        }
+      }
+      __syncwarp();
+      if (++slot == a.depth) slot = 0;
       ++item;
     }
-    if (++slot == kDepth) slot = 0;
-  };
-  // groups in flight: the weights of the first pieces, then their h, then both per piece
-  int pi = i0, ps = my_stage, pslot = 0;
-  if (my_stage >= S) pi = i1;
-  {
-    int item = pi, s = ps, slot = pslot;
-    for (int i = 0; i < kDepth - 1 && item < i1; ++i) {
-      request_weights(item, s, slot);
-      advance(item, s, slot);
-    }
-    cp_async_commit();
-    grid_dependency_wait();  // h
-    for (int i = 0; i < kDepth - 1; ++i) {
-      if (pi < i1) {
-        request_h(pi, ps, pslot);
-        advance(pi, ps, pslot);
-      }
-      cp_async_commit();
-    }
+    cp_async_wait<0>();
   }
-  int slot = 0;
-  for (int item = i0; item < i1 && my_stage < S; ++item) {
-    float tot[4] = {};
-    for (int s = my_stage; s < S; s += W) {
-      cp_async_wait<kDepth - 2>();
-      __syncwarp();
-      if (pi < i1) {
-        request_weights(pi, ps, pslot);
-        request_h(pi, ps, pslot);
-        advance(pi, ps, pslot);
-      }
-      cp_async_commit();
-      const int kk_n = s == S - 1 ? steps_of_last : 8, ng = kk_n * 16 / min(G, kk_n * 16), per = kk_n / ng;
-      const uint32_t at = ring + slot * a.slot_bytes, wat = at + kHBytes;
-      for (int j = 0; j < ng; ++j) {
-        float part[4] = {}, sum[4] = {};
-        for (int q = 0; q < per; q += 2) {
-          const int kk = j * per + q;
-          const uint4 b = lds128(at + (kk / 2) * 512 + lane * 16);
-          const uint2 word = lds64(wat + 64 * ng + (kk / 4) * 512 + lane * 16 + (kk % 4) * 4);
-          const uint32_t ones[4] = {kOnes<kBf16>, kOnes<kBf16>, kOnes<kBf16>, kOnes<kBf16>};
-          uint32_t af[4];
-          mma<kBf16>(sum, ones, b.x, b.y);
-          codes<kBf16>(word.x, af);
-          mma<kBf16>(part, af, b.x, b.y);
-          mma<kBf16>(sum, ones, b.z, b.w);
-          codes<kBf16>(word.y, af);
-          mma<kBf16>(part, af, b.z, b.w);
-        }
-        apply_group<kBf16>(tot, part, sum, lds64(wat + (lane >> 2) * (8 * ng) + j * 8), a.affine);
-      }
-      __syncwarp();
-      if (++slot == kDepth) slot = 0;
-    }
-    // columns 2 n and 2 n + 1 are token n's hi and lo
-    const int p = r.pair[item][lane & 3];
-    if (p >= 0) {
-      float* const dst = acc + (p / a.k) * 17 + (lane >> 2);
-      dst[0] = fmaf(r.w[p], tot[0] + tot[1], dst[0]);
-      dst[8] = fmaf(r.w[p], tot[2] + tot[3], dst[8]);
-    }
-    __syncwarp();
-  }
-  cp_async_wait<0>();
   __syncthreads();
-  constexpr int kType = kBf16 ? 1 : 0;
-  const float* const all = reinterpret_cast<const float*>(smem + kWarps * kDepth * a.slot_bytes);
-  for (int o = tid; o < a.T * 16; o += kThreads) {
-    const int t = o >> 4, i = o & 15;
-    float v = 0.f;
-    for (int w = 0; w < sets * W; ++w) v += all[(w * a.T + t) * 17 + i];
-    const size_t at = static_cast<size_t>(t) * a.d + strip * 16 + i;
-    if (a.residual) v += from16<kType>(static_cast<const uint16_t*>(a.residual)[at]);
-    static_cast<uint16_t*>(a.out)[at] = to16<kType>(v);
+  // the CTA's sums over its sets, in their order: 32 columns of a pair of strips by a warp
+  const int row = a.T * kAccRow, pair_groups = warps / kSets;
+#pragma unroll 1
+  for (int t = warp; t < a.T; t += warps)
+#pragma unroll 2
+    for (int g = 0; g < pair_groups; ++g) {
+      float* const at = all + g * (kSets * row) + t * kAccRow + lane;
+      at[0] = ((at[0] + at[row]) + at[2 * row]) + at[3 * row];
+    }
+  if (C > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // (token, pair of strips) by a warp of the cluster
+  const int cols = a.strips * 16;
+#pragma unroll 1
+  for (int o = rank * warps + warp; o < a.T * pair_groups; o += C * warps) {
+    const int t = o / pair_groups, g = o - t * pair_groups, col = tile * cols + g * 32 + lane;
+    if (col >= a.d) continue;
+    const uint32_t at = smem_addr(all + g * (kSets * row) + t * kAccRow + lane);
+    float part[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      part[q] = 0.f;
+      if (q < C) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part[q]) : "r"(cluster_addr(at, q)) : "memory");
+    }
+    float v = part[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q)
+      if (q < C) v += part[q];
+    v *= 1.f / kUnit<kBf16>;
+    const size_t dst = static_cast<size_t>(t) * a.d + col;
+    if (a.residual) v += from16<kType>(static_cast<const uint16_t*>(a.residual)[dst]);
+    static_cast<uint16_t*>(a.out)[dst] = to16<kType>(v);
   }
+  if (C > 1) cluster_sync();  // the sums are read before their CTA leaves
 }
 
-constexpr int kSmemLimit = 160 * 1024;  // of dynamic shared memory: both kernels at their largest
+constexpr int kSmemLimit = 226 * 1024;  // of a CTA, static and dynamic
+constexpr int up_static(int pairs) { return int(sizeof(Routing)) + kUpWarps * (pairs * 128 + 8) * 4 + 64; }
+constexpr int kDownStatic = sizeof(Routing) + 64;
+constexpr int kEarlyTokens = 8;  // tokens up to which the down launch starts beside the gate_up launch
+int g_clusters[9];  // clusters of so many CTAs of the down kernel that run at a time
 
 using Kernel = void (*)(Args);
-Kernel gate_up_of(int type, int g) {
-  if (type == 1)
-    return g == 32 ? few_gate_up_kernel<true, 32> : g == 64 ? few_gate_up_kernel<true, 64> : few_gate_up_kernel<true, 128>;
-  return g == 32 ? few_gate_up_kernel<false, 32> : g == 64 ? few_gate_up_kernel<false, 64>
-                                                           : few_gate_up_kernel<false, 128>;
+template <bool kBf16, int kPairs>
+Kernel gate_up_of(int g) {
+  return g == 32 ? few_gate_up_kernel<kBf16, 32, kPairs>
+                 : g == 64 ? few_gate_up_kernel<kBf16, 64, kPairs> : few_gate_up_kernel<kBf16, 128, kPairs>;
+}
+Kernel gate_up_of(int type, int g, int pairs) {
+  return type == 1 ? pairs == 2 ? gate_up_of<true, 2>(g) : gate_up_of<true, 1>(g)
+                   : pairs == 2 ? gate_up_of<false, 2>(g) : gate_up_of<false, 1>(g);
 }
 Kernel down_of(int type, int g) {
   if (type == 1)
@@ -441,23 +676,61 @@ Kernel down_of(int type, int g) {
   return g == 32 ? few_down_kernel<false, 32> : g == 64 ? few_down_kernel<false, 64> : few_down_kernel<false, 128>;
 }
 
+struct DownLaunch {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  DownLaunch(int tiles, int cluster, int threads, size_t smem, cudaStream_t st) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(tiles * cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
 }  // namespace
 
-size_t few_ws_bytes(const Dims& s) { return s.T ? size_t(s.pairs()) * 2 * s.f * 2 : 16; }
+// Workspace: routing lists | h | sums of h.
+size_t few_ws_bytes(const Dims& s) {
+  return sizeof(Routing) + size_t(s.pairs()) * s.f * 4 + size_t(s.pairs()) * (s.f / 8) * 4;
+}
+
+// Room for the kernel's shared memory, and an SM divided for as much of it as there is: a CTA of the down launch
+// that finds it divided otherwise waits until the SM is empty.
+static cudaError_t set_up(Kernel k, int smem) {
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  return e;
+}
 
 cudaError_t init_few_kernels() {
+  cudaError_t e = cudaSuccess;
   for (int type = 0; type < 2; ++type)
-    for (int g : {32, 64, 128})
-      for (Kernel k : {gate_up_of(type, g), down_of(type, g)}) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-        if (e != cudaSuccess) return e;
-      }
-  return cudaSuccess;
+    for (int g : {32, 64, 128}) {
+      for (int pairs : {1, 2})
+        if (e == cudaSuccess)
+          e = set_up(gate_up_of(type, g, pairs), kSmemLimit - up_static(pairs));
+      if (e == cudaSuccess)
+        e = set_up(down_of(type, g), kSmemLimit - kDownStatic);
+    }
+  for (int c = 1; c <= 8 && e == cudaSuccess; ++c) {
+    const DownLaunch l(1, c, 3 * kSets * 32, 128 * 1024, nullptr);
+    e = cudaOccupancyMaxActiveClusters(&g_clusters[c], down_of(0, 64), &l.cfg);
+  }
+  return e;
 }
 
 cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logits, const uint8_t* w_gate_up,
                        const uint8_t* w_down, const void* residual, int32_t* topk_idx, float* topk_w, void* out,
                        void* workspace, int num_sms, cudaStream_t st) {
+  const int pairs = int(s.pairs());
   Args a{};
   a.x = x;
   a.logits = logits;
@@ -465,7 +738,9 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.topk_idx = topk_idx;
   a.topk_w = topk_w;
   a.out = out;
-  a.h = static_cast<uint16_t*>(workspace);
+  a.routing = workspace;
+  a.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + sizeof(Routing));
+  a.hsum = reinterpret_cast<float*>(a.h + size_t(pairs) * 2 * s.f);
   a.T = s.T;
   a.d = s.d;
   a.f = s.f;
@@ -473,27 +748,50 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.k = s.k;
   a.act = s.act;
   a.affine = s.fmt == 1;
-  // gate_up
+  // The down launch: the fewest strips per CTA for which all clusters run at a time.
+  const int strips = s.d / 16, down_stages = (s.f + kStageCols - 1) / kStageCols;
+  a.cluster = down_stages < 8 ? down_stages : 8;
+  a.strips = 2;
+  while (a.strips < 2 * kDownMaxPairs && (strips + a.strips - 1) / a.strips > g_clusters[a.cluster]) a.strips += 2;
+  const int slot = 2 * (1024 + 64 * (kStageCols / s.g2)), fixed = pairs * (kPairBytes + kStageCols / s.g2 * 4);
+  const auto room = [&](int limit) {  // pieces of a warp that fit
+    const int warps = a.strips / 2 * kSets;
+    return (limit - kDownStatic - fixed - warps * s.T * kAccRow * 4) / (warps * slot);
+  };
+  // For few tokens it fits beside a shallow gate_up ring, and its start is hidden; otherwise it gets the lists from
+  // the gate_up launch.
+  const int stages = s.d / kStageCols;
+  a.stage_warps = stages >= 12 ? 16 : stages >= 6 ? 8 : 4;
+  const int shares = kUpWarps / a.stage_warps, piece = kUpWarps * 2 * (1024 + 64 * (kStageCols / s.g1));
+  const auto beside = [&](int depth) { return kSmemLimit - up_static(1) - depth * piece; };
+  const int up_depth = room(beside(3)) >= 2 ? 3 : 2;
+  a.listed = s.T > kEarlyTokens || room(beside(up_depth)) < 2;
+  while (a.listed && a.strips > 2 && room(kSmemLimit) < 2) a.strips -= 2;
+  const int down_depth = std::min(room(a.listed ? kSmemLimit : beside(up_depth)), kMaxDepth);
+  // gate_up: two pairs per warp halve what a unit costs beside its weights, where the units are many
+  const int per_warp = a.listed && pairs * (s.f / 16 / shares) >= 16 * num_sms && s.f / 16 % (2 * shares) == 0 ? 2 : 1;
   a.w = w_gate_up;
   a.K = s.d;
-  a.block_bytes = int64_t(kBlockRows) * (s.d / 2 + s.d / s.g1 * 4);
-  a.expert_bytes = a.block_bytes * (s.f / 64);
-  const int stages = s.d / kStageCols;
-  a.stage_warps = stages >= 8 ? 8 : stages >= 4 ? 4 : 2;
-  a.slot_bytes = 2 * (1024 + 64 * (kStageCols / s.g1)) + (s.T < kUpTokens ? s.T : kUpTokens) * kXRow;
-  const int units = int(s.pairs()) * (s.f / 16 / (kWarps / a.stage_warps));
-  cudaError_t err = launch_pdl(gate_up_of(type, s.g1), dim3(units < num_sms ? units : num_sms), dim3(kThreads),
-                               size_t(kWarps) * kDepth * a.slot_bytes, st, a);
+  a.block16 = uint32_t(kBlockRows) * (s.d / 2 + s.d / s.g1 * 4) / 16;
+  a.expert16 = a.block16 * (s.f / 64);
+  a.per_item = s.f / 16 / (per_warp * shares);
+  a.per_item_inv = 1.f / a.per_item;
+  const int units = pairs * a.per_item, grid = units < num_sms ? units : num_sms;
+  a.step_items = grid / a.per_item;
+  a.step_rest = grid % a.per_item;
+  a.depth = a.listed ? std::min((kSmemLimit - up_static(per_warp)) / (per_warp * piece), 3) : up_depth;
+  cudaError_t err = launch_pdl(gate_up_of(type, s.g1, per_warp), dim3(grid), dim3(kUpThreads),
+                               size_t(a.depth) * per_warp * piece, st, a);
   if (err != cudaSuccess) return err;
-  // down
   a.w = w_down;
   a.K = s.f;
-  a.block_bytes = int64_t(kBlockRows) * (s.f / 2 + s.f / s.g2 * 4);
-  a.expert_bytes = a.block_bytes * (s.d / kBlockRows);
-  a.stage_warps = kWarps / 2;
-  a.slot_bytes = 1024 + 64 * (kStageCols / s.g2) + kHBytes;
-  return launch_pdl(down_of(type, s.g2), dim3(s.d / 16), dim3(kThreads),
-                    size_t(kWarps) * (kDepth * a.slot_bytes + s.T * 17 * 4), st, a);
+  a.block16 = uint32_t(kBlockRows) * (s.f / 2 + s.f / s.g2 * 4) / 16;
+  a.expert16 = a.block16 * (s.d / kBlockRows);
+  a.depth = down_depth;
+  const int warps = a.strips / 2 * kSets;
+  const DownLaunch l((strips + a.strips - 1) / a.strips, a.cluster, warps * 32,
+                     size_t(fixed) + warps * (a.depth * slot + s.T * kAccRow * 4), st);
+  return cudaLaunchKernelEx(&l.cfg, down_of(type, s.g2), a);
 }
 
 }  // namespace moe
