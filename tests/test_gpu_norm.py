@@ -5,8 +5,9 @@ row's sum of squares passes through at most 64 + 5 + 16 roundings (a thread's ch
 warps), all terms positive; the mean and eps add three, the inverse root halves what comes in and adds one: its
 relative error is at most r = (88 / 2 + 1) v. The other sums over a row are off by 85 v of the sum of their terms'
 magnitudes. Each product or addition on the way adds v of its value, and a term's error is carried through the
-formulas below by its magnitude; the last rounding adds u of the result, or half of fp16's smallest step. Sums
-over rows pass through at most R / 304 + 1 rows of a unit, 8 units of a CTA and 304 / 32 + 32 partial sums.
+formulas below by its magnitude; the last rounding adds u of the result, or half of fp16's smallest step. The
+gradient's sum of w dv m over a row is taken as the three sums that make it up (g = dout + r gamma_pre du - n mean), so
+its error is that of the sum of the three's magnitudes. Sums over rows pass through at most R / 304 + 1 rows of a unit, 8 units of a CTA and 304 / 32 + 32 partial sums.
 """
 import numpy as np
 import pytest
@@ -134,6 +135,7 @@ def _want(s, R, gate_rows, scale, stream, dout, du):
     """The gradients in 64 bits and what the kernel's may be off by before their last rounding."""
     g = dout.double() if dout is not None else 0.0 * (du if du is not None else stream).double()
     eg = torch.zeros_like(g)
+    parts = g.abs()  # the magnitudes of what g is made of
     want, lim = {}, {}
     rows = R / 304 + 1 + 8 + 10 + 32
     if du is not None:
@@ -144,6 +146,7 @@ def _want(s, R, gate_rows, scale, stream, dout, du):
         mean = (w * n).mean(1, keepdim=True)
         em = r * (ROW + 2 * V) * (w * o).abs().mean(1, keepdim=True) + mean.abs() * (RMS + 3 * V)
         g = g + r * (w - n * mean)
+        parts = parts + r * (w.abs() + (n * mean).abs())
         eg = r * ((w.abs() + (n * mean).abs()) * (2 * RMS + 6 * V) + n.abs() * em) + V * g.abs()
         want["gamma_pre"] = (du.double() * n).sum(0)
         lim["gamma_pre"] = (du.double() * n).abs().sum(0) * (RMS + (2 + rows) * V)
@@ -156,7 +159,8 @@ def _want(s, R, gate_rows, scale, stream, dout, du):
             r = _rinv(y)
             m = y * r
             mean = (w * dv * m).mean(1, keepdim=True)
-            em = r * ((w.abs() * edv + (ROW + 4 * V) * (w * dv).abs()) * y.abs()).mean(1, keepdim=True) + \
+            em = r * ((w.abs() * edv + (ROW + 6 * V) * (w * q).abs() * parts) * y.abs()).mean(
+                1, keepdim=True) + \
                 mean.abs() * (RMS + 3 * V)
             want["y"] = r * (w * dv - m * mean)
             lim["y"] = r * (w.abs() * edv + ((w * dv).abs() + (m * mean).abs()) * (2 * RMS + 6 * V) + m.abs() * em)

@@ -4,14 +4,15 @@
 //   norm = sqrt(sum over all tensors of g^2),   out = g min(1, max_norm / norm)
 //
 // Two passes over the data, each bound by memory: the sum of the squares, and the scaling, which is
-// left out where it would change nothing. The tensors are cut into chunks that persistent CTAs
-// take in turn; a launch carries its tensors' addresses as kernel parameters (up to kLarge of
+// left out where it would change nothing. The tensors are cut into chunks, and every CTA takes a
+// contiguous run of them, so it looks for its first tensor once; a launch carries its tensors' addresses as kernel parameters (up to kLarge of
 // them), so nothing is kept on the device from call to call and a captured graph holds its own.
 //
 // Squares are summed in fp32 over the 64 to 128 bytes that a thread takes of a chunk, in fp64 from
 // there on: an fp64 addition per element would be the bound (its rate is a hundredth of fp32's), one
 // per chunk is not seen. Where such a sum leaves the range in which fp32 squares keep their digits,
 // it is taken again in fp64. All orders are fixed: the same bits in every run.
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -28,7 +29,7 @@ constexpr int kChunkBytes = kThreads * kLoads * 16;    // 32 KB
 // Tensors per launch: 23 KB of parameters, or 2.3 KB for short lists (the parameters are copied a few
 // times on their way to the device).
 constexpr int kLarge = 640, kSmall = 64;
-constexpr int kCtas = 608;                             // four on each of 152 SMs
+constexpr int kCtas = 608;                             // four on each of 152 SMs (at most 64 registers a thread)
 
 struct Entry {
   const void* data;
@@ -60,6 +61,11 @@ __device__ __forceinline__ int find(const Table<kTable>& t, int chunk) {
   return lo;
 }
 
+// The first chunk of CTA b.
+__device__ __forceinline__ int share(int chunks, int b) {
+  return static_cast<int>(static_cast<int64_t>(chunks) * b / gridDim.x);
+}
+
 // Element i of 16 bytes (eight of 16 bits, four of 32).
 template <int kType>
 __device__ __forceinline__ float value(const void* p, int64_t i) {
@@ -67,9 +73,14 @@ __device__ __forceinline__ float value(const void* p, int64_t i) {
   else return from16<kType>(static_cast<const uint16_t*>(p)[i]);
 }
 template <int kType>
-__device__ __forceinline__ void put(void* p, int64_t i, float v) {
-  if constexpr (kType == 2) static_cast<float*>(p)[i] = v;
-  else static_cast<uint16_t*>(p)[i] = to16<kType>(v);
+__device__ __forceinline__ void put_scaled(const Entry& e, int64_t i, float factor) {
+  if constexpr (kType == 2) {
+    const float v = static_cast<const float*>(e.data)[i];
+    static_cast<float*>(e.out)[i] = factor != 1.f ? v * factor : v;
+  } else {
+    const uint16_t v = static_cast<const uint16_t*>(e.data)[i];
+    static_cast<uint16_t*>(e.out)[i] = factor != 1.f ? to16<kType>(from16<kType>(v) * factor) : v;
+  }
 }
 
 // Sum of the squares of a thread's share of a chunk: pieces v, v + kThreads, .. counted from the
@@ -125,6 +136,7 @@ __device__ double chunk_square(const Entry& e, int chunk) {
   return d;
 }
 
+// The sum over the CTA, in thread 0 alone: fp64 operations of all threads would take their time.
 __device__ __forceinline__ double cta_sum(double v) {
   __shared__ double part[kThreads / 32];
 #pragma unroll
@@ -132,20 +144,22 @@ __device__ __forceinline__ double cta_sum(double v) {
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   double s = 0.0;
+  if (threadIdx.x == 0)
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) s += part[w];
+    for (int w = 0; w < kThreads / 32; ++w) s += part[w];
   return s;
 }
 
 template <int kTable>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     clip_square_kernel(const __grid_constant__ Table<kTable> t, double* partial) {
   grid_dependents_launch();
   grid_dependency_wait();
   double s = 0.0;
-  const int chunks = t.first[t.n];
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = find(t, c);
+  const int c0 = share(t.first[t.n], blockIdx.x), c1 = share(t.first[t.n], blockIdx.x + 1);
+  int i = c0 < c1 ? find(t, c0) : 0;
+  for (int c = c0; c < c1; ++c) {
+    while (t.first[i + 1] <= c) ++i;
     const Entry& e = t.e[i];
     const int k = c - t.first[i];
     s += e.type == 0 ? chunk_square<0>(e, k) : e.type == 1 ? chunk_square<1>(e, k) : chunk_square<2>(e, k);
@@ -166,62 +180,78 @@ __global__ void __launch_bounds__(kThreads) clip_total_kernel(double* partial, i
 
 template <int kType>
 __device__ void scale_chunk(const Entry& e, int chunk, float factor) {
-  constexpr int N = Vec<kType>::n;
-  const int64_t v0 = static_cast<int64_t>(chunk) * (kThreads * kLoads) + threadIdx.x;
+  constexpr int N = Vec<kType>::n, kBatch = 4;
   const int64_t end = e.shift + e.count;
   const auto* src = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(e.data) & ~uintptr_t(15));
   auto* dst = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(e.out) & ~uintptr_t(15));
   // the output's pieces lie as the input's do, or it is written by elements
   const bool alike = ((reinterpret_cast<uintptr_t>(e.data) ^ reinterpret_cast<uintptr_t>(e.out)) & 15u) == 0;
-  uint4 x[kLoads];
+#pragma unroll 1
+  for (int l0 = 0; l0 < kLoads; l0 += kBatch) {
+    const int64_t v0 = static_cast<int64_t>(chunk) * (kThreads * kLoads) + l0 * kThreads + threadIdx.x;
+    if (alike && v0 * N >= e.shift && (v0 + (kBatch - 1) * kThreads + 1) * N <= end) {  // whole pieces only
+      uint4 x[kBatch];
 #pragma unroll
-  for (int l = 0; l < kLoads; ++l) {
-    const int64_t v = v0 + l * kThreads;
-    if (v * N >= e.shift && (v + 1) * N <= end) x[l] = src[v];
-  }
+      for (int l = 0; l < kBatch; ++l) x[l] = src[v0 + l * kThreads];
 #pragma unroll
-  for (int l = 0; l < kLoads; ++l) {
-    const int64_t v = v0 + l * kThreads;
-    if (v * N >= end) continue;
-    if (v * N >= e.shift && (v + 1) * N <= end) {
-      float f[N];
-      Vec<kType>::load(x[l], f);
-      if (factor != 1.f) {  // else the bits are copied, a NaN's too
+      for (int l = 0; l < kBatch; ++l) {
+        if (factor != 1.f) {  // else the bits are copied, a NaN's too
+          float f[N];
+          Vec<kType>::load(x[l], f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] *= factor;
-        x[l] = Vec<kType>::store(f);
+          for (int i = 0; i < N; ++i) f[i] *= factor;
+          x[l] = Vec<kType>::store(f);
+        }
+        dst[v0 + l * kThreads] = x[l];
       }
-      if (alike) {
-        dst[v] = x[l];
-      } else {
-        if (factor == 1.f) Vec<kType>::load(x[l], f);
-        for (int i = 0; i < N; ++i) put<kType>(e.out, v * N + i - e.shift, f[i]);
-      }
-    } else {
+      continue;
+    }
+#pragma unroll 1
+    for (int l = 0; l < kBatch; ++l) {
+      const int64_t at0 = (v0 + l * kThreads) * N;
+#pragma unroll 1
       for (int i = 0; i < N; ++i) {
-        const int64_t at = v * N + i;
-        if (at >= e.shift && at < end) put<kType>(e.out, at - e.shift, value<kType>(e.data, at - e.shift) * factor);
+        const int64_t at = at0 + i;
+        if (at >= e.shift && at < end) put_scaled<kType>(e, at - e.shift, factor);
       }
     }
   }
 }
 
-// Every CTA adds up the partial sums itself, in the same order. Chunks are taken from the last one
-// back: what the pass before read last is still in L2.
+// The square root in fp32 (fp64's takes a microsecond here): of the value between 1 and 4 that a power of four leaves.
+__device__ __forceinline__ float root(double s) {
+  if (!(s > 0.0 && s < INFINITY)) return static_cast<float>(s);
+  const int64_t bits = __double_as_longlong(s);
+  const int e = (static_cast<int>(bits >> 52) - 1023) >> 1;  // floor: s = m 4^e (below 2^-1022, which squares do not reach, m is off)
+  const double m = __longlong_as_double(bits - static_cast<int64_t>(2 * e) * (int64_t(1) << 52));
+  return ldexpf(sqrtf(static_cast<float>(m)), e);
+}
+
+// Every CTA adds up the partial sums itself, in the same order. Chunks are taken from a run's last one
+// back: what the pass before read last is still in L2. copies: a tensor is scaled to another place.
 template <int kTable>
-__global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ Table<kTable> t,
-                                                              const double* partial, int n_partial, double max_norm,
-                                                              float* norm) {
+__global__ void __launch_bounds__(kThreads, 4)
+    clip_scale_kernel(const __grid_constant__ Table<kTable> t, const double* partial, int n_partial, float max_norm,
+                      bool copies, float* norm) {
   grid_dependents_launch();
   grid_dependency_wait();
   double s = 0.0;
   for (int i = threadIdx.x; i < n_partial; i += kThreads) s += partial[i];
-  s = sqrt(cta_sum(s));
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(s);
-  // a norm that is no number, or infinite, leaves the values as they are
-  const float factor = s > max_norm && s < INFINITY ? static_cast<float>(max_norm / s) : 1.f;
-  for (int c = t.first[t.n] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
-    const int i = find(t, c);
+  __shared__ float shared_factor;
+  s = cta_sum(s);
+  if (threadIdx.x == 0) {
+    const float v = root(s);
+    if (norm && blockIdx.x == 0) *norm = v;
+    // a norm that is no number, or infinite, leaves the values as they are
+    shared_factor = v > max_norm && v < INFINITY ? max_norm / v : 1.f;
+  }
+  __syncthreads();
+  const float factor = shared_factor;
+  if (factor == 1.f && !copies) return;
+  const int c0 = share(t.first[t.n], blockIdx.x), c1 = share(t.first[t.n], blockIdx.x + 1);
+  int i = c0 < c1 ? find(t, c1 - 1) : 0;
+  for (int c = c1 - 1; c >= c0; --c) {
+    while (t.first[i] > c) --i;
     const Entry& e = t.e[i];
     if (!e.out || (factor == 1.f && e.out == e.data)) continue;
     const int k = c - t.first[i];
@@ -259,6 +289,7 @@ template <int kTable>
 cudaError_t run(const moe_w4a16_tensor* tensors, int n, double max_norm, float* norm, double* partial, cudaStream_t st) {
   static thread_local Table<kTable> t;
   cudaError_t err = cudaSuccess;
+  const float bound = max_norm > FLT_MAX ? INFINITY : static_cast<float>(max_norm);
   int sums = 0, launches = 0;
   for (int at = 0; at < n || launches == 0; ++launches) {
     at += fill(t, tensors + at, n - at);
@@ -274,11 +305,13 @@ cudaError_t run(const moe_w4a16_tensor* tensors, int n, double max_norm, float* 
   }
   for (int at = 0, i = 0; i < launches; ++i) {
     if (launches > 1) at += fill(t, tensors + at, n - at);
-    bool scaled = false;  // whether a value may have to be written
-    for (int j = 0; j < t.n; ++j) scaled |= t.e[j].out && (max_norm < INFINITY || t.e[j].out != t.e[j].data);
+    bool copies = false, scaled = max_norm < INFINITY;  // whether a value may have to be written
+    for (int j = 0; j < t.n; ++j) copies |= t.e[j].out && t.e[j].out != t.e[j].data;
+    scaled |= copies;
     if (i > 0 && !scaled) continue;
     if ((err = launch_pdl(clip_scale_kernel<kTable>, dim3(scaled ? ctas_of(t.first[t.n]) : 1), dim3(kThreads), 0, st, t,
-                          static_cast<const double*>(partial), sums, max_norm, i == 0 ? norm : nullptr)) != cudaSuccess)
+                          static_cast<const double*>(partial), sums, bound, copies,
+                          i == 0 ? norm : nullptr)) != cudaSuccess)
       return err;
   }
   return cudaSuccess;

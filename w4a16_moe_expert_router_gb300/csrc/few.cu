@@ -22,6 +22,7 @@
 // ascending by their number modulo four), so the result does not depend on the other
 // tokens and is the same in every run.
 #include <algorithm>
+#include <cmath>
 
 #include "activation.cuh"
 #include "internal.h"
@@ -36,10 +37,10 @@ namespace {
 constexpr int kMaxItems = kFewTokens * kMaxTopK;  // as many as pairs
 constexpr int kItemTokens = 4;                    // tokens of an item
 constexpr int kUpThreads = 512, kUpWarps = kUpThreads / 32;
-constexpr int kSets = 4;                          // down: warps per pair of strips, each for every fourth expert
+constexpr int kDownWarps = 4;                     // down: warps per pair of strips, each for every fourth item
 constexpr int kDownMaxPairs = 4;                  // down: pairs of strips of a CTA
 constexpr int kPairBytes = 512;                   // a pair's h of one stage: (hi, lo) x 128 columns
-constexpr int kAccRow = 33;                       // down: a token's 32 sums of a warp, and one word between tokens
+constexpr int kRowWords = 33;                     // down: a pair's 32 rows of two strips, and one word between pairs
 
 struct Args {
   const void* x;
@@ -49,27 +50,25 @@ struct Args {
   int32_t* topk_idx;
   float* topk_w;
   void* out;
-  uint16_t* h;            // [pairs][2][f], in the order of the down launch's fragments
-  float* hsum;            // [pairs][f / 8]: sums of eight columns of h, in the partial sums' units
+  uint8_t* h;             // [stages][pairs][kPairBytes], as the down launch holds it
+  float* hsum;            // [stages][pairs][16]: sums of eight columns of h, in the partial sums' units
   void* routing;          // the lists, for a down launch that does not form them
   int listed;
   int T, d, f, E, k, act, affine;
   int K;                  // contraction: d or f
   uint32_t expert16;      // 16-byte pieces of an expert's weights
   uint32_t block16;       // and of a block of 128 rows
-  int stage_warps;        // gate_up: warps that share an item's contraction
+  int stage_warps;        // gate_up: warps of a group, which share a unit's contraction
   int per_item;           // gate_up: units of an item
   float per_item_inv;
-  int step_items, step_rest;  // and how far gridDim.x units are
+  int step_items, step_rest;  // and how far the units of all groups are
   int strips, cluster;    // down: strips of a CTA, CTAs that share the contraction
   int depth;              // pieces of a warp in its ring
 };
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Routing and items, formed by every CTA. One token needs little time for anything but this, and code
-// that runs once waits for its instructions: the loops here and below are kept rolled on purpose (the choice
-// of one token took 3.0 us unrolled over its eight rounds).
+// Routing and items, formed by every CTA.
 struct alignas(16) Routing {
   int32_t sel[kMaxItems];
   float w[kMaxItems];                     // a pair's value, then its weight
@@ -79,11 +78,15 @@ struct alignas(16) Routing {
   uint8_t token[kMaxItems][kItemTokens];
   uint8_t expert[kMaxItems];              // expert of an item
   uint8_t count[kMaxItems];               // its tokens
-  int32_t first[kSets + 1];               // first item of a set of experts, and the end
+  int32_t items;
 };
 
+__device__ __forceinline__ float key_value(uint32_t key) {  // the value of an order_key
+  return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
 // The choice of one token by one warp, as topk_softmax_warp makes it: the largest logits, ties to the
-// lower expert, and their softmax summed in rank order. Lane l holds experts l + 32 j.
+// lower expert; w gets their values. Lane l holds experts l + 32 j.
 template <int NS>
 __device__ __forceinline__ void choose(const float* row, int E, int k, int lane, int32_t* sel, float* w) {
   uint32_t key[NS];
@@ -106,12 +109,16 @@ __device__ __forceinline__ void choose(const float* row, int E, int k, int lane,
       winner = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(e) : ~0u) & 31u);
     if (lane == winner) {
       sel[r] = e;
-      w[r] = __uint_as_float((top & 0x80000000u) ? top ^ 0x80000000u : ~top);
+      w[r] = key_value(top);
 #pragma unroll
       for (int j = 0; j < NS; ++j)
         if (j == first) key[j] = 0u;
     }
   }
+}
+
+// The softmax over the k chosen values of a token, summed in rank order, by one warp.
+__device__ __forceinline__ void weigh(float* w, int k, int lane) {
   __syncwarp();
   const float v = lane < k ? expf(w[lane] - w[0]) : 0.f;
   __syncwarp();
@@ -123,11 +130,73 @@ __device__ __forceinline__ void choose(const float* row, int E, int k, int lane,
     if (r < k) den += w[r];
   __syncwarp();
   if (lane < k) w[lane] = v / den;
+  __syncwarp();
 }
 
-// Lists the items by expert modulo kSets, then by expert ascending. Ends with a barrier.
-__device__ __forceinline__ void form_routing(Routing& r, const Args& a) {
+// The choice of a single token by the CTA: an expert's rank is the number of keys that are not below its own,
+// counted by the threads of the expert, each over a part of the keys (1.0 us, where eight rounds of a
+// warp take 1.8; the work grows with the square of the experts, and several tokens gain nothing).
+// Tied keys leave a rank open: false. keys: two words per expert, padded to 128 or 256.
+__device__ __forceinline__ bool choose_by_rank(Routing& r, const Args& a, uint32_t* keys) {
+  const int tid = threadIdx.x, n = blockDim.x, shift = a.E > 128 ? 8 : 7, E = 1 << shift;
+  uint32_t* const rank = keys + E;
+  for (int e = tid; e < E; e += n) {
+    keys[e] = e < a.E ? order_key(__ldcg(a.logits + e)) : 0u;  // below every real key
+    rank[e] = 0u;
+  }
+  if (tid < kMaxTopK) r.sel[tid] = -1;
+  __syncthreads();
+  const int parts = n >> shift, part = tid >> shift, e = tid & (E - 1);
+  const int chunk = ((E + parts - 1) / parts + 3) & ~3, j0 = part * chunk, j1 = min(E, j0 + chunk);
+  if (part < parts) {
+    const uint32_t mine = keys[e];
+    int count = 0;
+#pragma unroll 8
+    for (int j = j0; j < j1; j += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + j);
+      count += (v.x >= mine) + (v.y >= mine) + (v.z >= mine) + (v.w >= mine);
+    }
+    atomicAdd(rank + e, static_cast<uint32_t>(count));
+  }
+  __syncthreads();
+  for (int i = tid; i < a.E; i += n) {
+    const int at = static_cast<int>(rank[i]) - 1;
+    if (at < a.k) {
+      r.sel[at] = i;
+      r.w[at] = key_value(keys[i]);
+    }
+  }
+  __syncthreads();
+  const int lane = tid & 31;
+  return !__any_sync(0xffffffffu, lane < a.k && r.sel[lane] < 0);  // the same in every warp
+}
+
+// Lists the items by expert ascending; a pair's w is its value (weigh() follows).
+// Ends with a barrier. scratch: kScratchBytes of free shared memory.
+constexpr int kScratchBytes = 2 * kMaxExperts * 4;
+__device__ __forceinline__ void form_routing(Routing& r, const Args& a, uint8_t* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x, pairs = a.T * a.k;
+  if (a.T == 1) {
+    if (n < (a.E > 128 ? 256 : 128) || !choose_by_rank(r, a, reinterpret_cast<uint32_t*>(scratch))) {
+      if (warp == 0) a.E <= 128 ? choose<4>(a.logits, a.E, a.k, lane, r.sel, r.w) : choose<8>(a.logits, a.E, a.k, lane, r.sel, r.w);
+      __syncthreads();
+    }
+    // every choice is an item; its place is the number of those that come before it (the same in every warp)
+    const int e = lane < a.k ? r.sel[lane] : 0;
+    int at = 0;
+#pragma unroll
+    for (int q = 0; q < kMaxTopK; ++q)
+      if (q < a.k) at += r.sel[q] < e;
+    if (lane < a.k) {
+      *reinterpret_cast<uint2*>(r.pair[at]) = make_uint2(lane, 0u);
+      *reinterpret_cast<uint32_t*>(r.token[at]) = 0u;
+      r.expert[at] = static_cast<uint8_t>(e);
+      r.count[at] = 1;
+    }
+    r.items = a.k;
+    __syncthreads();
+    return;
+  }
 #pragma unroll 1
   for (int i = tid; i < kMaxExperts; i += n) r.mask[i] = 0u;
 #pragma unroll 1
@@ -143,53 +212,32 @@ __device__ __forceinline__ void form_routing(Routing& r, const Args& a) {
       choose<4>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k);
     else
       choose<8>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k);
+    __syncwarp();
     if (lane < a.k) atomicOr(&r.mask[r.sel[t * a.k + lane]], 1u << t);
   }
   __syncthreads();
-  // every warp forms the same list. Lane l takes the experts 4 l + s of set s, and 128 on; the counts of two
-  // sets at a time go through the scan in the halves of a word
-  static_assert(kSets == 4, "two words of two sets");
-  const int rounds = a.E > 128 ? 2 : 1;
-  int own[2][kSets], before[2][kSets], total[kSets] = {};
+  // every warp forms the same list
+  constexpr int kPer = kMaxExperts / 32;  // lane l takes experts kPer l .. kPer l + 7
+  int own[kPer], sum = 0;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-#pragma unroll
-    for (int s = 0; s < kSets; ++s) {
-      const int e = 128 * half + 4 * lane + s;
-      own[half][s] = e < a.E ? (__popc(r.mask[e]) + kItemTokens - 1) / kItemTokens : 0;
-    }
-    if (half < rounds) {
-      uint32_t v[2] = {static_cast<uint32_t>(own[half][0] | own[half][1] << 16),
-                       static_cast<uint32_t>(own[half][2] | own[half][3] << 16)};
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t o = __shfl_up_sync(0xffffffffu, v[i], off);
-          if (lane >= off) v[i] += o;
-        }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t sum = __shfl_sync(0xffffffffu, v[i], 31);
-        before[half][2 * i] = total[2 * i] + static_cast<int>(v[i] & 0xffffu) - own[half][2 * i];
-        before[half][2 * i + 1] = total[2 * i + 1] + static_cast<int>(v[i] >> 16) - own[half][2 * i + 1];
-        total[2 * i] += sum & 0xffffu;
-        total[2 * i + 1] += sum >> 16;
-      }
-    }
+  for (int j = 0; j < kPer; ++j) {
+    const int e = lane * kPer + j;
+    own[j] = e < a.E ? (__popc(r.mask[e]) + kItemTokens - 1) / kItemTokens : 0;
+    sum += own[j];
   }
-  int first = 0;
+  int incl = sum;
 #pragma unroll
-  for (int s = 0; s < kSets; ++s) {
-    if (lane == 0) r.first[s] = first;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int e = 128 * half + 4 * lane + s;
-      if (half < rounds && e < a.E) r.base[e] = first + before[half][s];
-    }
-    first += total[s];
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
   }
-  if (lane == 0) r.first[kSets] = first;
+  int at = incl - sum;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (lane * kPer + j < a.E) r.base[lane * kPer + j] = at;
+    at += own[j];
+  }
+  if (lane == 31) r.items = incl;
   __syncwarp();
 #pragma unroll 1
   for (int p = tid; p < pairs; p += n) {
@@ -308,24 +356,52 @@ __device__ __forceinline__ void strip_stage(float (&tot)[4], uint32_t at, const 
   }
 }
 
-// The place of column c (0..63 of 64) in h's fragment order: [tq][step][value], value
-// 0..3 the columns 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 of a 16-column step.
-__device__ __forceinline__ int h_place(int c) {
-  const int step = c >> 4, r = c & 15;
-  return ((r & 7) >> 1) * 16 + step * 4 + (r & 1) + 2 * (r >> 3);
+// The byte of column c (0..127 of a stage) of a pair's h, `part` 0 hi and 1 lo: [part][chunk of 64][tq][half][step of
+// two][value], value 0..3 the columns 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9 of a 16-column step. The two halves
+// of lo change places: a warp's reads of hi and lo then meet different banks.
+__device__ __forceinline__ int h_place(int c, int part) {
+  const int step = (c >> 4) & 3, r = c & 15;
+  const int piece = (c >> 6) * 8 + ((r & 7) >> 1) * 2 + (step >> 1);
+  return part * 256 + (piece ^ part) * 16 + (step & 1) * 8 + (r & 1) * 2 + (r >> 3) * 4;
 }
 
 // ------------------------------------------------------------------ gate_up
 //
-// A unit is an item and kPairs x kUpWarps / stage_warps pairs of strips (16 gate and 16 up rows each);
-// warp w takes kPairs pairs, w / stage_warps of them, and the stages w % stage_warps, + stage_warps, ..
-// The fragments of x come from L1.
+// A unit is an item and kPairs pairs of strips (16 gate and 16 up rows each). A group of 4 or 16 warps takes a
+// unit, its warp w the stages w, w + 4 (16), ..; the units are dealt to all groups in turn. Sixteen warps have
+// a unit soonest, four need their barriers and the epilogue less often. Their sums meet in shared
+// memory, of several units before the warps finish them together (after every unit, two or four of
+// sixteen warps would have work, and the others wait). Both group sizes add a strip's stages in the same
+// order: stages q, q + 4, .. one after the other for q = 0..3, then the four sums in a tree.
+// The fragments of x come from L1; a single token's are the same for all units and loaded once.
+constexpr int kRoundStrips = 8;  // strips of a warp in a round of a group of 16; half of it for 4
+// words of a warp's sums: [strip][value][token / 2][row], shifted by eight banks from warp to warp
+constexpr int kRedWarp = kRoundStrips * 4 * 16 + 8;
+
+// Fragments of x of a stage, and its sums over the groups: a product with ones (in the units of the codes).
+__device__ __forceinline__ void load_x(const uint32_t* row, bool on, uint32_t (&b)[8][2]) {
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+    for (int v = 0; v < 2; ++v) b[kk][v] = on ? row[kk * 8 + v * 4] : 0u;
+}
+template <bool kBf16, int NG>
+__device__ __forceinline__ void sum_x(const uint32_t (&b)[8][2], float (&sum)[NG][2]) {
+  const uint32_t ones[4] = {kOne<kBf16>, kOne<kBf16>, kOne<kBf16>, kOne<kBf16>};
+#pragma unroll
+  for (int j = 0; j < NG; ++j) {
+    float part[4] = {};
+#pragma unroll
+    for (int q = 0; q < 8 / NG; ++q) mma<kBf16>(part, ones, b[j * (8 / NG) + q][0], b[j * (8 / NG) + q][1]);
+    sum[j][0] = part[0];
+    sum[j][1] = part[1];
+  }
+}
+
 template <bool kBf16, int G, int kPairs>
-__global__ void __launch_bounds__(kUpThreads) few_gate_up_kernel(const Args a) {
-  constexpr int NG = kStageCols / G, kStripBytes = 1024 + 64 * NG, kSlot = 2 * kPairs * kStripBytes;
-  constexpr int kType = kBf16 ? 1 : 0, kStrips = 2 * kPairs;
-  // words of a warp's sums: [strip][value][token / 2][row], shifted by eight banks from warp to warp
-  constexpr int kRedWarp = kStrips * 4 * 16 + 8;
+__global__ void __launch_bounds__(kUpThreads, kPairs == 1 ? 2 : 1) few_gate_up_kernel(const Args a) {
+  constexpr int NG = kStageCols / G, kStripBytes = 1024 + 64 * NG, kStrips = 2 * kPairs, kSlot = kStrips * kStripBytes;
+  constexpr int kType = kBf16 ? 1 : 0;
   extern __shared__ __align__(16) uint8_t smem[];  // rings
   __shared__ Routing r;
   __shared__ float red[kUpWarps * kRedWarp];
@@ -335,40 +411,51 @@ __global__ void __launch_bounds__(kUpThreads) few_gate_up_kernel(const Args a) {
   grid_dependency_wait();    // the logits, x, and h, which the call before may still read
   grid_dependents_launch();  // only now: the down launch reads logits and weights before it waits
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int S = a.K / kStageCols;
+  const int S = a.K / kStageCols, W = a.stage_warps, my_stage = warp & (W - 1);
+  const bool wide = W == kUpWarps;  // one group of 16, else four of 4
+  const int team = wide ? 0 : warp >> 2, round = (wide ? kRoundStrips : kRoundStrips / 2) / kStrips;
+  const auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(W * 32) : "memory"); };
   const uint32_t ring = smem_addr(smem) + warp * a.depth * kSlot;
-  const auto* const x = static_cast<const uint32_t*>(a.x);
-  form_routing(r, a);
-  const int items = r.first[kSets], W = a.stage_warps, my_pair = warp / W, my_stage = warp & (W - 1);
+  const auto* const x = static_cast<const uint32_t*>(a.x) + (lane & 3);
+  uint32_t b[8][2], next[8][2];  // fragments of x, with two pairs loaded a piece ahead
+  float sum[NG][2];
+  const bool fixed = a.T == 1 && S <= W;
+  if (fixed && my_stage < S) {
+    load_x(x + my_stage * 64, lane < 4, b);
+    sum_x<kBf16, NG>(b, sum);
+  }
+  const auto load = [&](int i, int stage, uint32_t (&f)[8][2]) {  // columns behind the item's tokens are not used
+    load_x(x + static_cast<size_t>(r.token[i][(lane >> 2) & 3]) * (a.d / 2) + stage * 64, (lane >> 2) < r.count[i], f);
+  };
+  form_routing(r, a, smem);
+  const int items = r.items, pairs = a.T * a.k, unit0 = blockIdx.x * (wide ? 1 : 4) + team;
 
   // the piece to request next
-  int pi = static_cast<int>((blockIdx.x + 0.5f) * a.per_item_inv), pg = blockIdx.x - pi * a.per_item;  // exact: below 2^12
+  int pi = static_cast<int>((unit0 + 0.5f) * a.per_item_inv), pg = unit0 - pi * a.per_item;  // exact: below 2^12
   int ps = my_stage, pslot = 0;
   int item = pi, group = pg, slot = 0, ahead = a.depth - 1;
-  const uint32_t warp_pair = my_pair * kPairs, unit_pairs = kPairs * (kUpWarps / W);
-  float tot[kStrips][4];
-#pragma unroll
-  for (int h = 0; h < kStrips; ++h)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tot[h][i] = 0.f;
-  int s = my_stage;
-  bool first_piece = true;
+  float tot[kStrips][4] = {};
+  int s = my_stage, in_round = 0, round_item = item, round_group = group;
+  bool first_piece = true, first_x = true;
+  const auto step = [&](int& i, int& g) {
+    i += a.step_items;
+    g += a.step_rest;
+    if (g >= a.per_item) {
+      g -= a.per_item;
+      ++i;
+    }
+  };
 #pragma unroll 1
   while (true) {
     if (pi < items && ps < S) {
-      const uint32_t pair = pg * unit_pairs + warp_pair;
+      const uint32_t pair = pg * kPairs;
       const uint32_t off = r.expert[pi] * a.expert16 + (pair >> 2) * a.block16 +
                            static_cast<uint32_t>(ps) * (8 * kStripBytes / 16) + (pair & 3) * (2 * kStripBytes / 16);
       copy_warp<kSlot>(ring + pslot * kSlot, a.w + static_cast<size_t>(off) * 16, lane);
       ps += W;
       if (ps >= S) {
         ps = my_stage;
-        pi += a.step_items;
-        pg += a.step_rest;
-        if (pg >= a.per_item) {
-          pg -= a.per_item;
-          ++pi;
-        }
+        step(pi, pg);
       }
       if (++pslot == a.depth) pslot = 0;
     }
@@ -379,106 +466,119 @@ __global__ void __launch_bounds__(kUpThreads) few_gate_up_kernel(const Args a) {
     }
     if (first_piece) {  // what others want of the routing, while the first pieces arrive
       first_piece = false;
-      if (blockIdx.x == 0)
-#pragma unroll 1
-        for (int i = tid; i < a.T * a.k; i += kUpThreads) {
-          if (a.topk_idx) a.topk_idx[i] = r.sel[i];
-          if (a.topk_w) a.topk_w[i] = r.w[i];
-        }
       if (a.listed && blockIdx.x == gridDim.x - 1)
 #pragma unroll 1
         for (int i = tid; i < static_cast<int>(sizeof(Routing) / 16); i += kUpThreads)
           reinterpret_cast<uint4*>(a.routing)[i] = reinterpret_cast<const uint4*>(&r)[i];
-    }
-    if (item >= items) break;
-    if (s < S) {  // (a warp without a stage takes part in the sums alone)
-      uint32_t b[8][2];
-      const bool on = (lane >> 2) < r.count[item];  // columns behind the item's tokens are not used
-      const uint32_t* const row =
-          x + static_cast<size_t>(r.token[item][(lane >> 2) & 3]) * (a.d / 2) + s * 64 + (lane & 3);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) b[kk][v] = on ? row[kk * 8 + v * 4] : 0u;
-      // the sums of x over the groups: a product with ones (in the units of the codes)
-      const uint32_t ones[4] = {kOne<kBf16>, kOne<kBf16>, kOne<kBf16>, kOne<kBf16>};
-      float sum[NG][2];
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        float part[4] = {};
-#pragma unroll
-        for (int q = 0; q < 8 / NG; ++q) mma<kBf16>(part, ones, b[j * (8 / NG) + q][0], b[j * (8 / NG) + q][1]);
-        sum[j][0] = part[0];
-        sum[j][1] = part[1];
+      if (blockIdx.x == 0) {
+        __syncthreads();
+#pragma unroll 1
+        for (int t = warp; t < a.T; t += kUpWarps) {
+          weigh(r.w + t * a.k, a.k, lane);
+          if (lane < a.k && a.topk_idx) a.topk_idx[t * a.k + lane] = r.sel[t * a.k + lane];
+          if (lane < a.k && a.topk_w) a.topk_w[t * a.k + lane] = r.w[t * a.k + lane];
+        }
       }
-      wait_piece(a.depth);
-      __syncwarp();
-      const uint32_t at = ring + slot * kSlot;
-#pragma unroll kPairs == 1 ? 1 : kStrips
-      for (int h = 0; h < kStrips; ++h) {
-        float t[4] = {};
-        strip_stage<kBf16, G, 8>(t, at + h * kStripBytes, b, sum, lane, a.affine);
-#pragma unroll
-        for (int g = 0; g < kStrips; ++g)
-          if (g == h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tot[g][i] += t[i];
-      }
-      __syncwarp();  // the slot is read before it is requested again
-      if (++slot == a.depth) slot = 0;
-      s += W;
-      if (s < S) continue;
     }
-    __syncthreads();  // the unit before has been finished
-    if ((lane & 3) < 2)
+    if (item < items) {
+      if (s < S) {  // (a warp without a stage takes part in the sums alone)
+        if (!fixed) {
+          if (kPairs == 1) load(item, s, b);
+          if (kPairs == 2) {
+            if (first_x) load(item, s, next);
+            first_x = false;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+              for (int v = 0; v < 2; ++v) b[kk][v] = next[kk][v];
+            int i = item, g = group, st = s + W;
+            if (st >= S) {
+              st = my_stage;
+              step(i, g);
+            }
+            if (i < items) load(i, st, next);
+          }
+          sum_x<kBf16, NG>(b, sum);
+        }
+        wait_piece(a.depth);
+        __syncwarp();
+        const uint32_t at = ring + slot * kSlot;
+#pragma unroll
+        for (int h = 0; h < kStrips; ++h) {
+          float t[4] = {};
+          strip_stage<kBf16, G, 8>(t, at + h * kStripBytes, b, sum, lane, a.affine);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tot[h][i] += t[i];
+        }
+        __syncwarp();  // the slot is read before it is requested again
+        if (++slot == a.depth) slot = 0;
+        s += W;
+        if (s < S) continue;
+      }
+      s = my_stage;
+      if (in_round == 0) team_sync();  // the round before has been finished
+      if ((lane & 3) < 2)
+#pragma unroll
+        for (int h = 0; h < kStrips; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            red[warp * kRedWarp + ((in_round * kStrips + h) * 4 + i) * 16 + (lane & 3) * 8 + (lane >> 2)] = tot[h][i];
 #pragma unroll
       for (int h = 0; h < kStrips; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          red[warp * kRedWarp + (h * 4 + i) * 16 + (lane & 3) * 8 + (lane >> 2)] = tot[h][i];
-    __syncthreads();
-    // h of token n and column c: four threads add the sums of every fourth warp
-    constexpr int kToken = 64 * kPairs;  // threads of a token
-    const int n = tid / kToken, c = (tid % kToken) >> 2, q = tid & 3;
-    if (n < r.count[item])  // whole warps (and n < 4)
+        for (int i = 0; i < 4; ++i) tot[h][i] = 0.f;
+      step(item, group);
+      ++in_round;
+      if (in_round < round && item < items) continue;
+    } else if (in_round == 0) {
+      break;
+    }
+    team_sync();
+    // Each warp takes a unit of the round, one of its strips and every second (or every) token: h of 8 columns, the
+    // warps' sums of a column added by four lanes, every fourth warp's by each.
+    const int local = warp & (W - 1), mine = local & (round - 1), sub = local / round;
+    const int h = sub & (kStrips - 1), c = lane >> 2, q = lane & 3;
+    if (mine < in_round) {
+      int i = round_item, g = round_group;
 #pragma unroll 1
-      for (int m = 0; m < kUpWarps / W; ++m) {
-        float gate = 0.f, up = 0.f;
+      for (int j = 0; j < mine; ++j) step(i, g);
 #pragma unroll 1
-        for (int w = m * W + q; w < (m + 1) * W; w += 4) {
-          const float* const p = red + w * kRedWarp + ((c >> 3) * 4 + (n & 1)) * 16 + (n >> 1) * 8 + (c & 7);
-          gate += p[0];
-          up += p[32];
+      for (int n = sub / kStrips; n < r.count[i]; n += wide ? 2 : 1) {
+        const float* const p =
+            red + (warp - local) * kRedWarp + ((mine * kStrips + h) * 4 + (n & 1)) * 16 + (n >> 1) * 8 + c;
+        float gate[kUpWarps / 4], up[kUpWarps / 4];
+#pragma unroll
+        for (int w = 0; w < kUpWarps / 4; ++w) {
+          const bool on = q + 4 * w < W;
+          gate[w] = on ? p[(q + 4 * w) * kRedWarp] : 0.f;
+          up[w] = on ? p[(q + 4 * w) * kRedWarp + 32] : 0.f;
+        }
+#pragma unroll
+        for (int w = 1; w < kUpWarps / 4; ++w) {
+          gate[0] += gate[w];
+          up[0] += up[w];
         }
 #pragma unroll
         for (int off = 1; off < 4; off <<= 1) {
-          gate += __shfl_xor_sync(0xffffffffu, gate, off);
-          up += __shfl_xor_sync(0xffffffffu, up, off);
+          gate[0] += __shfl_xor_sync(0xffffffffu, gate[0], off);
+          up[0] += __shfl_xor_sync(0xffffffffu, up[0], off);
         }
         constexpr float kBack = 1.f / kUnit<kBf16>;
-        const float v = activate(gate * kBack, a.act) * (up * kBack);
+        const float v = activate(gate[0] * kBack, a.act) * (up[0] * kBack);
         const uint16_t hi = to16<kType>(v), lo = to16<kType>(v - from16<kType>(hi));
-        float sum = from16<kType>(hi) + from16<kType>(lo);
+        const int col = 16 * (g * kPairs) + 8 * h + c;
+        const size_t at = static_cast<size_t>(col >> 7) * pairs + r.pair[i][n];
+        if (q < 2) *reinterpret_cast<uint16_t*>(a.h + at * kPairBytes + h_place(col & 127, q)) = q ? lo : hi;
+        float sums = from16<kType>(hi) + from16<kType>(lo);
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const size_t p = r.pair[item][n];
-        const int col = 16 * static_cast<int>(group * unit_pairs + m * kPairs) + c;
-        uint16_t* const dst = a.h + p * 2 * a.f + (col & ~63) + h_place(col & 63);
-        if (q == 0) dst[0] = hi;
-        if (q == 1) dst[a.f] = lo;
-        if (lane == 0) a.hsum[p * (a.f / 8) + col / 8] = sum * kUnit<kBf16>;
+        for (int off = 4; off < 32; off <<= 1) sums += __shfl_xor_sync(0xffffffffu, sums, off);
+        if (lane == 0) a.hsum[at * 16 + ((col & 127) >> 3)] = sums * kUnit<kBf16>;
       }
-#pragma unroll
-    for (int h = 0; h < kStrips; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tot[h][i] = 0.f;
-    s = my_stage;
-    item += a.step_items;
-    group += a.step_rest;
-    if (group >= a.per_item) {
-      group -= a.per_item;
-      ++item;
     }
+    in_round = 0;
+    round_item = item;
+    round_group = group;
+    if (item >= items) break;
   }
   cp_async_wait<0>();
 }
@@ -486,27 +586,26 @@ __global__ void __launch_bounds__(kUpThreads) few_gate_up_kernel(const Args a) {
 // --------------------------------------------------------------------- down
 //
 // A CTA takes up to 2 kDownMaxPairs strips of 16 rows and one stage of 128 columns of every item (the
-// stages rank, + cluster, .. of its cluster), kSets warps per pair of strips, each for the items of the
-// experts of its own number modulo kSets. h of the stage is held for all pairs. At the end the
-// cluster's CTAs add up their sums, each for a part of the outputs.
+// stages rank, + cluster, .. of its cluster), kDownWarps warps per pair of strips, each for every fourth
+// item. h of the stage is held for all pairs, and so are the products' rows: a token's are then
+// added in its experts' rank order, whichever warp made them. At the end the cluster's CTAs add up their
+// sums, each for a part of the outputs.
 template <bool kBf16, int G>
-__global__ void __launch_bounds__(kDownMaxPairs * kSets * 32) few_down_kernel(const Args a) {
+__global__ void __launch_bounds__(kDownMaxPairs * kDownWarps * 32, 2) few_down_kernel(const Args a) {
   constexpr int kMaxNg = kStageCols / G, kStrip = 1024 + 64 * kMaxNg, kSlot = 2 * kStrip, kType = kBf16 ? 1 : 0;
   constexpr int kHalfNg = G < 64 ? 2 : 1, kHalfStrip = 512 + 64 * kHalfNg;  // a last stage of 64 columns
-  // h [pairs][512] | rings | sums of h [pairs][groups of a stage] | acc [warps][T][33]
+  // h [pairs][512] | rings | sums of h [pairs][groups of a stage] | rows [pairs of strips][pairs][33]
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Routing r;
   grid_dependents_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
   const int C = a.cluster, rank = static_cast<int>(cluster_rank()), tile = static_cast<int>(blockIdx.x) / C;
   const int S = (a.K + kStageCols - 1) / kStageCols, pairs = a.T * a.k;
-  const int set = warp & (kSets - 1), strip = tile * a.strips + (warp / kSets) * 2;
+  const int turn = warp & (kDownWarps - 1), strip = tile * a.strips + (warp / kDownWarps) * 2;
   const uint32_t hs = smem_addr(smem), ring = hs + pairs * kPairBytes + warp * a.depth * kSlot;
   float* const hsum = reinterpret_cast<float*>(smem + pairs * kPairBytes + warps * a.depth * kSlot);
   float* const all = hsum + pairs * kMaxNg;
-  float* const acc = all + warp * a.T * kAccRow;
-#pragma unroll 1
-  for (int i = lane; i < a.T * kAccRow; i += 32) acc[i] = 0.f;
+  float* const rows = all + (warp / kDownWarps) * pairs * kRowWords + (lane >> 2);
   if (a.listed) {  // it could not start beside the gate_up launch: the lists are there
     grid_dependency_wait();
 #pragma unroll 1
@@ -514,57 +613,60 @@ __global__ void __launch_bounds__(kDownMaxPairs * kSets * 32) few_down_kernel(co
       reinterpret_cast<uint4*>(&r)[i] = __ldcg(reinterpret_cast<const uint4*>(a.routing) + i);
     __syncthreads();
   } else {
-    form_routing(r, a);
+    form_routing(r, a, smem);
   }
-  const int i0 = r.first[set], i1 = strip * 16 >= a.d ? i0 : r.first[set + 1];  // no items for strips behind the last one
+  const int items = strip * 16 >= a.d ? 0 : r.items;  // no items for strips behind the last one
+  bool weighed = false;
 #pragma unroll 1
   for (int s = rank; s < S; s += C) {
     const bool whole = (s + 1) * kStageCols <= a.K;
     const uint8_t* const src = a.w + (static_cast<size_t>(strip >> 3) * a.block16 + s * (8 * kStrip / 16) +
                                       (strip & 7) * ((whole ? kStrip : kHalfStrip) / 16)) * 16;
-    int pi = i0, pslot = 0, slot = 0, item = i0, ahead = a.depth - 1;
+    int put = turn, pslot = 0, slot = 0, item = turn, ahead = a.depth - 1;
 #pragma unroll 1
     while (true) {
-      if (pi < i1) {
-        const uint8_t* const from = src + static_cast<size_t>(r.expert[pi] * a.expert16) * 16;
+      if (put < items) {
+        const uint8_t* const from = src + static_cast<size_t>(r.expert[put] * a.expert16) * 16;
         if (whole)
           copy_warp<kSlot>(ring + pslot * kSlot, from, lane);
         else
           copy_warp<2 * kHalfStrip>(ring + pslot * kSlot, from, lane);
-        ++pi;
+        put += kDownWarps;
         if (++pslot == a.depth) pslot = 0;
       }
       cp_async_commit();
       if (ahead > 0) {
         if (--ahead > 0) continue;
+        if (!weighed)
+#pragma unroll 1
+          for (int t = warp; t < a.T; t += warps) weigh(r.w + t * a.k, a.k, lane);
+        weighed = true;
         if (s == rank)
           grid_dependency_wait();  // h
         else
           __syncthreads();  // h of the stage before has been read
-        const int per = whole ? 32 : 16;  // 16-byte pieces of a pair: [hi, lo][chunk][tq][half]
-#pragma unroll 1
-        for (int i = tid; i < pairs * per; i += threads) {
-          const int p = whole ? i >> 5 : i >> 4, j = i & (per - 1), part = j >= per / 2, rest = j & (per / 2 - 1);
-          // the two halves change places in lo's rows, which would meet hi's banks
-          cp_async_16(hs + p * kPairBytes + part * 256 + ((rest ^ part) * 16),
-                      a.h + (static_cast<size_t>(p) * 2 + part) * a.f + s * kStageCols + rest * 8);
-        }
+        const uint8_t* const h = a.h + static_cast<size_t>(s) * pairs * kPairBytes;
+#pragma unroll 4
+        for (int i = tid; i < pairs * (kPairBytes / 16); i += threads) cp_async_16(hs + i * 16, h + i * 16);
         cp_async_commit();
         const int ng = whole ? kMaxNg : kHalfNg, eights = (whole ? kStageCols / kMaxNg : 64 / kHalfNg) / 8;
 #pragma unroll 1
         for (int i = tid; i < pairs * ng; i += threads) {
-          const int p = i / ng, j = i - p * ng;
-          const float* const part = a.hsum + p * (a.f / 8) + s * 16 + j * eights;
+          const int p = whole ? i / kMaxNg : i / kHalfNg, j = i - p * ng;
+          const float* const part = a.hsum + (static_cast<size_t>(s) * pairs + p) * 16 + j * eights;
           float v = 0.f;
-#pragma unroll 8
-          for (int q = 0; q < eights; ++q) v += __ldcg(part + q);
+#pragma unroll 4
+          for (int q = 0; q < eights; q += 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(part + q));
+            v += (f.x + f.y) + (f.z + f.w);
+          }
           hsum[p * kMaxNg + j] = v;
         }
         cp_async_wait<0>();
         __syncthreads();
         continue;
       }
-      if (item >= i1) break;
+      if (item >= items) break;
       const int mine = r.pair[item][lane >> 3], p = r.pair[item][lane & 3];
       const uint32_t hat = hs + mine * kPairBytes + ((lane >> 2) & 1) * 256 + (lane & 3) * 32;
       uint32_t b[8][2];
@@ -576,19 +678,18 @@ __global__ void __launch_bounds__(kDownMaxPairs * kSets * 32) few_down_kernel(co
         b[kk + 1][0] = v.z;
         b[kk + 1][1] = v.w;
       }
-      wait_piece(a.depth);
-      __syncwarp();
-      const uint32_t at = ring + slot * kSlot;
-      const bool on = (lane & 3) < r.count[item];
-      const float weight = r.w[p];
       float sum[kMaxNg][2];
 #pragma unroll
       for (int j = 0; j < kMaxNg; ++j) {
         sum[j][0] = hsum[p * kMaxNg + j];
         sum[j][1] = 0.f;
       }
-      float* const dst = acc + r.token[item][lane & 3] * kAccRow + (lane >> 2);
-#pragma unroll 1
+      wait_piece(a.depth);
+      __syncwarp();
+      const uint32_t at = ring + slot * kSlot;
+      const bool on = (lane & 3) < r.count[item];
+      float* const dst = rows + p * kRowWords;
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
         // columns 2 n and 2 n + 1 are token n's hi and lo: their sum counts, and the sum of h once
         float t[4] = {};
@@ -604,27 +705,33 @@ __global__ void __launch_bounds__(kDownMaxPairs * kSets * 32) few_down_kernel(co
           }
           strip_stage<kBf16, G, 4>(t, at + h * kHalfStrip, half, part, lane, a.affine);
         }
-        if (on) {
-          dst[16 * h] = fmaf(weight, t[0] + t[1], dst[16 * h]);
-          dst[16 * h + 8] = fmaf(weight, t[2] + t[3], dst[16 * h + 8]);
+        if (on) {  // (stages of the CTA after its first are added to it)
+          const float lo = t[0] + t[1], hi = t[2] + t[3];
+          dst[16 * h] = s == rank ? lo : dst[16 * h] + lo;
+          dst[16 * h + 8] = s == rank ? hi : dst[16 * h + 8] + hi;
         }
       }
       __syncwarp();
       if (++slot == a.depth) slot = 0;
-      ++item;
+      item += kDownWarps;
     }
     cp_async_wait<0>();
   }
   __syncthreads();
-  // the CTA's sums over its sets, in their order: 32 columns of a pair of strips by a warp
-  const int row = a.T * kAccRow, pair_groups = warps / kSets;
+  // a token's rows over its experts in rank order, into its first pair's place: 32 columns by a warp
+  const int strip_pairs = warps / kDownWarps;
 #pragma unroll 1
-  for (int t = warp; t < a.T; t += warps)
-#pragma unroll 2
-    for (int g = 0; g < pair_groups; ++g) {
-      float* const at = all + g * (kSets * row) + t * kAccRow + lane;
-      at[0] = ((at[0] + at[row]) + at[2 * row]) + at[3 * row];
-    }
+  for (int o = warp; o < a.T * strip_pairs; o += warps) {
+    const int t = o / strip_pairs, g = o - t * strip_pairs;
+    float* const at = all + (g * pairs + t * a.k) * kRowWords + lane;
+    float part[kMaxTopK], v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kMaxTopK; ++q) part[q] = q < a.k ? at[q * kRowWords] : 0.f;
+#pragma unroll
+    for (int q = 0; q < kMaxTopK; ++q)
+      if (q < a.k) v = fmaf(r.w[t * a.k + q], part[q], v);
+    at[0] = v;
+  }
   if (C > 1)
     cluster_sync();
   else
@@ -632,10 +739,10 @@ __global__ void __launch_bounds__(kDownMaxPairs * kSets * 32) few_down_kernel(co
   // (token, pair of strips) by a warp of the cluster
   const int cols = a.strips * 16;
 #pragma unroll 1
-  for (int o = rank * warps + warp; o < a.T * pair_groups; o += C * warps) {
-    const int t = o / pair_groups, g = o - t * pair_groups, col = tile * cols + g * 32 + lane;
+  for (int o = rank * warps + warp; o < a.T * strip_pairs; o += C * warps) {
+    const int t = o / strip_pairs, g = o - t * strip_pairs, col = tile * cols + g * 32 + lane;
     if (col >= a.d) continue;
-    const uint32_t at = smem_addr(all + g * (kSets * row) + t * kAccRow + lane);
+    const uint32_t at = smem_addr(all + (g * pairs + t * a.k) * kRowWords + lane);
     float part[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -655,9 +762,8 @@ __global__ void __launch_bounds__(kDownMaxPairs * kSets * 32) few_down_kernel(co
 }
 
 constexpr int kSmemLimit = 226 * 1024;  // of a CTA, static and dynamic
-constexpr int up_static(int pairs) { return int(sizeof(Routing)) + kUpWarps * (pairs * 128 + 8) * 4 + 64; }
+constexpr int kUpStatic = sizeof(Routing) + kUpWarps * kRedWarp * 4 + 64;
 constexpr int kDownStatic = sizeof(Routing) + 64;
-constexpr int kEarlyTokens = 8;  // tokens up to which the down launch starts beside the gate_up launch
 int g_clusters[9];  // clusters of so many CTAs of the down kernel that run at a time
 
 using Kernel = void (*)(Args);
@@ -697,9 +803,8 @@ struct DownLaunch {
 }  // namespace
 
 // Workspace: routing lists | h | sums of h.
-size_t few_ws_bytes(const Dims& s) {
-  return sizeof(Routing) + size_t(s.pairs()) * s.f * 4 + size_t(s.pairs()) * (s.f / 8) * 4;
-}
+static int down_stages(const Dims& s) { return (s.f + kStageCols - 1) / kStageCols; }
+size_t few_ws_bytes(const Dims& s) { return sizeof(Routing) + size_t(down_stages(s)) * s.pairs() * (kPairBytes + 64); }
 
 // Room for the kernel's shared memory, and an SM divided for as much of it as there is: a CTA of the down launch
 // that finds it divided otherwise waits until the SM is empty.
@@ -716,12 +821,12 @@ cudaError_t init_few_kernels() {
     for (int g : {32, 64, 128}) {
       for (int pairs : {1, 2})
         if (e == cudaSuccess)
-          e = set_up(gate_up_of(type, g, pairs), kSmemLimit - up_static(pairs));
+          e = set_up(gate_up_of(type, g, pairs), kSmemLimit - kUpStatic);
       if (e == cudaSuccess)
         e = set_up(down_of(type, g), kSmemLimit - kDownStatic);
     }
   for (int c = 1; c <= 8 && e == cudaSuccess; ++c) {
-    const DownLaunch l(1, c, 3 * kSets * 32, 128 * 1024, nullptr);
+    const DownLaunch l(1, c, 3 * kDownWarps * 32, 128 * 1024, nullptr);
     e = cudaOccupancyMaxActiveClusters(&g_clusters[c], down_of(0, 64), &l.cfg);
   }
   return e;
@@ -739,8 +844,8 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.topk_w = topk_w;
   a.out = out;
   a.routing = workspace;
-  a.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + sizeof(Routing));
-  a.hsum = reinterpret_cast<float*>(a.h + size_t(pairs) * 2 * s.f);
+  a.h = static_cast<uint8_t*>(workspace) + sizeof(Routing);
+  a.hsum = reinterpret_cast<float*>(a.h + size_t(down_stages(s)) * pairs * kPairBytes);
   a.T = s.T;
   a.d = s.d;
   a.f = s.f;
@@ -749,37 +854,50 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.act = s.act;
   a.affine = s.fmt == 1;
   // The down launch: the fewest strips per CTA for which all clusters run at a time.
-  const int strips = s.d / 16, down_stages = (s.f + kStageCols - 1) / kStageCols;
-  a.cluster = down_stages < 8 ? down_stages : 8;
+  const int strips = s.d / 16;
+  a.cluster = std::min(down_stages(s), 8);
   a.strips = 2;
   while (a.strips < 2 * kDownMaxPairs && (strips + a.strips - 1) / a.strips > g_clusters[a.cluster]) a.strips += 2;
   const int slot = 2 * (1024 + 64 * (kStageCols / s.g2)), fixed = pairs * (kPairBytes + kStageCols / s.g2 * 4);
   const auto room = [&](int limit) {  // pieces of a warp that fit
-    const int warps = a.strips / 2 * kSets;
-    return (limit - kDownStatic - fixed - warps * s.T * kAccRow * 4) / (warps * slot);
+    return (limit - kDownStatic - fixed - a.strips / 2 * pairs * kRowWords * 4) / (a.strips / 2 * kDownWarps * slot);
   };
-  // For few tokens it fits beside a shallow gate_up ring, and its start is hidden; otherwise it gets the lists from
-  // the gate_up launch.
-  const int stages = s.d / kStageCols;
-  a.stage_warps = stages >= 12 ? 16 : stages >= 6 ? 8 : 4;
-  const int shares = kUpWarps / a.stage_warps, piece = kUpWarps * 2 * (1024 + 64 * (kStageCols / s.g1));
-  const auto beside = [&](int depth) { return kSmemLimit - up_static(1) - depth * piece; };
-  const int up_depth = room(beside(3)) >= 2 ? 3 : 2;
-  a.listed = s.T > kEarlyTokens || room(beside(up_depth)) < 2;
+  // With one or two tokens it fits beside the gate_up launch, and its start is hidden; otherwise it gets the
+  // lists from the gate_up launch.
+  const int stages = s.d / kStageCols, piece = kUpWarps * 2 * (1024 + 64 * (kStageCols / s.g1));
+  const int beside = kSmemLimit - kUpStatic - 3 * piece;
+  a.listed = room(beside) < 2;
   while (a.listed && a.strips > 2 && room(kSmemLimit) < 2) a.strips -= 2;
-  const int down_depth = std::min(room(a.listed ? kSmemLimit : beside(up_depth)), kMaxDepth);
-  // gate_up: two pairs per warp halve what a unit costs beside its weights, where the units are many
-  const int per_warp = a.listed && pairs * (s.f / 16 / shares) >= 16 * num_sms && s.f / 16 % (2 * shares) == 0 ? 2 : 1;
+  const int down_depth = std::min(room(a.listed ? kSmemLimit : beside), kMaxDepth);
+  // gate_up: the group size and the pairs of strips per unit that take the least time, counted in pieces of one
+  // pair: two pairs at once take 1.6, a unit's barriers and epilogue 1 of a small group and 0.5 of a
+  // large one. (Which experts meet is not known here; their number is about that of evenly chosen ones.)
+  const double items = s.E * (1.0 - std::pow(1.0 - double(s.k) / s.E, s.T));
+  double least = 1e30;
+  int per_warp = 1;
+  a.stage_warps = kUpWarps;
+  for (int w : {kUpWarps, 4})
+    for (int p : {1, 2}) {
+      if ((w == 4 && stages > kUpWarps) || (p == 2 && !a.listed)) continue;  // (the sums' order; registers)
+      const double turns = std::ceil(items * (s.f / 16 / p) / (num_sms * (kUpWarps / w)));
+      const double time = turns * ((stages + w - 1) / w * (p == 2 ? 1.6 : 1.0) + (w == 4 ? 1.0 : 0.5));
+      if (time < least) {
+        least = time;
+        per_warp = p;
+        a.stage_warps = w;
+      }
+    }
   a.w = w_gate_up;
   a.K = s.d;
   a.block16 = uint32_t(kBlockRows) * (s.d / 2 + s.d / s.g1 * 4) / 16;
   a.expert16 = a.block16 * (s.f / 64);
-  a.per_item = s.f / 16 / (per_warp * shares);
+  a.per_item = s.f / 16 / per_warp;
   a.per_item_inv = 1.f / a.per_item;
-  const int units = pairs * a.per_item, grid = units < num_sms ? units : num_sms;
-  a.step_items = grid / a.per_item;
-  a.step_rest = grid % a.per_item;
-  a.depth = a.listed ? std::min((kSmemLimit - up_static(per_warp)) / (per_warp * piece), 3) : up_depth;
+  const int teams = kUpWarps / a.stage_warps, units = pairs * a.per_item;
+  const int grid = std::min((units + teams - 1) / teams, num_sms);
+  a.step_items = grid * teams / a.per_item;
+  a.step_rest = grid * teams % a.per_item;
+  a.depth = a.listed ? std::min((kSmemLimit - kUpStatic) / (per_warp * piece), 3) : 3;
   cudaError_t err = launch_pdl(gate_up_of(type, s.g1, per_warp), dim3(grid), dim3(kUpThreads),
                                size_t(a.depth) * per_warp * piece, st, a);
   if (err != cudaSuccess) return err;
@@ -788,9 +906,9 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.block16 = uint32_t(kBlockRows) * (s.f / 2 + s.f / s.g2 * 4) / 16;
   a.expert16 = a.block16 * (s.d / kBlockRows);
   a.depth = down_depth;
-  const int warps = a.strips / 2 * kSets;
+  const int warps = a.strips / 2 * kDownWarps;
   const DownLaunch l((strips + a.strips - 1) / a.strips, a.cluster, warps * 32,
-                     size_t(fixed) + warps * (a.depth * slot + s.T * kAccRow * 4), st);
+                     size_t(fixed) + warps * a.depth * slot + a.strips / 2 * pairs * kRowWords * 4, st);
   return cudaLaunchKernelEx(&l.cfg, down_of(type, s.g2), a);
 }
 

@@ -228,7 +228,7 @@ cudaError_t launch_linear_dbias(const LinearDims& s, const int32_t* offsets, con
                                 cudaStream_t st);
 
 // The norms around a block and their gradient (norm.cu).
-constexpr int kNormCtas = 304;  // CTAs of the gradient at most: two on each of 152 SMs
+constexpr int kNormSms = 152;  // the SMs that the rows are dealt to
 struct NormDims {
   int R, d, type, gate_rows;  // type: 0 fp16, 1 bf16, 2 fp32
   float scale, eps;

@@ -9,9 +9,16 @@
 //   dv = gate g       dy = r1 (gamma_post dv - m mean(m gamma_post dv))
 //   dgamma_pre = sum du n,  dgamma_post = sum dv m,  dgate = sum g v  (over the rows they are shared by)
 //
-// Both directions read every row once and hold it in registers until its sums are known, so they
-// move 4 and 6 rows per row and are bound by memory; the arithmetic is a dozen operations an element.
-// Everything between load and store is fp32; u is the norm of the unrounded out.
+// Both directions read every row once, 4 and 6 rows of memory traffic per row, and are bound by memory.
+// A group of threads, a multiple of 32 that covers a row with kPieces 16-byte pieces each, takes a
+// contiguous run of rows (a "unit"): a thread's columns stay the same, and with them the weights in
+// its registers. Rows arrive by cp.async in a ring, several ahead; a thread copies what it will
+// read itself, so the ring needs no barrier. (Loads into registers a row ahead reached 4.9 TB/s: an SM
+// needs some 60 KB in flight all the time.) The arithmetic is fp32 from load to store, on pairs (the
+// gradient spent 53 instructions an element, 63 % of the issue slots, one value at a time); u is the
+// norm of the unrounded out.
+#include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "internal.h"
@@ -21,153 +28,65 @@
 namespace moe {
 namespace {
 
-struct Args {
-  const uint4 *x, *y;
-  const float *gamma_post, *gate, *gamma_pre;
-  uint4 *out, *u;
-  int R, d, nvec, gate_rows;
-  float scale, eps;
+constexpr int kMaxThreads = 512;
+
+// Two fp32 values in one operation each.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// 16 bytes of a row as pairs, and back.
+template <int kType>
+struct Pairs {
+  static constexpr int n = Vec<kType>::n / 2;
+  static __device__ __forceinline__ void load(uint32_t addr, float2 (&p)[n]) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    float f[2 * n];
+    Vec<kType>::load(v, f);
+#pragma unroll
+    for (int i = 0; i < n; ++i) p[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  }
+  static __device__ __forceinline__ uint4 store(const float2 (&p)[n]) {
+    float f[2 * n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      f[2 * i] = p[i].x;
+      f[2 * i + 1] = p[i].y;
+    }
+    return Vec<kType>::store(f);
+  }
 };
-
-template <int N>
-__device__ __forceinline__ void load_floats(const float* p, float (&f)[N]) {
+template <int n>
+__device__ __forceinline__ void load_pairs(const float* p, float2 (&v)[n]) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p + i);
-    f[i] = v.x;
-    f[i + 1] = v.y;
-    f[i + 2] = v.z;
-    f[i + 3] = v.w;
+  for (int i = 0; i < n; i += 2) {
+    const float4 q = *reinterpret_cast<const float4*>(p + 2 * i);
+    v[i] = make_float2(q.x, q.y);
+    v[i + 1] = make_float2(q.z, q.w);
   }
 }
-
-template <int N>
-__device__ __forceinline__ void store_floats(float* p, const float (&f)[N]) {
+template <int n>
+__device__ __forceinline__ void store_pairs(float* p, const float2 (&v)[n]) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  for (int i = 0; i < n; i += 2)
+    *reinterpret_cast<float4*>(p + 2 * i) = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
-
-// ----------------------------------------------------------------- forward
-//
-// A row by one warp (eight rows per CTA) or by one CTA; a thread holds kPieces 16-byte pieces of it.
-template <bool kWarp>
-__device__ __forceinline__ float row_sum(float v, float* part) {
-  v = warp_sum(v);
-  if constexpr (kWarp) return v;
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += part[w];
-  return s;
-}
-
-constexpr int kForwardThreads = 256;  // of a CTA whose warps take a row each
-
-template <int kType, int kPieces, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? kForwardThreads : 512) norm_kernel(const Args a) {
-  constexpr int N = Vec<kType>::n;
-  __shared__ float part[2][16];
-  grid_dependents_launch();
-  grid_dependency_wait();
-  const int step = kWarp ? 32 : blockDim.x, at = kWarp ? threadIdx.x & 31 : threadIdx.x;
-  const int row = kWarp ? blockIdx.x * (kForwardThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
-  if (kWarp && row >= a.R) return;
-  const size_t base = static_cast<size_t>(row) * a.nvec;
-  uint4 xv[kPieces], yv[kPieces];
-#pragma unroll
-  for (int p = 0; p < kPieces; ++p) {
-    const int c = at + p * step;
-    xv[p] = yv[p] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < a.nvec) {
-      if (a.y) yv[p] = a.y[base + c];
-      if (a.x) xv[p] = a.x[base + c];
-    }
-  }
-  float r1 = 1.f;
-  if (a.gamma_post) {
-    float ss = 0.f;
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-      float f[N], s = 0.f;
-      Vec<kType>::load(yv[p], f);
-#pragma unroll
-      for (int i = 0; i < N; ++i) s = fmaf(f[i], f[i], s);
-      ss += s;
-    }
-    r1 = __frsqrt_rn(row_sum<kWarp>(ss, part[0]) / a.d + a.eps);
-  }
-  const float* gate = a.gate ? a.gate + static_cast<size_t>(row / a.gate_rows) * a.d : nullptr;
-  float o[kPieces][N], ss = 0.f;
-#pragma unroll
-  for (int p = 0; p < kPieces; ++p) {
-    const int c = at + p * step;
-    float f[N], s = 0.f;
-    Vec<kType>::load(xv[p], o[p]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[p][i] *= a.scale;
-    if (c < a.nvec) {
-      if (a.y) {
-        float w[N];
-        Vec<kType>::load(yv[p], f);
-        if (a.gamma_post) {
-          load_floats(a.gamma_post + c * N, w);
-#pragma unroll
-          for (int i = 0; i < N; ++i) f[i] = f[i] * r1 * w[i];
-        }
-        if (gate) {
-          load_floats(gate + c * N, w);
-#pragma unroll
-          for (int i = 0; i < N; ++i) o[p][i] = fmaf(w[i], f[i], o[p][i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) o[p][i] += f[i];
-        }
-      }
-      if (a.out) a.out[base + c] = Vec<kType>::store(o[p]);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) s = fmaf(o[p][i], o[p][i], s);
-    ss += s;
-  }
-  if (!a.u) return;
-  const float r2 = __frsqrt_rn(row_sum<kWarp>(ss, part[1]) / a.d + a.eps);
-#pragma unroll
-  for (int p = 0; p < kPieces; ++p) {
-    const int c = at + p * step;
-    if (c < a.nvec) {
-      float w[N];
-      load_floats(a.gamma_pre + c * N, w);
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[i] *= o[p][i] * r2;
-      a.u[base + c] = Vec<kType>::store(w);
-    }
-  }
-}
-
-// ---------------------------------------------------------------- backward
-//
-// A group of threads, a multiple of 32 that covers a row with kPieces pieces each, takes a
-// contiguous run of rows ("unit"), so a thread's columns stay the same and the weights' gradients
-// are summed in its registers. The sums over the units follow in a second launch, in the order of
-// the units: no atomics, the same bits in every run. A gate row whose rows lie in one unit is
-// written at once; the others leave a partial sum per unit (the unit's first gate row in slot
-// 2 u, its last one in 2 u + 1).
-struct GradArgs {
-  const uint4 *y, *out, *dout, *du;
-  const float *gamma_post, *gate, *gamma_pre;
-  uint4 *dx, *dy;
-  float *part_post, *part_pre;  // [CTAs][d], or NULL where not wanted
-  float *dgate, *slots;         // [groups][d] or NULL; [2 units][d]
-  int R, d, nvec, gate_rows, group, units;
-  float scale, eps;
-};
-
+// Rows of unit u: unit_first(u) .. unit_first(u + 1) - 1.
 __host__ __device__ inline int unit_first(int u, int R, int units) {
   return static_cast<int>(static_cast<int64_t>(u) * R / units);
 }
@@ -175,203 +94,401 @@ __host__ __device__ inline int unit_of(int row, int R, int units) {
   return static_cast<int>(((static_cast<int64_t>(row) + 1) * units - 1) / R);
 }
 
-// Sums of kCount values over the group, the same in all its threads. `part` alternates between
-// two places from row to row: a thread that is a barrier ahead does not write what others still read.
+// Sums of kCount (1 or 6) values over the group, the same in all its threads. With six each step of a
+// warp's tree halves the values that a lane carries on (eight shuffles, not thirty). `part`
+// alternates between two places from call to call: a thread that is a barrier ahead does not write what
+// others still read.
 template <int kCount>
-__device__ __forceinline__ void group_sum(float (&v)[kCount], int group, int which, float (*part)[kCount]) {
+__device__ __forceinline__ void group_sum(float (&v)[kCount], int group, int which, float (*part)[8]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = group >> 5;
+  if constexpr (kCount == 1) {
 #pragma unroll
-  for (int i = 0; i < kCount; ++i) v[i] = warp_sum(v[i]);
-  if (group == 32) return;
-  const int warp = threadIdx.x >> 5, warps = group >> 5;
-  if ((threadIdx.x & 31) == 0)
+    for (int off = 16; off > 0; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    if (group == 32) return;
+    if (lane == 0) part[warp][0] = v[0];
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + which), "r"(group) : "memory");
+    float s = lane < warps ? part[which * warps + lane][0] : 0.f;  // 16 warps at most
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) part[warp][i] = v[i];
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + which), "r"(group) : "memory");
+    for (int off = 8; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    v[0] = __shfl_sync(0xffffffffu, s, 0);
+  } else {
+    static_assert(kCount == 6, "one or six");
+    float a[4];
+    const bool up16 = lane & 16, up8 = lane & 8, up4 = lane & 4;
 #pragma unroll
-  for (int i = 0; i < kCount; ++i) {
-    v[i] = 0.f;
-    for (int w = 0; w < warps; ++w) v[i] += part[which * warps + w][i];
+    for (int i = 0; i < 3; ++i)
+      a[i] = (up16 ? v[i + 3] : v[i]) + __shfl_xor_sync(0xffffffffu, up16 ? v[i] : v[i + 3], 16);
+    a[0] = (up8 ? a[2] : a[0]) + __shfl_xor_sync(0xffffffffu, up8 ? a[0] : a[2], 8);
+    a[1] += __shfl_xor_sync(0xffffffffu, a[1], 8);  // (of lanes & 8 it is not used)
+    a[0] = (up4 ? a[1] : a[0]) + __shfl_xor_sync(0xffffffffu, up4 ? a[0] : a[1], 4);
+    a[0] += __shfl_xor_sync(0xffffffffu, a[0], 2);
+    a[0] += __shfl_xor_sync(0xffffffffu, a[0], 1);
+    // lanes 4 j .. 4 j + 3 hold value 3 (j / 4) + 2 (j / 2 % 2) + j % 2; nothing where j % 4 is 3
+    int step = 4;
+    if (group > 32) {
+      if ((lane & 3) == 0) part[warp][lane >> 2] = a[0];
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + which), "r"(group) : "memory");
+      float s = 0.f;  // value lane % 8 of every fourth warp
+      for (int w = lane >> 3; w < warps; w += 4) s += part[which * warps + w][lane & 7];
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+      a[0] = s;
+      step = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, a[0], (i < 3 ? i : i + 1) * step);
   }
 }
 
-template <int kType, int kPieces>
-struct Held {
-  uint4 y[kPieces], out[kPieces], dout[kPieces], du[kPieces];
+// A thread's ring of rows: kDepth stages of kTensors tensors of kPieces pieces.
+template <int kTensors, int kPieces, int kDepth>
+struct Ring {
+  uint32_t at;     // the thread's place in the first stage
+  uint32_t pitch;  // bytes from piece to piece
+  int slot = 0, free = 0;
+
+  __device__ __forceinline__ Ring(uint8_t* smem) : at(smem_addr(smem) + threadIdx.x * 16), pitch(blockDim.x * 16) {
+    for (int i = 0; i < kDepth * kTensors * kPieces; ++i)  // what is never copied counts as zeros
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * pitch), "r"(0) : "memory");
+  }
+  __device__ __forceinline__ uint32_t piece(int stage, int tensor, int p) const {
+    return at + ((stage * kTensors + tensor) * kPieces + p) * pitch;
+  }
+  // Requests a row of every tensor that is there.
+  __device__ __forceinline__ void request(const uint4* const (&t)[kTensors], size_t base, int column, int nvec, int group,
+                                          bool more) {
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < kTensors; ++i)
+        if (t[i])
+#pragma unroll
+          for (int p = 0; p < kPieces; ++p)
+            if (column + p * group < nvec) cp_async_16(piece(free, i, p), t[i] + base + column + p * group);
+      if (++free == kDepth) free = 0;
+    }
+    cp_async_commit();
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == kDepth) slot = 0;
+  }
 };
 
-template <int kType, int kPieces>
-__device__ __forceinline__ void load_row(const GradArgs& a, int row, int at, Held<kType, kPieces>& h) {
-  const size_t base = static_cast<size_t>(row) * a.nvec;
+// ----------------------------------------------------------------- forward
+
+struct Args {
+  const uint4 *x, *y;
+  const float *gamma_post, *gate, *gamma_pre;
+  uint4 *out, *u;
+  int R, d, nvec, gate_rows, group, units;
+  float scale, eps;
+};
+
+// The factor of a thread's columns of y: gamma_post (with kPost) times the gate.
+template <int kPieces, int n, bool kPost, class A>
+__device__ __forceinline__ void factors(const A& a, int gate_row, int at, float2 (&w)[kPieces][n]) {
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
     const int c = at + p * a.group;
-    h.y[p] = h.out[p] = h.dout[p] = h.du[p] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < a.nvec) {
-      if (a.du) {
-        h.out[p] = a.out[base + c];
-        h.du[p] = a.du[base + c];
-      }
-      if (a.y) h.y[p] = a.y[base + c];
-      if (a.dout) h.dout[p] = a.dout[base + c];
+#pragma unroll
+    for (int i = 0; i < n; ++i) w[p][i] = both(1.f);
+    if (c >= a.nvec) continue;
+    if (kPost) load_pairs(a.gamma_post + c * 2 * n, w[p]);
+    if (a.gate) {
+      float2 q[n];
+      load_pairs(a.gate + static_cast<size_t>(gate_row) * a.d + c * 2 * n, q);
+#pragma unroll
+      for (int i = 0; i < n; ++i) w[p][i] = mul2(w[p][i], q[i]);
     }
   }
 }
 
-template <int kType, int kPieces>
-__global__ void __launch_bounds__(512) norm_backward_kernel(const GradArgs a) {
-  constexpr int N = Vec<kType>::n;
-  constexpr bool kAhead = kPieces == 1;  // the next row's loads on their way while one is summed
-  extern __shared__ float gammas[];      // [2][d], where a CTA has several groups
-  __shared__ float part_a[2][16][3], part_b[2][16][1];
+// kY: y is there; kU: u is wanted.
+template <int kType, int kPieces, int kDepth, bool kY, bool kU>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const Args a) {
+  constexpr int n = Pairs<kType>::n;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float part[2][16][8];
   grid_dependents_launch();
-  grid_dependency_wait();
+  Ring<2, kPieces, kDepth> ring(smem);
   const int which = threadIdx.x / a.group, at = threadIdx.x - which * a.group;
-  const int groups = blockDim.x / a.group, unit = blockIdx.x * groups + which;
-  float acc_post[kPieces][N], acc_pre[kPieces][N], acc_gate[kPieces][N];
+  const int unit = blockIdx.x * (blockDim.x / a.group) + which;
+  grid_dependency_wait();
+  if (unit >= a.units) return;
+  const int r0 = unit_first(unit, a.R, a.units), r1 = unit_first(unit + 1, a.R, a.units);
+  const uint4* const rows[2] = {a.x, kY ? a.y : nullptr};
+#pragma unroll 1
+  for (int i = 0; i < kDepth - 1; ++i)
+    ring.request(rows, static_cast<size_t>(r0 + i) * a.nvec, at, a.nvec, a.group, r0 + i < r1);
+  float2 w[kPieces][n], pre[kPieces][n];
+  int gate_row = kY && a.gate ? r0 / a.gate_rows : 0, gate_end = kY && a.gate ? (gate_row + 1) * a.gate_rows : r1;
+  const auto load_w = [&] {
+    if (a.gamma_post)
+      factors<kPieces, n, true>(a, gate_row, at, w);
+    else
+      factors<kPieces, n, false>(a, gate_row, at, w);
+  };
+  if (kY) load_w();
+  if (kU)
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p)
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc_post[p][i] = acc_pre[p][i] = acc_gate[p][i] = 0.f;
-  const int r0 = unit < a.units ? unit_first(unit, a.R, a.units) : 0;
-  const int r1 = unit < a.units ? unit_first(unit + 1, a.R, a.units) : 0;
-  const int first_gate = a.gate ? r0 / a.gate_rows : 0;
-  int gate_row = first_gate, gate_end = a.gate ? (first_gate + 1) * a.gate_rows : r1;
-  Held<kType, kPieces> h, next;
-  if (kAhead && r0 < r1) load_row(a, r0, at, h);
+    for (int p = 0; p < kPieces; ++p)
+      if (at + p * a.group < a.nvec) load_pairs(a.gamma_pre + (at + p * a.group) * 2 * n, pre[p]);
+  const float inv_d = 1.f / a.d;
+  int call = 0;
+#pragma unroll 1
   for (int row = r0; row < r1; ++row) {
-    if (kAhead) {
-      if (row + 1 < r1) load_row(a, row + 1, at, next);
-    } else {
-      load_row(a, row, at, h);
-    }
-    // sums of out^2, of gamma_pre du out and of y^2
-    float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-      const int c = at + p * a.group;
-      float o[N], f[N], w[N];
-      if (a.du && c < a.nvec) {
-        Vec<kType>::load(h.out[p], o);
-        Vec<kType>::load(h.du[p], f);
-        load_floats(a.gamma_pre + c * N, w);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          s[0] = fmaf(o[i], o[i], s[0]);
-          s[1] = fmaf(w[i] * f[i], o[i], s[1]);
-        }
-      }
-      Vec<kType>::load(h.y[p], f);
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[2] = fmaf(f[i], f[i], s[2]);
-    }
-    group_sum(s, a.group, which, part_a[row & 1]);
-    const float ra = __frsqrt_rn(s[0] / a.d + a.eps), mean_a = ra * s[1] / a.d;
-    const float rb = a.gamma_post ? __frsqrt_rn(s[2] / a.d + a.eps) : 1.f;
-    const float* gate = a.gate ? a.gate + static_cast<size_t>(gate_row) * a.d : nullptr;
-    float g[kPieces][N], t[1] = {0.f};
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-      const int c = at + p * a.group;
-      float o[N], f[N], w[N];
-      Vec<kType>::load(h.dout[p], g[p]);
-      if (c < a.nvec) {
-        if (a.du) {
-          Vec<kType>::load(h.out[p], o);
-          Vec<kType>::load(h.du[p], f);
-          load_floats(a.gamma_pre + c * N, w);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float n = o[i] * ra;
-            acc_pre[p][i] = fmaf(f[i], n, acc_pre[p][i]);
-            g[p][i] = fmaf(ra, fmaf(-n, mean_a, w[i] * f[i]), g[p][i]);
-          }
-        }
-        if (a.dx) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) f[i] = a.scale * g[p][i];
-          a.dx[static_cast<size_t>(row) * a.nvec + c] = Vec<kType>::store(f);
-        }
-        if (a.gamma_post) {
-          Vec<kType>::load(h.y[p], f);
-          load_floats(a.gamma_post + c * N, w);
-          if (gate) {
-            load_floats(gate + c * N, o);
-#pragma unroll
-            for (int i = 0; i < N; ++i) w[i] *= o[i];
-          }
-#pragma unroll
-          for (int i = 0; i < N; ++i) t[0] = fmaf(w[i] * g[p][i], f[i], t[0]);
-        }
-      }
-    }
-    float mean_b = 0.f;
-    if (a.gamma_post) {
-      group_sum(t, a.group, which, part_b[row & 1]);
-      mean_b = rb * t[0] / a.d;
-    }
-    if (a.y || a.dy) {
+    ring.request(rows, static_cast<size_t>(row + kDepth - 1) * a.nvec, at, a.nvec, a.group, row + kDepth - 1 < r1);
+    cp_async_wait<kDepth - 1>();
+    float r = 1.f;
+    if (kY && a.gamma_post) {
+      float2 ss = both(0.f);
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
-        const int c = at + p * a.group;
-        if (c >= a.nvec) continue;
-        float f[N], w[N], q[N];
-        Vec<kType>::load(h.y[p], f);
+        float2 y[n];
+        Pairs<kType>::load(ring.piece(ring.slot, 1, p), y);
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = q[i] = 1.f;
-        if (a.gamma_post) load_floats(a.gamma_post + c * N, w);
-        if (gate) load_floats(gate + c * N, q);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float m = f[i] * rb, dv = q[i] * g[p][i];
-          acc_post[p][i] = fmaf(dv, m, acc_post[p][i]);
-          acc_gate[p][i] = fmaf(g[p][i] * w[i], m, acc_gate[p][i]);
-          f[i] = a.gamma_post ? rb * fmaf(-m, mean_b, w[i] * dv) : dv;
-        }
-        if (a.dy) a.dy[static_cast<size_t>(row) * a.nvec + c] = Vec<kType>::store(f);
+        for (int i = 0; i < n; ++i) ss = fma2(y[i], y[i], ss);
       }
+      float s[1] = {ss.x + ss.y};
+      group_sum(s, a.group, which, part[call++ & 1]);
+      r = __frsqrt_rn(s[0] * inv_d + a.eps);
     }
-    if (a.dgate && (row + 1 == gate_end || row + 1 == r1)) {
-      const int last = min(gate_end, a.R) - 1;
-      const bool whole = unit_of(gate_row * a.gate_rows, a.R, a.units) == unit && last < r1;
-      float* dst = whole ? a.dgate + static_cast<size_t>(gate_row) * a.d
-                         : a.slots + (static_cast<size_t>(2 * unit) + (gate_row != first_gate)) * a.d;
+    float2 o[kPieces][n], ss = both(0.f);
+    const size_t base = static_cast<size_t>(row) * a.nvec + at;
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      Pairs<kType>::load(ring.piece(ring.slot, 0, p), o[p]);
+#pragma unroll
+      for (int i = 0; i < n; ++i) o[p][i] = mul2(o[p][i], both(a.scale));
+      if (kY) {
+        float2 y[n];
+        Pairs<kType>::load(ring.piece(ring.slot, 1, p), y);
+#pragma unroll
+        for (int i = 0; i < n; ++i) o[p][i] = fma2(w[p][i], mul2(y[i], both(r)), o[p][i]);
+      }
+      if (kU)
+#pragma unroll
+        for (int i = 0; i < n; ++i) ss = fma2(o[p][i], o[p][i], ss);
+      if (a.out && at + p * a.group < a.nvec) a.out[base + p * a.group] = Pairs<kType>::store(o[p]);
+    }
+    if (kU) {
+      float s[1] = {ss.x + ss.y};
+      group_sum(s, a.group, which, part[call++ & 1]);
+      const float r2 = __frsqrt_rn(s[0] * inv_d + a.eps);
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
-        const int c = at + p * a.group;
-        if (c < a.nvec) store_floats(dst + c * N, acc_gate[p]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc_gate[p][i] = 0.f;
+        for (int i = 0; i < n; ++i) o[p][i] = mul2(pre[p][i], mul2(o[p][i], both(r2)));
+        if (at + p * a.group < a.nvec) a.u[base + p * a.group] = Pairs<kType>::store(o[p]);
       }
     }
-    if (row + 1 == gate_end) {
+    ring.next();
+    if (kY && row + 1 == gate_end && row + 1 < r1) {
       ++gate_row;
       gate_end += a.gate_rows;
+      load_w();
     }
-    if (kAhead) h = next;
   }
+  cp_async_wait<0>();
+}
+
+// ---------------------------------------------------------------- backward
+//
+// What the gradient needs of a whole row is linear in sums that the loaded values give at once,
+//   mean(m gamma_post dv) = r1 / d (sum w y dout + r2 sum w y (gamma_pre du) - r2^2 c sum w y out),
+//   w = gamma_post gate, c = mean(n gamma_pre du),
+// so six sums of a row go through one reduction and one barrier. The gate's and gamma_post's gradients
+// come from the same sum over the rows of a gate row, P = sum g m: dgate = gamma_post P, dgamma_post +=
+// gate P, held in registers over a unit like gamma_pre's.
+// The sums over the units follow in a second launch, in the order of the units: no atomics, the same
+// bits in every run. With one gate row (or none) that launch gets the sums P; with several, a
+// gate row whose rows lie in one unit is written at once, and the others leave a partial sum per unit
+// (the unit's first gate row in slot 2 u, its last one in 2 u + 1).
+struct GradArgs {
+  const uint4 *y, *out, *dout, *du;
+  const float *gamma_post, *gate, *gamma_pre;
+  uint4 *dx, *dy;
+  float *part_post, *part_pre;  // [CTAs][d], or NULL where not wanted (part_post: sums P with one gate row)
+  float *dgate, *slots;         // [gate rows][d] or NULL; [2 units][d]
+  int R, d, nvec, gate_rows, group, units;
+  float scale, eps;
+};
+
+// kNext: du is there; kPost: y goes through its norm; kGates: there are several gate rows. (What is
+// missing counts as zeros.)
+template <int kType, int kPieces, int kDepth, bool kNext, bool kPost, bool kGates>
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const GradArgs a) {
+  constexpr int n = Pairs<kType>::n, N = 2 * n;
+  extern __shared__ __align__(16) uint8_t smem[];  // the ring; at the end [2][d] sums, where a CTA has several groups
+  __shared__ float part[2][16][8];
+  grid_dependents_launch();
+  Ring<4, kPieces, kDepth> ring(smem);
+  const int which = threadIdx.x / a.group, at = threadIdx.x - which * a.group;
+  const int groups = blockDim.x / a.group, unit = blockIdx.x * groups + which;
+  grid_dependency_wait();
+  const int r0 = unit < a.units ? unit_first(unit, a.R, a.units) : 0;
+  const int r1 = unit < a.units ? unit_first(unit + 1, a.R, a.units) : 0;
+  const uint4* const rows[4] = {a.dout, a.y, kNext ? a.out : nullptr, kNext ? a.du : nullptr};
+#pragma unroll 1
+  for (int i = 0; i < kDepth - 1; ++i)
+    ring.request(rows, static_cast<size_t>(r0 + i) * a.nvec, at, a.nvec, a.group, r0 + i < r1);
+  // of the thread's columns: gamma_pre, gamma_post times the gate; sums of du n, of g m over a gate row, of dv m
+  float2 pre[kPieces][n], w[kPieces][n], acc_pre[kPieces][n], acc[kPieces][n], acc_post[kPieces][n];
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) acc_pre[p][i] = acc[p][i] = acc_post[p][i] = pre[p][i] = both(0.f);
+    if (kNext && at + p * a.group < a.nvec) load_pairs(a.gamma_pre + (at + p * a.group) * N, pre[p]);
+  }
+  const int first_gate = kGates ? r0 / a.gate_rows : 0;
+  int gate_row = first_gate, gate_end = (first_gate + 1) * a.gate_rows;
+  const float inv_d = 1.f / a.d;
+  if (r0 < r1) factors<kPieces, n, kPost>(a, gate_row, at, w);
+#pragma unroll 1
+  for (int row = r0; row < r1; ++row) {
+    ring.request(rows, static_cast<size_t>(row + kDepth - 1) * a.nvec, at, a.nvec, a.group, row + kDepth - 1 < r1);
+    cp_async_wait<kDepth - 1>();
+    const int slot = ring.slot;
+    float2 g[kPieces][n], y[kPieces][n], o[kPieces][n], f[kPieces][n];
+    const auto load = [&](int p) {
+      Pairs<kType>::load(ring.piece(slot, 0, p), g[p]);
+      Pairs<kType>::load(ring.piece(slot, 1, p), y[p]);
+      if (kNext) {
+        Pairs<kType>::load(ring.piece(slot, 2, p), o[p]);
+        Pairs<kType>::load(ring.piece(slot, 3, p), f[p]);
+      }
+    };
+    // out^2, (gamma_pre du) out, y^2, and w y times dout, gamma_pre du and out
+    float2 t[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) t[i] = both(0.f);
+    if (kNext || kPost) {
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        load(p);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          float2 wd;
+          if (kNext) {
+            wd = mul2(pre[p][i], f[p][i]);
+            t[0] = fma2(o[p][i], o[p][i], t[0]);
+            t[1] = fma2(wd, o[p][i], t[1]);
+          }
+          if (kPost) {
+            const float2 wy = mul2(w[p][i], y[p][i]);
+            t[2] = fma2(y[p][i], y[p][i], t[2]);
+            t[3] = fma2(wy, g[p][i], t[3]);
+            if (kNext) {
+              t[4] = fma2(wy, wd, t[4]);
+              t[5] = fma2(wy, o[p][i], t[5]);
+            }
+          }
+        }
+      }
+    }
+    float s[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s[i] = t[i].x + t[i].y;
+    if (kNext || kPost) group_sum(s, a.group, which, part[row & 1]);
+    const float ra = kNext ? __frsqrt_rn(s[0] * inv_d + a.eps) : 0.f, ca = ra * ra * ra * (s[1] * inv_d);
+    const float rb = kPost ? __frsqrt_rn(s[2] * inv_d + a.eps) : 1.f;
+    // dy = w g rb - y cb
+    const float cb = kPost ? rb * rb * rb * (fmaf(ra, s[4], fmaf(-ca, s[5], s[3])) * inv_d) : 0.f;
+    const size_t base = static_cast<size_t>(row) * a.nvec + at;
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      // one piece stays in registers from the sums above; several are read again
+      if (kPieces > 1 || !(kNext || kPost)) load(p);
+      const bool on = at + p * a.group < a.nvec;
+      if (kNext) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const float2 fr = mul2(f[p][i], both(ra));
+          acc_pre[p][i] = fma2(fr, o[p][i], acc_pre[p][i]);
+          g[p][i] = fma2(both(-ca), o[p][i], fma2(pre[p][i], fr, g[p][i]));
+        }
+      }
+      if (a.dx && on) {
+        float2 v[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = mul2(g[p][i], both(a.scale));
+        a.dx[base + p * a.group] = Pairs<kType>::store(v);
+      }
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float2 gr = mul2(g[p][i], both(rb));
+        acc[p][i] = fma2(gr, y[p][i], acc[p][i]);
+        y[p][i] = fma2(both(-cb), y[p][i], mul2(w[p][i], gr));
+      }
+      if (a.dy && on) a.dy[base + p * a.group] = Pairs<kType>::store(y[p]);
+    }
+    ring.next();
+    if (kGates && (row + 1 == gate_end || row + 1 == r1)) {  // the end of a gate row, or of its part of the unit
+      const int last = min(gate_end, a.R) - 1;
+      const bool whole = unit_of(gate_row * a.gate_rows, a.R, a.units) == unit && last < r1;
+      float* const dst = !a.dgate ? nullptr
+                         : whole  ? a.dgate + static_cast<size_t>(gate_row) * a.d
+                                  : a.slots + (static_cast<size_t>(2 * unit) + (gate_row != first_gate)) * a.d;
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        const int c = at + p * a.group;
+        if (c < a.nvec) {
+          float2 q[n];
+          load_pairs(a.gate + static_cast<size_t>(gate_row) * a.d + c * N, q);
+#pragma unroll
+          for (int i = 0; i < n; ++i) acc_post[p][i] = fma2(q[i], acc[p][i], acc_post[p][i]);
+          if (dst) {
+            if (kPost) {
+              load_pairs(a.gamma_post + c * N, q);
+#pragma unroll
+              for (int i = 0; i < n; ++i) acc[p][i] = mul2(acc[p][i], q[i]);
+            }
+            store_pairs(dst + c * N, acc[p]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < n; ++i) acc[p][i] = both(0.f);
+      }
+      if (row + 1 < r1) {
+        ++gate_row;
+        gate_end += a.gate_rows;
+        factors<kPieces, n, kPost>(a, gate_row, at, w);
+      }
+    }
+  }
+  cp_async_wait<0>();
   if (groups == 1) {
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
       const int c = at + p * a.group;
       if (c >= a.nvec) continue;
-      if (a.part_post) store_floats(a.part_post + static_cast<size_t>(blockIdx.x) * a.d + c * N, acc_post[p]);
-      if (a.part_pre) store_floats(a.part_pre + static_cast<size_t>(blockIdx.x) * a.d + c * N, acc_pre[p]);
+      const size_t dst = static_cast<size_t>(blockIdx.x) * a.d + c * N;
+      if (a.part_post) store_pairs(a.part_post + dst, kGates ? acc_post[p] : acc[p]);
+      if (a.part_pre) store_pairs(a.part_pre + dst, acc_pre[p]);
     }
     return;
   }
+  auto* const gammas = reinterpret_cast<float*>(smem);
+  __syncthreads();  // the groups' rings are read
   for (int q = 0; q < groups; ++q) {  // the groups' sums in order
     if (q == which)
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
         const int c = at + p * a.group;
         if (c >= a.nvec) continue;
+        float2 post[n], before[n];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          float* const post = gammas + c * N + i;
-          float* const pre = post + a.d;
-          *post = (q ? *post : 0.f) + acc_post[p][i];
-          *pre = (q ? *pre : 0.f) + acc_pre[p][i];
+        for (int i = 0; i < n; ++i) post[i] = before[i] = both(0.f);
+        if (q) {
+          load_pairs(gammas + c * N, post);
+          load_pairs(gammas + a.d + c * N, before);
         }
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          post[i] = fma2(both(1.f), kGates ? acc_post[p][i] : acc[p][i], post[i]);
+          before[i] = fma2(both(1.f), acc_pre[p][i], before[i]);
+        }
+        store_pairs(gammas + c * N, post);
+        store_pairs(gammas + a.d + c * N, before);
       }
     __syncthreads();
   }
@@ -381,24 +498,34 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const GradArgs a) {
   }
 }
 
-// The second launch: 32 columns per CTA (8 lanes of four), 32 slices of the partial sums, which
-// meet in order. blockIdx.y 0 and 1: the gammas over the CTAs; from 2 on: gate rows with partial sums.
+// The second launch: 16 columns per CTA (4 lanes of four), 64 slices of the partial sums, which meet in
+// a fixed tree. blockIdx.y 0 and 1: over the CTAs, for gamma_post (and the gate, where it has one row) and
+// gamma_pre; from 2 on: gate rows with partial sums.
 struct SumArgs {
   const float *part_post, *part_pre, *slots;
+  const float *gamma_post, *gate;  // the factors of P with one gate row (NULL: one)
   float *dgamma_post, *dgamma_pre, *dgate;
-  int R, d, gate_rows, ctas, units, gates;
+  int R, d, gate_rows, ctas, units, gates;  // gates: gate rows to add up from slots
 };
 
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x;
+  a.y += b.y;
+  a.z += b.z;
+  a.w += b.w;
+}
+
 __global__ void __launch_bounds__(256) norm_sum_kernel(const SumArgs a) {
-  __shared__ float4 part[32][8];
+  __shared__ float4 part[2][8][4];
   grid_dependents_launch();
   grid_dependency_wait();
-  const int lane = threadIdx.x & 7, slice = threadIdx.x >> 3;
-  const int col = blockIdx.x * 32 + lane * 4;
+  const int lane = threadIdx.x & 3, slice = threadIdx.x >> 2, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 16 + lane * 4;
   const bool on = col < a.d;
   const int y = blockIdx.y;
   const bool gates = y >= 2;
-  if (!gates && !(y == 0 ? a.dgamma_post : a.dgamma_pre)) return;
+  if (!gates && !(y == 0 ? a.part_post : a.part_pre)) return;
+  int turn = 0;
   for (int g = gates ? y - 2 : 0; g < (gates ? a.gates : 1); g += gates ? gridDim.y - 2 : 1) {
     int u0 = 0, u1 = a.ctas - 1;
     if (gates) {
@@ -409,75 +536,118 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(const SumArgs a) {
     const float* src = gates ? a.slots : y == 0 ? a.part_post : a.part_pre;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on)
-      for (int u = u0 + slice; u <= u1; u += 32) {
+#pragma unroll 5
+      for (int u = u0 + slice; u <= u1; u += 64) {
         size_t at = u;
         if (gates) at = 2 * at + (unit_first(u, a.R, a.units) / a.gate_rows != g);
-        const float4 v = *reinterpret_cast<const float4*>(src + at * a.d + col);
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
+        add4(s, *reinterpret_cast<const float4*>(src + at * a.d + col));
       }
-    part[slice][lane] = s;
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1)
+      add4(s, make_float4(__shfl_xor_sync(0xffffffffu, s.x, off), __shfl_xor_sync(0xffffffffu, s.y, off),
+                          __shfl_xor_sync(0xffffffffu, s.z, off), __shfl_xor_sync(0xffffffffu, s.w, off)));
+    if ((threadIdx.x & 31) < 4) part[turn][warp][lane] = s;
     __syncthreads();
     if (slice == 0 && on) {
-      for (int k = 1; k < 32; ++k) {
-        const float4 v = part[k][lane];
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
-      }
-      float* dst = gates ? a.dgate + static_cast<size_t>(g) * a.d : y == 0 ? a.dgamma_post : a.dgamma_pre;
-      *reinterpret_cast<float4*>(dst + col) = s;
+      s = part[turn][0][lane];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) add4(s, part[turn][k][lane]);
+      const auto put = [&](float* dst, const float* factor) {
+        float4 v = s;
+        if (factor) {
+          const float4 f = *reinterpret_cast<const float4*>(factor + col);
+          v = make_float4(s.x * f.x, s.y * f.y, s.z * f.z, s.w * f.w);
+        }
+        *reinterpret_cast<float4*>(dst + col) = v;
+      };
+      if (gates)
+        put(a.dgate + static_cast<size_t>(g) * a.d, nullptr);
+      else if (y == 1)
+        put(a.dgamma_pre, nullptr);
+      if (y == 0 && a.dgamma_post) put(a.dgamma_post, a.gate);
+      if (y == 0 && a.gates == 0 && a.dgate) put(a.dgate, a.gamma_post);
     }
-    __syncthreads();
+    turn ^= 1;  // the next sums go elsewhere: no barrier before them
   }
 }
 
-template <int kType, int kPieces, bool kWarp>
-cudaError_t launch_forward(const Args& a, int threads, cudaStream_t st) {
-  const int per = kWarp ? kForwardThreads / 32 : 1;
-  return launch_pdl(norm_kernel<kType, kPieces, kWarp>, dim3((a.R + per - 1) / per), dim3(threads), 0, st, a);
-}
-
-// A warp per row needs no barrier, but with few rows the pieces are spread over more threads:
-// latency counts then.
-template <int kType>
-cudaError_t forward(const Args& a, cudaStream_t st) {
-  const auto threads = [&](int pieces) { return (a.nvec + 32 * pieces - 1) / (32 * pieces) * 32; };
-  if (a.R >= 152 * 8 && a.nvec <= 256) {
-    if (a.nvec <= 32) return launch_forward<kType, 1, true>(a, kForwardThreads, st);
-    if (a.nvec <= 64) return launch_forward<kType, 2, true>(a, kForwardThreads, st);
-    if (a.nvec <= 128) return launch_forward<kType, 4, true>(a, kForwardThreads, st);
-    return launch_forward<kType, 8, true>(a, kForwardThreads, st);
-  }
-  if (a.nvec <= 512 && a.R < 152 * 4) return launch_forward<kType, 1, false>(a, threads(1), st);
-  return launch_forward<kType, 4, false>(a, threads(4), st);
-}
-
-// Threads of a group and groups of a CTA of the gradient's kernel.
-struct GradShape {
+// Threads of a group, groups of a CTA and CTAs.
+struct GroupShape {
   int pieces, group, groups, ctas, units;
 };
-GradShape grad_shape(const NormDims& s) {
-  GradShape g;
-  const int nvec = s.nvec();
-  g.pieces = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-  g.group = (nvec + 32 * g.pieces - 1) / (32 * g.pieces) * 32;
+GroupShape group_shape(int rows, int nvec, int pieces, int max_ctas) {
+  GroupShape g;
+  g.pieces = pieces;
+  g.group = (nvec + 32 * pieces - 1) / (32 * pieces) * 32;
   g.groups = g.group >= 256 ? 1 : 256 / g.group;
-  const int rows = s.R > 0 ? s.R : 1;
+  if (g.groups > rows) g.groups = rows > 0 ? rows : 1;
   g.ctas = (rows + g.groups - 1) / g.groups;
-  if (g.ctas > kNormCtas) g.ctas = kNormCtas;
-  g.units = g.ctas * g.groups;
-  if (g.units > rows) g.units = rows;
+  if (g.ctas < 1) g.ctas = 1;
+  if (g.ctas > max_ctas) g.ctas = max_ctas;
+  g.units = std::min(g.ctas * g.groups, rows > 0 ? rows : 1);
   return g;
 }
 
-template <int kType, int kPieces>
-cudaError_t backward(const GradArgs& a, const GradShape& g, cudaStream_t st) {
-  return launch_pdl(norm_backward_kernel<kType, kPieces>, dim3(g.ctas), dim3(g.group * g.groups),
-                    g.groups > 1 ? size_t(2) * a.d * 4 : 0, st, a);
+constexpr int kSmem = 200 * 1024;  // of dynamic shared memory at most
+
+template <class K, class A>
+cudaError_t launch(K kernel, const GroupShape& g, size_t smem, cudaStream_t st, const A& a) {
+  if (smem > 40 * 1024) {  // with the static part past 48 KB
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kernel, dim3(g.ctas), dim3(g.group * g.groups), smem, st, a);
+}
+
+// Two CTAs of 256 threads on an SM, or what fits of larger ones.
+int ctas_at_a_time(int threads, size_t smem) {
+  const int by_threads = threads <= 256 ? 2 : 1, by_smem = smem > 110 * 1024 ? 1 : 2;
+  return kNormSms * std::min(by_threads, by_smem);
+}
+
+// Four pieces per thread where there are rows enough: a barrier less often; one piece where latency
+// counts.
+template <int kType, int kPieces, int kDepth>
+cudaError_t forward(Args a, cudaStream_t st) {
+  GroupShape g = group_shape(a.R, a.nvec, kPieces, INT32_MAX);
+  const size_t smem = size_t(kDepth) * 2 * kPieces * g.group * g.groups * 16;
+  g = group_shape(a.R, a.nvec, kPieces, ctas_at_a_time(g.group * g.groups, smem));
+  a.group = g.group;
+  a.units = g.units;
+  if (!a.y) return launch(norm_kernel<kType, kPieces, kDepth, false, true>, g, smem, st, a);
+  return a.u ? launch(norm_kernel<kType, kPieces, kDepth, true, true>, g, smem, st, a)
+             : launch(norm_kernel<kType, kPieces, kDepth, true, false>, g, smem, st, a);
+}
+template <int kType>
+cudaError_t forward(const Args& a, cudaStream_t st) {
+  if (a.nvec <= 32 || (a.nvec <= 512 && a.R <= 4 * kNormSms)) return forward<kType, 1, 3>(a, st);
+  if (a.nvec <= 64) return forward<kType, 2, 3>(a, st);
+  return forward<kType, 4, 3>(a, st);
+}
+
+GroupShape grad_shape(const NormDims& s) {
+  const int nvec = s.nvec(), pieces = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+  return group_shape(s.R, nvec, pieces, pieces == 1 && nvec <= 256 ? 2 * kNormSms : kNormSms);
+}
+
+template <int kType, int kPieces, int kDepth, bool kNext, bool kPost, bool kGates>
+cudaError_t backward(const GradArgs& a, const GroupShape& g, cudaStream_t st) {
+  const size_t ring = size_t(kDepth) * 4 * kPieces * g.group * g.groups * 16;
+  return launch(norm_backward_kernel<kType, kPieces, kDepth, kNext, kPost, kGates>, g, std::max(ring, size_t(8) * a.d),
+                st, a);
+}
+template <int kType, int kPieces, int kDepth, bool kGates>
+cudaError_t backward(const GradArgs& a, const GroupShape& g, cudaStream_t st) {
+  const bool next = a.du, post = a.gamma_post;
+  return next ? post ? backward<kType, kPieces, kDepth, true, true, kGates>(a, g, st)
+                     : backward<kType, kPieces, kDepth, true, false, kGates>(a, g, st)
+              : post ? backward<kType, kPieces, kDepth, false, true, kGates>(a, g, st)
+                     : backward<kType, kPieces, kDepth, false, false, kGates>(a, g, st);
+}
+template <int kType, int kPieces, int kDepth>
+cudaError_t backward(const GradArgs& a, const GroupShape& g, cudaStream_t st) {
+  return a.gate && a.gate_rows < a.R ? backward<kType, kPieces, kDepth, true>(a, g, st)
+                                     : backward<kType, kPieces, kDepth, false>(a, g, st);
 }
 
 }  // namespace
@@ -485,12 +655,13 @@ cudaError_t backward(const GradArgs& a, const GradShape& g, cudaStream_t st) {
 cudaError_t launch_norm(const NormDims& s, const void* x, const void* y, const float* gamma_post, const float* gate,
                         const float* gamma_pre, void* out, void* u, cudaStream_t st) {
   const Args a{static_cast<const uint4*>(x), static_cast<const uint4*>(y), gamma_post, gate, gamma_pre,
-               static_cast<uint4*>(out), static_cast<uint4*>(u), s.R, s.d, s.nvec(), s.gate_rows, s.scale, s.eps};
+               static_cast<uint4*>(out), static_cast<uint4*>(u), s.R, s.d, s.nvec(), s.gate_rows, 0, 0, s.scale, s.eps};
   return s.type == 0 ? forward<0>(a, st) : s.type == 1 ? forward<1>(a, st) : forward<2>(a, st);
 }
 
+// Workspace: sums P (or of gamma_post) by CTA | of gamma_pre by CTA | gate slots by unit.
 size_t norm_backward_ws_bytes(const NormDims& s) {
-  const GradShape g = grad_shape(s);
+  const GroupShape g = grad_shape(s);
   return (size_t(g.ctas) + g.units) * 2 * s.d * 4;
 }
 
@@ -498,12 +669,13 @@ cudaError_t launch_norm_backward(const NormDims& s, const void* y, const float* 
                                  const void* out, const float* gamma_pre, const void* dout, const void* du, void* dx,
                                  void* dy, float* dgamma_post, float* dgate, float* dgamma_pre, void* workspace,
                                  cudaStream_t st) {
-  const GradShape g = grad_shape(s);
+  const GroupShape g = grad_shape(s);
   auto* const ws = static_cast<float*>(workspace);
   float* const pre = ws + size_t(g.ctas) * s.d;
   float* const slots = pre + size_t(g.ctas) * s.d;
-  GradArgs a{};
+  const bool gates = gate && s.gate_rows < s.R;  // several gate rows
   const bool needs_y = (dy && gamma_post) || dgamma_post || dgate;
+  GradArgs a{};
   a.y = needs_y ? static_cast<const uint4*>(y) : nullptr;
   a.out = static_cast<const uint4*>(out);
   a.dout = static_cast<const uint4*>(dout);
@@ -513,7 +685,7 @@ cudaError_t launch_norm_backward(const NormDims& s, const void* y, const float* 
   a.gamma_pre = gamma_pre;
   a.dx = static_cast<uint4*>(dx);
   a.dy = static_cast<uint4*>(dy);
-  a.part_post = dgamma_post ? ws : nullptr;
+  a.part_post = dgamma_post || (dgate && !gates) ? ws : nullptr;
   a.part_pre = dgamma_pre ? pre : nullptr;
   a.dgate = dgate;
   a.slots = slots;
@@ -528,9 +700,9 @@ cudaError_t launch_norm_backward(const NormDims& s, const void* y, const float* 
   cudaError_t err;
   const auto run = [&](auto type) {
     constexpr int kType = decltype(type)::value;
-    if (g.pieces == 1) return backward<kType, 1>(a, g, st);
-    if (kType < 2 || g.pieces == 2) return backward<kType, 2>(a, g, st);  // 8192 16-bit columns at most
-    return backward<2, 4>(a, g, st);
+    if (g.pieces == 1) return backward<kType, 1, 4>(a, g, st);
+    if (kType < 2 || g.pieces == 2) return backward<kType, 2, 3>(a, g, st);  // 8192 16-bit columns at most
+    return backward<2, 4, 1>(a, g, st);  // a row of 8192 fp32 columns takes 128 KB of the ring
   };
   if (s.type == 0)
     err = run(std::integral_constant<int, 0>{});
@@ -539,10 +711,10 @@ cudaError_t launch_norm_backward(const NormDims& s, const void* y, const float* 
   else
     err = run(std::integral_constant<int, 2>{});
   if (err != cudaSuccess || (!dgamma_post && !dgamma_pre && !dgate)) return err;
-  const int gates = dgate ? (s.R + s.gate_rows - 1) / s.gate_rows : 0;
-  const SumArgs b{ws, pre, slots, dgamma_post, dgamma_pre, dgate, s.R, s.d, a.gate_rows, g.ctas, g.units, gates};
-  const int extra = gates > 64 ? 64 : gates;
-  return launch_pdl(norm_sum_kernel, dim3((s.d + 31) / 32, 2 + extra), dim3(256), 0, st, b);
+  const int rows = dgate && gates ? (s.R + s.gate_rows - 1) / s.gate_rows : 0, extra = rows > 64 ? 64 : rows;
+  const SumArgs b{a.part_post, a.part_pre, slots, gamma_post, gates ? nullptr : gate, dgamma_post, dgamma_pre, dgate,
+                  s.R, s.d, a.gate_rows, g.ctas, g.units, rows};
+  return launch_pdl(norm_sum_kernel, dim3((s.d + 15) / 16, 2 + extra), dim3(256), 0, st, b);
 }
 
 }  // namespace moe
