@@ -37,7 +37,7 @@ namespace {
 constexpr int kMaxItems = kFewTokens * kMaxTopK;  // as many as pairs
 constexpr int kItemTokens = 4;                    // tokens of an item
 constexpr int kUpThreads = 512, kUpWarps = kUpThreads / 32;
-constexpr int kDownWarps = 4;                     // down: warps per pair of strips, each for every fourth item
+constexpr int kDownWarps = 6;                     // down: warps per pair of strips at most
 constexpr int kDownMaxPairs = 4;                  // down: pairs of strips of a CTA
 constexpr int kPairBytes = 512;                   // a pair's h of one stage: (hi, lo) x 128 columns
 constexpr int kRowWords = 33;                     // down: a pair's 32 rows of two strips, and one word between pairs
@@ -61,8 +61,11 @@ struct Args {
   int stage_warps;        // gate_up: warps of a group, which share a unit's contraction
   int per_item;           // gate_up: units of an item
   float per_item_inv;
-  int step_items, step_rest;  // and how far the units of all groups are
+  int step_items[2], step_rest[2];  // and how far the units of all groups are, of small groups and of large ones
+  float turn_inv;         // gate_up: one over the units of all small groups
+  int tail;               // gate_up: turns of large groups that take less than one of small ones
   int strips, cluster;    // down: strips of a CTA, CTAs that share the contraction
+  int down_warps;         // down: warps per pair of strips, each for every so-manieth item
   int depth;              // pieces of a warp in its ring
 };
 
@@ -86,35 +89,42 @@ __device__ __forceinline__ float key_value(uint32_t key) {  // the value of an o
 }
 
 // The choice of one token by one warp, as topk_softmax_warp makes it: the largest logits, ties to the
-// lower expert; w gets their values. Lane l holds experts l + 32 j.
-template <int NS>
-__device__ __forceinline__ void choose(const float* row, int E, int k, int lane, int32_t* sel, float* w) {
+// lower expert; w gets their values. Lane l holds experts l + 32 j. Without kTies every lane that holds the
+// largest key takes it for its own, which saves the vote on who does; false where two did.
+template <int NS, bool kTies>
+__device__ __forceinline__ bool choose(const float* row, int E, int k, int lane, int32_t* sel, float* w) {
   uint32_t key[NS];
 #pragma unroll
   for (int j = 0; j < NS; ++j) key[j] = lane + 32 * j < E ? order_key(__ldcg(row + lane + 32 * j)) : 0u;
+  int taken = 0;
 #pragma unroll 1
   for (int r = 0; r < k; ++r) {
     uint32_t best = key[0];
 #pragma unroll
     for (int j = 1; j < NS; ++j) best = max(best, key[j]);
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const unsigned tied = __ballot_sync(0xffffffffu, best == top);
     int first = 0;  // the lane's first expert of that key
 #pragma unroll
     for (int j = NS - 1; j >= 0; --j)
       if (key[j] == top) first = j;
     const int e = lane + 32 * first;
-    int winner = __ffs(tied) - 1;
-    if (tied & (tied - 1u))
-      winner = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<uint32_t>(e) : ~0u) & 31u);
-    if (lane == winner) {
+    bool mine = best == top;
+    if (kTies) mine = __reduce_min_sync(0xffffffffu, mine ? static_cast<uint32_t>(e) : ~0u) == static_cast<uint32_t>(e);
+    if (mine) {
       sel[r] = e;
       w[r] = key_value(top);
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-        if (j == first) key[j] = 0u;
+      ++taken;
     }
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+      if (mine && j == first) key[j] = 0u;
   }
+  __syncwarp();
+  return kTies || __reduce_add_sync(0xffffffffu, taken) == k;
+}
+template <int NS>
+__device__ __forceinline__ void choose(const float* row, int E, int k, int lane, int32_t* sel, float* w) {
+  if (!choose<NS, false>(row, E, k, lane, sel, w)) choose<NS, true>(row, E, k, lane, sel, w);
 }
 
 // The softmax over the k chosen values of a token, summed in rank order, by one warp.
@@ -398,8 +408,9 @@ __device__ __forceinline__ void sum_x(const uint32_t (&b)[8][2], float (&sum)[NG
   }
 }
 
-template <bool kBf16, int G, int kPairs>
-__global__ void __launch_bounds__(kUpThreads, kPairs == 1 ? 2 : 1) few_gate_up_kernel(const Args a) {
+// kBeside: with half of an SM's registers, so that a CTA of the down launch fits beside it.
+template <bool kBf16, int G, int kPairs, bool kBeside>
+__global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kernel(const Args a) {
   constexpr int NG = kStageCols / G, kStripBytes = 1024 + 64 * NG, kStrips = 2 * kPairs, kSlot = kStrips * kStripBytes;
   constexpr int kType = kBf16 ? 1 : 0;
   extern __shared__ __align__(16) uint8_t smem[];  // rings
@@ -411,174 +422,195 @@ __global__ void __launch_bounds__(kUpThreads, kPairs == 1 ? 2 : 1) few_gate_up_k
   grid_dependency_wait();    // the logits, x, and h, which the call before may still read
   grid_dependents_launch();  // only now: the down launch reads logits and weights before it waits
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int S = a.K / kStageCols, W = a.stage_warps, my_stage = warp & (W - 1);
-  const bool wide = W == kUpWarps;  // one group of 16, else four of 4
-  const int team = wide ? 0 : warp >> 2, round = (wide ? kRoundStrips : kRoundStrips / 2) / kStrips;
-  const auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(W * 32) : "memory"); };
+  const int S = a.K / kStageCols;
   const uint32_t ring = smem_addr(smem) + warp * a.depth * kSlot;
   const auto* const x = static_cast<const uint32_t*>(a.x) + (lane & 3);
-  uint32_t b[8][2], next[8][2];  // fragments of x, with two pairs loaded a piece ahead
+  uint32_t b[8][2], next[8][2];  // fragments of x, loaded a piece ahead where registers allow
   float sum[NG][2];
-  const bool fixed = a.T == 1 && S <= W;
-  if (fixed && my_stage < S) {
-    load_x(x + my_stage * 64, lane < 4, b);
+  const bool fixed = a.T == 1 && S <= a.stage_warps;  // (then all turns are of large groups, or each warp has one stage)
+  if (fixed && (warp & (a.stage_warps - 1)) < S) {
+    load_x(x + (warp & (a.stage_warps - 1)) * 64, lane < 4, b);
     sum_x<kBf16, NG>(b, sum);
   }
   const auto load = [&](int i, int stage, uint32_t (&f)[8][2]) {  // columns behind the item's tokens are not used
     load_x(x + static_cast<size_t>(r.token[i][(lane >> 2) & 3]) * (a.d / 2) + stage * 64, (lane >> 2) < r.count[i], f);
   };
   form_routing(r, a, smem);
-  const int items = r.items, pairs = a.T * a.k, unit0 = blockIdx.x * (wide ? 1 : 4) + team;
-
-  // the piece to request next
-  int pi = static_cast<int>((unit0 + 0.5f) * a.per_item_inv), pg = unit0 - pi * a.per_item;  // exact: below 2^12
-  int ps = my_stage, pslot = 0;
-  int item = pi, group = pg, slot = 0, ahead = a.depth - 1;
+  const int pairs = a.T * a.k, all_units = r.items * a.per_item;
+  // Small groups take whole turns of units; what is left over goes to large groups where those finish it sooner.
+  int narrow = all_units;
+  if (a.stage_warps == kUpWarps) {
+    narrow = 0;
+  } else {
+    const int turns = static_cast<int>((all_units + 0.5f) * a.turn_inv), whole = turns * static_cast<int>(gridDim.x) * 4;
+    if (all_units - whole <= a.tail * static_cast<int>(gridDim.x)) narrow = whole;
+  }
+  int slot = 0, pslot = 0;
+  bool first_piece = true;
   float tot[kStrips][4] = {};
-  int s = my_stage, in_round = 0, round_item = item, round_group = group;
-  bool first_piece = true, first_x = true;
-  const auto step = [&](int& i, int& g) {
-    i += a.step_items;
-    g += a.step_rest;
-    if (g >= a.per_item) {
-      g -= a.per_item;
-      ++i;
-    }
-  };
 #pragma unroll 1
-  while (true) {
-    if (pi < items && ps < S) {
-      const uint32_t pair = pg * kPairs;
-      const uint32_t off = r.expert[pi] * a.expert16 + (pair >> 2) * a.block16 +
-                           static_cast<uint32_t>(ps) * (8 * kStripBytes / 16) + (pair & 3) * (2 * kStripBytes / 16);
-      copy_warp<kSlot>(ring + pslot * kSlot, a.w + static_cast<size_t>(off) * 16, lane);
-      ps += W;
-      if (ps >= S) {
-        ps = my_stage;
-        step(pi, pg);
+  for (int large = narrow == 0; large < 2; ++large) {
+    const bool wide = large;  // one group of 16, else four of 4
+    const int W = wide ? kUpWarps : kUpWarps / 4, my_stage = warp & (W - 1), team = wide ? 0 : warp >> 2;
+    const int round = (wide ? kRoundStrips : kRoundStrips / 2) / kStrips;
+    const int unit0 = wide ? narrow + blockIdx.x : blockIdx.x * 4 + team, units = wide ? all_units : narrow;
+    const auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(wide ? 0 : 1 + team), "r"(W * 32) : "memory"); };
+
+    // the piece to request next: unit pu, which is unit pg of item pi
+    struct Place {
+      int unit, item, group;
+    };
+    Place put{unit0, static_cast<int>((unit0 + 0.5f) * a.per_item_inv), 0}, got;  // exact: below 2^14
+    put.group = unit0 - put.item * a.per_item;
+    got = put;
+    const auto step = [&](Place& p) {
+      p.unit += static_cast<int>(gridDim.x) * (wide ? 1 : 4);
+      p.item += a.step_items[large];
+      p.group += a.step_rest[large];
+      if (p.group >= a.per_item) {
+        p.group -= a.per_item;
+        ++p.item;
       }
-      if (++pslot == a.depth) pslot = 0;
-    }
-    cp_async_commit();
-    if (ahead > 0) {
-      --ahead;
-      continue;
-    }
-    if (first_piece) {  // what others want of the routing, while the first pieces arrive
-      first_piece = false;
-      if (a.listed && blockIdx.x == gridDim.x - 1)
+    };
+    int ps = my_stage, s = my_stage, ahead = a.depth - 1, in_round = 0;
+    bool first_x = true;
+    Place round_place = got;
 #pragma unroll 1
-        for (int i = tid; i < static_cast<int>(sizeof(Routing) / 16); i += kUpThreads)
-          reinterpret_cast<uint4*>(a.routing)[i] = reinterpret_cast<const uint4*>(&r)[i];
-      if (blockIdx.x == 0) {
-        __syncthreads();
-#pragma unroll 1
-        for (int t = warp; t < a.T; t += kUpWarps) {
-          weigh(r.w + t * a.k, a.k, lane);
-          if (lane < a.k && a.topk_idx) a.topk_idx[t * a.k + lane] = r.sel[t * a.k + lane];
-          if (lane < a.k && a.topk_w) a.topk_w[t * a.k + lane] = r.w[t * a.k + lane];
+    while (true) {
+      if (put.unit < units && ps < S) {
+        const uint32_t pair = put.group * kPairs;
+        const uint32_t off = r.expert[put.item] * a.expert16 + (pair >> 2) * a.block16 +
+                             static_cast<uint32_t>(ps) * (8 * kStripBytes / 16) + (pair & 3) * (2 * kStripBytes / 16);
+        copy_warp<kSlot>(ring + pslot * kSlot, a.w + static_cast<size_t>(off) * 16, lane);
+        ps += W;
+        if (ps >= S) {
+          ps = my_stage;
+          step(put);
         }
+        if (++pslot == a.depth) pslot = 0;
       }
-    }
-    if (item < items) {
-      if (s < S) {  // (a warp without a stage takes part in the sums alone)
-        if (!fixed) {
-          if (kPairs == 1) load(item, s, b);
-          if (kPairs == 2) {
-            if (first_x) load(item, s, next);
-            first_x = false;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-              for (int v = 0; v < 2; ++v) b[kk][v] = next[kk][v];
-            int i = item, g = group, st = s + W;
-            if (st >= S) {
-              st = my_stage;
-              step(i, g);
-            }
-            if (i < items) load(i, st, next);
+      cp_async_commit();
+      if (ahead > 0) {
+        --ahead;
+        continue;
+      }
+      if (first_piece) {  // what others want of the routing, while the first pieces arrive
+        first_piece = false;
+        if (a.listed && blockIdx.x == gridDim.x - 1)
+#pragma unroll 1
+          for (int i = tid; i < static_cast<int>(sizeof(Routing) / 16); i += kUpThreads)
+            reinterpret_cast<uint4*>(a.routing)[i] = reinterpret_cast<const uint4*>(&r)[i];
+        if (blockIdx.x == 0) {
+          __syncthreads();
+#pragma unroll 1
+          for (int t = warp; t < a.T; t += kUpWarps) {
+            weigh(r.w + t * a.k, a.k, lane);
+            if (lane < a.k && a.topk_idx) a.topk_idx[t * a.k + lane] = r.sel[t * a.k + lane];
+            if (lane < a.k && a.topk_w) a.topk_w[t * a.k + lane] = r.w[t * a.k + lane];
           }
-          sum_x<kBf16, NG>(b, sum);
         }
-        wait_piece(a.depth);
-        __syncwarp();
-        const uint32_t at = ring + slot * kSlot;
-#pragma unroll
-        for (int h = 0; h < kStrips; ++h) {
-          float t[4] = {};
-          strip_stage<kBf16, G, 8>(t, at + h * kStripBytes, b, sum, lane, a.affine);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tot[h][i] += t[i];
-        }
-        __syncwarp();  // the slot is read before it is requested again
-        if (++slot == a.depth) slot = 0;
-        s += W;
-        if (s < S) continue;
       }
-      s = my_stage;
-      if (in_round == 0) team_sync();  // the round before has been finished
-      if ((lane & 3) < 2)
+      if (got.unit < units) {
+        if (s < S) {  // (a warp without a stage takes part in the sums alone)
+          if (!fixed) {
+            if (kBeside) load(got.item, s, b);
+            if (!kBeside) {
+              if (first_x) load(got.item, s, next);
+              first_x = false;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) b[kk][v] = next[kk][v];
+              Place p = got;
+              int st = s + W;
+              if (st >= S) {
+                st = my_stage;
+                step(p);
+              }
+              if (p.unit < units) load(p.item, st, next);
+            }
+            sum_x<kBf16, NG>(b, sum);
+          }
+          wait_piece(a.depth);
+          __syncwarp();
+          const uint32_t at = ring + slot * kSlot;
+#pragma unroll
+          for (int h = 0; h < kStrips; ++h) {
+            float t[4] = {};
+            strip_stage<kBf16, G, 8>(t, at + h * kStripBytes, b, sum, lane, a.affine);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tot[h][i] += t[i];
+          }
+          __syncwarp();  // the slot is read before it is requested again
+          if (++slot == a.depth) slot = 0;
+          s += W;
+          if (s < S) continue;
+        }
+        s = my_stage;
+        if (in_round == 0) team_sync();  // the round before has been finished
+        if ((lane & 3) < 2)
+#pragma unroll
+          for (int h = 0; h < kStrips; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              red[warp * kRedWarp + ((in_round * kStrips + h) * 4 + i) * 16 + (lane & 3) * 8 + (lane >> 2)] = tot[h][i];
 #pragma unroll
         for (int h = 0; h < kStrips; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            red[warp * kRedWarp + ((in_round * kStrips + h) * 4 + i) * 16 + (lane & 3) * 8 + (lane >> 2)] = tot[h][i];
-#pragma unroll
-      for (int h = 0; h < kStrips; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tot[h][i] = 0.f;
-      step(item, group);
-      ++in_round;
-      if (in_round < round && item < items) continue;
-    } else if (in_round == 0) {
-      break;
-    }
-    team_sync();
-    // Each warp takes a unit of the round, one of its strips and every second (or every) token: h of 8 columns, the
-    // warps' sums of a column added by four lanes, every fourth warp's by each.
-    const int local = warp & (W - 1), mine = local & (round - 1), sub = local / round;
-    const int h = sub & (kStrips - 1), c = lane >> 2, q = lane & 3;
-    if (mine < in_round) {
-      int i = round_item, g = round_group;
-#pragma unroll 1
-      for (int j = 0; j < mine; ++j) step(i, g);
-#pragma unroll 1
-      for (int n = sub / kStrips; n < r.count[i]; n += wide ? 2 : 1) {
-        const float* const p =
-            red + (warp - local) * kRedWarp + ((mine * kStrips + h) * 4 + (n & 1)) * 16 + (n >> 1) * 8 + c;
-        float gate[kUpWarps / 4], up[kUpWarps / 4];
-#pragma unroll
-        for (int w = 0; w < kUpWarps / 4; ++w) {
-          const bool on = q + 4 * w < W;
-          gate[w] = on ? p[(q + 4 * w) * kRedWarp] : 0.f;
-          up[w] = on ? p[(q + 4 * w) * kRedWarp + 32] : 0.f;
-        }
-#pragma unroll
-        for (int w = 1; w < kUpWarps / 4; ++w) {
-          gate[0] += gate[w];
-          up[0] += up[w];
-        }
-#pragma unroll
-        for (int off = 1; off < 4; off <<= 1) {
-          gate[0] += __shfl_xor_sync(0xffffffffu, gate[0], off);
-          up[0] += __shfl_xor_sync(0xffffffffu, up[0], off);
-        }
-        constexpr float kBack = 1.f / kUnit<kBf16>;
-        const float v = activate(gate[0] * kBack, a.act) * (up[0] * kBack);
-        const uint16_t hi = to16<kType>(v), lo = to16<kType>(v - from16<kType>(hi));
-        const int col = 16 * (g * kPairs) + 8 * h + c;
-        const size_t at = static_cast<size_t>(col >> 7) * pairs + r.pair[i][n];
-        if (q < 2) *reinterpret_cast<uint16_t*>(a.h + at * kPairBytes + h_place(col & 127, q)) = q ? lo : hi;
-        float sums = from16<kType>(hi) + from16<kType>(lo);
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) sums += __shfl_xor_sync(0xffffffffu, sums, off);
-        if (lane == 0) a.hsum[at * 16 + ((col & 127) >> 3)] = sums * kUnit<kBf16>;
+          for (int i = 0; i < 4; ++i) tot[h][i] = 0.f;
+        step(got);
+        ++in_round;
+        if (in_round < round && got.unit < units) continue;
+      } else if (in_round == 0) {
+        break;
       }
+      team_sync();
+      // Each warp takes a unit of the round, one of its strips and every second (or every) token: h of 8 columns, the
+      // warps' sums of a column added by four lanes, every fourth warp's by each.
+      const int local = warp & (W - 1), mine = local & (round - 1), sub = local / round;
+      const int h = sub & (kStrips - 1), c = lane >> 2, q = lane & 3;
+      if (mine < in_round) {
+        Place p = round_place;
+#pragma unroll 1
+        for (int j = 0; j < mine; ++j) step(p);
+        const int i = p.item;
+#pragma unroll 1
+        for (int n = sub / kStrips; n < r.count[i]; n += wide ? 2 : 1) {
+          const float* const from =
+              red + (warp - local) * kRedWarp + ((mine * kStrips + h) * 4 + (n & 1)) * 16 + (n >> 1) * 8 + c;
+          float gate[kUpWarps / 4], up[kUpWarps / 4];
+#pragma unroll
+          for (int w = 0; w < kUpWarps / 4; ++w) {
+            const bool on = q + 4 * w < W;
+            gate[w] = on ? from[(q + 4 * w) * kRedWarp] : 0.f;
+            up[w] = on ? from[(q + 4 * w) * kRedWarp + 32] : 0.f;
+          }
+#pragma unroll
+          for (int w = 1; w < kUpWarps / 4; ++w) {
+            gate[0] += gate[w];
+            up[0] += up[w];
+          }
+#pragma unroll
+          for (int off = 1; off < 4; off <<= 1) {
+            gate[0] += __shfl_xor_sync(0xffffffffu, gate[0], off);
+            up[0] += __shfl_xor_sync(0xffffffffu, up[0], off);
+          }
+          constexpr float kBack = 1.f / kUnit<kBf16>;
+          const float v = activate(gate[0] * kBack, a.act) * (up[0] * kBack);
+          const uint16_t hi = to16<kType>(v), lo = to16<kType>(v - from16<kType>(hi));
+          const int col = 16 * (p.group * kPairs) + 8 * h + c;
+          const size_t at = static_cast<size_t>(col >> 7) * pairs + r.pair[i][n];
+          if (q < 2) *reinterpret_cast<uint16_t*>(a.h + at * kPairBytes + h_place(col & 127, q)) = q ? lo : hi;
+          float sums = from16<kType>(hi) + from16<kType>(lo);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) sums += __shfl_xor_sync(0xffffffffu, sums, off);
+          if (lane == 0) a.hsum[at * 16 + ((col & 127) >> 3)] = sums * kUnit<kBf16>;
+        }
+      }
+      in_round = 0;
+      round_place = got;
+      if (got.unit >= units) break;
     }
-    in_round = 0;
-    round_item = item;
-    round_group = group;
-    if (item >= items) break;
   }
   cp_async_wait<0>();
 }
@@ -586,12 +618,12 @@ __global__ void __launch_bounds__(kUpThreads, kPairs == 1 ? 2 : 1) few_gate_up_k
 // --------------------------------------------------------------------- down
 //
 // A CTA takes up to 2 kDownMaxPairs strips of 16 rows and one stage of 128 columns of every item (the
-// stages rank, + cluster, .. of its cluster), kDownWarps warps per pair of strips, each for every fourth
-// item. h of the stage is held for all pairs, and so are the products' rows: a token's are then
+// stages rank, + cluster, .. of its cluster), down_warps warps per pair of strips, which take the items in
+// turn. h of the stage is held for all pairs, and so are the products' rows: a token's are then
 // added in its experts' rank order, whichever warp made them. At the end the cluster's CTAs add up their
 // sums, each for a part of the outputs.
 template <bool kBf16, int G>
-__global__ void __launch_bounds__(kDownMaxPairs * kDownWarps * 32, 2) few_down_kernel(const Args a) {
+__global__ void __launch_bounds__(kDownMaxPairs * kDownWarps * 32, 1) few_down_kernel(const Args a) {
   constexpr int kMaxNg = kStageCols / G, kStrip = 1024 + 64 * kMaxNg, kSlot = 2 * kStrip, kType = kBf16 ? 1 : 0;
   constexpr int kHalfNg = G < 64 ? 2 : 1, kHalfStrip = 512 + 64 * kHalfNg;  // a last stage of 64 columns
   // h [pairs][512] | rings | sums of h [pairs][groups of a stage] | rows [pairs of strips][pairs][33]
@@ -601,11 +633,11 @@ __global__ void __launch_bounds__(kDownMaxPairs * kDownWarps * 32, 2) few_down_k
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
   const int C = a.cluster, rank = static_cast<int>(cluster_rank()), tile = static_cast<int>(blockIdx.x) / C;
   const int S = (a.K + kStageCols - 1) / kStageCols, pairs = a.T * a.k;
-  const int turn = warp & (kDownWarps - 1), strip = tile * a.strips + (warp / kDownWarps) * 2;
+  const int turn = warp % a.down_warps, strip_pair = warp / a.down_warps, strip = tile * a.strips + strip_pair * 2;
   const uint32_t hs = smem_addr(smem), ring = hs + pairs * kPairBytes + warp * a.depth * kSlot;
   float* const hsum = reinterpret_cast<float*>(smem + pairs * kPairBytes + warps * a.depth * kSlot);
   float* const all = hsum + pairs * kMaxNg;
-  float* const rows = all + (warp / kDownWarps) * pairs * kRowWords + (lane >> 2);
+  float* const rows = all + strip_pair * pairs * kRowWords + (lane >> 2);
   if (a.listed) {  // it could not start beside the gate_up launch: the lists are there
     grid_dependency_wait();
 #pragma unroll 1
@@ -631,7 +663,7 @@ __global__ void __launch_bounds__(kDownMaxPairs * kDownWarps * 32, 2) few_down_k
           copy_warp<kSlot>(ring + pslot * kSlot, from, lane);
         else
           copy_warp<2 * kHalfStrip>(ring + pslot * kSlot, from, lane);
-        put += kDownWarps;
+        put += a.down_warps;
         if (++pslot == a.depth) pslot = 0;
       }
       cp_async_commit();
@@ -713,13 +745,13 @@ __global__ void __launch_bounds__(kDownMaxPairs * kDownWarps * 32, 2) few_down_k
       }
       __syncwarp();
       if (++slot == a.depth) slot = 0;
-      item += kDownWarps;
+      item += a.down_warps;
     }
     cp_async_wait<0>();
   }
   __syncthreads();
   // a token's rows over its experts in rank order, into its first pair's place: 32 columns by a warp
-  const int strip_pairs = warps / kDownWarps;
+  const int strip_pairs = a.strips / 2;
 #pragma unroll 1
   for (int o = warp; o < a.T * strip_pairs; o += warps) {
     const int t = o / strip_pairs, g = o - t * strip_pairs;
@@ -767,14 +799,17 @@ constexpr int kDownStatic = sizeof(Routing) + 64;
 int g_clusters[9];  // clusters of so many CTAs of the down kernel that run at a time
 
 using Kernel = void (*)(Args);
-template <bool kBf16, int kPairs>
+template <bool kBf16, int kPairs, bool kBeside>
 Kernel gate_up_of(int g) {
-  return g == 32 ? few_gate_up_kernel<kBf16, 32, kPairs>
-                 : g == 64 ? few_gate_up_kernel<kBf16, 64, kPairs> : few_gate_up_kernel<kBf16, 128, kPairs>;
+  return g == 32 ? few_gate_up_kernel<kBf16, 32, kPairs, kBeside>
+                 : g == 64 ? few_gate_up_kernel<kBf16, 64, kPairs, kBeside> : few_gate_up_kernel<kBf16, 128, kPairs, kBeside>;
 }
-Kernel gate_up_of(int type, int g, int pairs) {
-  return type == 1 ? pairs == 2 ? gate_up_of<true, 2>(g) : gate_up_of<true, 1>(g)
-                   : pairs == 2 ? gate_up_of<false, 2>(g) : gate_up_of<false, 1>(g);
+template <bool kBf16>
+Kernel gate_up_of(int g, int pairs, bool beside) {
+  return beside ? gate_up_of<kBf16, 1, true>(g) : pairs == 1 ? gate_up_of<kBf16, 1, false>(g) : gate_up_of<kBf16, 2, false>(g);
+}
+Kernel gate_up_of(int type, int g, int pairs, bool beside) {
+  return type == 1 ? gate_up_of<true>(g, pairs, beside) : gate_up_of<false>(g, pairs, beside);
 }
 Kernel down_of(int type, int g) {
   if (type == 1)
@@ -819,9 +854,8 @@ cudaError_t init_few_kernels() {
   cudaError_t e = cudaSuccess;
   for (int type = 0; type < 2; ++type)
     for (int g : {32, 64, 128}) {
-      for (int pairs : {1, 2})
-        if (e == cudaSuccess)
-          e = set_up(gate_up_of(type, g, pairs), kSmemLimit - kUpStatic);
+      for (Kernel k : {gate_up_of(type, g, 1, true), gate_up_of(type, g, 1, false), gate_up_of(type, g, 2, false)})
+        if (e == cudaSuccess) e = set_up(k, kSmemLimit - kUpStatic);
       if (e == cudaSuccess)
         e = set_up(down_of(type, g), kSmemLimit - kDownStatic);
     }
@@ -860,19 +894,22 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   while (a.strips < 2 * kDownMaxPairs && (strips + a.strips - 1) / a.strips > g_clusters[a.cluster]) a.strips += 2;
   const int slot = 2 * (1024 + 64 * (kStageCols / s.g2)), fixed = pairs * (kPairBytes + kStageCols / s.g2 * 4);
   const auto room = [&](int limit) {  // pieces of a warp that fit
-    return (limit - kDownStatic - fixed - a.strips / 2 * pairs * kRowWords * 4) / (a.strips / 2 * kDownWarps * slot);
+    return (limit - kDownStatic - fixed - a.strips / 2 * pairs * kRowWords * 4) / (a.strips / 2 * a.down_warps * slot);
   };
   // With one or two tokens it fits beside the gate_up launch, and its start is hidden; otherwise it gets the
   // lists from the gate_up launch.
   const int stages = s.d / kStageCols, piece = kUpWarps * 2 * (1024 + 64 * (kStageCols / s.g1));
   const int beside = kSmemLimit - kUpStatic - 3 * piece;
+  a.down_warps = 4;
   a.listed = room(beside) < 2;
+  if (a.listed) a.down_warps = kDownWarps;
   while (a.listed && a.strips > 2 && room(kSmemLimit) < 2) a.strips -= 2;
   const int down_depth = std::min(room(a.listed ? kSmemLimit : beside), kMaxDepth);
   // gate_up: the group size and the pairs of strips per unit that take the least time, counted in pieces of one
   // pair: two pairs at once take 1.6, a unit's barriers and epilogue 1 of a small group and 0.5 of a
   // large one. (Which experts meet is not known here; their number is about that of evenly chosen ones.)
   const double items = s.E * (1.0 - std::pow(1.0 - double(s.k) / s.E, s.T));
+  const auto cost = [&](int w, int p) { return (stages + w - 1) / w * (p == 2 ? 1.6 : 1.0) + (w == 4 ? 1.0 : 0.5); };
   double least = 1e30;
   int per_warp = 1;
   a.stage_warps = kUpWarps;
@@ -880,7 +917,7 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
     for (int p : {1, 2}) {
       if ((w == 4 && stages > kUpWarps) || (p == 2 && !a.listed)) continue;  // (the sums' order; registers)
       const double turns = std::ceil(items * (s.f / 16 / p) / (num_sms * (kUpWarps / w)));
-      const double time = turns * ((stages + w - 1) / w * (p == 2 ? 1.6 : 1.0) + (w == 4 ? 1.0 : 0.5));
+      const double time = turns * cost(w, p);
       if (time < least) {
         least = time;
         per_warp = p;
@@ -895,10 +932,14 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.per_item_inv = 1.f / a.per_item;
   const int teams = kUpWarps / a.stage_warps, units = pairs * a.per_item;
   const int grid = std::min((units + teams - 1) / teams, num_sms);
-  a.step_items = grid * teams / a.per_item;
-  a.step_rest = grid * teams % a.per_item;
+  for (int large = 0; large < 2; ++large) {
+    a.step_items[large] = grid * (large ? 1 : 4) / a.per_item;
+    a.step_rest[large] = grid * (large ? 1 : 4) % a.per_item;
+  }
+  a.turn_inv = 1.f / (4 * grid);
+  a.tail = stages <= kUpWarps ? int((cost(4, per_warp) - 0.5) / cost(kUpWarps, per_warp)) : 0;  // (0.5: a gap between them)
   a.depth = a.listed ? std::min((kSmemLimit - kUpStatic) / (per_warp * piece), 3) : 3;
-  cudaError_t err = launch_pdl(gate_up_of(type, s.g1, per_warp), dim3(grid), dim3(kUpThreads),
+  cudaError_t err = launch_pdl(gate_up_of(type, s.g1, per_warp, !a.listed), dim3(grid), dim3(kUpThreads),
                                size_t(a.depth) * per_warp * piece, st, a);
   if (err != cudaSuccess) return err;
   a.w = w_down;
@@ -906,7 +947,7 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.block16 = uint32_t(kBlockRows) * (s.f / 2 + s.f / s.g2 * 4) / 16;
   a.expert16 = a.block16 * (s.d / kBlockRows);
   a.depth = down_depth;
-  const int warps = a.strips / 2 * kDownWarps;
+  const int warps = a.strips / 2 * a.down_warps;
   const DownLaunch l((strips + a.strips - 1) / a.strips, a.cluster, warps * 32,
                      size_t(fixed) + warps * a.depth * slot + a.strips / 2 * pairs * kRowWords * 4, st);
   return cudaLaunchKernelEx(&l.cfg, down_of(type, s.g2), a);
