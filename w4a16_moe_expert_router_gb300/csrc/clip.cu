@@ -5,8 +5,9 @@
 //
 // Two passes over the data, each bound by memory: the sum of the squares, and the scaling, which is
 // left out where it would change nothing. The tensors are cut into chunks, and every CTA takes a
-// contiguous run of them, so it looks for its first tensor once; a launch carries its tensors' addresses as kernel parameters (up to kLarge of
-// them), so nothing is kept on the device from call to call and a captured graph holds its own.
+// contiguous run of them, so it looks for its first tensor once. A launch carries its tensors'
+// addresses as kernel parameters (up to kLarge of them), so nothing is kept on the device from call
+// to call and a captured graph holds its own.
 //
 // Squares are summed in fp32 over the 64 to 128 bytes that a thread takes of a chunk, in fp64 from
 // there on: an fp64 addition per element would be the bound (its rate is a hundredth of fp32's), one
@@ -19,6 +20,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "row_vec.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 namespace {
@@ -83,39 +85,65 @@ __device__ __forceinline__ void put_scaled(const Entry& e, int64_t i, float fact
   }
 }
 
-// Sum of the squares of a thread's share of a chunk: pieces v, v + kThreads, .. counted from the
-// 16-byte boundary below the tensor; the pieces that the tensor fills in part are read by elements.
+// A chunk of a tensor: pieces of 16 bytes from the boundary below the tensor on, of whose elements lo .. hi - 1 are
+// the tensor's.
+template <int kType>
+struct Chunk {
+  static constexpr int N = Vec<kType>::n, kElements = kThreads * kLoads * N;
+  const uint4* pieces;
+  int64_t first;  // the tensor's element at the chunk's element 0 (below zero where the tensor starts later)
+  int lo, hi;
+
+  __device__ __forceinline__ Chunk(const Entry& e, int chunk) {
+    pieces = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(e.data) & ~uintptr_t(15)) +
+             static_cast<int64_t>(chunk) * (kThreads * kLoads);
+    first = static_cast<int64_t>(chunk) * kElements - e.shift;
+    lo = first < 0 ? static_cast<int>(-first) : 0;
+    hi = static_cast<int>(min(e.count - first, static_cast<int64_t>(kElements)));
+  }
+  __device__ __forceinline__ bool whole() const { return lo == 0 && hi == kElements; }
+  // Whether the tensor fills the piece.
+  __device__ __forceinline__ bool full(int piece) const { return piece * N >= lo && (piece + 1) * N <= hi; }
+  // The element of the thread, or -1: those of the pieces at the tensor's ends that it fills in part are taken one
+  // by one by the first threads of two warps.
+  __device__ __forceinline__ int edge() const {
+    const int head = lo / N, tail = hi / N, t = threadIdx.x;
+    int i = -1;
+    if (t < N && lo % N) i = head * N + t;
+    if (t >= 32 && t < 32 + N && hi % N && !(lo % N && head == tail)) i = tail * N + t - 32;
+    return i >= lo && i < hi ? i : -1;
+  }
+};
+
+// Sum of the squares of a thread's share of a chunk.
 template <int kType>
 __device__ double chunk_square(const Entry& e, int chunk) {
   constexpr int N = Vec<kType>::n;
-  const int64_t v0 = static_cast<int64_t>(chunk) * (kThreads * kLoads) + threadIdx.x;
-  const int64_t end = e.shift + e.count;  // virtual elements: e.shift .. end - 1
-  const auto* aligned = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(e.data) & ~uintptr_t(15));
+  const Chunk<kType> c(e, chunk);
   uint4 x[kLoads];
+  if (c.whole()) {
 #pragma unroll
-  for (int l = 0; l < kLoads; ++l) {
-    const int64_t v = v0 + l * kThreads;
-    x[l] = make_uint4(0u, 0u, 0u, 0u);
-    if (v * N >= e.shift && (v + 1) * N <= end) x[l] = aligned[v];
+    for (int l = 0; l < kLoads; ++l) x[l] = c.pieces[threadIdx.x + l * kThreads];
+  } else {
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      x[l] = make_uint4(0u, 0u, 0u, 0u);
+      if (c.full(threadIdx.x + l * kThreads)) x[l] = c.pieces[threadIdx.x + l * kThreads];
+    }
   }
   float s = 0.f;
   uint32_t any = 0u;
+  int edge = -1;
+  if (!c.whole() && (edge = c.edge()) >= 0) {
+    const float f = value<kType>(e.data, c.first + edge);
+    any = __float_as_uint(f);
+    s = f * f;
+  }
 #pragma unroll
   for (int l = 0; l < kLoads; ++l) {
-    const int64_t v = v0 + l * kThreads;
-    float f[N];
-    if (v * N < end && (v * N < e.shift || (v + 1) * N > end)) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int64_t at = v * N + i;
-        f[i] = at >= e.shift && at < end ? value<kType>(e.data, at - e.shift) : 0.f;
-        any |= __float_as_uint(f[i]);
-      }
-    } else {
-      Vec<kType>::load(x[l], f);
-      any |= (x[l].x | x[l].y) | (x[l].z | x[l].w);
-    }
-    float q = 0.f;
+    float f[N], q = 0.f;
+    Vec<kType>::load(x[l], f);
+    any |= (x[l].x | x[l].y) | (x[l].z | x[l].w);
 #pragma unroll
     for (int i = 0; i < N; ++i) q = fmaf(f[i], f[i], q);
     s += q;
@@ -125,14 +153,20 @@ __device__ double chunk_square(const Entry& e, int chunk) {
   if (s >= 0x1p-100f && s <= 0x1p127f) return s;
   if ((any & (kType == 2 ? 0x7fffffffu : 0x7fff7fffu)) == 0u) return 0.0;
   double d = 0.0;
-  for (int l = 0; l < kLoads; ++l)
+  if (edge >= 0) {
+    const double f = value<kType>(e.data, c.first + edge);
+    d = f * f;
+  }
+#pragma unroll 1
+  for (int l = 0; l < kLoads; ++l) {
+    const int piece = threadIdx.x + l * kThreads;
+    if (!c.full(piece)) continue;
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
-      const int64_t at = (v0 + l * kThreads) * N + i;
-      if (at >= e.shift && at < end) {
-        const double f = value<kType>(e.data, at - e.shift);
-        d = fma(f, f, d);
-      }
+      const double f = value<kType>(e.data, c.first + piece * N + i);
+      d = fma(f, f, d);
     }
+  }
   return d;
 }
 
@@ -150,71 +184,52 @@ __device__ __forceinline__ double cta_sum(double v) {
   return s;
 }
 
-template <int kTable>
-__global__ void __launch_bounds__(kThreads, 4)
-    clip_square_kernel(const __grid_constant__ Table<kTable> t, double* partial) {
-  grid_dependents_launch();
-  grid_dependency_wait();
-  double s = 0.0;
-  const int c0 = share(t.first[t.n], blockIdx.x), c1 = share(t.first[t.n], blockIdx.x + 1);
-  int i = c0 < c1 ? find(t, c0) : 0;
-  for (int c = c0; c < c1; ++c) {
-    while (t.first[i + 1] <= c) ++i;
-    const Entry& e = t.e[i];
-    const int k = c - t.first[i];
-    s += e.type == 0 ? chunk_square<0>(e, k) : e.type == 1 ? chunk_square<1>(e, k) : chunk_square<2>(e, k);
-  }
-  s = cta_sum(s);
-  if (threadIdx.x == 0) partial[blockIdx.x] = s;
-}
-
-// Partial sums of several launches into the first place.
-__global__ void __launch_bounds__(kThreads) clip_total_kernel(double* partial, int n) {
-  grid_dependents_launch();
-  grid_dependency_wait();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) s += partial[i];
-  s = cta_sum(s);  // its barrier: all have read before the first place is written
-  if (threadIdx.x == 0) partial[0] = s;
-}
-
 template <int kType>
 __device__ void scale_chunk(const Entry& e, int chunk, float factor) {
   constexpr int N = Vec<kType>::n, kBatch = 4;
-  const int64_t end = e.shift + e.count;
-  const auto* src = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(e.data) & ~uintptr_t(15));
-  auto* dst = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(e.out) & ~uintptr_t(15));
+  const Chunk<kType> c(e, chunk);
+  auto* const dst = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(e.out) & ~uintptr_t(15)) +
+                    static_cast<int64_t>(chunk) * (kThreads * kLoads);
+  const auto scaled = [&](uint4 x) {
+    if (factor != 1.f) {  // else the bits are copied, a NaN's too
+      float f[N];
+      Vec<kType>::load(x, f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] *= factor;
+      x = Vec<kType>::store(f);
+    }
+    return x;
+  };
   // the output's pieces lie as the input's do, or it is written by elements
   const bool alike = ((reinterpret_cast<uintptr_t>(e.data) ^ reinterpret_cast<uintptr_t>(e.out)) & 15u) == 0;
+  if (alike && c.whole()) {
 #pragma unroll 1
-  for (int l0 = 0; l0 < kLoads; l0 += kBatch) {
-    const int64_t v0 = static_cast<int64_t>(chunk) * (kThreads * kLoads) + l0 * kThreads + threadIdx.x;
-    if (alike && v0 * N >= e.shift && (v0 + (kBatch - 1) * kThreads + 1) * N <= end) {  // whole pieces only
+    for (int l0 = 0; l0 < kLoads; l0 += kBatch) {
       uint4 x[kBatch];
 #pragma unroll
-      for (int l = 0; l < kBatch; ++l) x[l] = src[v0 + l * kThreads];
+      for (int l = 0; l < kBatch; ++l) x[l] = c.pieces[threadIdx.x + (l0 + l) * kThreads];
 #pragma unroll
-      for (int l = 0; l < kBatch; ++l) {
-        if (factor != 1.f) {  // else the bits are copied, a NaN's too
-          float f[N];
-          Vec<kType>::load(x[l], f);
+      for (int l = 0; l < kBatch; ++l) dst[threadIdx.x + (l0 + l) * kThreads] = scaled(x[l]);
+    }
+    return;
+  }
+  const int edge = c.edge();
+  if (edge >= 0) put_scaled<kType>(e, c.first + edge, factor);
+  if (alike) {
+#pragma unroll 1
+    for (int l0 = 0; l0 < kLoads; l0 += kBatch) {
+      uint4 x[kBatch];
 #pragma unroll
-          for (int i = 0; i < N; ++i) f[i] *= factor;
-          x[l] = Vec<kType>::store(f);
-        }
-        dst[v0 + l * kThreads] = x[l];
-      }
-      continue;
+      for (int l = 0; l < kBatch; ++l)
+        if (c.full(threadIdx.x + (l0 + l) * kThreads)) x[l] = c.pieces[threadIdx.x + (l0 + l) * kThreads];
+#pragma unroll
+      for (int l = 0; l < kBatch; ++l)
+        if (c.full(threadIdx.x + (l0 + l) * kThreads)) dst[threadIdx.x + (l0 + l) * kThreads] = scaled(x[l]);
     }
-#pragma unroll 1
-    for (int l = 0; l < kBatch; ++l) {
-      const int64_t at0 = (v0 + l * kThreads) * N;
-#pragma unroll 1
-      for (int i = 0; i < N; ++i) {
-        const int64_t at = at0 + i;
-        if (at >= e.shift && at < end) put_scaled<kType>(e, at - e.shift, factor);
-      }
-    }
+  } else {  // neighbouring threads take neighbouring elements
+    const int from = (c.lo + N - 1) / N * N, to = c.hi / N * N;
+#pragma unroll 4
+    for (int i = from + static_cast<int>(threadIdx.x); i < to; i += kThreads) put_scaled<kType>(e, c.first + i, factor);
   }
 }
 
@@ -222,33 +237,27 @@ __device__ void scale_chunk(const Entry& e, int chunk, float factor) {
 __device__ __forceinline__ float root(double s) {
   if (!(s > 0.0 && s < INFINITY)) return static_cast<float>(s);
   const int64_t bits = __double_as_longlong(s);
-  const int e = (static_cast<int>(bits >> 52) - 1023) >> 1;  // floor: s = m 4^e (below 2^-1022, which squares do not reach, m is off)
+  const int e = (static_cast<int>(bits >> 52) - 1023) >> 1;  // floor: s = m 4^e (squares do not reach fp64's subnormals)
   const double m = __longlong_as_double(bits - static_cast<int64_t>(2 * e) * (int64_t(1) << 52));
   return ldexpf(sqrtf(static_cast<float>(m)), e);
 }
 
-// Every CTA adds up the partial sums itself, in the same order. Chunks are taken from a run's last one
-// back: what the pass before read last is still in L2. copies: a tensor is scaled to another place.
+// Sum of the squares of a CTA's run of chunks, in thread 0.
 template <int kTable>
-__global__ void __launch_bounds__(kThreads, 4)
-    clip_scale_kernel(const __grid_constant__ Table<kTable> t, const double* partial, int n_partial, float max_norm,
-                      bool copies, float* norm) {
-  grid_dependents_launch();
-  grid_dependency_wait();
+__device__ __forceinline__ double run_square(const Table<kTable>& t, int c0, int c1) {
   double s = 0.0;
-  for (int i = threadIdx.x; i < n_partial; i += kThreads) s += partial[i];
-  __shared__ float shared_factor;
-  s = cta_sum(s);
-  if (threadIdx.x == 0) {
-    const float v = root(s);
-    if (norm && blockIdx.x == 0) *norm = v;
-    // a norm that is no number, or infinite, leaves the values as they are
-    shared_factor = v > max_norm && v < INFINITY ? max_norm / v : 1.f;
+  int i = c0 < c1 ? find(t, c0) : 0;
+  for (int c = c0; c < c1; ++c) {
+    while (t.first[i + 1] <= c) ++i;
+    const Entry& e = t.e[i];
+    const int k = c - t.first[i];
+    s += e.type == 0 ? chunk_square<0>(e, k) : e.type == 1 ? chunk_square<1>(e, k) : chunk_square<2>(e, k);
   }
-  __syncthreads();
-  const float factor = shared_factor;
-  if (factor == 1.f && !copies) return;
-  const int c0 = share(t.first[t.n], blockIdx.x), c1 = share(t.first[t.n], blockIdx.x + 1);
+  return cta_sum(s);
+}
+// The run scaled, from its last chunk back: what the pass before read last is still in L2.
+template <int kTable>
+__device__ __forceinline__ void run_scale(const Table<kTable>& t, int c0, int c1, float factor) {
   int i = c0 < c1 ? find(t, c1 - 1) : 0;
   for (int c = c1 - 1; c >= c0; --c) {
     while (t.first[i] > c) --i;
@@ -262,6 +271,84 @@ __global__ void __launch_bounds__(kThreads, 4)
     else
       scale_chunk<2>(e, k, factor);
   }
+}
+// The factor, from the sum of the squares; a norm that is no number, or infinite, leaves the values as they are.
+__device__ __forceinline__ float factor_of(double square, float max_norm, float* norm) {
+  const float v = root(square);
+  if (norm) *norm = v;
+  return v > max_norm && v < INFINITY ? max_norm / v : 1.f;
+}
+
+template <int kTable>
+__global__ void __launch_bounds__(kThreads, 4)
+    clip_square_kernel(const __grid_constant__ Table<kTable> t, double* partial) {
+  grid_dependents_launch();
+  grid_dependency_wait();
+  const int chunks = t.first[t.n];
+  const double s = run_square(t, share(chunks, blockIdx.x), share(chunks, blockIdx.x + 1));
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// Partial sums of several launches into the first place.
+__global__ void __launch_bounds__(kThreads) clip_total_kernel(double* partial, int n) {
+  grid_dependents_launch();
+  grid_dependency_wait();
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) s += partial[i];
+  s = cta_sum(s);  // its barrier: all have read before the first place is written
+  if (threadIdx.x == 0) partial[0] = s;
+}
+
+// One warp of every CTA adds up the partial sums, all in the same order (eight of four CTAs keep an SM's fp64
+// unit busy for 2 us). copies: a tensor is scaled to another place.
+template <int kTable>
+__global__ void __launch_bounds__(kThreads, 4)
+    clip_scale_kernel(const __grid_constant__ Table<kTable> t, const double* partial, int n_partial, float max_norm,
+                      bool copies, float* norm) {
+  __shared__ float shared_factor;
+  grid_dependents_launch();
+  grid_dependency_wait();
+  if (threadIdx.x < 32) {
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 5
+    for (int i = threadIdx.x; i < n_partial; i += 128)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i + 32 * q < n_partial) s[q] += __ldcg(partial + i + 32 * q);
+    double sum = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (threadIdx.x == 0) shared_factor = factor_of(sum, max_norm, blockIdx.x == 0 ? norm : nullptr);
+  }
+  __syncthreads();
+  const float factor = shared_factor;
+  if (factor == 1.f && !copies) return;
+  const int chunks = t.first[t.n];
+  run_scale(t, share(chunks, blockIdx.x), share(chunks, blockIdx.x + 1), factor);
+}
+
+// Few chunks: one launch of one cluster, whose CTAs read each other's sums.
+constexpr int kCluster = 8, kClusterChunks = 16;
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    clip_cluster_kernel(const __grid_constant__ Table<kSmall> t, float max_norm, float* norm) {
+  __shared__ double sum;
+  __shared__ float shared_factor;
+  grid_dependents_launch();
+  grid_dependency_wait();
+  const int chunks = t.first[t.n], c0 = share(chunks, blockIdx.x), c1 = share(chunks, blockIdx.x + 1);
+  const double s = run_square(t, c0, c1);
+  if (threadIdx.x == 0) sum = s;
+  cluster_sync();
+  if (threadIdx.x == 0) {
+    double part[kCluster];
+#pragma unroll
+    for (int q = 0; q < kCluster; ++q)
+      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(part[q]) : "r"(cluster_addr(smem_addr(&sum), q)) : "memory");
+    const double all = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+    shared_factor = factor_of(all, max_norm, blockIdx.x == 0 ? norm : nullptr);
+  }
+  cluster_sync();  // the sums are read before their CTA leaves, and the factor is there
+  run_scale(t, c0, c1, shared_factor);
 }
 
 // The next tensors of a list, up to kTable; returns how many it took.
@@ -286,13 +373,17 @@ int fill(Table<kTable>& t, const moe_w4a16_tensor* tensors, int n) {
 int ctas_of(int chunks) { return chunks < 1 ? 1 : chunks < kCtas ? chunks : kCtas; }
 
 template <int kTable>
-cudaError_t run(const moe_w4a16_tensor* tensors, int n, double max_norm, float* norm, double* partial, cudaStream_t st) {
+cudaError_t run(const moe_w4a16_tensor* tensors, int n, double max_norm, float* norm, double* partial,
+                cudaStream_t st) {
   static thread_local Table<kTable> t;
   cudaError_t err = cudaSuccess;
   const float bound = max_norm > FLT_MAX ? INFINITY : static_cast<float>(max_norm);
   int sums = 0, launches = 0;
   for (int at = 0; at < n || launches == 0; ++launches) {
     at += fill(t, tensors + at, n - at);
+    if constexpr (kTable == kSmall)
+      if (t.first[t.n] <= kClusterChunks)
+        return launch_pdl(clip_cluster_kernel, dim3(kCluster), dim3(kThreads), 0, st, t, bound, norm);
     const int ctas = ctas_of(t.first[t.n]);
     if ((err = launch_pdl(clip_square_kernel<kTable>, dim3(ctas), dim3(kThreads), 0, st, t, partial + sums)) !=
         cudaSuccess)

@@ -155,8 +155,8 @@ struct Ring {
     return at + ((stage * kTensors + tensor) * kPieces + p) * pitch;
   }
   // Requests a row of every tensor that is there.
-  __device__ __forceinline__ void request(const uint4* const (&t)[kTensors], size_t base, int column, int nvec, int group,
-                                          bool more) {
+  __device__ __forceinline__ void request(const uint4* const (&t)[kTensors], size_t base, int column, int nvec,
+                                          int group, bool more) {
     if (more) {
 #pragma unroll
       for (int i = 0; i < kTensors; ++i)
@@ -528,10 +528,12 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(const SumArgs a) {
   int turn = 0;
   for (int g = gates ? y - 2 : 0; g < (gates ? a.gates : 1); g += gates ? gridDim.y - 2 : 1) {
     int u0 = 0, u1 = a.ctas - 1;
+    bool earlier = false;
     if (gates) {
       u0 = unit_of(g * a.gate_rows, a.R, a.units);
       u1 = unit_of(min((g + 1) * a.gate_rows, a.R) - 1, a.R, a.units);
       if (u0 == u1) continue;  // written by its unit
+      earlier = unit_first(u0, a.R, a.units) < g * a.gate_rows;
     }
     const float* src = gates ? a.slots : y == 0 ? a.part_post : a.part_pre;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -539,7 +541,7 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(const SumArgs a) {
 #pragma unroll 5
       for (int u = u0 + slice; u <= u1; u += 64) {
         size_t at = u;
-        if (gates) at = 2 * at + (unit_first(u, a.R, a.units) / a.gate_rows != g);
+        if (gates) at = 2 * at + (u == u0 && earlier);  // only the first unit may have begun with an earlier gate row
         add4(s, *reinterpret_cast<const float4*>(src + at * a.d + col));
       }
 #pragma unroll
