@@ -187,3 +187,37 @@ def test_structs_match_the_header(tmp_path):
     for cname, cls in structs.items():
         assert got[(cname, "size")] == ctypes.sizeof(cls)
         assert all(got[(cname, f)] == getattr(cls, f).offset for f, _ in cls._fields_)
+
+
+def test_a_blocks_buffers_are_ready_for_any_stream(monkeypatch):
+    """Its own buffers are allocated before those of its layer, whose constructor ends when the stream has."""
+    from w4a16_moe_expert_router_gb300 import runtime
+    seen, empty = [], torch.empty
+
+    class Stream:
+        def synchronize(self):
+            seen.append("synchronize")
+
+    monkeypatch.setattr(B, "moe_w4a16_workspace_init", lambda ws, stream=None: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: seen.append("empty") or empty(*a, **k))
+    runtime.Block16(4, 64, 64, 4, 2, gate_rows=3, device="cpu")
+    assert seen.count("synchronize") == 1 and seen[-1] == "synchronize"
+
+
+def test_layer16_without_its_residual(monkeypatch):
+    """The layer adds x and its gradient only where it was asked to."""
+    from w4a16_moe_expert_router_gb300 import runtime
+    seen = []
+    for name in [n for n in vars(B) if n.startswith("moe_w4a16_") and not n.endswith("_bytes")]:
+        monkeypatch.setattr(B, name, lambda *a, name=name: seen.append((name, a)))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    layer = runtime.Layer16(4, 64, 64, 4, 2, device="cpu")
+    x, dout = object(), object()
+    for residual in (True, False):
+        seen.clear()
+        layer.forward(x, None, None, None, None, None, residual)
+        layer.backward(dout)
+        rows = [a for n, a in seen if n == "moe_w4a16_combine_rows"]
+        assert [a[4] for a in rows] == ([x, dout] if residual else [None, None])

@@ -128,7 +128,9 @@ CASES = [  # T, d, f, E, k, g1, g2, format, activation, type
     (3, 384, 192, 5, 3, 32, 32, 2, 0, 0), (4, 1152, 448, 60, 3, 32, 64, 2, 1, 1), (5, 640, 320, 256, 8, 128, 64, 0, 0, 1),
     (7, 128, 1024, 129, 7, 32, 128, 1, 0, 0), (8, 2048, 704, 128, 8, 128, 64, 1, 0, 1), (9, 256, 64, 3, 3, 64, 32, 0, 1, 0),
     (16, 1024, 512, 128, 8, 64, 64, 0, 0, 0), (17, 512, 576, 31, 5, 128, 64, 2, 0, 1), (31, 256, 256, 7, 4, 64, 64, 0, 0, 0),
-    (32, 384, 128, 255, 8, 32, 128, 1, 1, 1), (32, 1280, 832, 16, 8, 64, 32, 0, 0, 0), (6, 8192, 128, 4, 2, 128, 64, 0, 0, 0),
+    (1, 4096, 192, 3, 2, 64, 32, 1, 0, 1), (2, 2048, 704, 128, 8, 64, 64, 2, 0, 0), (3, 256, 1600, 8, 2, 64, 64, 0, 0, 0),
+    (12, 512, 2048, 6, 3, 128, 128, 1, 0, 1), (16, 2048, 704, 128, 8, 64, 64, 0, 0, 1), (20, 4096, 512, 48, 4, 64, 64, 0, 1, 0),
+    (24, 2048, 256, 200, 8, 32, 32, 0, 0, 0), (32, 384, 128, 255, 8, 32, 128, 1, 1, 1), (32, 1280, 832, 16, 8, 64, 32, 0, 0, 0), (6, 8192, 128, 4, 2, 128, 64, 0, 0, 0),
 ]
 IDS = ["-".join(map(str, c)) for c in CASES]
 
@@ -170,6 +172,12 @@ def test_a_token_does_not_depend_on_the_others(B, typ):
     for tokens in (slice(0, 1), slice(5, 14), slice(31, 32), slice(8, 32)):
         part = layer.run(tokens)
         assert all(torch.equal(a[tokens], b) for a, b in zip(whole, part))
+    # the sizes for which the layer's contraction is shared in several ways
+    for d, f, E, k in ((2048, 704, 128, 8), (1152, 448, 60, 3), (384, 1600, 16, 2)):
+        big = Layer(B, 32, d, f, E, k, 64, 64, 0, 0, typ, residual=False)
+        whole_big = big.run()
+        for tokens in (slice(0, 1), slice(3, 5), slice(7, 11), slice(0, 16), slice(1, 18)):
+            assert all(torch.equal(a[tokens], b) for a, b in zip(whole_big, big.run(tokens)))
     layer.x[7] = float("inf")  # nor on what is no number there
     layer.x[8] = float("nan")
     broken = layer.run()
