@@ -6,11 +6,17 @@
 // A few tokens meet almost as many experts as they have choices, and an expert's weights are used
 // for one or two of them: the time is the way of the chosen experts' weights from memory (19 MB for
 // one token of top-8, d 2048, f 704: 2.9 us), and, for one token, what is not hidden behind it. So
-//  - every CTA forms the routing itself (a warp per token), instead of a launch for it;
-//  - the down launch starts while the gate_up launch runs, forms the routing too and requests its
-//    first weights before it waits for h;
+//  - every CTA forms the routing itself, instead of a launch for it;
+//  - with one or two tokens the down launch starts while the gate_up launch runs, forms the routing too
+//    and requests its first weights before it waits for h (for more its shared memory does not fit
+//    beside the other's; it gets the lists then);
 //  - the contraction is shared by the warps of a CTA (gate_up) or by the CTAs of a cluster (down);
-//    each warp streams its own stages with cp.async, several ahead, also across work items.
+//    each warp streams its own stages with cp.async, some ahead, also across work items.
+// Measured in a replayed graph: 1 token 13.4 us (1.4 TB/s), 4 tokens of bf16 35 (1.9), 16 tokens 61 (3.3).
+// One token is bound by the chain routing 2.0 us, first weights 2.3, products 2, the way to the down
+// launch 0.9, its h, products and sums 3.5; sixteen by the issue of instructions (some 180 to take a
+// 16 x 128 strip of codes through, a third of them masks and shifts of the codes) and by the parts
+// in which no weights move: routing 3.8, the lists' way 1.5, both ends' sums 4.
 //
 // The weights stay integers: a group's codes are multiplied as they are (exact products in the fp32
 // accumulators), then scale and zero-point are applied to the group's sum,
@@ -18,9 +24,8 @@
 // The sums of x come from one more matrix instruction with ones for two or four strips, the sums of h
 // from the gate_up launch. h is kept as two 16-bit values, h = hi + lo, which take two columns of
 // one instruction (four tokens per instruction, not eight): 22 bits of h for fp16, 16 for bf16. Every
-// sum has an order of its own (stages, then warps or CTAs in their order; a token's experts
-// ascending by their number modulo four), so the result does not depend on the other
-// tokens and is the same in every run.
+// sum has an order of its own (stages, then warps or CTAs in their order; a token's experts in rank
+// order), so the result does not depend on the other tokens and is the same in every run.
 #include <algorithm>
 #include <cmath>
 
@@ -65,7 +70,7 @@ struct Args {
   float turn_inv;         // gate_up: one over the units of all small groups
   int tail;               // gate_up: turns of large groups that take less than one of small ones
   int strips, cluster;    // down: strips of a CTA, CTAs that share the contraction
-  int down_warps;         // down: warps per pair of strips, each for every so-manieth item
+  int down_warps;         // down: warps per pair of strips, which take the items in turn
   int depth;              // pieces of a warp in its ring
 };
 
@@ -181,14 +186,16 @@ __device__ __forceinline__ bool choose_by_rank(Routing& r, const Args& a, uint32
   return !__any_sync(0xffffffffu, lane < a.k && r.sel[lane] < 0);  // the same in every warp
 }
 
-// Lists the items by expert ascending; a pair's w is its value (weigh() follows).
-// Ends with a barrier. scratch: kScratchBytes of free shared memory.
+// Lists the items (in any order that the choices alone decide); a pair's w is its value (weigh() follows).
+// What a warp reads of it afterwards is there (each wrote it, or a barrier came last). scratch: kScratchBytes of
+// free shared memory.
 constexpr int kScratchBytes = 2 * kMaxExperts * 4;
 __device__ __forceinline__ void form_routing(Routing& r, const Args& a, uint8_t* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x, pairs = a.T * a.k;
   if (a.T == 1) {
     if (n < (a.E > 128 ? 256 : 128) || !choose_by_rank(r, a, reinterpret_cast<uint32_t*>(scratch))) {
-      if (warp == 0) a.E <= 128 ? choose<4>(a.logits, a.E, a.k, lane, r.sel, r.w) : choose<8>(a.logits, a.E, a.k, lane, r.sel, r.w);
+      if (warp == 0 && a.E <= 128) choose<4>(a.logits, a.E, a.k, lane, r.sel, r.w);
+      if (warp == 0 && a.E > 128) choose<8>(a.logits, a.E, a.k, lane, r.sel, r.w);
       __syncthreads();
     }
     // every choice is an item; its place is the number of those that come before it (the same in every warp)
@@ -207,6 +214,43 @@ __device__ __forceinline__ void form_routing(Routing& r, const Args& a, uint8_t*
     __syncthreads();
     return;
   }
+  const auto choose_all = [&] {
+#pragma unroll 1
+    for (int t = warp; t < a.T; t += n >> 5) {
+      const float* const row = a.logits + static_cast<size_t>(t) * a.E;
+      if (a.E <= 128)
+        choose<4>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k);
+      else
+        choose<8>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k);
+      __syncwarp();
+      if (a.T > kItemTokens && lane < a.k) atomicOr(&r.mask[r.sel[t * a.k + lane]], 1u << t);
+    }
+    __syncthreads();
+  };
+  if (a.T <= kItemTokens) {
+    // An expert is an item, in the order of its first pair; a pair per lane, the same in every warp.
+    static_assert(kItemTokens * kMaxTopK <= 32, "a pair per lane");
+    choose_all();
+    const int e = lane < pairs ? r.sel[lane] : -1 - lane;
+    const unsigned peers = __match_any_sync(0xffffffffu, e), earlier = (1u << lane) - 1u;
+    const unsigned firsts = __ballot_sync(0xffffffffu, lane < pairs && (peers & earlier) == 0u);
+    const int leader = __ffs(peers) - 1, item = __popc(firsts & ((1u << leader) - 1u));
+    if (lane < pairs && lane == leader) {
+      r.expert[item] = static_cast<uint8_t>(e);
+      r.count[item] = static_cast<uint8_t>(__popc(peers));
+    }
+#pragma unroll
+    for (int j = 0; j < kItemTokens; ++j) {  // pair and token 0 behind the last one
+      const int nth = __popc(peers & earlier);
+      if (lane < pairs && (nth == j || (lane == leader && __popc(peers) <= j))) {
+        r.pair[item][j] = nth == j ? static_cast<int16_t>(lane) : int16_t(0);
+        r.token[item][j] = nth == j ? static_cast<uint8_t>(lane / a.k) : uint8_t(0);
+      }
+    }
+    if (lane == 0) r.items = __popc(firsts);
+    __syncwarp();
+    return;
+  }
 #pragma unroll 1
   for (int i = tid; i < kMaxExperts; i += n) r.mask[i] = 0u;
 #pragma unroll 1
@@ -215,17 +259,7 @@ __device__ __forceinline__ void form_routing(Routing& r, const Args& a, uint8_t*
     reinterpret_cast<uint32_t*>(r.token)[i] = 0u;
   }
   __syncthreads();
-#pragma unroll 1
-  for (int t = warp; t < a.T; t += n >> 5) {
-    const float* const row = a.logits + static_cast<size_t>(t) * a.E;
-    if (a.E <= 128)
-      choose<4>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k);
-    else
-      choose<8>(row, a.E, a.k, lane, r.sel + t * a.k, r.w + t * a.k);
-    __syncwarp();
-    if (lane < a.k) atomicOr(&r.mask[r.sel[t * a.k + lane]], 1u << t);
-  }
-  __syncthreads();
+  choose_all();
   // every warp forms the same list
   constexpr int kPer = kMaxExperts / 32;  // lane l takes experts kPer l .. kPer l + 7
   int own[kPer], sum = 0;
@@ -418,7 +452,8 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
   __shared__ float red[kUpWarps * kRedWarp];
   // the way to the logits and x (their pages' addresses) is found while the launch before runs
   for (int i = threadIdx.x; i * 32 < a.T * a.E; i += kUpThreads) prefetch_l2(a.logits + i * 32);
-  for (int i = threadIdx.x; i * 64 < a.T * a.d; i += kUpThreads) prefetch_l2(static_cast<const uint16_t*>(a.x) + i * 64);
+  for (int i = threadIdx.x; i * 64 < a.T * a.d; i += kUpThreads)
+    prefetch_l2(static_cast<const uint16_t*>(a.x) + i * 64);
   grid_dependency_wait();    // the logits, x, and h, which the call before may still read
   grid_dependents_launch();  // only now: the down launch reads logits and weights before it waits
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -427,7 +462,7 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
   const auto* const x = static_cast<const uint32_t*>(a.x) + (lane & 3);
   uint32_t b[8][2], next[8][2];  // fragments of x, loaded a piece ahead where registers allow
   float sum[NG][2];
-  const bool fixed = a.T == 1 && S <= a.stage_warps;  // (then all turns are of large groups, or each warp has one stage)
+  const bool fixed = a.T == 1 && S <= a.stage_warps;  // a warp has one stage, in groups of both sizes
   if (fixed && (warp & (a.stage_warps - 1)) < S) {
     load_x(x + (warp & (a.stage_warps - 1)) * 64, lane < 4, b);
     sum_x<kBf16, NG>(b, sum);
@@ -442,7 +477,8 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
   if (a.stage_warps == kUpWarps) {
     narrow = 0;
   } else {
-    const int turns = static_cast<int>((all_units + 0.5f) * a.turn_inv), whole = turns * static_cast<int>(gridDim.x) * 4;
+    const int turns = static_cast<int>((all_units + 0.5f) * a.turn_inv);
+    const int whole = turns * static_cast<int>(gridDim.x) * 4;
     if (all_units - whole <= a.tail * static_cast<int>(gridDim.x)) narrow = whole;
   }
   int slot = 0, pslot = 0;
@@ -796,17 +832,19 @@ __global__ void __launch_bounds__(kDownMaxPairs * kDownWarps * 32, 1) few_down_k
 constexpr int kSmemLimit = 226 * 1024;  // of a CTA, static and dynamic
 constexpr int kUpStatic = sizeof(Routing) + kUpWarps * kRedWarp * 4 + 64;
 constexpr int kDownStatic = sizeof(Routing) + 64;
+static_assert(kScratchBytes <= 4 * 2 * 2 * 1088, "the smallest rings hold what the choice of one token takes");
 int g_clusters[9];  // clusters of so many CTAs of the down kernel that run at a time
 
 using Kernel = void (*)(Args);
 template <bool kBf16, int kPairs, bool kBeside>
 Kernel gate_up_of(int g) {
-  return g == 32 ? few_gate_up_kernel<kBf16, 32, kPairs, kBeside>
-                 : g == 64 ? few_gate_up_kernel<kBf16, 64, kPairs, kBeside> : few_gate_up_kernel<kBf16, 128, kPairs, kBeside>;
+  if (g == 32) return few_gate_up_kernel<kBf16, 32, kPairs, kBeside>;
+  return g == 64 ? few_gate_up_kernel<kBf16, 64, kPairs, kBeside> : few_gate_up_kernel<kBf16, 128, kPairs, kBeside>;
 }
 template <bool kBf16>
 Kernel gate_up_of(int g, int pairs, bool beside) {
-  return beside ? gate_up_of<kBf16, 1, true>(g) : pairs == 1 ? gate_up_of<kBf16, 1, false>(g) : gate_up_of<kBf16, 2, false>(g);
+  if (beside) return gate_up_of<kBf16, 1, true>(g);
+  return pairs == 1 ? gate_up_of<kBf16, 1, false>(g) : gate_up_of<kBf16, 2, false>(g);
 }
 Kernel gate_up_of(int type, int g, int pairs, bool beside) {
   return type == 1 ? gate_up_of<true>(g, pairs, beside) : gate_up_of<false>(g, pairs, beside);
@@ -937,7 +975,8 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
     a.step_rest[large] = grid * (large ? 1 : 4) % a.per_item;
   }
   a.turn_inv = 1.f / (4 * grid);
-  a.tail = stages <= kUpWarps ? int((cost(4, per_warp) - 0.5) / cost(kUpWarps, per_warp)) : 0;  // (0.5: a gap between them)
+  // (0.5: the gap between the two)
+  a.tail = stages <= kUpWarps ? int((cost(4, per_warp) - 0.5) / cost(kUpWarps, per_warp)) : 0;
   a.depth = a.listed ? std::min((kSmemLimit - kUpStatic) / (per_warp * piece), 3) : 3;
   cudaError_t err = launch_pdl(gate_up_of(type, s.g1, per_warp, !a.listed), dim3(grid), dim3(kUpThreads),
                                size_t(a.depth) * per_warp * piece, st, a);
