@@ -203,3 +203,152 @@ def test_gradient_matches_the_definition(B, R, d, typ, form, gate_rows, scale):
     for n in got:
         alone = _backward(B, cfg, s, stream, dout, du, R, d, dt, (n,))
         assert torch.equal(alone[n], got[n]), n
+
+
+# A gate row per row, in every number of pieces; gate rows that go on in the next unit, in two units and in many.
+GATES = [
+    (2000, 2048, 1, "xypu", 1, 1.0), (1500, 520, 2, "xypu", 1, 0.5), (900, 1032, 0, "xyu", 1, 1.0), (650, 4096, 2, "xyp", 1, 1.0),
+    (640, 8192, 2, "xypu", 1, 2.0), (700, 8192, 1, "yp", 1, 1.0), (3, 264, 0, "xypu", 1, 1.0), (20000, 8, 2, "xypu", 1, 1.0),
+    (3001, 2048, 0, "xypu", 2, 1.0), (4097, 1200, 1, "xypu", 31, 1.0), (2500, 712, 2, "xypu", 900, 1.0), (1999, 4104, 0, "xyp", 500, 1.0),
+    (30000, 16, 1, "ypu", 17, 0.5), (800, 1344, 0, "xypu", 799, 1.0), (2000, 1536, 1, "xu", 0, 1.0), (2000, 5000, 2, "xyp", 0, 1.0),
+]
+GATE_IDS = ["-".join(map(str, c)) for c in GATES]
+
+
+@pytest.mark.parametrize("R,d,typ,form,gate_rows,scale", GATES, ids=GATE_IDS)
+def test_gate_rows_and_widths(B, R, d, typ, form, gate_rows, scale):
+    test_norm_matches_the_definition(B, R, d, typ, form, gate_rows, scale)
+    test_gradient_matches_the_definition(B, R, d, typ, form, gate_rows, scale)
+
+
+@pytest.mark.parametrize("R,d,typ,form,gate_rows", [(700, 1032, 1, "xypu", 1), (1300, 256, 0, "xu", 0), (650, 8192, 2, "xypu", 9),
+                                                    (5, 2048, 1, "xyu", 2)])
+def test_outputs_in_place_of_inputs(B, R, d, typ, form, gate_rows):
+    dt = TYPES[typ]
+    s = _inputs(R, d, typ, form, gate_rows)
+    cfg = B.make_norm(R, d, typ, gate_rows, 0.5, EPS)
+
+    def forward(x, y, out, u):
+        B.moe_w4a16_norm(cfg, x, y, s.get("gamma_post"), s.get("gate"), s["gamma_pre"], out, u)
+        return out, u
+
+    new = lambda: torch.full((R, d), 7, dtype=dt, device="cuda")
+    want = forward(s["x"], s.get("y"), new(), new())
+    for swap in (False, True):
+        x, y = s["x"].clone(), s["y"].clone() if "y" in s else new()
+        got = forward(x, y if "y" in s else None, *((y, x) if swap else (x, y)))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    if "y" not in s:
+        return
+    dout, du = _normal((R, d), 31, dt), _normal((R, d), 32, dt)
+    ws = torch.empty(B.moe_w4a16_norm_backward_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+
+    def backward(dout, du, dx, dy):
+        B.moe_w4a16_norm_backward(cfg, s["y"], s.get("gamma_post"), s.get("gate"), want[0], s["gamma_pre"], dout, du, dx, dy,
+                                  None, None, None, ws)
+        return dx, dy
+
+    wanted = backward(dout, du, new(), new())
+    for swap in (False, True):
+        a, b = dout.clone(), du.clone()
+        got = backward(a, b, *((b, a) if swap else (a, b)))
+        assert all(torch.equal(p, q) for p, q in zip(got, wanted))
+
+
+@pytest.mark.parametrize("R,d,typ,form,gate_rows", [(333, 1032, 1, "xypu", 7), (40, 512, 0, "xu", 0), (900, 264, 2, "xypu", 1)])
+def test_a_gradient_of_the_next_norm_alone(B, R, d, typ, form, gate_rows):
+    """No gradient arrives at out: the same as one of zeros."""
+    dt = TYPES[typ]
+    s = _inputs(R, d, typ, form, gate_rows)
+    s.pop("x")
+    stream, du = _normal((R, d), 21, dt, 2.0), _normal((R, d), 23, dt)
+    cfg = B.make_norm(R, d, typ, gate_rows, 1.0, EPS)
+    got = _backward(B, cfg, s, stream, None, du, R, d, dt, ALL)
+    zeros = _backward(B, cfg, s, stream, torch.zeros_like(du), du, R, d, dt, ALL)
+    assert all(torch.equal(got[n], zeros[n]) for n in zeros)
+
+
+def test_no_rows_clear_the_sums(B):
+    cfg = B.make_norm(0, 264, 1, 4)
+    empty = torch.empty((0, 264), dtype=torch.bfloat16, device="cuda")
+    gamma, post, pre = (torch.full((264,), 7.0, device="cuda") for _ in range(3))
+    ws = torch.empty(max(B.moe_w4a16_norm_backward_workspace_bytes(cfg), 16), dtype=torch.uint8, device="cuda")
+    B.moe_w4a16_norm(cfg, empty, empty, gamma, None, gamma, empty, empty)
+    B.moe_w4a16_norm_backward(cfg, empty, gamma, None, empty, gamma, empty, empty, empty, empty, post, None, pre, ws)
+    assert not bool(post.any()) and not bool(pre.any()) and bool((gamma == 7).all())
+
+
+def test_a_row_that_is_no_number_stays_its_own(B):
+    """Infinities and NaN of one row reach no other row."""
+    for R, d, typ, gate_rows in ((700, 1032, 1, 1), (700, 256, 0, 300), (3, 8192, 2, 3)):
+        dt = TYPES[typ]
+        s = _inputs(R, d, typ, "xypu", gate_rows)
+        cfg = B.make_norm(R, d, typ, gate_rows, 1.0, EPS)
+
+        def forward():
+            out, u = (torch.full((R, d), 7, dtype=dt, device="cuda") for _ in range(2))
+            B.moe_w4a16_norm(cfg, s["x"], s["y"], s["gamma_post"], s["gate"], s["gamma_pre"], out, u)
+            return out, u
+
+        want = forward()
+        s["x"][1, 5], s["y"][R - 1, 3] = float("inf"), float("nan")
+        got = forward()
+        keep = [r for r in range(R) if r not in (1, R - 1)]
+        assert all(torch.equal(a[keep], b[keep]) for a, b in zip(got, want))
+        assert not bool(torch.isfinite(got[1][1, 5])) and not bool(torch.isfinite(got[1][R - 1]).any())
+
+
+def test_streams_and_a_replayed_graph(B):
+    """Forward and backward captured together, replayed with other inputs, beside an eager call on another stream."""
+    R, d, typ = 777, 1032, 1
+    dt = TYPES[typ]
+    s, other = (_inputs(R, d, typ, "xypu", 9, seed=i) for i in (0, 50))
+    dout, du = _normal((R, d), 61, dt), _normal((R, d), 62, dt)
+    cfg = B.make_norm(R, d, typ, 9, 0.5, EPS)
+
+    def step(s):
+        out, u = torch.empty((R, d), dtype=dt, device="cuda"), torch.empty((R, d), dtype=dt, device="cuda")
+        B.moe_w4a16_norm(cfg, s["x"], s["y"], s["gamma_post"], s["gate"], s["gamma_pre"], out, u)
+        return [out, u, *_backward(B, cfg, s, out, dout, du, R, d, dt, ALL).values()]
+
+    want, want_other = step(s), step(other)
+    live = {k: v.clone() for k, v in s.items()}
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = step(live)
+    side = torch.cuda.Stream()
+    for source, ref in ((s, want), (other, want_other), (s, want)):
+        for k in live:
+            live[k].copy_(source[k])
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            beside = step(other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        assert all(torch.equal(a, b) for a, b in zip(beside, want_other))
+
+
+def test_rows_past_32_bits_of_offset(B):
+    R, d, dt = (1 << 20) + 3, 4104, torch.bfloat16  # 4.3 billion elements
+    x = torch.empty((R, d), dtype=dt, device="cuda")
+    for i in range(0, R, 1 << 17):
+        x[i:i + (1 << 17)].normal_()
+    gamma = _normal((d,), 5, torch.float32, 0.1, 1.0)
+    u, gx, gg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(gamma)
+
+    def step(R, x, u, gx):
+        cfg = B.make_norm(R, d, 1, 0, 1.0, EPS)
+        ws = torch.empty(B.moe_w4a16_norm_backward_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+        B.moe_w4a16_norm(cfg, x, None, None, None, gamma, None, u)
+        B.moe_w4a16_norm_backward(cfg, None, None, None, x, gamma, None, u, gx, None, None, None, gg, ws)
+        return u, gx
+
+    step(R, x, u, gx)
+    tail = x[-5:].clone()
+    want = step(5, tail, torch.empty_like(tail), torch.empty_like(tail))
+    assert torch.equal(u[-5:], want[0]) and torch.equal(gx[-5:], want[1])
+    middle = x[1046500:1046505].clone()  # on both sides of 2^32 elements
+    want = step(5, middle, torch.empty_like(middle), torch.empty_like(middle))
+    assert torch.equal(u[1046500:1046505], want[0]) and torch.equal(gx[1046500:1046505], want[1])

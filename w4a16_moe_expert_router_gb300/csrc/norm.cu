@@ -14,10 +14,11 @@
 // contiguous run of rows (a "unit"): a thread's columns stay the same, and with them the weights in
 // its registers. Rows arrive by cp.async in a ring, several ahead; a thread copies what it will
 // read itself, so the ring needs no barrier. (Loads into registers a row ahead reached 4.9 TB/s: an SM
-// needs some 60 KB in flight all the time.) The arithmetic is fp32 from load to store, on pairs (the
-// gradient spent 53 instructions an element, 63 % of the issue slots, one value at a time); u is the
-// norm of the unrounded out.
-// Measured: 16384 rows of 2048 bf16 columns with both norms and a gate 48.7 us (5.5 TB/s), their gradient
+// needs some 60 KB in flight all the time.) Where every row has a gate row of its own, that comes by the ring
+// as well (loaded when its row began: 4099 rows of 4000 fp32 columns 72.6 us, now 52.8; the gradient 113 and 92).
+// The arithmetic is fp32 from load to store, on pairs (the gradient spent 53 instructions an element, 63 %
+// of the issue slots, one value at a time); u is the norm of the unrounded out.
+// Measured: 16384 rows of 2048 bf16 columns with both norms and a gate 48.9 us (5.5 TB/s), their gradient
 // 71 us (5.6 TB/s, 45 instructions an element); one row 2.1 us.
 #include <algorithm>
 #include <atomic>
@@ -89,13 +90,16 @@ __device__ __forceinline__ void store_pairs(float* p, const float2 (&v)[n]) {
     *reinterpret_cast<float4*>(p + 2 * i) = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
 }
 
-// Rows of unit u: unit_first(u) .. unit_first(u + 1) - 1.
-__host__ __device__ inline int unit_first(int u, int R, int units) {
-  return static_cast<int>(static_cast<int64_t>(u) * R / units);
-}
-__host__ __device__ inline int unit_of(int row, int R, int units) {
-  return static_cast<int>(((static_cast<int64_t>(row) + 1) * units - 1) / R);
-}
+// The rows of the units: the first `more` have base + 1, the others base.
+struct Units {
+  int count, base, more;
+  // Rows of unit u: first(u) .. first(u + 1) - 1.
+  __device__ __forceinline__ int first(int u) const { return u * base + min(u, more); }
+  __device__ __forceinline__ int of(int row) const {
+    const int longer = more * (base + 1);
+    return row < longer ? row / (base + 1) : more + (row - longer) / base;
+  }
+};
 
 // Sums of kCount (1 or 6) values over the group, the same in all its threads. With six each step of a
 // warp's tree halves the values that a lane carries on (eight shuffles, not thirty). `part`
@@ -143,23 +147,30 @@ __device__ __forceinline__ void group_sum(float (&v)[kCount], int group, int whi
   }
 }
 
-// A thread's ring of rows: kDepth stages of kTensors tensors of kPieces pieces.
-template <int kTensors, int kPieces, int kDepth>
+// A thread's ring of rows: kDepth stages of kTensors tensors of kPieces pieces, and of a gate row of its
+// own per row, where there is one, kGate 16-byte parts per piece (two where the rows have 16 bits).
+template <int kTensors, int kPieces, int kDepth, int kGate>
 struct Ring {
   uint32_t at;     // the thread's place in the first stage
   uint32_t pitch;  // bytes from piece to piece
   int slot = 0, free = 0;
 
   __device__ __forceinline__ Ring(uint8_t* smem) : at(smem_addr(smem) + threadIdx.x * 16), pitch(blockDim.x * 16) {
-    for (int i = 0; i < kDepth * kTensors * kPieces; ++i)  // what is never copied counts as zeros
+    for (int i = 0; i < kDepth * (kTensors + kGate) * kPieces; ++i)  // what is never copied counts as zeros
       asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + i * pitch), "r"(0) : "memory");
+    if (kGate > 1) __syncwarp();
   }
   __device__ __forceinline__ uint32_t piece(int stage, int tensor, int p) const {
-    return at + ((stage * kTensors + tensor) * kPieces + p) * pitch;
+    return at + ((stage * (kTensors + kGate) + tensor) * kPieces + p) * pitch;
   }
-  // Requests a row of every tensor that is there.
-  __device__ __forceinline__ void request(const uint4* const (&t)[kTensors], size_t base, int column, int nvec,
-                                          int group, bool more) {
+  // Part h of the gate beside piece p.
+  __device__ __forceinline__ uint32_t gate(int stage, int p, int h) const {
+    return piece(stage, kTensors, 0) + (p * kGate + h) * pitch;
+  }
+  // Requests a row of every tensor that is there, and its gate.
+  __device__ __forceinline__ void request(const uint4* const (&t)[kTensors], const uint4* gates, size_t base,
+                                          int column, int nvec, int group, bool more) {
+    if (kGate > 1) __syncwarp();  // the row that was there has been read
     if (more) {
 #pragma unroll
       for (int i = 0; i < kTensors; ++i)
@@ -167,12 +178,38 @@ struct Ring {
 #pragma unroll
           for (int p = 0; p < kPieces; ++p)
             if (column + p * group < nvec) cp_async_16(piece(free, i, p), t[i] + base + column + p * group);
+      if (kGate > 0)
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+          for (int i = 0; i < kGate; ++i) {
+            // of two parts, two neighbours copy first the one's and then the other's: whole sectors
+            const int owner = kGate == 1 ? 0 : i - static_cast<int>(threadIdx.x & 1);
+            const int part = kGate == 1 ? 0 : threadIdx.x & 1, c = column + p * group + owner;
+            if (c < nvec) cp_async_16(gate(free, p, part) + owner * 16, gates + (base + c) * kGate + part);
+          }
       if (++free == kDepth) free = 0;
     }
     cp_async_commit();
   }
+  // Until the oldest row requested is there.
+  __device__ __forceinline__ void wait() const {
+    cp_async_wait<kDepth - 1>();
+    if (kGate > 1) __syncwarp();
+  }
   __device__ __forceinline__ void next() {
     if (++slot == kDepth) slot = 0;
+  }
+  // The gate of piece p of the oldest row, times w.
+  template <int n>
+  __device__ __forceinline__ void times_gate(int p, const float2 (&w)[n], float2 (&q)[n]) const {
+    float2 f[2];
+#pragma unroll
+    for (int h = 0; h < kGate; ++h) {
+      Pairs<2>::load(gate(slot, p, h), f);
+      q[2 * h] = mul2(f[0], w[2 * h]);
+      q[2 * h + 1] = mul2(f[1], w[2 * h + 1]);
+    }
   }
 };
 
@@ -182,12 +219,13 @@ struct Args {
   const uint4 *x, *y;
   const float *gamma_post, *gate, *gamma_pre;
   uint4 *out, *u;
-  int R, d, nvec, gate_rows, group, units;
+  int R, d, nvec, gate_rows, group;
+  Units units;
   float scale, eps;
 };
 
-// The factor of a thread's columns of y: gamma_post (with kPost) times the gate.
-template <int kPieces, int n, bool kPost, class A>
+// The factor of a thread's columns of y: gamma_post (with kPost) times the gate (with kGate, where there is one).
+template <int kPieces, int n, bool kPost, bool kGate, class A>
 __device__ __forceinline__ void factors(const A& a, int gate_row, int at, float2 (&w)[kPieces][n]) {
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) {
@@ -196,7 +234,7 @@ __device__ __forceinline__ void factors(const A& a, int gate_row, int at, float2
     for (int i = 0; i < n; ++i) w[p][i] = both(1.f);
     if (c >= a.nvec) continue;
     if (kPost) load_pairs(a.gamma_post + c * 2 * n, w[p]);
-    if (a.gate) {
+    if (kGate && a.gate) {
       float2 q[n];
       load_pairs(a.gate + static_cast<size_t>(gate_row) * a.d + c * 2 * n, q);
 #pragma unroll
@@ -205,30 +243,32 @@ __device__ __forceinline__ void factors(const A& a, int gate_row, int at, float2
   }
 }
 
-// kY: y is there; kU: u is wanted.
-template <int kType, int kPieces, int kDepth, bool kY, bool kU>
+// kY: y is there; kU: u is wanted; kByRow: every row has a gate row of its own.
+template <int kType, int kPieces, int kDepth, bool kY, bool kU, bool kByRow>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const Args a) {
   constexpr int n = Pairs<kType>::n;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[2][16][8];
   grid_dependents_launch();
-  Ring<2, kPieces, kDepth> ring(smem);
+  Ring<2, kPieces, kDepth, kByRow ? n / 2 : 0> ring(smem);
   const int which = threadIdx.x / a.group, at = threadIdx.x - which * a.group;
   const int unit = blockIdx.x * (blockDim.x / a.group) + which;
   grid_dependency_wait();
-  if (unit >= a.units) return;
-  const int r0 = unit_first(unit, a.R, a.units), r1 = unit_first(unit + 1, a.R, a.units);
+  if (unit >= a.units.count) return;
+  const int r0 = a.units.first(unit), r1 = a.units.first(unit + 1);
   const uint4* const rows[2] = {a.x, kY ? a.y : nullptr};
+  const auto* const gates = reinterpret_cast<const uint4*>(a.gate);
 #pragma unroll 1
   for (int i = 0; i < kDepth - 1; ++i)
-    ring.request(rows, static_cast<size_t>(r0 + i) * a.nvec, at, a.nvec, a.group, r0 + i < r1);
+    ring.request(rows, gates, static_cast<size_t>(r0 + i) * a.nvec, at, a.nvec, a.group, r0 + i < r1);
   float2 w[kPieces][n], pre[kPieces][n];
-  int gate_row = kY && a.gate ? r0 / a.gate_rows : 0, gate_end = kY && a.gate ? (gate_row + 1) * a.gate_rows : r1;
+  const bool gated = kY && !kByRow && a.gate;
+  int gate_row = gated ? r0 / a.gate_rows : 0, gate_end = gated ? (gate_row + 1) * a.gate_rows : r1;
   const auto load_w = [&] {
     if (a.gamma_post)
-      factors<kPieces, n, true>(a, gate_row, at, w);
+      factors<kPieces, n, true, !kByRow>(a, gate_row, at, w);
     else
-      factors<kPieces, n, false>(a, gate_row, at, w);
+      factors<kPieces, n, false, !kByRow>(a, gate_row, at, w);
   };
   if (kY) load_w();
   if (kU)
@@ -239,8 +279,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const Args a) {
   int call = 0;
 #pragma unroll 1
   for (int row = r0; row < r1; ++row) {
-    ring.request(rows, static_cast<size_t>(row + kDepth - 1) * a.nvec, at, a.nvec, a.group, row + kDepth - 1 < r1);
-    cp_async_wait<kDepth - 1>();
+    ring.request(rows, gates, static_cast<size_t>(row + kDepth - 1) * a.nvec, at, a.nvec, a.group,
+                 row + kDepth - 1 < r1);
+    ring.wait();
     float r = 1.f;
     if (kY && a.gamma_post) {
       float2 ss = both(0.f);
@@ -265,8 +306,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const Args a) {
       if (kY) {
         float2 y[n];
         Pairs<kType>::load(ring.piece(ring.slot, 1, p), y);
+        float2 q[n];
+        if constexpr (kByRow) ring.times_gate(p, w[p], q);
 #pragma unroll
-        for (int i = 0; i < n; ++i) o[p][i] = fma2(w[p][i], mul2(y[i], both(r)), o[p][i]);
+        for (int i = 0; i < n; ++i) o[p][i] = fma2(kByRow ? q[i] : w[p][i], mul2(y[i], both(r)), o[p][i]);
       }
       if (kU)
 #pragma unroll
@@ -285,7 +328,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const Args a) {
       }
     }
     ring.next();
-    if (kY && row + 1 == gate_end && row + 1 < r1) {
+    if (kY && !kByRow && row + 1 == gate_end && row + 1 < r1) {
       ++gate_row;
       gate_end += a.gate_rows;
       load_w();
@@ -312,28 +355,48 @@ struct GradArgs {
   uint4 *dx, *dy;
   float *part_post, *part_pre;  // [CTAs][d], or NULL where not wanted (part_post: sums P with one gate row)
   float *dgate, *slots;         // [gate rows][d] or NULL; [2 units][d]
-  int R, d, nvec, gate_rows, group, units;
+  int R, d, nvec, gate_rows, group;
+  Units units;
   float scale, eps;
 };
 
-// kNext: du is there; kPost: y goes through its norm; kGates: there are several gate rows. (What is
-// missing counts as zeros.)
-template <int kType, int kPieces, int kDepth, bool kNext, bool kPost, bool kGates>
-__global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const GradArgs a) {
+// kNext: du is there; kPost: y goes through its norm; kGates: one gate row or none, several, one per row, or no
+// y at all. (What else is missing counts as zeros.)
+enum { kOneGate, kSeveralGates, kGateByRow, kNoY };
+// CTAs of 256 threads for which an SM has registers: three where 80 a thread do without spills (16384 rows
+// of 2048 bf16 columns, the norm before a block alone: 51.6 us with two, 49.4 with three; the norm after it 57.7 and
+// 51.9).
+constexpr int grad_ctas(int type, int pieces, bool next, int gates) {
+  if (pieces > 1) return 1;
+  if (type == 2) return !next || gates == kOneGate || gates == kNoY ? 3 : 2;
+  return (next && gates == kNoY) || (!next && gates == kOneGate) ? 3 : 2;
+}
+template <int kType, int kPieces, int kDepth, bool kNext, bool kPost, int kGates>
+__global__ void __launch_bounds__(kPieces == 1 ? 256 : kMaxThreads, grad_ctas(kType, kPieces, kNext, kGates))
+    norm_backward_kernel(const GradArgs a) {
   constexpr int n = Pairs<kType>::n, N = 2 * n;
+  constexpr bool kByRow = kGates == kGateByRow, kY = kGates != kNoY;
+  constexpr int kTensors = (kNext ? 3 : 1) + kY, kYAt = kNext ? 3 : 1;  // dout, out, du, y
   extern __shared__ __align__(16) uint8_t smem[];  // the ring; at the end [2][d] sums, where a CTA has several groups
   __shared__ float part[2][16][8];
   grid_dependents_launch();
-  Ring<4, kPieces, kDepth> ring(smem);
+  Ring<kTensors, kPieces, kDepth, kByRow ? n / 2 : 0> ring(smem);
   const int which = threadIdx.x / a.group, at = threadIdx.x - which * a.group;
   const int groups = blockDim.x / a.group, unit = blockIdx.x * groups + which;
   grid_dependency_wait();
-  const int r0 = unit < a.units ? unit_first(unit, a.R, a.units) : 0;
-  const int r1 = unit < a.units ? unit_first(unit + 1, a.R, a.units) : 0;
-  const uint4* const rows[4] = {a.dout, a.y, kNext ? a.out : nullptr, kNext ? a.du : nullptr};
+  const int r0 = unit < a.units.count ? a.units.first(unit) : 0;
+  const int r1 = unit < a.units.count ? a.units.first(unit + 1) : 0;
+  const uint4* rows[kTensors];
+  rows[0] = a.dout;
+  if constexpr (kNext) {
+    rows[1] = a.out;
+    rows[2] = a.du;
+  }
+  if constexpr (kY) rows[kYAt] = a.y;
+  const auto* const gates = reinterpret_cast<const uint4*>(a.gate);
 #pragma unroll 1
   for (int i = 0; i < kDepth - 1; ++i)
-    ring.request(rows, static_cast<size_t>(r0 + i) * a.nvec, at, a.nvec, a.group, r0 + i < r1);
+    ring.request(rows, gates, static_cast<size_t>(r0 + i) * a.nvec, at, a.nvec, a.group, r0 + i < r1);
   // of the thread's columns: gamma_pre, gamma_post times the gate; sums of du n, of g m over a gate row, of dv m
   float2 pre[kPieces][n], w[kPieces][n], acc_pre[kPieces][n], acc[kPieces][n], acc_post[kPieces][n];
 #pragma unroll
@@ -342,22 +405,23 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Gra
     for (int i = 0; i < n; ++i) acc_pre[p][i] = acc[p][i] = acc_post[p][i] = pre[p][i] = both(0.f);
     if (kNext && at + p * a.group < a.nvec) load_pairs(a.gamma_pre + (at + p * a.group) * N, pre[p]);
   }
-  const int first_gate = kGates ? r0 / a.gate_rows : 0;
+  const int first_gate = kGates == kSeveralGates ? r0 / a.gate_rows : 0;
   int gate_row = first_gate, gate_end = (first_gate + 1) * a.gate_rows;
   const float inv_d = 1.f / a.d;
-  if (r0 < r1) factors<kPieces, n, kPost>(a, gate_row, at, w);
+  if (kY && r0 < r1) factors<kPieces, n, kPost, !kByRow>(a, gate_row, at, w);
 #pragma unroll 1
   for (int row = r0; row < r1; ++row) {
-    ring.request(rows, static_cast<size_t>(row + kDepth - 1) * a.nvec, at, a.nvec, a.group, row + kDepth - 1 < r1);
-    cp_async_wait<kDepth - 1>();
+    ring.request(rows, gates, static_cast<size_t>(row + kDepth - 1) * a.nvec, at, a.nvec, a.group,
+                 row + kDepth - 1 < r1);
+    ring.wait();
     const int slot = ring.slot;
     float2 g[kPieces][n], y[kPieces][n], o[kPieces][n], f[kPieces][n];
     const auto load = [&](int p) {
       Pairs<kType>::load(ring.piece(slot, 0, p), g[p]);
-      Pairs<kType>::load(ring.piece(slot, 1, p), y[p]);
+      if (kY) Pairs<kType>::load(ring.piece(slot, kYAt, p), y[p]);
       if (kNext) {
-        Pairs<kType>::load(ring.piece(slot, 2, p), o[p]);
-        Pairs<kType>::load(ring.piece(slot, 3, p), f[p]);
+        Pairs<kType>::load(ring.piece(slot, 1, p), o[p]);
+        Pairs<kType>::load(ring.piece(slot, 2, p), f[p]);
       }
     };
     // out^2, (gamma_pre du) out, y^2, and w y times dout, gamma_pre du and out
@@ -368,6 +432,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Gra
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
         load(p);
+        float2 q[n];
+        if constexpr (kByRow && kPost) ring.times_gate(p, w[p], q);
 #pragma unroll
         for (int i = 0; i < n; ++i) {
           float2 wd;
@@ -377,7 +443,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Gra
             t[1] = fma2(wd, o[p][i], t[1]);
           }
           if (kPost) {
-            const float2 wy = mul2(w[p][i], y[p][i]);
+            const float2 wy = mul2(kByRow ? q[i] : w[p][i], y[p][i]);
             t[2] = fma2(y[p][i], y[p][i], t[2]);
             t[3] = fma2(wy, g[p][i], t[3]);
             if (kNext) {
@@ -416,18 +482,33 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Gra
         for (int i = 0; i < n; ++i) v[i] = mul2(g[p][i], both(a.scale));
         a.dx[base + p * a.group] = Pairs<kType>::store(v);
       }
+      if constexpr (kByRow) {
+        float2 one[n], q[n], dq[n];
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const float2 gr = mul2(g[p][i], both(rb));
-        acc[p][i] = fma2(gr, y[p][i], acc[p][i]);
-        y[p][i] = fma2(both(-cb), y[p][i], mul2(w[p][i], gr));
+        for (int i = 0; i < n; ++i) one[i] = both(1.f);
+        ring.times_gate(p, one, q);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const float2 gr = mul2(g[p][i], both(rb)), gm = mul2(gr, y[p][i]);
+          acc_post[p][i] = fma2(q[i], gm, acc_post[p][i]);
+          dq[i] = kPost ? mul2(w[p][i], gm) : gm;
+          y[p][i] = fma2(both(-cb), y[p][i], mul2(kPost ? mul2(q[i], w[p][i]) : q[i], gr));
+        }
+        if (a.dgate && on) store_pairs(a.dgate + (base + p * a.group) * N, dq);
+      } else if constexpr (kY) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const float2 gr = mul2(g[p][i], both(rb));
+          acc[p][i] = fma2(gr, y[p][i], acc[p][i]);
+          y[p][i] = fma2(both(-cb), y[p][i], mul2(w[p][i], gr));
+        }
       }
-      if (a.dy && on) a.dy[base + p * a.group] = Pairs<kType>::store(y[p]);
+      if (kY && a.dy && on) a.dy[base + p * a.group] = Pairs<kType>::store(y[p]);
     }
     ring.next();
-    if (kGates && (row + 1 == gate_end || row + 1 == r1)) {  // the end of a gate row, or of its part of the unit
+    if (kGates == kSeveralGates && (row + 1 == gate_end || row + 1 == r1)) {  // a gate row ends, or its part of the unit
       const int last = min(gate_end, a.R) - 1;
-      const bool whole = unit_of(gate_row * a.gate_rows, a.R, a.units) == unit && last < r1;
+      const bool whole = gate_row * a.gate_rows >= r0 && last < r1;
       float* const dst = !a.dgate ? nullptr
                          : whole  ? a.dgate + static_cast<size_t>(gate_row) * a.d
                                   : a.slots + (static_cast<size_t>(2 * unit) + (gate_row != first_gate)) * a.d;
@@ -454,7 +535,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Gra
       if (row + 1 < r1) {
         ++gate_row;
         gate_end += a.gate_rows;
-        factors<kPieces, n, kPost>(a, gate_row, at, w);
+        factors<kPieces, n, kPost, true>(a, gate_row, at, w);
       }
     }
   }
@@ -501,14 +582,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Gra
   }
 }
 
-// The second launch: 16 columns per CTA (4 lanes of four), 64 slices of the partial sums, which meet in
-// a fixed tree. blockIdx.y 0 and 1: over the CTAs, for gamma_post (and the gate, where it has one row) and
-// gamma_pre; from 2 on: gate rows with partial sums.
+// The second launch. First, by CTAs of 16 columns: the sums over the CTAs, for gamma_post (and the gate, where it
+// has one row) and for gamma_pre, in 64 slices that meet in a fixed tree. Then the gate rows with partial
+// sums: in the same way, where a gate row spreads over many units; else (`thin`) a CTA of 1024 columns for
+// every unit whose last gate row goes on in the next one.
 struct SumArgs {
   const float *part_post, *part_pre, *slots;
   const float *gamma_post, *gate;  // the factors of P with one gate row (NULL: one)
   float *dgamma_post, *dgamma_pre, *dgate;
-  int R, d, gate_rows, ctas, units, gates;  // gates: gate rows to add up from slots
+  int R, d, gate_rows, ctas, columns;  // columns: CTAs of 16 columns
+  Units units;
+  bool thin;
 };
 
 __device__ __forceinline__ void add4(float4& a, const float4& b) {
@@ -519,66 +603,76 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) {
 }
 
 __global__ void __launch_bounds__(256) norm_sum_kernel(const SumArgs a) {
-  __shared__ float4 part[2][8][4];
+  __shared__ float4 part[8][4];
   grid_dependents_launch();
   grid_dependency_wait();
-  const int lane = threadIdx.x & 3, slice = threadIdx.x >> 2, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 16 + lane * 4;
-  const bool on = col < a.d;
-  const int y = blockIdx.y;
-  const bool gates = y >= 2;
-  if (!gates && !(y == 0 ? a.part_post : a.part_pre)) return;
-  int turn = 0;
-  for (int g = gates ? y - 2 : 0; g < (gates ? a.gates : 1); g += gates ? gridDim.y - 2 : 1) {
-    int u0 = 0, u1 = a.ctas - 1;
-    bool earlier = false;
-    if (gates) {
-      u0 = unit_of(g * a.gate_rows, a.R, a.units);
-      u1 = unit_of(min((g + 1) * a.gate_rows, a.R) - 1, a.R, a.units);
-      if (u0 == u1) continue;  // written by its unit
-      earlier = unit_first(u0, a.R, a.units) < g * a.gate_rows;
+  const int kind = blockIdx.x / a.columns;  // 0, 1: gamma_post, gamma_pre; from 2 on: gate rows
+  int u0 = 0, u1 = a.ctas - 1, g = kind - 2;
+  bool earlier = false;  // whether the first unit began with an earlier gate row: its part is in the second slot then
+  if (kind >= 2) {
+    const int i = (blockIdx.x - 2 * a.columns) / ((a.d + 1023) / 1024);  // thin: the unit
+    if (a.thin) g = a.units.first(i + 1) / a.gate_rows;
+    const int begin = g * a.gate_rows;
+    // nothing goes on, or an earlier unit's CTA has it
+    if (a.thin && (begin == a.units.first(i + 1) || begin < a.units.first(i))) return;
+    u0 = a.units.of(begin);
+    u1 = a.units.of(min(begin + a.gate_rows, a.R) - 1);
+    if (u0 == u1) return;  // written by its unit
+    earlier = a.units.first(u0) < begin;
+    if (a.thin) {
+      const int col = (blockIdx.x - 2 * a.columns - i * ((a.d + 1023) / 1024)) * 1024 + threadIdx.x * 4;
+      if (col >= a.d) return;
+      float4 s = *reinterpret_cast<const float4*>(a.slots + static_cast<size_t>(2 * u0 + earlier) * a.d + col);
+#pragma unroll 4
+      for (int u = u0 + 1; u <= u1; ++u)
+        add4(s, *reinterpret_cast<const float4*>(a.slots + static_cast<size_t>(2 * u) * a.d + col));
+      *reinterpret_cast<float4*>(a.dgate + static_cast<size_t>(g) * a.d + col) = s;
+      return;
     }
-    const float* src = gates ? a.slots : y == 0 ? a.part_post : a.part_pre;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on)
-#pragma unroll 5
-      for (int u = u0 + slice; u <= u1; u += 64) {
-        size_t at = u;
-        if (gates) at = 2 * at + (u == u0 && earlier);  // only the first unit may have begun with an earlier gate row
-        add4(s, *reinterpret_cast<const float4*>(src + at * a.d + col));
-      }
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1)
-      add4(s, make_float4(__shfl_xor_sync(0xffffffffu, s.x, off), __shfl_xor_sync(0xffffffffu, s.y, off),
-                          __shfl_xor_sync(0xffffffffu, s.z, off), __shfl_xor_sync(0xffffffffu, s.w, off)));
-    if ((threadIdx.x & 31) < 4) part[turn][warp][lane] = s;
-    __syncthreads();
-    if (slice == 0 && on) {
-      s = part[turn][0][lane];
-#pragma unroll
-      for (int k = 1; k < 8; ++k) add4(s, part[turn][k][lane]);
-      const auto put = [&](float* dst, const float* factor) {
-        float4 v = s;
-        if (factor) {
-          const float4 f = *reinterpret_cast<const float4*>(factor + col);
-          v = make_float4(s.x * f.x, s.y * f.y, s.z * f.z, s.w * f.w);
-        }
-        *reinterpret_cast<float4*>(dst + col) = v;
-      };
-      if (gates)
-        put(a.dgate + static_cast<size_t>(g) * a.d, nullptr);
-      else if (y == 1)
-        put(a.dgamma_pre, nullptr);
-      if (y == 0 && a.dgamma_post) put(a.dgamma_post, a.gate);
-      if (y == 0 && a.gates == 0 && a.dgate) put(a.dgate, a.gamma_post);
-    }
-    turn ^= 1;  // the next sums go elsewhere: no barrier before them
   }
+  const int lane = threadIdx.x & 3, slice = threadIdx.x >> 2, warp = threadIdx.x >> 5;
+  const int col = (blockIdx.x - kind * a.columns) * 16 + lane * 4;
+  const bool on = col < a.d;
+  const float* const src = kind >= 2 ? a.slots : kind == 0 ? a.part_post : a.part_pre;
+  if (!src) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (on)
+#pragma unroll 5
+    for (int u = u0 + slice; u <= u1; u += 64) {
+      size_t at = u;
+      if (kind >= 2) at = 2 * at + (u == u0 && earlier);
+      add4(s, *reinterpret_cast<const float4*>(src + at * a.d + col));
+    }
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1)
+    add4(s, make_float4(__shfl_xor_sync(0xffffffffu, s.x, off), __shfl_xor_sync(0xffffffffu, s.y, off),
+                        __shfl_xor_sync(0xffffffffu, s.z, off), __shfl_xor_sync(0xffffffffu, s.w, off)));
+  if ((threadIdx.x & 31) < 4) part[warp][lane] = s;
+  __syncthreads();
+  if (slice != 0 || !on) return;
+  s = part[0][lane];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) add4(s, part[k][lane]);
+  const auto put = [&](float* dst, const float* factor) {
+    float4 v = s;
+    if (factor) {
+      const float4 f = *reinterpret_cast<const float4*>(factor + col);
+      v = make_float4(s.x * f.x, s.y * f.y, s.z * f.z, s.w * f.w);
+    }
+    *reinterpret_cast<float4*>(dst + col) = v;
+  };
+  if (kind >= 2)
+    put(a.dgate + static_cast<size_t>(g) * a.d, nullptr);
+  else if (kind == 1)
+    put(a.dgamma_pre, nullptr);
+  if (kind == 0 && a.dgamma_post) put(a.dgamma_post, a.gate);
+  if (kind == 0 && a.dgate && a.gate_rows >= a.R) put(a.dgate, a.gamma_post);
 }
 
 // Threads of a group, groups of a CTA and CTAs.
 struct GroupShape {
-  int pieces, group, groups, ctas, units;
+  int pieces, group, groups, ctas;
+  Units units;
 };
 GroupShape group_shape(int rows, int nvec, int pieces, int max_ctas) {
   GroupShape g;
@@ -589,7 +683,8 @@ GroupShape group_shape(int rows, int nvec, int pieces, int max_ctas) {
   g.ctas = (rows + g.groups - 1) / g.groups;
   if (g.ctas < 1) g.ctas = 1;
   if (g.ctas > max_ctas) g.ctas = max_ctas;
-  g.units = std::min(g.ctas * g.groups, rows > 0 ? rows : 1);
+  const int units = std::min(g.ctas * g.groups, rows > 0 ? rows : 1);
+  g.units = Units{units, rows / units, rows % units};
   return g;
 }
 
@@ -597,7 +692,8 @@ constexpr int kSmem = 200 * 1024;  // of dynamic shared memory at most
 
 // `room` says on which devices the kernel has been given room for its shared memory.
 template <class K, class A>
-cudaError_t launch(K kernel, std::atomic<uint64_t>& room, const GroupShape& g, size_t smem, cudaStream_t st, const A& a) {
+cudaError_t launch(K kernel, std::atomic<uint64_t>& room, const GroupShape& g, size_t smem, cudaStream_t st,
+                   const A& a) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -609,64 +705,93 @@ cudaError_t launch(K kernel, std::atomic<uint64_t>& room, const GroupShape& g, s
   return launch_pdl(kernel, dim3(g.ctas), dim3(g.group * g.groups), smem, st, a);
 }
 
-// Two CTAs of 256 threads on an SM, or what fits of larger ones.
-int ctas_at_a_time(int threads, size_t smem) {
-  const int by_threads = threads <= 256 ? 2 : 1, by_smem = smem > 110 * 1024 ? 1 : 2;
-  return kNormSms * std::min(by_threads, by_smem);
+// CTAs that an SM holds at a time: each of its four parts has registers for so many warps, and a group's barrier is
+// chosen at run time, so a CTA has 16 of the SM's 64.
+int fitting(int registers, int threads, size_t smem) {
+  const int warps = 4 * std::min(512 / registers, 16);
+  return std::max(std::min({warps / (threads / 32), 226 * 1024 / (int(smem) + 2048), 4}), 1);
 }
 
-// Four pieces per thread where there are rows enough: a barrier less often; one piece where latency
-// counts.
 template <int kType, int kPieces, int kDepth>
 cudaError_t forward(Args a, cudaStream_t st) {
+  const bool by_row = a.gate && a.gate_rows == 1;
   GroupShape g = group_shape(a.R, a.nvec, kPieces, INT32_MAX);
-  const size_t smem = size_t(kDepth) * 2 * kPieces * g.group * g.groups * 16;
-  g = group_shape(a.R, a.nvec, kPieces, ctas_at_a_time(g.group * g.groups, smem));
+  const int threads = g.group * g.groups;
+  const size_t smem = size_t(kDepth) * (2 + (by_row ? kType == 2 ? 1 : 2 : 0)) * kPieces * threads * 16;
+  const int registers = kPieces == 4   ? 128
+                        : kPieces == 2 ? (kType == 2 ? 72 : by_row ? 112 : 96)
+                                       : (kType == 2 ? 48 : 72);
+  g = group_shape(a.R, a.nvec, kPieces, kNormSms * fitting(registers, threads, smem));
   a.group = g.group;
   a.units = g.units;
-  static std::atomic<uint64_t> room[3];
-  if (!a.y) return launch(norm_kernel<kType, kPieces, kDepth, false, true>, room[0], g, smem, st, a);
-  return a.u ? launch(norm_kernel<kType, kPieces, kDepth, true, true>, room[1], g, smem, st, a)
-             : launch(norm_kernel<kType, kPieces, kDepth, true, false>, room[2], g, smem, st, a);
+  static std::atomic<uint64_t> room[5];
+  if (!a.y) return launch(norm_kernel<kType, kPieces, kDepth, false, true, false>, room[0], g, smem, st, a);
+  if (by_row)
+    return a.u ? launch(norm_kernel<kType, kPieces, kDepth, true, true, true>, room[1], g, smem, st, a)
+               : launch(norm_kernel<kType, kPieces, kDepth, true, false, true>, room[2], g, smem, st, a);
+  return a.u ? launch(norm_kernel<kType, kPieces, kDepth, true, true, false>, room[3], g, smem, st, a)
+             : launch(norm_kernel<kType, kPieces, kDepth, true, false, false>, room[4], g, smem, st, a);
 }
+// Pieces per thread: four, where there are rows enough (a barrier less often), two where four would leave a fifth of
+// the threads without columns (8000 rows of 1344 bf16 columns 15.8 -> 14.6 us), one where latency counts.
 template <int kType>
 cudaError_t forward(const Args& a, cudaStream_t st) {
   if (a.nvec <= 32 || (a.nvec <= 512 && a.R <= 4 * kNormSms)) return forward<kType, 1, 3>(a, st);
-  if (a.nvec <= 64) return forward<kType, 2, 3>(a, st);
+  const bool by_row = a.gate && a.gate_rows == 1;  // the ring holds the gate too
+  const bool full = 4 * ((a.nvec + 127) / 128 * 128) <= 5 * a.nvec;
+  if ((a.nvec <= 256 && !full) || (by_row && a.nvec <= 1024)) return forward<kType, 2, 3>(a, st);
+  if (kType == 2 && by_row) return forward<2, 4, 2>(a, st);
   return forward<kType, 4, 3>(a, st);
 }
 
-// As many CTAs on an SM as its registers and shared memory hold: 128 registers a thread (96 for one piece of fp32) and
-// rings of four, three or one rows (7518 rows of 1344 fp32 columns 40.4 -> 32.7 us against one CTA per SM). One piece
-// where 256 threads hold the row: two pieces of narrower rows leave the threads half used.
-int grad_depth(int pieces) { return pieces == 1 ? 4 : pieces == 2 ? 3 : 1; }
-GroupShape grad_shape(const NormDims& s) {
-  const int nvec = s.nvec(), pieces = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+// Rows of a ring: with four tensors four rows of one piece, three of two (two with the gates) and one of four (a row of
+// 8192 fp32 columns takes 128 KB); with fewer tensors, what fits in the same memory.
+constexpr int grad_tensors(bool next, int gates) { return (next ? 3 : 1) + (gates != kNoY); }
+constexpr int grad_parts(int type, bool next, int gates) {  // 16-byte parts of a piece
+  return grad_tensors(next, gates) + (gates == kGateByRow ? type == 2 ? 1 : 2 : 0);
+}
+constexpr int grad_depth(int type, int pieces, bool next, int gates) {
+  const int all = grad_parts(type, true, gates == kGateByRow ? kGateByRow : kOneGate);
+  const int most = pieces == 1 ? 4 * all : pieces == 2 ? gates == kGateByRow ? 2 * all : 12 : all;
+  return std::max(most / grad_parts(type, next, gates), 1);
+}
+size_t grad_ring(int type, int pieces, bool next, int gates, int threads) {
+  return size_t(grad_depth(type, pieces, next, gates)) * grad_parts(type, next, gates) * pieces * threads * 16;
+}
+// As many CTAs as fit (7518 rows of 1344 fp32 columns 40.4 -> 32.7 us against one per SM). One piece per thread
+// where the rows fill 128 or 256 threads; between them two, in smaller groups of which more fit (8000
+// rows of 1200 fp16 columns 39.6 -> 31.2 us; at 2048 columns one is better by 6 % with several gate rows).
+GroupShape grad_shape(const NormDims& s, bool next, int gates) {
+  const int nvec = s.nvec(), pieces = nvec <= 128 || (nvec > 192 && nvec <= 256) ? 1 : nvec <= 1024 ? 2 : 4;
   const GroupShape g = group_shape(s.R, nvec, pieces, INT32_MAX);
-  const int threads = g.group * g.groups, smem = grad_depth(pieces) * 4 * pieces * threads * 16 + 2048;
-  const int fit = std::min(65536 / ((s.type == 2 && pieces == 1 ? 96 : 128) * threads), 226 * 1024 / smem);
-  return group_shape(s.R, nvec, pieces, kNormSms * std::max(fit, 1));
+  const int threads = g.group * g.groups;
+  const int registers = grad_ctas(s.type, pieces, next, gates) == 3 ? 80 : s.type == 2 && pieces == 1 ? 96 : 128;
+  const int fit = fitting(registers, threads, grad_ring(s.type, pieces, next, gates, threads));
+  return group_shape(s.R, nvec, pieces, kNormSms * fit);
 }
 
-template <int kType, int kPieces, int kDepth, bool kNext, bool kPost, bool kGates>
+template <int kType, int kPieces, int kGates, bool kNext, bool kPost>
 cudaError_t backward(const GradArgs& a, const GroupShape& g, cudaStream_t st) {
-  const size_t ring = size_t(kDepth) * 4 * kPieces * g.group * g.groups * 16;
+  constexpr int kDepth = grad_depth(kType, kPieces, kNext, kGates);
+  static_assert(kDepth <= 16, "registers of the ring");
   static std::atomic<uint64_t> room;
   return launch(norm_backward_kernel<kType, kPieces, kDepth, kNext, kPost, kGates>, room, g,
-                std::max(ring, size_t(8) * a.d), st, a);
+                std::max(grad_ring(kType, kPieces, kNext, kGates, g.group * g.groups), size_t(8) * a.d), st, a);
 }
-template <int kType, int kPieces, int kDepth, bool kGates>
+template <int kType, int kPieces, int kGates>
 cudaError_t backward(const GradArgs& a, const GroupShape& g, cudaStream_t st) {
   const bool next = a.du, post = a.gamma_post;
-  return next ? post ? backward<kType, kPieces, kDepth, true, true, kGates>(a, g, st)
-                     : backward<kType, kPieces, kDepth, true, false, kGates>(a, g, st)
-              : post ? backward<kType, kPieces, kDepth, false, true, kGates>(a, g, st)
-                     : backward<kType, kPieces, kDepth, false, false, kGates>(a, g, st);
+  return next ? post ? backward<kType, kPieces, kGates, true, true>(a, g, st)
+                     : backward<kType, kPieces, kGates, true, false>(a, g, st)
+              : post ? backward<kType, kPieces, kGates, false, true>(a, g, st)
+                     : backward<kType, kPieces, kGates, false, false>(a, g, st);
 }
-template <int kType, int kPieces, int kDepth>
-cudaError_t backward(const GradArgs& a, const GroupShape& g, cudaStream_t st) {
-  return a.gate && a.gate_rows < a.R ? backward<kType, kPieces, kDepth, true>(a, g, st)
-                                     : backward<kType, kPieces, kDepth, false>(a, g, st);
+template <int kType, int kPieces>
+cudaError_t backward(const GradArgs& a, const GroupShape& g, int gates, cudaStream_t st) {
+  if (gates == kNoY) return backward<kType, kPieces, kNoY, true, false>(a, g, st);
+  return gates == kOneGate        ? backward<kType, kPieces, kOneGate>(a, g, st)
+         : gates == kSeveralGates ? backward<kType, kPieces, kSeveralGates>(a, g, st)
+                                  : backward<kType, kPieces, kGateByRow>(a, g, st);
 }
 
 }  // namespace
@@ -674,26 +799,35 @@ cudaError_t backward(const GradArgs& a, const GroupShape& g, cudaStream_t st) {
 cudaError_t launch_norm(const NormDims& s, const void* x, const void* y, const float* gamma_post, const float* gate,
                         const float* gamma_pre, void* out, void* u, cudaStream_t st) {
   const Args a{static_cast<const uint4*>(x), static_cast<const uint4*>(y), gamma_post, gate, gamma_pre,
-               static_cast<uint4*>(out), static_cast<uint4*>(u), s.R, s.d, s.nvec(), s.gate_rows, 0, 0, s.scale, s.eps};
+               static_cast<uint4*>(out), static_cast<uint4*>(u), s.R, s.d, s.nvec(), gate ? s.gate_rows : s.R, 0,
+               Units{}, s.scale, s.eps};
   return s.type == 0 ? forward<0>(a, st) : s.type == 1 ? forward<1>(a, st) : forward<2>(a, st);
 }
 
-// Workspace: sums P (or of gamma_post) by CTA | of gamma_pre by CTA | gate slots by unit.
+// Workspace: sums P (or of gamma_post) by CTA | of gamma_pre by CTA | gate slots by unit; of the call that has most.
 size_t norm_backward_ws_bytes(const NormDims& s) {
-  const GroupShape g = grad_shape(s);
-  return (size_t(g.ctas) + g.units) * 2 * s.d * 4;
+  size_t most = 0;
+  for (bool next : {false, true})
+    for (int gates : {kOneGate, kSeveralGates, kGateByRow, kNoY}) {
+      const GroupShape g = grad_shape(s, next, gates);
+      most = std::max(most, (size_t(g.ctas) + g.units.count) * 2 * s.d * 4);
+    }
+  return most;
 }
 
 cudaError_t launch_norm_backward(const NormDims& s, const void* y, const float* gamma_post, const float* gate,
                                  const void* out, const float* gamma_pre, const void* dout, const void* du, void* dx,
                                  void* dy, float* dgamma_post, float* dgate, float* dgamma_pre, void* workspace,
                                  cudaStream_t st) {
-  const GroupShape g = grad_shape(s);
+  const bool several = gate && s.gate_rows < s.R;
+  const bool needs_y = (dy && gamma_post) || dgamma_post || dgate;
+  const int all = !several ? kOneGate : s.gate_rows > 1 ? kSeveralGates : kGateByRow;
+  const int gates = du && !needs_y && !dy ? kNoY : all;
+  // The inputs alone decide who takes which rows: an output has the same bits whichever others are wanted.
+  const GroupShape g = grad_shape(s, du, du && !y && !gamma_post && !gate ? kNoY : all);
   auto* const ws = static_cast<float*>(workspace);
   float* const pre = ws + size_t(g.ctas) * s.d;
   float* const slots = pre + size_t(g.ctas) * s.d;
-  const bool gates = gate && s.gate_rows < s.R;  // several gate rows
-  const bool needs_y = (dy && gamma_post) || dgamma_post || dgate;
   GradArgs a{};
   a.y = needs_y ? static_cast<const uint4*>(y) : nullptr;
   a.out = static_cast<const uint4*>(out);
@@ -704,7 +838,7 @@ cudaError_t launch_norm_backward(const NormDims& s, const void* y, const float* 
   a.gamma_pre = gamma_pre;
   a.dx = static_cast<uint4*>(dx);
   a.dy = static_cast<uint4*>(dy);
-  a.part_post = dgamma_post || (dgate && !gates) ? ws : nullptr;
+  a.part_post = dgamma_post || (dgate && !several) ? ws : nullptr;
   a.part_pre = dgamma_pre ? pre : nullptr;
   a.dgate = dgate;
   a.slots = slots;
@@ -719,9 +853,9 @@ cudaError_t launch_norm_backward(const NormDims& s, const void* y, const float* 
   cudaError_t err;
   const auto run = [&](auto type) {
     constexpr int kType = decltype(type)::value;
-    if (g.pieces == 1) return backward<kType, 1, 4>(a, g, st);  // (grad_depth's rings)
-    if (kType < 2 || g.pieces == 2) return backward<kType, 2, 3>(a, g, st);  // 8192 16-bit columns at most
-    return backward<2, 4, 1>(a, g, st);  // a row of 8192 fp32 columns takes 128 KB of the ring
+    if (g.pieces == 1) return backward<kType, 1>(a, g, gates, st);
+    if (kType < 2 || g.pieces == 2) return backward<kType, 2>(a, g, gates, st);  // 8192 16-bit columns at most
+    return backward<2, 4>(a, g, gates, st);
   };
   if (s.type == 0)
     err = run(std::integral_constant<int, 0>{});
@@ -730,10 +864,13 @@ cudaError_t launch_norm_backward(const NormDims& s, const void* y, const float* 
   else
     err = run(std::integral_constant<int, 2>{});
   if (err != cudaSuccess || (!dgamma_post && !dgamma_pre && !dgate)) return err;
-  const int rows = dgate && gates ? (s.R + s.gate_rows - 1) / s.gate_rows : 0, extra = rows > 64 ? 64 : rows;
-  const SumArgs b{a.part_post, a.part_pre, slots, gamma_post, gates ? nullptr : gate, dgamma_post, dgamma_pre, dgate,
-                  s.R, s.d, a.gate_rows, g.ctas, g.units, rows};
-  return launch_pdl(norm_sum_kernel, dim3((s.d + 15) / 16, 2 + extra), dim3(256), 0, st, b);
+  const int columns = (s.d + 15) / 16, gate_count = (s.R + a.gate_rows - 1) / a.gate_rows;
+  const bool thin = int64_t(g.units.count) * a.gate_rows <= int64_t(8) * s.R;  // a gate row in some eight units at most
+  const int shared = !dgate || !several || a.gate_rows == 1 ? 0  // (a gate row of one row is in one unit)
+                     : thin ? (g.units.count - 1) * ((s.d + 1023) / 1024) : gate_count * columns;
+  const SumArgs b{a.part_post, a.part_pre, slots, gamma_post, several ? nullptr : gate, dgamma_post, dgamma_pre, dgate,
+                  s.R, s.d, a.gate_rows, g.ctas, columns, g.units, thin};
+  return launch_pdl(norm_sum_kernel, dim3(2 * columns + shared), dim3(256), 0, st, b);
 }
 
 }  // namespace moe
