@@ -185,3 +185,41 @@ def test_an_element_past_32_bits_of_offset(B):
     t[0] = 4.0
     assert float(_clip(B, [t], 2.5)) == 5.0
     assert float(t[n - 1]) == 1.5 and float(t[0]) == 2.0
+
+
+@pytest.mark.parametrize("count", [64, 65, 640, 641, 1300])
+def test_lists_of_views_of_one_buffer(B, count):
+    """Tensors end to end, wherever that puts them, scaled in place; the list is as long as a launch takes, or longer."""
+    g = torch.Generator().manual_seed(count)
+    sizes = torch.randint(0, 3000, (count,), generator=g).tolist()
+    flat = torch.randn(sum(sizes) + 2, device="cuda").to(B16)
+    before = flat.clone()
+    tensors = list(torch.split(flat[1:-1], sizes))
+    want = _norm([before[1:-1]])
+    norm = _clip(B, tensors, 0.5 * want)
+    assert abs(float(norm) - want) <= 9 * V * want
+    _check([flat[1:-1]], [before[1:-1]], 0.5)
+    assert float(flat[0]) == float(before[0]) and float(flat[-1]) == float(before[-1])
+
+
+def test_a_list_of_nothing(B):
+    for tensors in ([], [torch.empty(0, device="cuda")] * 3, [torch.empty(0, device="cuda")] * 700):
+        assert float(_clip(B, tensors, 1.0)) == 0.0
+
+
+def test_two_calls_at_once(B):
+    """On two streams, each with a workspace of its own."""
+    lists = [_tensors([90001, 7, 300], [B16, F32], 11), _tensors([5, 1000], [F32], 12)]
+    outs = [[torch.empty_like(t) for t in lst] for lst in lists]
+    want = [(_clip(B, lst, 0.5, out).clone(), [o.clone() for o in out]) for lst, out in zip(lists, outs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in lists]
+    got = []
+    for _ in range(10):
+        for lst, s in zip(lists, streams):
+            with torch.cuda.stream(s):
+                new = [torch.empty_like(t) for t in lst]
+                got.append((_clip(B, lst, 0.5, new), new))
+    torch.cuda.synchronize()
+    for i, (norm, new) in enumerate(got):
+        assert torch.equal(norm, want[i % 2][0]) and all(torch.equal(a, b) for a, b in zip(new, want[i % 2][1]))

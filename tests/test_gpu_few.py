@@ -233,3 +233,53 @@ def test_streams_and_a_replayed_graph_with_new_inputs(B):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ref[2])
+
+
+@pytest.mark.parametrize("case", [(1, 128, 64, 256, 8, 128, 64, 0, 0, 0), (1, 256, 64, 129, 3, 64, 32, 1, 1, 1),
+                                  (4, 256, 128, 9, 8, 64, 64, 2, 0, 1), (2, 512, 2048, 200, 8, 64, 64, 0, 0, 0),
+                                  (4, 8192, 64, 40, 6, 128, 64, 0, 0, 1)], ids=lambda c: "-".join(map(str, c)))
+def test_few_tokens_over_many_and_few_experts(B, case):
+    layer = Layer(B, *case, seed=sum(case))
+    layer.check(layer.run())
+
+
+@pytest.mark.parametrize("E", [5, 128, 200, 256])
+def test_equal_logits_of_a_single_token(B, E):
+    for k in (1, 4, 5):
+        for logits in (torch.zeros(1, E), torch.arange(E).float()[None] // 3, -torch.arange(E).float()[None] % 4):
+            layer = Layer(B, 1, 128, 64, E, k, 64, 64, 0, 0, 0, logits=logits.cuda().contiguous())
+            layer.check(layer.run())
+
+
+@pytest.mark.parametrize("T", [1, 3, 4, 13])
+def test_logits_that_are_no_numbers_choose_in_bounds(B, T):
+    """Their choice is unspecified; it is one of k experts of the layer, each once, and leaves other tokens alone."""
+    layer = Layer(B, T, 256, 128, 40, 6, 64, 64, 0, 0, 1)
+    want = layer.run()
+    for value in (float("nan"), float("inf"), -float("inf")):
+        for part in (slice(0, 40), slice(0, 37), slice(3, 9)):
+            kept = layer.logits[T - 1].clone()
+            layer.logits[T - 1, part] = value
+            idx, _, out = layer.run()
+            layer.logits[T - 1] = kept
+            row = idx[T - 1].tolist()
+            assert len(set(row)) == 6 and min(row) >= 0 and max(row) < 40
+            assert torch.equal(out[:T - 1], want[2][:T - 1]) and torch.equal(idx[:T - 1], want[0][:T - 1])
+
+
+def test_two_calls_at_once(B):
+    """On two streams, each with a workspace of its own."""
+    layers = [Layer(B, T, 1024, 320, 32, 4, 64, 64, 0, 0, 0, seed=T) for T in (1, 5)]
+    want = [layer.run() for layer in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(20):
+        for layer, s in zip(layers, streams):
+            with torch.cuda.stream(s):
+                got.append(layer.run())
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
