@@ -42,7 +42,8 @@ namespace {
 constexpr int kMaxItems = kFewTokens * kMaxTopK;  // as many as pairs
 constexpr int kItemTokens = 4;                    // tokens of an item
 constexpr int kUpThreads = 512, kUpWarps = kUpThreads / 32;
-constexpr int kDownWarps = 6;                     // down: warps per pair of strips at most
+constexpr int kDownWarps = 24;                    // down: warps of a CTA at most, and where one of gate_up is beside it
+constexpr int kDownBeside = 12;
 constexpr int kDownMaxPairs = 4;                  // down: pairs of strips of a CTA
 constexpr int kPairBytes = 512;                   // a pair's h of one stage: (hi, lo) x 128 columns
 constexpr int kRowWords = 33;                     // down: a pair's 32 rows of two strips, and one word between pairs
@@ -536,15 +537,6 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
 #pragma unroll 1
           for (int i = tid; i < static_cast<int>(sizeof(Routing) / 16); i += kUpThreads)
             reinterpret_cast<uint4*>(a.routing)[i] = reinterpret_cast<const uint4*>(&r)[i];
-        if (blockIdx.x == 0) {
-          __syncthreads();
-#pragma unroll 1
-          for (int t = warp; t < a.T; t += kUpWarps) {
-            weigh(r.w + t * a.k, a.k, lane);
-            if (lane < a.k && a.topk_idx) a.topk_idx[t * a.k + lane] = r.sel[t * a.k + lane];
-            if (lane < a.k && a.topk_w) a.topk_w[t * a.k + lane] = r.w[t * a.k + lane];
-          }
-        }
       }
       if (got.unit < units) {
         if (s < S) {  // (a warp without a stage takes part in the sums alone)
@@ -659,7 +651,7 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
 // added in its experts' rank order, whichever warp made them. At the end the cluster's CTAs add up their
 // sums, each for a part of the outputs.
 template <bool kBf16, int G>
-__global__ void __launch_bounds__(kDownMaxPairs * kDownWarps * 32, 1) few_down_kernel(const Args a) {
+__global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args a) {
   constexpr int kMaxNg = kStageCols / G, kStrip = 1024 + 64 * kMaxNg, kSlot = 2 * kStrip, kType = kBf16 ? 1 : 0;
   constexpr int kHalfNg = G < 64 ? 2 : 1, kHalfStrip = 512 + 64 * kHalfNg;  // a last stage of 64 columns
   // h [pairs][512] | rings | sums of h [pairs][groups of a stage] | rows [pairs of strips][pairs][33]
@@ -707,7 +699,13 @@ __global__ void __launch_bounds__(kDownMaxPairs * kDownWarps * 32, 1) few_down_k
         if (--ahead > 0) continue;
         if (!weighed)
 #pragma unroll 1
-          for (int t = warp; t < a.T; t += warps) weigh(r.w + t * a.k, a.k, lane);
+          for (int t = warp; t < a.T; t += warps) {
+            weigh(r.w + t * a.k, a.k, lane);
+            if (blockIdx.x == 0 && lane < a.k) {
+              if (a.topk_idx) a.topk_idx[t * a.k + lane] = r.sel[t * a.k + lane];
+              if (a.topk_w) a.topk_w[t * a.k + lane] = r.w[t * a.k + lane];
+            }
+          }
         weighed = true;
         if (s == rank)
           grid_dependency_wait();  // h
@@ -898,7 +896,7 @@ cudaError_t init_few_kernels() {
         e = set_up(down_of(type, g), kSmemLimit - kDownStatic);
     }
   for (int c = 1; c <= 8 && e == cudaSuccess; ++c) {
-    const DownLaunch l(1, c, 3 * kDownWarps * 32, 128 * 1024, nullptr);
+    const DownLaunch l(1, c, 18 * 32, 128 * 1024, nullptr);
     e = cudaOccupancyMaxActiveClusters(&g_clusters[c], down_of(0, 64), &l.cfg);
   }
   return e;
@@ -931,18 +929,20 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.strips = 2;
   while (a.strips < 2 * kDownMaxPairs && (strips + a.strips - 1) / a.strips > g_clusters[a.cluster]) a.strips += 2;
   const int slot = 2 * (1024 + 64 * (kStageCols / s.g2)), fixed = pairs * (kPairBytes + kStageCols / s.g2 * 4);
-  const auto room = [&](int limit) {  // pieces of a warp that fit
-    return (limit - kDownStatic - fixed - a.strips / 2 * pairs * kRowWords * 4) / (a.strips / 2 * a.down_warps * slot);
+  const auto room = [&](int limit, int warps) {  // pieces of a warp that fit
+    return (limit - kDownStatic - fixed - a.strips / 2 * pairs * kRowWords * 4) / (a.strips / 2 * warps * slot);
   };
   // With one or two tokens it fits beside the gate_up launch, and its start is hidden; otherwise it gets the
   // lists from the gate_up launch.
   const int stages = s.d / kStageCols, piece = kUpWarps * 2 * (1024 + 64 * (kStageCols / s.g1));
   const int beside = kSmemLimit - kUpStatic - 3 * piece;
-  a.down_warps = 4;
-  a.listed = room(beside) < 2;
-  if (a.listed) a.down_warps = kDownWarps;
-  while (a.listed && a.strips > 2 && room(kSmemLimit) < 2) a.strips -= 2;
-  const int down_depth = std::min(room(a.listed ? kSmemLimit : beside), kMaxDepth);
+  a.listed = room(beside, 4) < 2;
+  const int least_warps = kDownWarps / kDownMaxPairs, limit = a.listed ? kSmemLimit : beside;
+  while (a.listed && a.strips > 2 && room(kSmemLimit, least_warps) < 2) a.strips -= 2;
+  // as many warps as there are items for
+  a.down_warps = std::max(std::min((a.listed ? kDownWarps : kDownBeside) / (a.strips / 2), pairs), 1);
+  while (a.down_warps > 1 && room(limit, a.down_warps) < 2) --a.down_warps;
+  const int down_depth = std::min(room(limit, a.down_warps), kMaxDepth);
   // gate_up: the group size and the pairs of strips per unit that take the least time, counted in pieces of one
   // pair: two pairs at once take 1.6, a unit's barriers and epilogue 1 of a small group and 0.5 of a
   // large one. (Which experts meet is not known here; their number is about that of evenly chosen ones.)
