@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
     const bool wide = large;  // one group of 16, else four of 4
     const int W = wide ? kUpWarps : kUpWarps / 4, my_stage = warp & (W - 1), team = wide ? 0 : warp >> 2;
     const int round = (wide ? kRoundStrips : kRoundStrips / 2) / kStrips;
-    const int unit0 = wide ? narrow + blockIdx.x : blockIdx.x * 4 + team, units = wide ? all_units : narrow;
+    const int unit0 = blockIdx.x + (wide ? narrow : team * static_cast<int>(gridDim.x)), units = wide ? all_units : narrow;
     const auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(wide ? 0 : 1 + team), "r"(W * 32) : "memory"); };
 
     // the piece to request next: unit pu, which is unit pg of item pi
@@ -593,46 +593,42 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
         break;
       }
       team_sync();
-      // Each warp takes a unit of the round, one of its strips and every second (or every) token: h of 8 columns, the
-      // warps' sums of a column added by four lanes, every fourth warp's by each.
-      const int local = warp & (W - 1), mine = local & (round - 1), sub = local / round;
-      const int h = sub & (kStrips - 1), c = lane >> 2, q = lane & 3;
+      // A warp takes a strip of a unit of the round, a lane a column of h for a token: the sums of the warps with stages
+      // q, q + 4, .. one after the other, then over q in a tree.
+      const int local = warp & (W - 1), mine = local / kStrips, h = local & (kStrips - 1);
       if (mine < in_round) {
         Place p = round_place;
 #pragma unroll 1
         for (int j = 0; j < mine; ++j) step(p);
-        const int i = p.item;
-#pragma unroll 1
-        for (int n = sub / kStrips; n < r.count[i]; n += wide ? 2 : 1) {
-          const float* const from =
-              red + (warp - local) * kRedWarp + ((mine * kStrips + h) * 4 + (n & 1)) * 16 + (n >> 1) * 8 + c;
-          float gate[kUpWarps / 4], up[kUpWarps / 4];
+        const int i = p.item, c = lane & 7, n = lane >> 3;
+        const float* const from =
+            red + (warp - local) * kRedWarp + ((mine * kStrips + h) * 4 + (n & 1)) * 16 + (n >> 1) * 8 + c;
+        float gate[4], up[4];
 #pragma unroll
-          for (int w = 0; w < kUpWarps / 4; ++w) {
-            const bool on = q + 4 * w < W;
-            gate[w] = on ? from[(q + 4 * w) * kRedWarp] : 0.f;
-            up[w] = on ? from[(q + 4 * w) * kRedWarp + 32] : 0.f;
-          }
+        for (int q = 0; q < 4; ++q) {
+          gate[q] = from[q * kRedWarp];
+          up[q] = from[q * kRedWarp + 32];
+        }
+        if (wide)
 #pragma unroll
-          for (int w = 1; w < kUpWarps / 4; ++w) {
-            gate[0] += gate[w];
-            up[0] += up[w];
+          for (int w = 4; w < kUpWarps; ++w) {
+            gate[w & 3] += from[w * kRedWarp];
+            up[w & 3] += from[w * kRedWarp + 32];
           }
+        constexpr float kBack = 1.f / kUnit<kBf16>;
+        const float g = (gate[0] + gate[1]) + (gate[2] + gate[3]), u = (up[0] + up[1]) + (up[2] + up[3]);
+        const float v = activate(g * kBack, a.act) * (u * kBack);
+        const uint16_t hi = to16<kType>(v), lo = to16<kType>(v - from16<kType>(hi));
+        float sums = from16<kType>(hi) + from16<kType>(lo);
 #pragma unroll
-          for (int off = 1; off < 4; off <<= 1) {
-            gate[0] += __shfl_xor_sync(0xffffffffu, gate[0], off);
-            up[0] += __shfl_xor_sync(0xffffffffu, up[0], off);
-          }
-          constexpr float kBack = 1.f / kUnit<kBf16>;
-          const float v = activate(gate[0] * kBack, a.act) * (up[0] * kBack);
-          const uint16_t hi = to16<kType>(v), lo = to16<kType>(v - from16<kType>(hi));
+        for (int off = 1; off < 8; off <<= 1) sums += __shfl_xor_sync(0xffffffffu, sums, off);
+        if (n < r.count[i]) {
           const int col = 16 * (p.group * kPairs) + 8 * h + c;
           const size_t at = static_cast<size_t>(col >> 7) * pairs + r.pair[i][n];
-          if (q < 2) *reinterpret_cast<uint16_t*>(a.h + at * kPairBytes + h_place(col & 127, q)) = q ? lo : hi;
-          float sums = from16<kType>(hi) + from16<kType>(lo);
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) sums += __shfl_xor_sync(0xffffffffu, sums, off);
-          if (lane == 0) a.hsum[at * 16 + ((col & 127) >> 3)] = sums * kUnit<kBf16>;
+          uint8_t* const dst = a.h + at * kPairBytes;
+          *reinterpret_cast<uint16_t*>(dst + h_place(col & 127, 0)) = hi;
+          *reinterpret_cast<uint16_t*>(dst + h_place(col & 127, 1)) = lo;
+          if (c == 0) a.hsum[at * 16 + ((col & 127) >> 3)] = sums * kUnit<kBf16>;
         }
       }
       in_round = 0;
@@ -677,6 +673,18 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
   }
   const int items = strip * 16 >= a.d ? 0 : r.items;  // no items for strips behind the last one
   bool weighed = false;
+  const auto weigh_all = [&] {  // while something is on its way
+    if (!weighed)
+#pragma unroll 1
+      for (int t = warp; t < a.T; t += warps) {
+        weigh(r.w + t * a.k, a.k, lane);
+        if (blockIdx.x == 0 && lane < a.k) {
+          if (a.topk_idx) a.topk_idx[t * a.k + lane] = r.sel[t * a.k + lane];
+          if (a.topk_w) a.topk_w[t * a.k + lane] = r.w[t * a.k + lane];
+        }
+      }
+    weighed = true;
+  };
 #pragma unroll 1
   for (int s = rank; s < S; s += C) {
     const bool whole = (s + 1) * kStageCols <= a.K;
@@ -697,16 +705,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
       cp_async_commit();
       if (ahead > 0) {
         if (--ahead > 0) continue;
-        if (!weighed)
-#pragma unroll 1
-          for (int t = warp; t < a.T; t += warps) {
-            weigh(r.w + t * a.k, a.k, lane);
-            if (blockIdx.x == 0 && lane < a.k) {
-              if (a.topk_idx) a.topk_idx[t * a.k + lane] = r.sel[t * a.k + lane];
-              if (a.topk_w) a.topk_w[t * a.k + lane] = r.w[t * a.k + lane];
-            }
-          }
-        weighed = true;
+        if (!a.listed) weigh_all();
         if (s == rank)
           grid_dependency_wait();  // h
         else
@@ -728,6 +727,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
           }
           hsum[p * kMaxNg + j] = v;
         }
+        weigh_all();
         cp_async_wait<0>();
         __syncthreads();
         continue;
@@ -968,8 +968,8 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.expert16 = a.block16 * (s.f / 64);
   a.per_item = s.f / 16 / per_warp;
   a.per_item_inv = 1.f / a.per_item;
-  const int teams = kUpWarps / a.stage_warps, units = pairs * a.per_item;
-  const int grid = std::min((units + teams - 1) / teams, num_sms);
+  const int units = pairs * a.per_item;
+  const int grid = std::min(units, num_sms);
   for (int large = 0; large < 2; ++large) {
     a.step_items[large] = grid * (large ? 1 : 4) / a.per_item;
     a.step_rest[large] = grid * (large ? 1 : 4) % a.per_item;
