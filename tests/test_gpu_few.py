@@ -283,3 +283,14 @@ def test_two_calls_at_once(B):
     torch.cuda.synchronize()
     for i, g in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
+
+
+@pytest.mark.parametrize("typ", [0, 1], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("d,f,E,k,fmt", [(512, 256, 200, 8, 0), (1024, 128, 196, 7, 1), (384, 384, 152, 8, 2), (256, 448, 128, 6, 0)])
+def test_many_experts_of_a_small_layer(B, d, f, E, k, fmt, typ):
+    """More items than one set of CTAs takes: the same bits as for a token alone."""
+    layer = Layer(B, 32, d, f, E, k, 64, 64, fmt, 0, typ, seed=d)
+    whole = layer.run()
+    layer.check(whole)
+    for tokens in (slice(0, 1), slice(3, 5), slice(7, 11), slice(0, 16), slice(1, 23)):
+        assert all(torch.equal(a[tokens], b) for a, b in zip(whole, layer.run(tokens)))

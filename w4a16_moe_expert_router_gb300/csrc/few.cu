@@ -12,7 +12,7 @@
 //    beside the other's; it gets the lists then);
 //  - the contraction is shared by the warps of a CTA (gate_up) or by the CTAs of a cluster (down);
 //    each warp streams its own stages with cp.async, some ahead, also across work items.
-// Measured in a replayed graph: 1 token 13.4 us (1.4 TB/s), 4 tokens of bf16 35 (1.9), 16 tokens 61 (3.3).
+// Measured in a replayed graph: 1 token 13.3 us (1.5 TB/s), 4 tokens of bf16 34.7 (2.0), 16 tokens 59.5 (3.4).
 // One token is bound by the chain routing 2.0 us, first weights 2.3, products 2, the way to the down
 // launch 0.9, its h, products and sums 3.5; sixteen by the issue of instructions (some 180 to take a
 // 16 x 128 strip of codes through, a third of them masks and shifts of the codes) and by the parts
@@ -70,7 +70,8 @@ struct Args {
   int step_items[2], step_rest[2];  // and how far the units of all groups are, of small groups and of large ones
   float turn_inv;         // gate_up: one over the units of all small groups
   int tail;               // gate_up: turns of large groups that take less than one of small ones
-  int strips, cluster;    // down: strips of a CTA, CTAs that share the contraction
+  int strips, cluster;    // down: strips of a CTA, CTAs that share the contraction and the items
+  int stage_ranks, parts; // of them: for the stages, and for each the items
   int down_warps;         // down: warps per pair of strips, which take the items in turn
   int depth;              // pieces of a warp in its ring
 };
@@ -87,6 +88,7 @@ struct alignas(16) Routing {
   uint8_t token[kMaxItems][kItemTokens];
   uint8_t expert[kMaxItems];              // expert of an item
   uint8_t count[kMaxItems];               // its tokens
+  uint8_t item[kMaxItems];                // item of a pair
   int32_t items;
 };
 
@@ -206,6 +208,7 @@ __device__ __forceinline__ void form_routing(Routing& r, const Args& a, uint8_t*
     for (int q = 0; q < kMaxTopK; ++q)
       if (q < a.k) at += r.sel[q] < e;
     if (lane < a.k) {
+      r.item[lane] = static_cast<uint8_t>(at);
       *reinterpret_cast<uint2*>(r.pair[at]) = make_uint2(lane, 0u);
       *reinterpret_cast<uint32_t*>(r.token[at]) = 0u;
       r.expert[at] = static_cast<uint8_t>(e);
@@ -236,6 +239,7 @@ __device__ __forceinline__ void form_routing(Routing& r, const Args& a, uint8_t*
     const unsigned peers = __match_any_sync(0xffffffffu, e), earlier = (1u << lane) - 1u;
     const unsigned firsts = __ballot_sync(0xffffffffu, lane < pairs && (peers & earlier) == 0u);
     const int leader = __ffs(peers) - 1, item = __popc(firsts & ((1u << leader) - 1u));
+    if (lane < pairs) r.item[lane] = static_cast<uint8_t>(item);
     if (lane < pairs && lane == leader) {
       r.expert[item] = static_cast<uint8_t>(e);
       r.count[item] = static_cast<uint8_t>(__popc(peers));
@@ -289,6 +293,7 @@ __device__ __forceinline__ void form_routing(Routing& r, const Args& a, uint8_t*
     const int t = p / a.k, e = r.sel[p];
     const uint32_t m = r.mask[e];
     const int nth = __popc(m & ((1u << t) - 1u)), item = r.base[e] + nth / kItemTokens;
+    r.item[p] = static_cast<uint8_t>(item);
     r.pair[item][nth % kItemTokens] = static_cast<int16_t>(p);
     r.token[item][nth % kItemTokens] = static_cast<uint8_t>(t);
     if (nth % kItemTokens == 0) {
@@ -347,6 +352,11 @@ __device__ __forceinline__ void apply_group(float (&tot)[4], const float (&part)
   tot[3] = fmaf(s_hi, part[3], fmaf(c_hi, sum1, tot[3]));
 }
 
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {  // of a CTA of the cluster
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(addr, rank)) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -642,10 +652,11 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
 // --------------------------------------------------------------------- down
 //
 // A CTA takes up to 2 kDownMaxPairs strips of 16 rows and one stage of 128 columns of every item (the
-// stages rank, + cluster, .. of its cluster), down_warps warps per pair of strips, which take the items in
-// turn. h of the stage is held for all pairs, and so are the products' rows: a token's are then
-// added in its experts' rank order, whichever warp made them. At the end the cluster's CTAs add up their
-// sums, each for a part of the outputs.
+// stages rank, + ranks, .. of its cluster) or, where that leaves SMs without work, of a part of the items
+// (22 tokens of 512 columns, for which 32 CTAs took 8 us: 27.5 -> 24.1 us in all); down_warps warps per pair of
+// strips take the items in turn. h of the stage is held for all pairs, and so are the products' rows: a
+// token's are then added in its experts' rank order, whichever warp or CTA made them. At the end the cluster's
+// CTAs add up their sums, each for a part of the outputs.
 template <bool kBf16, int G>
 __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args a) {
   constexpr int kMaxNg = kStageCols / G, kStrip = 1024 + 64 * kMaxNg, kSlot = 2 * kStrip, kType = kBf16 ? 1 : 0;
@@ -657,7 +668,9 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
   const int C = a.cluster, rank = static_cast<int>(cluster_rank()), tile = static_cast<int>(blockIdx.x) / C;
   const int S = (a.K + kStageCols - 1) / kStageCols, pairs = a.T * a.k;
-  const int turn = warp % a.down_warps, strip_pair = warp / a.down_warps, strip = tile * a.strips + strip_pair * 2;
+  const int stage_rank = rank % a.stage_ranks, part = rank / a.stage_ranks;
+  const int turn = (warp % a.down_warps) * a.parts + part, item_step = a.down_warps * a.parts;
+  const int strip_pair = warp / a.down_warps, strip = tile * a.strips + strip_pair * 2;
   const uint32_t hs = smem_addr(smem), ring = hs + pairs * kPairBytes + warp * a.depth * kSlot;
   float* const hsum = reinterpret_cast<float*>(smem + pairs * kPairBytes + warps * a.depth * kSlot);
   float* const all = hsum + pairs * kMaxNg;
@@ -686,7 +699,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
     weighed = true;
   };
 #pragma unroll 1
-  for (int s = rank; s < S; s += C) {
+  for (int s = stage_rank; s < S; s += a.stage_ranks) {
     const bool whole = (s + 1) * kStageCols <= a.K;
     const uint8_t* const src = a.w + (static_cast<size_t>(strip >> 3) * a.block16 + s * (8 * kStrip / 16) +
                                       (strip & 7) * ((whole ? kStrip : kHalfStrip) / 16)) * 16;
@@ -699,14 +712,14 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
           copy_warp<kSlot>(ring + pslot * kSlot, from, lane);
         else
           copy_warp<2 * kHalfStrip>(ring + pslot * kSlot, from, lane);
-        put += a.down_warps;
+        put += item_step;
         if (++pslot == a.depth) pslot = 0;
       }
       cp_async_commit();
       if (ahead > 0) {
         if (--ahead > 0) continue;
         if (!a.listed) weigh_all();
-        if (s == rank)
+        if (s == stage_rank)
           grid_dependency_wait();  // h
         else
           __syncthreads();  // h of the stage before has been read
@@ -773,13 +786,13 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
         }
         if (on) {  // (stages of the CTA after its first are added to it)
           const float lo = t[0] + t[1], hi = t[2] + t[3];
-          dst[16 * h] = s == rank ? lo : dst[16 * h] + lo;
-          dst[16 * h + 8] = s == rank ? hi : dst[16 * h + 8] + hi;
+          dst[16 * h] = s == stage_rank ? lo : dst[16 * h] + lo;
+          dst[16 * h + 8] = s == stage_rank ? hi : dst[16 * h + 8] + hi;
         }
       }
       __syncwarp();
       if (++slot == a.depth) slot = 0;
-      item += a.down_warps;
+      item += item_step;
     }
     cp_async_wait<0>();
   }
@@ -787,7 +800,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
   // a token's rows over its experts in rank order, into its first pair's place: 32 columns by a warp
   const int strip_pairs = a.strips / 2;
 #pragma unroll 1
-  for (int o = warp; o < a.T * strip_pairs; o += warps) {
+  for (int o = warp; o < a.T * strip_pairs && a.parts == 1; o += warps) {
     const int t = o / strip_pairs, g = o - t * strip_pairs;
     float* const at = all + (g * pairs + t * a.k) * kRowWords + lane;
     float part[kMaxTopK], v = 0.f;
@@ -809,16 +822,33 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
     const int t = o / strip_pairs, g = o - t * strip_pairs, col = tile * cols + g * 32 + lane;
     if (col >= a.d) continue;
     const uint32_t at = smem_addr(all + (g * pairs + t * a.k) * kRowWords + lane);
-    float part[8];
+    float sum[8];  // of the stages of a rank
+    if (a.parts == 1) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      part[q] = 0.f;
-      if (q < C) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part[q]) : "r"(cluster_addr(at, q)) : "memory");
+      for (int q = 0; q < 8; ++q) {
+        sum[q] = 0.f;
+        if (q < C) sum[q] = ld_cluster(at, q);
+      }
+    } else {  // the same sums, from the CTAs that have a pair's item
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[c] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < a.stage_ranks) {
+          float part[kMaxTopK];
+#pragma unroll
+          for (int q = 0; q < kMaxTopK; ++q)
+            if (q < a.k)
+              part[q] = ld_cluster(at + q * kRowWords * 4, c + r.item[t * a.k + q] % a.parts * a.stage_ranks);
+#pragma unroll
+          for (int q = 0; q < kMaxTopK; ++q)
+            if (q < a.k) sum[c] = fmaf(r.w[t * a.k + q], part[q], sum[c]);
+        }
     }
-    float v = part[0];
+    float v = sum[0];
 #pragma unroll
     for (int q = 1; q < 8; ++q)
-      if (q < C) v += part[q];
+      if (q < a.stage_ranks) v += sum[q];
     v *= 1.f / kUnit<kBf16>;
     const size_t dst = static_cast<size_t>(t) * a.d + col;
     if (a.residual) v += from16<kType>(static_cast<const uint16_t*>(a.residual)[dst]);
@@ -830,7 +860,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
 constexpr int kSmemLimit = 226 * 1024;  // of a CTA, static and dynamic
 constexpr int kUpStatic = sizeof(Routing) + kUpWarps * kRedWarp * 4 + 64;
 constexpr int kDownStatic = sizeof(Routing) + 64;
-static_assert(kScratchBytes <= 4 * 2 * 2 * 1088, "the smallest rings hold what the choice of one token takes");
+static_assert(kScratchBytes <= 2 * 2 * 1088, "the smallest rings hold what the choice of one token takes");
 int g_clusters[9];  // clusters of so many CTAs of the down kernel that run at a time
 
 using Kernel = void (*)(Args);
@@ -928,6 +958,15 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.cluster = std::min(down_stages(s), 8);
   a.strips = 2;
   while (a.strips < 2 * kDownMaxPairs && (strips + a.strips - 1) / a.strips > g_clusters[a.cluster]) a.strips += 2;
+  // Where few strips and stages leave SMs without work, more CTAs share the items, as long as each of their warps has
+  // one (8 tokens of top-3 lose 1.3 us to a larger cluster). Which experts meet is not known here; their number is
+  // about that of evenly chosen ones.
+  const double items = s.E * (1.0 - std::pow(1.0 - double(s.k) / s.E, s.T));
+  a.stage_ranks = a.cluster;
+  a.parts = 1;
+  for (int p = 2; a.strips == 2 && p <= 8 / a.stage_ranks && items >= kDownWarps * p; ++p)
+    if ((strips + 1) / 2 <= g_clusters[a.stage_ranks * p]) a.parts = p;
+  a.cluster = a.stage_ranks * a.parts;
   const int slot = 2 * (1024 + 64 * (kStageCols / s.g2)), fixed = pairs * (kPairBytes + kStageCols / s.g2 * 4);
   const auto room = [&](int limit, int warps) {  // pieces of a warp that fit
     return (limit - kDownStatic - fixed - a.strips / 2 * pairs * kRowWords * 4) / (a.strips / 2 * warps * slot);
@@ -940,13 +979,12 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   const int least_warps = kDownWarps / kDownMaxPairs, limit = a.listed ? kSmemLimit : beside;
   while (a.listed && a.strips > 2 && room(kSmemLimit, least_warps) < 2) a.strips -= 2;
   // as many warps as there are items for
-  a.down_warps = std::max(std::min((a.listed ? kDownWarps : kDownBeside) / (a.strips / 2), pairs), 1);
+  a.down_warps = std::max(std::min((a.listed ? kDownWarps : kDownBeside) / (a.strips / 2), (pairs + a.parts - 1) / a.parts), 1);
   while (a.down_warps > 1 && room(limit, a.down_warps) < 2) --a.down_warps;
   const int down_depth = std::min(room(limit, a.down_warps), kMaxDepth);
   // gate_up: the group size and the pairs of strips per unit that take the least time, counted in pieces of one
   // pair: two pairs at once take 1.6, a unit's barriers and epilogue 1 of a small group and 0.5 of a
-  // large one. (Which experts meet is not known here; their number is about that of evenly chosen ones.)
-  const double items = s.E * (1.0 - std::pow(1.0 - double(s.k) / s.E, s.T));
+  // large one.
   const auto cost = [&](int w, int p) { return (stages + w - 1) / w * (p == 2 ? 1.6 : 1.0) + (w == 4 ? 1.0 : 0.5); };
   double least = 1e30;
   int per_warp = 1;
