@@ -500,7 +500,8 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
     const bool wide = large;  // one group of 16, else four of 4
     const int W = wide ? kUpWarps : kUpWarps / 4, my_stage = warp & (W - 1), team = wide ? 0 : warp >> 2;
     const int round = (wide ? kRoundStrips : kRoundStrips / 2) / kStrips;
-    const int unit0 = blockIdx.x + (wide ? narrow : team * static_cast<int>(gridDim.x)), units = wide ? all_units : narrow;
+    const int unit0 = blockIdx.x + (wide ? narrow : team * static_cast<int>(gridDim.x));
+    const int units = wide ? all_units : narrow;
     const auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(wide ? 0 : 1 + team), "r"(W * 32) : "memory"); };
 
     // the piece to request next: unit pu, which is unit pg of item pi
@@ -603,8 +604,8 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
         break;
       }
       team_sync();
-      // A warp takes a strip of a unit of the round, a lane a column of h for a token: the sums of the warps with stages
-      // q, q + 4, .. one after the other, then over q in a tree.
+      // A warp takes a strip of a unit of the round, a lane a column of h for a token: the sums of the warps with
+      // stages q, q + 4, .. one after the other, then over q in a tree.
       const int local = warp & (W - 1), mine = local / kStrips, h = local & (kStrips - 1);
       if (mine < in_round) {
         Place p = round_place;
@@ -953,16 +954,30 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.k = s.k;
   a.act = s.act;
   a.affine = s.fmt == 1;
-  // The down launch: the fewest strips per CTA for which all clusters run at a time.
-  const int strips = s.d / 16;
-  a.cluster = std::min(down_stages(s), 8);
-  a.strips = 2;
-  while (a.strips < 2 * kDownMaxPairs && (strips + a.strips - 1) / a.strips > g_clusters[a.cluster]) a.strips += 2;
+  // The down launch: CTAs for the stages and strips of each so that it takes least, counted in stages of two strips,
+  // with 1.5 for h and 1 for the start of a wave of clusters. (10 tokens of 2048 x 1408: 79 us with a CTA per stage, of
+  // which one cluster had to wait for the others, now 51.5.) The number of tokens has no part in it, so a sum's
+  // order does not depend on it.
+  const int strips = s.d / 16, down_count = down_stages(s);
+  int rounds = 1;
+  double least = 1e30;
+  for (int c = 1; c <= std::min(down_count, 8); ++c) {
+    const int at_a_time = std::max(g_clusters[c], 1), r = (down_count + c - 1) / c;
+    int n = 2;
+    while (n < 2 * kDownMaxPairs && (strips + n - 1) / n > at_a_time) n += 2;
+    const int tiles = (strips + n - 1) / n;
+    const double time = (tiles + at_a_time - 1) / at_a_time * (r * (n / 2 + 1.5) + 1);
+    if (time < least) {
+      least = time;
+      a.stage_ranks = c;
+      a.strips = n;
+      rounds = r;
+    }
+  }
   // Where few strips and stages leave SMs without work, more CTAs share the items, as long as each of their warps has
   // one (8 tokens of top-3 lose 1.3 us to a larger cluster). Which experts meet is not known here; their number is
   // about that of evenly chosen ones.
   const double items = s.E * (1.0 - std::pow(1.0 - double(s.k) / s.E, s.T));
-  a.stage_ranks = a.cluster;
   a.parts = 1;
   for (int p = 2; a.strips == 2 && p <= 8 / a.stage_ranks && items >= kDownWarps * p; ++p)
     if ((strips + 1) / 2 <= g_clusters[a.stage_ranks * p]) a.parts = p;
@@ -971,22 +986,24 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   const auto room = [&](int limit, int warps) {  // pieces of a warp that fit
     return (limit - kDownStatic - fixed - a.strips / 2 * pairs * kRowWords * 4) / (a.strips / 2 * warps * slot);
   };
-  // With one or two tokens it fits beside the gate_up launch, and its start is hidden; otherwise it gets the
-  // lists from the gate_up launch.
+  // With few items it runs beside the gate_up launch, which hides its start; where it does not fit there, or its fewer
+  // warps would have more than three pieces each, it gets the lists from the gate_up launch (2 tokens of top-8,
+  // 768 x 1856: 33.0 us beside it, 24.4 after it).
   const int stages = s.d / kStageCols, piece = kUpWarps * 2 * (1024 + 64 * (kStageCols / s.g1));
   const int beside = kSmemLimit - kUpStatic - 3 * piece;
-  a.listed = room(beside, 4) < 2;
+  a.listed = room(beside, 4) < 2 || items * rounds > 3 * (kDownBeside / (a.strips / 2));
   const int least_warps = kDownWarps / kDownMaxPairs, limit = a.listed ? kSmemLimit : beside;
   while (a.listed && a.strips > 2 && room(kSmemLimit, least_warps) < 2) a.strips -= 2;
   // as many warps as there are items for
-  a.down_warps = std::max(std::min((a.listed ? kDownWarps : kDownBeside) / (a.strips / 2), (pairs + a.parts - 1) / a.parts), 1);
+  const int most = (a.listed ? kDownWarps : kDownBeside) / (a.strips / 2);
+  a.down_warps = std::max(std::min(most, (pairs + a.parts - 1) / a.parts), 1);
   while (a.down_warps > 1 && room(limit, a.down_warps) < 2) --a.down_warps;
   const int down_depth = std::min(room(limit, a.down_warps), kMaxDepth);
   // gate_up: the group size and the pairs of strips per unit that take the least time, counted in pieces of one
   // pair: two pairs at once take 1.6, a unit's barriers and epilogue 1 of a small group and 0.5 of a
   // large one.
   const auto cost = [&](int w, int p) { return (stages + w - 1) / w * (p == 2 ? 1.6 : 1.0) + (w == 4 ? 1.0 : 0.5); };
-  double least = 1e30;
+  least = 1e30;
   int per_warp = 1;
   a.stage_warps = kUpWarps;
   for (int w : {kUpWarps, 4})
