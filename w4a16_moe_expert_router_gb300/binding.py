@@ -561,17 +561,19 @@ def moe_w4a16_norm_backward(cfg: Norm, y, gamma_post, gate, out, gamma_pre, grad
                             grad_gamma_post, grad_gate, grad_gamma_pre, workspace, stream=None) -> None:
     types, _, f32, device, current = _CONTEXT or _context()
     dev, dt, d = device(), types.get(cfg.type), cfg.hidden
-    n, g = cfg.rows * d, _gate_elements(cfg)
-
-    def rows(t):
-        return t if t is None else _tptr(t, dt, n, dev)
-
-    def vec(t, count=d):
-        return t if t is None else _tptr(t, f32, count, dev)
-
+    n = cfg.rows * d
+    g = 0 if gate is None and grad_gate is None else _gate_elements(cfg)
     st = lib().moe_w4a16_norm_backward(
-        ctypes.byref(cfg), rows(y), vec(gamma_post), vec(gate, g), rows(out), vec(gamma_pre), rows(grad_out),
-        rows(grad_u), rows(grad_x), rows(grad_y), vec(grad_gamma_post), vec(grad_gate, g), vec(grad_gamma_pre),
+        ctypes.byref(cfg), y if y is None else _tptr(y, dt, n, dev),
+        gamma_post if gamma_post is None else _tptr(gamma_post, f32, d, dev),
+        gate if gate is None else _tptr(gate, f32, g, dev), out if out is None else _tptr(out, dt, n, dev),
+        gamma_pre if gamma_pre is None else _tptr(gamma_pre, f32, d, dev),
+        grad_out if grad_out is None else _tptr(grad_out, dt, n, dev),
+        grad_u if grad_u is None else _tptr(grad_u, dt, n, dev), grad_x if grad_x is None else _tptr(grad_x, dt, n, dev),
+        grad_y if grad_y is None else _tptr(grad_y, dt, n, dev),
+        grad_gamma_post if grad_gamma_post is None else _tptr(grad_gamma_post, f32, d, dev),
+        grad_gate if grad_gate is None else _tptr(grad_gate, f32, g, dev),
+        grad_gamma_pre if grad_gamma_pre is None else _tptr(grad_gamma_pre, f32, d, dev),
         workspace if workspace is None else _wptr(workspace, dev), 0 if workspace is None else _nbytes(workspace),
         current(dev) if stream is None else _stream(stream))
     if st:

@@ -698,9 +698,9 @@ cudaError_t launch(K kernel, std::atomic<uint64_t>& room, const GroupShape& g, s
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (!(room.load(std::memory_order_relaxed) & bit)) {
+  if (!(room.load(std::memory_order_acquire) & bit)) {
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
-    room.fetch_or(bit, std::memory_order_relaxed);
+    room.fetch_or(bit, std::memory_order_release);
   }
   return launch_pdl(kernel, dim3(g.ctas), dim3(g.group * g.groups), smem, st, a);
 }
@@ -807,11 +807,15 @@ cudaError_t launch_norm(const NormDims& s, const void* x, const void* y, const f
 // Workspace: sums P (or of gamma_post) by CTA | of gamma_pre by CTA | gate slots by unit; of the call that has most.
 size_t norm_backward_ws_bytes(const NormDims& s) {
   size_t most = 0;
-  for (bool next : {false, true})
-    for (int gates : {kOneGate, kSeveralGates, kGateByRow, kNoY}) {
-      const GroupShape g = grad_shape(s, next, gates);
-      most = std::max(most, (size_t(g.ctas) + g.units.count) * 2 * s.d * 4);
-    }
+  const auto take = [&](bool next, int gates) {
+    const GroupShape g = grad_shape(s, next, gates);
+    most = std::max(most, (size_t(g.ctas) + g.units.count) * 2 * s.d * 4);
+  };
+  take(false, kOneGate);
+  take(true, kOneGate);
+  take(true, kNoY);
+  if (s.gate_rows < s.R)
+    for (bool next : {false, true}) take(next, s.gate_rows > 1 ? kSeveralGates : kGateByRow);
   return most;
 }
 
