@@ -12,7 +12,7 @@
 //    beside the other's; it gets the lists then);
 //  - the contraction is shared by the warps of a CTA (gate_up) or by the CTAs of a cluster (down);
 //    each warp streams its own stages with cp.async, some ahead, also across work items.
-// Measured in a replayed graph: 1 token 13.3 us (1.5 TB/s), 4 tokens of bf16 34.7 (2.0), 16 tokens 59.5 (3.4).
+// Measured in a replayed graph: 1 token 13.3 us (1.5 TB/s), 4 tokens of bf16 34.6 (2.0), 16 tokens 58.2 (3.5).
 // One token is bound by the chain routing 2.0 us, first weights 2.3, products 2, the way to the down
 // launch 0.9, its h, products and sums 3.5; sixteen by the issue of instructions (some 180 to take a
 // 16 x 128 strip of codes through, a third of them masks and shifts of the codes) and by the parts
@@ -73,7 +73,7 @@ struct Args {
   int strips, cluster;    // down: strips of a CTA, CTAs that share the contraction and the items
   int stage_ranks, parts; // of them: for the stages, and for each the items
   int down_warps;         // down: warps per pair of strips, which take the items in turn
-  int depth;              // pieces of a warp in its ring
+  int depth;              // down: pieces of a warp in its ring
 };
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -389,26 +389,36 @@ __device__ __forceinline__ void wait_piece(int depth) {
     cp_async_wait<1>();
 }
 
-// A stage of KK steps of one strip: b holds the other operand's fragments.
+// A stage of KK steps of two strips (`pitch` bytes apart): b holds the other operand's fragments. The chains of
+// products of both strips' groups take turns (one strip after the other: 16 tokens 60.0 us, now 58.2).
 template <bool kBf16, int G, int KK>
-__device__ __forceinline__ void strip_stage(float (&tot)[4], uint32_t at, const uint32_t (&b)[KK][2],
-                                            const float (&sum)[KK * 16 / G][2], int lane, int affine) {
+__device__ __forceinline__ void strips_stage(float (&tot)[2][4], uint32_t at, uint32_t pitch,
+                                             const uint32_t (&b)[KK][2], const float (&sum)[KK * 16 / G][2], int lane,
+                                             int affine) {
   constexpr int NG = KK * 16 / G, kSteps = KK / NG;
-  uint4 word[KK / 4];
+  uint4 word[2][KK / 4];
 #pragma unroll
-  for (int v = 0; v < KK / 4; ++v) word[v] = lds128(at + 64 * NG + v * 512 + lane * 16);
+  for (int v = 0; v < KK / 4; ++v)
 #pragma unroll
-  for (int j = 0; j < NG; ++j) {
-    float part[4] = {};
+    for (int h = 0; h < 2; ++h) word[h][v] = lds128(at + h * pitch + 64 * NG + v * 512 + lane * 16);
+  float part[2][NG][4] = {};
 #pragma unroll
-    for (int q = 0; q < kSteps; ++q) {
-      const int kk = j * kSteps + q;
-      uint32_t af[4];
-      codes<kBf16>(word_of(word[kk / 4], kk % 4), af);
-      mma<kBf16>(part, af, b[kk][0], b[kk][1]);
-    }
-    apply_group<kBf16>(tot, part, sum[j][0], sum[j][1], lds64(at + (lane >> 2) * (8 * NG) + j * 8), affine);
-  }
+  for (int q = 0; q < kSteps; ++q)
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int kk = j * kSteps + q;
+        uint32_t af[4];
+        codes<kBf16>(word_of(word[h][kk / 4], kk % 4), af);
+        mma<kBf16>(part[h][j], af, b[kk][0], b[kk][1]);
+      }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+      apply_group<kBf16>(tot[h], part[h][j], sum[j][0], sum[j][1],
+                         lds64(at + h * pitch + (lane >> 2) * (8 * NG) + j * 8), affine);
 }
 
 // The byte of column c (0..127 of a stage) of a pair's h, `part` 0 hi and 1 lo: [part][chunk of 64][tq][half][step of
@@ -433,7 +443,9 @@ constexpr int kRoundStrips = 8;  // strips of a warp in a round of a group of 16
 // words of a warp's sums: [strip][value][token / 2][row], shifted by eight banks from warp to warp
 constexpr int kRedWarp = kRoundStrips * 4 * 16 + 8;
 
-// Fragments of x of a stage, and its sums over the groups: a product with ones (in the units of the codes).
+// Fragments of x of a stage, and its sums over the groups: a product with ones (in the units of the codes). With
+// one pair of strips all columns are loaded (the ragged layer 17.5 -> 17.0 us), with two the ones behind an item's
+// tokens are zeros (16 tokens 62.6 -> 60.0: their rows' lines cost more than the selection).
 __device__ __forceinline__ void load_x(const uint32_t* row, bool on, uint32_t (&b)[8][2]) {
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
@@ -453,11 +465,15 @@ __device__ __forceinline__ void sum_x(const uint32_t (&b)[8][2], float (&sum)[NG
   }
 }
 
+// Pieces of a warp in its ring: what an SM's shared memory holds.
+template <int kPairs>
+constexpr int kUpDepth = kPairs == 1 ? 3 : 2;
+
 // kBeside: with half of an SM's registers, so that a CTA of the down launch fits beside it.
 template <bool kBf16, int G, int kPairs, bool kBeside>
 __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kernel(const Args a) {
   constexpr int NG = kStageCols / G, kStripBytes = 1024 + 64 * NG, kStrips = 2 * kPairs, kSlot = kStrips * kStripBytes;
-  constexpr int kType = kBf16 ? 1 : 0;
+  constexpr int kType = kBf16 ? 1 : 0, kDepth = kUpDepth<kPairs>;
   extern __shared__ __align__(16) uint8_t smem[];  // rings
   __shared__ Routing r;
   __shared__ float red[kUpWarps * kRedWarp];
@@ -469,17 +485,17 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
   grid_dependents_launch();  // only now: the down launch reads logits and weights before it waits
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = a.K / kStageCols;
-  const uint32_t ring = smem_addr(smem) + warp * a.depth * kSlot;
+  const uint32_t ring = smem_addr(smem) + warp * kDepth * kSlot;
   const auto* const x = static_cast<const uint32_t*>(a.x) + (lane & 3);
   uint32_t b[8][2], next[8][2];  // fragments of x, loaded a piece ahead where registers allow
   float sum[NG][2];
   const bool fixed = a.T == 1 && S <= a.stage_warps;  // a warp has one stage, in groups of both sizes
   if (fixed && (warp & (a.stage_warps - 1)) < S) {
-    load_x(x + (warp & (a.stage_warps - 1)) * 64, lane < 4, b);
+    load_x(x + (warp & (a.stage_warps - 1)) * 64, true, b);
     sum_x<kBf16, NG>(b, sum);
   }
   const auto load = [&](int i, int stage, uint32_t (&f)[8][2]) {  // columns behind the item's tokens are not used
-    load_x(x + static_cast<size_t>(r.token[i][(lane >> 2) & 3]) * (a.d / 2) + stage * 64, (lane >> 2) < r.count[i], f);
+    load_x(x + r.token[i][(lane >> 2) & 3] * (a.d / 2) + stage * 64, kPairs == 1 || (lane >> 2) < r.count[i], f);
   };
   form_routing(r, a, smem);
   const int pairs = a.T * a.k, all_units = r.items * a.per_item;
@@ -520,7 +536,7 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
         ++p.item;
       }
     };
-    int ps = my_stage, s = my_stage, ahead = a.depth - 1, in_round = 0;
+    int ps = my_stage, s = my_stage, ahead = kDepth - 1, in_round = 0;
     bool first_x = true;
     Place round_place = got;
 #pragma unroll 1
@@ -535,7 +551,7 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
           ps = my_stage;
           step(put);
         }
-        if (++pslot == a.depth) pslot = 0;
+        if (++pslot == kDepth) pslot = 0;
       }
       cp_async_commit();
       if (ahead > 0) {
@@ -570,18 +586,18 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
             }
             sum_x<kBf16, NG>(b, sum);
           }
-          wait_piece(a.depth);
+          cp_async_wait<kDepth - 1>();
           __syncwarp();
           const uint32_t at = ring + slot * kSlot;
 #pragma unroll
-          for (int h = 0; h < kStrips; ++h) {
-            float t[4] = {};
-            strip_stage<kBf16, G, 8>(t, at + h * kStripBytes, b, sum, lane, a.affine);
+          for (int h = 0; h < kStrips; h += 2) {
+            float t[2][4] = {};
+            strips_stage<kBf16, G, 8>(t, at + h * kStripBytes, kStripBytes, b, sum, lane, a.affine);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tot[h][i] += t[i];
+            for (int i = 0; i < 8; ++i) tot[h + i / 4][i % 4] += t[i / 4][i % 4];
           }
           __syncwarp();  // the slot is read before it is requested again
-          if (++slot == a.depth) slot = 0;
+          if (++slot == kDepth) slot = 0;
           s += W;
           if (s < S) continue;
         }
@@ -769,24 +785,24 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
       const uint32_t at = ring + slot * kSlot;
       const bool on = (lane & 3) < r.count[item];
       float* const dst = rows + p * kRowWords;
+      // columns 2 n and 2 n + 1 are token n's hi and lo: their sum counts, and the sum of h once
+      float t[2][4] = {};
+      if (whole) {
+        strips_stage<kBf16, G, 8>(t, at, kStrip, b, sum, lane, a.affine);
+      } else if constexpr (G <= 64) {
+        const uint32_t half[4][2] = {{b[0][0], b[0][1]}, {b[1][0], b[1][1]}, {b[2][0], b[2][1]}, {b[3][0], b[3][1]}};
+        float part[64 / G][2];
+#pragma unroll
+        for (int j = 0; j < 64 / G; ++j) {
+          part[j][0] = sum[j][0];
+          part[j][1] = 0.f;
+        }
+        strips_stage<kBf16, G, 4>(t, at, kHalfStrip, half, part, lane, a.affine);
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        // columns 2 n and 2 n + 1 are token n's hi and lo: their sum counts, and the sum of h once
-        float t[4] = {};
-        if (whole) {
-          strip_stage<kBf16, G, 8>(t, at + h * kStrip, b, sum, lane, a.affine);
-        } else if constexpr (G <= 64) {
-          const uint32_t half[4][2] = {{b[0][0], b[0][1]}, {b[1][0], b[1][1]}, {b[2][0], b[2][1]}, {b[3][0], b[3][1]}};
-          float part[64 / G][2];
-#pragma unroll
-          for (int j = 0; j < 64 / G; ++j) {
-            part[j][0] = sum[j][0];
-            part[j][1] = 0.f;
-          }
-          strip_stage<kBf16, G, 4>(t, at + h * kHalfStrip, half, part, lane, a.affine);
-        }
         if (on) {  // (stages of the CTA after its first are added to it)
-          const float lo = t[0] + t[1], hi = t[2] + t[3];
+          const float lo = t[h][0] + t[h][1], hi = t[h][2] + t[h][3];
           dst[16 * h] = s == stage_rank ? lo : dst[16 * h] + lo;
           dst[16 * h + 8] = s == stage_rank ? hi : dst[16 * h + 8] + hi;
         }
@@ -861,6 +877,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, 1) few_down_kernel(const Args
 constexpr int kSmemLimit = 226 * 1024;  // of a CTA, static and dynamic
 constexpr int kUpStatic = sizeof(Routing) + kUpWarps * kRedWarp * 4 + 64;
 constexpr int kDownStatic = sizeof(Routing) + 64;
+static_assert(kUpDepth<2> * 2 * kUpWarps * 2 * (1024 + 64 * 4) <= kSmemLimit - kUpStatic, "groups of 32");
 static_assert(kScratchBytes <= 2 * 2 * 1088, "the smallest rings hold what the choice of one token takes");
 int g_clusters[9];  // clusters of so many CTAs of the down kernel that run at a time
 
@@ -1032,9 +1049,8 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   a.turn_inv = 1.f / (4 * grid);
   // (0.5: the gap between the two)
   a.tail = stages <= kUpWarps ? int((cost(4, per_warp) - 0.5) / cost(kUpWarps, per_warp)) : 0;
-  a.depth = a.listed ? std::min((kSmemLimit - kUpStatic) / (per_warp * piece), 3) : 3;
   cudaError_t err = launch_pdl(gate_up_of(type, s.g1, per_warp, !a.listed), dim3(grid), dim3(kUpThreads),
-                               size_t(a.depth) * per_warp * piece, st, a);
+                               size_t(per_warp == 1 ? kUpDepth<1> : 2 * kUpDepth<2>) * piece, st, a);
   if (err != cudaSuccess) return err;
   a.w = w_down;
   a.K = s.f;
