@@ -294,3 +294,13 @@ def test_many_experts_of_a_small_layer(B, d, f, E, k, fmt, typ):
     layer.check(whole)
     for tokens in (slice(0, 1), slice(3, 5), slice(7, 11), slice(0, 16), slice(1, 23)):
         assert all(torch.equal(a[tokens], b) for a, b in zip(whole, layer.run(tokens)))
+
+
+@pytest.mark.parametrize("case", [(1, 8192, 8192, 2, 2, 128, 128, 0, 0, 0), (32, 128, 8192, 3, 2, 64, 32, 1, 0, 1),
+                                  (32, 8192, 1024, 4, 4, 32, 32, 2, 0, 1), (3, 4096, 4096, 6, 2, 64, 64, 0, 1, 0),
+                                  (32, 8192, 64, 9, 8, 32, 32, 0, 0, 0)], ids=lambda c: "-".join(map(str, c)))
+def test_few_tokens_of_large_layers(B, case):
+    layer = Layer(B, *case, seed=sum(case))
+    whole = layer.run()
+    layer.check(whole)
+    assert all(torch.equal(a[:1], b) for a, b in zip(whole, layer.run(slice(0, 1))))
