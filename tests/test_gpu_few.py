@@ -304,3 +304,13 @@ def test_few_tokens_of_large_layers(B, case):
     whole = layer.run()
     layer.check(whole)
     assert all(torch.equal(a[:1], b) for a, b in zip(whole, layer.run(slice(0, 1))))
+
+
+@pytest.mark.parametrize("typ", [0, 1], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_tokens_of_one_sign(B, typ, fmt):
+    """The sums of the tokens are as large as they get, and the zero-points take most of the products back."""
+    for T, d, f, g in ((2, 2048, 704, 64), (8, 512, 256, 128), (5, 4096, 128, 32)):
+        layer = Layer(B, T, d, f, 16, 4, g, min(g, 64), fmt, 0, typ, seed=T)
+        layer.x = layer.x.abs() + 1
+        layer.check(layer.run())

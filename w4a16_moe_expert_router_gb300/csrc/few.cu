@@ -12,7 +12,7 @@
 //    beside the other's; it gets the lists then);
 //  - the contraction is shared by the warps of a CTA (gate_up) or by the CTAs of a cluster (down);
 //    each warp streams its own stages with cp.async, some ahead, also across work items.
-// Measured in a replayed graph: 1 token 13.3 us (1.5 TB/s), 4 tokens of bf16 34.6 (2.0), 16 tokens 58.2 (3.5).
+// Measured in a replayed graph: 1 token 13.3 us (1.5 TB/s), 4 tokens of bf16 33.0 (2.1), 16 tokens 58.2 (3.5).
 // One token is bound by the chain routing 2.0 us, first weights 2.3, products 2, the way to the down
 // launch 0.9, its h, products and sums 3.5; sixteen by the issue of instructions (some 180 to take a
 // 16 x 128 strip of codes through, a third of them masks and shifts of the codes) and by the parts
@@ -307,7 +307,12 @@ __device__ __forceinline__ void form_routing(Routing& r, const Args& a, uint8_t*
 
 // One word of codes -> an m16n8k16 A fragment of codes. fp16: masks alone, the codes as
 // subnormals (2^-24 for rows g, 2^-20 for rows g + 8, whose nibbles sit four bits higher). bf16, whose
-// subnormals would fall out of fp32's range: 128 + q from exponent bits, less 128 (exact).
+// subnormals would fall out of fp32's range: kBias + q, with the bias taken off the group's sum. (The partial sums
+// are up to 17 times as large, and so are their fp32 roundings: some 2^-19 of a group's products, where the
+// tokens themselves have 2^-9. A subtraction per pair of codes was a sixth of all instructions: 4 tokens 34.5 us,
+// now 33.0.)
+template <bool kBf16>
+constexpr float kBias = kBf16 ? 128.f : 0.f;
 template <bool kBf16>
 __device__ __forceinline__ void codes(uint32_t w, uint32_t (&a)[4]) {
   if constexpr (!kBf16) {
@@ -317,14 +322,8 @@ __device__ __forceinline__ void codes(uint32_t w, uint32_t (&a)[4]) {
     a[2] = w8 & 0x000f000fu;
     a[3] = w8 & 0x00f000f0u;
   } else {
-    const uint32_t k128 = 0x43004300u;
-    const __nv_bfloat162 minus = *reinterpret_cast<const __nv_bfloat162*>(&k128);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = and_or(w >> (4 * i), 0x000f000fu, k128);
-      const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), minus);
-      a[i] = *reinterpret_cast<const uint32_t*>(&q);
-    }
+    for (int i = 0; i < 4; ++i) a[i] = and_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
   }
 }
 template <bool kBf16>
@@ -340,13 +339,17 @@ constexpr float kUnit = kBf16 ? 1.f : 0x1p-24f;
 template <bool kBf16>
 constexpr uint32_t kOne = kBf16 ? 0x3f803f80u : 0x00010001u;  // two of them
 
-// A group's sums into the totals: tot += s part + c sum, for rows g (first two) and g + 8.
+// A group's sums into the totals: tot += s part + (c - bias s) sum, for rows g (first two) and g + 8.
 template <bool kBf16>
 __device__ __forceinline__ void apply_group(float (&tot)[4], const float (&part)[4], float sum0, float sum1, uint2 sz,
                                             int affine) {
   const float2 lo = __half22float2(bits_h2(sz.x)), hi = __half22float2(bits_h2(sz.y));
   const float s_hi = kBf16 ? hi.x : hi.x * 0.0625f;
-  const float c_lo = affine ? lo.y : -lo.x * lo.y, c_hi = affine ? hi.y : -hi.x * hi.y;
+  float c_lo = affine ? lo.y : -lo.x * lo.y, c_hi = affine ? hi.y : -hi.x * hi.y;
+  if (kBf16) {
+    c_lo = fmaf(-kBias<kBf16>, lo.x, c_lo);
+    c_hi = fmaf(-kBias<kBf16>, hi.x, c_hi);
+  }
   tot[0] = fmaf(lo.x, part[0], fmaf(c_lo, sum0, tot[0]));
   tot[1] = fmaf(lo.x, part[1], fmaf(c_lo, sum1, tot[1]));
   tot[2] = fmaf(s_hi, part[2], fmaf(c_hi, sum0, tot[2]));
