@@ -7,12 +7,12 @@
 // for one or two of them: the time is the way of the chosen experts' weights from memory (19 MB for
 // one token of top-8, d 2048, f 704: 2.9 us), and, for one token, what is not hidden behind it. So
 //  - every CTA forms the routing itself, instead of a launch for it;
-//  - with one or two tokens the down launch starts while the gate_up launch runs, forms the routing too
-//    and requests its first weights before it waits for h (for more its shared memory does not fit
-//    beside the other's; it gets the lists then);
+//  - with few items (an expert and at most four of its tokens) the down launch starts while the gate_up launch
+//    runs, forms the routing too and requests its first weights before it waits for h (with more its shared
+//    memory does not fit beside the other's, or its warps there are too few; it gets the lists then);
 //  - the contraction is shared by the warps of a CTA (gate_up) or by the CTAs of a cluster (down);
 //    each warp streams its own stages with cp.async, some ahead, also across work items.
-// Measured in a replayed graph: 1 token 13.3 us (1.5 TB/s), 4 tokens of bf16 33.0 (2.1), 16 tokens 58.2 (3.5).
+// Measured in a replayed graph: 1 token 13.3 us (1.5 TB/s), 4 tokens of bf16 33.0 (2.1), 16 tokens 58.1 (3.5).
 // One token is bound by the chain routing 2.0 us, first weights 2.3, products 2, the way to the down
 // launch 0.9, its h, products and sums 3.5; sixteen by the issue of instructions (some 180 to take a
 // 16 x 128 strip of codes through, a third of them masks and shifts of the codes) and by the parts
