@@ -187,7 +187,9 @@ __device__ __forceinline__ bool choose_by_rank(Routing& r, const Args& a, uint32
   }
   __syncthreads();
   const int lane = tid & 31;
-  return !__any_sync(0xffffffffu, lane < a.k && r.sel[lane] < 0);  // the same in every warp
+  const bool open = __any_sync(0xffffffffu, lane < a.k && r.sel[lane] < 0);
+  if (open) __syncthreads();  // all warps have found it open before one of them makes the choice anew
+  return !open;               // the same in every warp
 }
 
 // Lists the items (in any order that the choices alone decide); a pair's w is its value (weigh() follows).
