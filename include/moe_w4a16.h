@@ -493,7 +493,7 @@ typedef struct {
 } moe_w4a16_norm_cfg;
 
 /* Forward.  The norm before a block alone takes x and gives u; the one after it takes y
- * (and x) and gives out; both together give out and u.
+ * (and x) and gives out; both together give out and u.  x alone with out alone is residual_scale x.
  *   x, y        type [R][d], each NULL where it does not take part (one at least does)
  *   gamma_post  fp32 [d] or NULL     gate  fp32 [ceil(R / gate_rows)][d] or NULL     (both NULL without y)
  *   gamma_pre   fp32 [d], given exactly where u is wanted

@@ -724,8 +724,10 @@ cudaError_t forward(Args a, cudaStream_t st) {
   g = group_shape(a.R, a.nvec, kPieces, kNormSms * fitting(registers, threads, smem));
   a.group = g.group;
   a.units = g.units;
-  static std::atomic<uint64_t> room[5];
-  if (!a.y) return launch(norm_kernel<kType, kPieces, kDepth, false, true, false>, room[0], g, smem, st, a);
+  static std::atomic<uint64_t> room[6];
+  if (!a.y)
+    return a.u ? launch(norm_kernel<kType, kPieces, kDepth, false, true, false>, room[0], g, smem, st, a)
+               : launch(norm_kernel<kType, kPieces, kDepth, false, false, false>, room[5], g, smem, st, a);
   if (by_row)
     return a.u ? launch(norm_kernel<kType, kPieces, kDepth, true, true, true>, room[1], g, smem, st, a)
                : launch(norm_kernel<kType, kPieces, kDepth, true, false, true>, room[2], g, smem, st, a);
