@@ -307,25 +307,27 @@ __device__ __forceinline__ void form_routing(Routing& r, const Args& a, uint8_t*
   __syncthreads();
 }
 
-// One word of codes -> an m16n8k16 A fragment of codes. fp16: masks alone, the codes as
-// subnormals (2^-24 for rows g, 2^-20 for rows g + 8, whose nibbles sit four bits higher). bf16, whose
-// subnormals would fall out of fp32's range: kBias + q, with the bias taken off the group's sum. (The partial sums
-// are up to 17 times as large, and so are their fp32 roundings: some 2^-19 of a group's products, where the
-// tokens themselves have 2^-9. A subtraction per pair of codes was a sixth of all instructions: 4 tokens 34.5 us,
-// now 33.0.)
+// One word of codes -> an m16n8k16 A fragment of codes. A sum in the matrix pipe keeps some 24 bits below its largest
+// product's exponent, which counts a subnormal's leading zeros too; what a bias takes up is lost as well. So the codes sit
+// as high as their shifts allow. fp16: as subnormals, by two shifts and masks (2^-22 for rows g, 2^-18 for rows g + 8, whose
+// nibbles sit four bits higher); a group's sum is off by 2^-23 of it, without the two bits by 2^-20 (one shift; 16 tokens
+// 60.7 us, now 62.6). bf16, whose subnormals would fall out of fp32's range: kBias + q, the code at the mantissa's top, with
+// the bias taken off the group's sum, off by 2^-23 of it; with 128 + q, at its bottom, by up to 2^-19 (a shift in four
+// less; 4 tokens 31.4 us, now 31.9). A subtraction per pair of codes was a sixth of all instructions.
 template <bool kBf16>
-constexpr float kBias = kBf16 ? 128.f : 0.f;
+constexpr float kBias = kBf16 ? 16.f : 0.f;
 template <bool kBf16>
 __device__ __forceinline__ void codes(uint32_t w, uint32_t (&a)[4]) {
   if constexpr (!kBf16) {
-    const uint32_t w8 = w >> 8;
-    a[0] = w & 0x000f000fu;
-    a[1] = w & 0x00f000f0u;
-    a[2] = w8 & 0x000f000fu;
-    a[3] = w8 & 0x00f000f0u;
+    const uint32_t low = w << 2, high = w >> 6;
+    a[0] = low & 0x003c003cu;
+    a[1] = low & 0x03c003c0u;
+    a[2] = high & 0x003c003cu;
+    a[3] = high & 0x03c003c0u;
   } else {
+    a[0] = and_or(w << 3, 0x00780078u, 0x41804180u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = and_or(w >> (4 * i), 0x000f000fu, 0x43004300u);
+    for (int i = 1; i < 4; ++i) a[i] = and_or(w >> (4 * i - 3), 0x00780078u, 0x41804180u);
   }
 }
 template <bool kBf16>
@@ -337,9 +339,9 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 }
 // Totals and the sums of x and h are kept in the units of rows g's partial sums.
 template <bool kBf16>
-constexpr float kUnit = kBf16 ? 1.f : 0x1p-24f;
+constexpr float kUnit = kBf16 ? 1.f : 0x1p-22f;
 template <bool kBf16>
-constexpr uint32_t kOne = kBf16 ? 0x3f803f80u : 0x00010001u;  // two of them
+constexpr uint32_t kOne = kBf16 ? 0x3f803f80u : 0x3c003c00u;  // two of them
 
 // A group's sums into the totals: tot += s part + (c - bias s) sum, for rows g (first two) and g + 8.
 template <bool kBf16>
@@ -449,7 +451,8 @@ constexpr int kRoundStrips = 8;  // strips of a warp in a round of a group of 16
 // words of a warp's sums: [strip][value][token / 2][row], shifted by eight banks from warp to warp
 constexpr int kRedWarp = kRoundStrips * 4 * 16 + 8;
 
-// Fragments of x of a stage, and its sums over the groups: a product with ones (in the units of the codes). With
+// Fragments of x of a stage, and its sums over the groups: a product with ones, into the units of the totals (ones in
+// the units of the codes, subnormals, lost ten bits of the sum, which the zero-point multiplies). With
 // one pair of strips all columns are loaded (the ragged layer 17.5 -> 17.0 us), with two the ones behind an item's
 // tokens are zeros (16 tokens 62.6 -> 60.0: their rows' lines cost more than the selection).
 __device__ __forceinline__ void load_x(const uint32_t* row, bool on, uint32_t (&b)[8][2]) {
@@ -466,8 +469,8 @@ __device__ __forceinline__ void sum_x(const uint32_t (&b)[8][2], float (&sum)[NG
     float part[4] = {};
 #pragma unroll
     for (int q = 0; q < 8 / NG; ++q) mma<kBf16>(part, ones, b[j * (8 / NG) + q][0], b[j * (8 / NG) + q][1]);
-    sum[j][0] = part[0];
-    sum[j][1] = part[1];
+    sum[j][0] = part[0] * kUnit<kBf16>;
+    sum[j][1] = part[1] * kUnit<kBf16>;
   }
 }
 
