@@ -117,3 +117,20 @@ def test_a_kernel_reads_what_its_launch_has(run):
     assert len(forms) > 20
     for kinds in forms:
         assert len(kinds) == 1 and kinds[0][1] == kinds[0][2] == kinds[0][3], kinds
+
+
+def test_a_devices_plan_is_its_own(run):
+    """The plan for a few tokens (how many CTAs share a sum, and so its order) does not change when another device,
+    on which fewer clusters fit, is used for the first time."""
+    seen = run("""
+        shapes = [(1, 2048, 704, 128, 8, 64, 64), (16, 2048, 704, 128, 8, 64, 64), (22, 512, 256, 200, 8, 64, 64),
+                  (10, 2048, 1408, 64, 4, 64, 64)]
+        room[0], room[1] = 152, 24
+        first = [few(*s) for s in shapes]
+        device.value = 1
+        other = [few(*s) for s in shapes]
+        device.value = 0
+        print(json.dumps([first, other, [few(*s) for s in shapes]]))
+    """)
+    first, other, again = seen
+    assert first != other and again == first

@@ -46,6 +46,7 @@ struct DeviceState {
   bool ready = false;
   moe_w4a16_status status = MOE_W4A16_OK;
   int num_sms = 0;
+  moe::FewClusters few_clusters = {};
 };
 constexpr int kMaxDevices = 64;
 DeviceState g_dev[kMaxDevices];
@@ -69,7 +70,7 @@ moe_w4a16_status device_state(const DeviceState** out) {
       st.num_sms = sms;
       st.status = (moe::init_gemm_kernels() == cudaSuccess && moe::init_block_kernels() == cudaSuccess &&
                    moe::init_linear_kernels() == cudaSuccess && moe::init_linear_small_kernels() == cudaSuccess &&
-                   moe::init_few_kernels() == cudaSuccess)
+                   moe::init_few_kernels(st.few_clusters) == cudaSuccess)
                       ? MOE_W4A16_OK
                       : MOE_W4A16_ERR_CUDA;
     }
@@ -83,10 +84,11 @@ moe_w4a16_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_W4A1
 
 }  // namespace
 
-moe_w4a16_status moe::current_device(int* num_sms) {
+moe_w4a16_status moe::current_device(int* num_sms, const FewClusters** clusters) {
   const DeviceState* dev = nullptr;
   const moe_w4a16_status st = device_state(&dev);
   if (st == MOE_W4A16_OK) *num_sms = dev->num_sms;
+  if (st == MOE_W4A16_OK && clusters) *clusters = &dev->few_clusters;
   return st;
 }
 

@@ -58,9 +58,10 @@ moe_w4a16_status moe_w4a16_few(const moe_w4a16_shape* shape, int32_t type, const
     return MOE_W4A16_ERR_ALIGN;
   if (workspace_bytes < moe::few_ws_bytes(s)) return MOE_W4A16_ERR_WORKSPACE;
   int sms = 0;
-  if ((st = moe::current_device(&sms)) != MOE_W4A16_OK) return st;
+  const moe::FewClusters* clusters = nullptr;
+  if ((st = moe::current_device(&sms, &clusters)) != MOE_W4A16_OK) return st;
   return cuda_status(moe::launch_few(s, type, x, logits, weights->gate_up, weights->down, residual, topk_idx, topk_w,
-                                     out, workspace, sms, static_cast<cudaStream_t>(stream)));
+                                     out, workspace, sms, *clusters, static_cast<cudaStream_t>(stream)));
 }
 
 moe_w4a16_status moe_w4a16_norm(const moe_w4a16_norm_cfg* cfg, const void* x, const void* y, const float* gamma_post,

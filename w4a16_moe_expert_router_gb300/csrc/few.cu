@@ -888,7 +888,6 @@ constexpr int kUpStatic = sizeof(Routing) + kUpWarps * kRedWarp * 4 + 64;
 constexpr int kDownStatic = sizeof(Routing) + 64;
 static_assert(kUpDepth<2> * 2 * kUpWarps * 2 * (1024 + 64 * 4) <= kSmemLimit - kUpStatic, "groups of 32");
 static_assert(kScratchBytes <= 2 * 2 * 1088, "the smallest rings hold what the choice of one token takes");
-int g_clusters[9];  // clusters of so many CTAs of the down kernel that run at a time
 
 using Kernel = void (*)(Args);
 template <bool kBf16, int kPairs, bool kBeside>
@@ -943,7 +942,7 @@ static cudaError_t set_up(Kernel k, int smem) {
   return e;
 }
 
-cudaError_t init_few_kernels() {
+cudaError_t init_few_kernels(FewClusters& clusters) {
   cudaError_t e = cudaSuccess;
   for (int type = 0; type < 2; ++type)
     for (int g : {32, 64, 128}) {
@@ -954,14 +953,14 @@ cudaError_t init_few_kernels() {
     }
   for (int c = 1; c <= 8 && e == cudaSuccess; ++c) {
     const DownLaunch l(1, c, 18 * 32, 128 * 1024, nullptr);
-    e = cudaOccupancyMaxActiveClusters(&g_clusters[c], down_of(0, 64), &l.cfg);
+    e = cudaOccupancyMaxActiveClusters(&clusters[c], down_of(0, 64), &l.cfg);
   }
   return e;
 }
 
 cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logits, const uint8_t* w_gate_up,
                        const uint8_t* w_down, const void* residual, int32_t* topk_idx, float* topk_w, void* out,
-                       void* workspace, int num_sms, cudaStream_t st) {
+                       void* workspace, int num_sms, const FewClusters& clusters, cudaStream_t st) {
   const int pairs = int(s.pairs());
   Args a{};
   a.x = x;
@@ -988,7 +987,7 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   int rounds = 1;
   double least = 1e30;
   for (int c = 1; c <= std::min(down_count, 8); ++c) {
-    const int at_a_time = std::max(g_clusters[c], 1), r = (down_count + c - 1) / c;
+    const int at_a_time = std::max(clusters[c], 1), r = (down_count + c - 1) / c;
     int n = 2;
     while (n < 2 * kDownMaxPairs && (strips + n - 1) / n > at_a_time) n += 2;
     const int tiles = (strips + n - 1) / n;
@@ -1006,7 +1005,7 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   const double items = s.E * (1.0 - std::pow(1.0 - double(s.k) / s.E, s.T));
   a.parts = 1;
   for (int p = 2; a.strips == 2 && p <= 8 / a.stage_ranks && items >= kDownWarps * p; ++p)
-    if ((strips + 1) / 2 <= g_clusters[a.stage_ranks * p]) a.parts = p;
+    if ((strips + 1) / 2 <= clusters[a.stage_ranks * p]) a.parts = p;
   a.cluster = a.stage_ranks * a.parts;
   const int slot = 2 * (1024 + 64 * (kStageCols / s.g2)), fixed = pairs * (kPairBytes + kStageCols / s.g2 * 4);
   const auto room = [&](int limit, int warps) {  // pieces of a warp that fit

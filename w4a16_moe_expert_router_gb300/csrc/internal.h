@@ -252,13 +252,14 @@ cudaError_t launch_clip(const moe_w4a16_tensor* tensors, int n, double max_norm,
 // The whole layer for a few tokens (few.cu).
 constexpr int kFewTokens = 32;
 size_t few_ws_bytes(const Dims& s);
-cudaError_t init_few_kernels();
+using FewClusters = int[9];  // a device's clusters of 1..8 CTAs of the down launch that run at a time
+cudaError_t init_few_kernels(FewClusters& clusters);
 cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logits, const uint8_t* w_gate_up,
                        const uint8_t* w_down, const void* residual, int32_t* topk_idx, float* topk_w, void* out,
-                       void* workspace, int num_sms, cudaStream_t st);
+                       void* workspace, int num_sms, const FewClusters& clusters, cudaStream_t st);
 
-// The current device's state: MOE_W4A16_OK with its SM count, or why it cannot be used.
-moe_w4a16_status current_device(int* num_sms);
+// The current device's state: MOE_W4A16_OK with its SM count (and its clusters), or why it cannot be used.
+moe_w4a16_status current_device(int* num_sms, const FewClusters** clusters = nullptr);
 
 // Self-test of the expert launch's bounded waits: waits that cannot complete (an
 // mbarrier phase, then the counter *flag, which must stay 0) give up after limit_ns
