@@ -76,14 +76,21 @@ __device__ __forceinline__ float value(const void* p, int64_t i) {
   if constexpr (kType == 2) return static_cast<const float*>(p)[i];
   else return from16<kType>(static_cast<const uint16_t*>(p)[i]);
 }
+// max_norm / norm, in two parts where the quotient is below fp32's normal range (a bound of 1e-3 on a norm of 1e37): as a
+// number of its own it would have lost digits, or be zero, where its products with the values are not.
+struct Factor {
+  float first, second;
+  __device__ __forceinline__ bool one() const { return first == 1.f; }
+  __device__ __forceinline__ float of(float v) const { return v * first * second; }
+};
 template <int kType>
-__device__ __forceinline__ void put_scaled(const Entry& e, int64_t i, float factor) {
+__device__ __forceinline__ void put_scaled(const Entry& e, int64_t i, Factor factor) {
   if constexpr (kType == 2) {
     const float v = static_cast<const float*>(e.data)[i];
-    static_cast<float*>(e.out)[i] = factor != 1.f ? v * factor : v;
+    static_cast<float*>(e.out)[i] = factor.one() ? v : factor.of(v);
   } else {
     const uint16_t v = static_cast<const uint16_t*>(e.data)[i];
-    static_cast<uint16_t*>(e.out)[i] = factor != 1.f ? to16<kType>(from16<kType>(v) * factor) : v;
+    static_cast<uint16_t*>(e.out)[i] = factor.one() ? v : to16<kType>(factor.of(from16<kType>(v)));
   }
 }
 
@@ -187,17 +194,17 @@ __device__ __forceinline__ double cta_sum(double v) {
 }
 
 template <int kType>
-__device__ void scale_chunk(const Entry& e, int chunk, float factor) {
+__device__ void scale_chunk(const Entry& e, int chunk, Factor factor) {
   constexpr int N = Vec<kType>::n, kBatch = 4;
   const Chunk<kType> c(e, chunk);
   auto* const dst = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(e.out) & ~uintptr_t(15)) +
                     static_cast<int64_t>(chunk) * (kThreads * kLoads);
   const auto scaled = [&](uint4 x) {
-    if (factor != 1.f) {  // else the bits are copied, a NaN's too
+    if (!factor.one()) {  // else the bits are copied, a NaN's too
       float f[N];
       Vec<kType>::load(x, f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) f[i] *= factor;
+      for (int i = 0; i < N; ++i) f[i] = factor.of(f[i]);
       x = Vec<kType>::store(f);
     }
     return x;
@@ -259,12 +266,12 @@ __device__ __forceinline__ double run_square(const Table<kTable>& t, int c0, int
 }
 // The run scaled, from its last chunk back: what the pass before read last is still in L2.
 template <int kTable>
-__device__ __forceinline__ void run_scale(const Table<kTable>& t, int c0, int c1, float factor) {
+__device__ __forceinline__ void run_scale(const Table<kTable>& t, int c0, int c1, Factor factor) {
   int i = c0 < c1 ? find(t, c1 - 1) : 0;
   for (int c = c1 - 1; c >= c0; --c) {
     while (t.first[i] > c) --i;
     const Entry& e = t.e[i];
-    if (!e.out || (factor == 1.f && e.out == e.data)) continue;
+    if (!e.out || (factor.one() && e.out == e.data)) continue;
     const int k = c - t.first[i];
     if (e.type == 0)
       scale_chunk<0>(e, k, factor);
@@ -275,10 +282,12 @@ __device__ __forceinline__ void run_scale(const Table<kTable>& t, int c0, int c1
   }
 }
 // The factor, from the sum of the squares; a norm that is no number, or infinite, leaves the values as they are.
-__device__ __forceinline__ float factor_of(double square, float max_norm, float* norm) {
+__device__ __forceinline__ Factor factor_of(double square, float max_norm, float* norm) {
   const float v = root(square);
   if (norm) *norm = v;
-  return v > max_norm && v < INFINITY ? max_norm / v : 1.f;
+  if (!(v > max_norm && v < INFINITY)) return Factor{1.f, 1.f};
+  const float q = max_norm / v;
+  return q < FLT_MIN ? Factor{max_norm * 0x1p126f / v, 0x1p-126f} : Factor{q, 1.f};  // (max_norm is below 4 then)
 }
 
 template <int kTable>
@@ -307,7 +316,7 @@ template <int kTable>
 __global__ void __launch_bounds__(kThreads, 4)
     clip_scale_kernel(const __grid_constant__ Table<kTable> t, const double* partial, int n_partial, float max_norm,
                       bool copies, float* norm) {
-  __shared__ float shared_factor;
+  __shared__ Factor shared_factor;
   grid_dependents_launch();
   grid_dependency_wait();
   if (threadIdx.x < 32) {
@@ -323,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (threadIdx.x == 0) shared_factor = factor_of(sum, max_norm, blockIdx.x == 0 ? norm : nullptr);
   }
   __syncthreads();
-  const float factor = shared_factor;
-  if (factor == 1.f && !copies) return;
+  const Factor factor = shared_factor;
+  if (factor.one() && !copies) return;
   const int chunks = t.first[t.n];
   run_scale(t, share(chunks, blockIdx.x), share(chunks, blockIdx.x + 1), factor);
 }
@@ -334,7 +343,7 @@ constexpr int kCluster = 8, kClusterChunks = 16;
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     clip_cluster_kernel(const __grid_constant__ Table<kSmall> t, float max_norm, float* norm) {
   __shared__ double sum;
-  __shared__ float shared_factor;
+  __shared__ Factor shared_factor;
   grid_dependents_launch();
   grid_dependency_wait();
   const int chunks = t.first[t.n], c0 = share(chunks, blockIdx.x), c1 = share(chunks, blockIdx.x + 1);
