@@ -36,6 +36,13 @@ cudaError_t cudaOccupancyMaxActiveClusters(int *n, const void *f, const cudaLaun
     if (c->attrs[i].id == cudaLaunchAttributeClusterDimension) *n = fake_room[fake_device] / c->attrs[i].val.clusterDim.x;
   return cudaSuccess;
 }
+struct { const void *kernel; const char *name; } fake_kernels[1024];  /* what the library registers when it is loaded */
+int fake_registered = 0;
+void __cudaRegisterFunction(void **h, const char *kernel, char *d, const char *name, int limit, void *t, void *b, void *bd,
+                            void *gd, int *w) {
+  fake_kernels[fake_registered].kernel = kernel;
+  fake_kernels[fake_registered++].name = name;
+}
 cudaError_t cudaGetLastError(void) { return cudaSuccess; }
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *c, const void *f, void **args) {
   launch_t *l = &fake_launches[fake_count++ % 64];
@@ -75,6 +82,12 @@ def few(*shape):
 def norm(R, d, typ, gate_rows, x, y, post, gate, pre, out, u):
     cfg = B.make_norm(R, d, typ, gate_rows)
     return launches(lambda: lib.moe_w4a16_norm(ctypes.byref(cfg), x, y, post, gate, pre, out, u, None))
+
+def kernels(part):  # of one of the library's files, by the name that the compiler gave them
+    class Kernel(ctypes.Structure):
+        _fields_ = [("kernel", ctypes.c_void_p), ("name", ctypes.c_char_p)]
+    n = ctypes.c_int.in_dll(fake, "fake_registered").value
+    return {k.kernel: k.name.decode() for k in (Kernel * 1024).in_dll(fake, "fake_kernels")[:n] if part in k.name.decode()}
 """
 
 
@@ -134,3 +147,27 @@ def test_a_devices_plan_is_its_own(run):
     """)
     first, other, again = seen
     assert first != other and again == first
+
+
+def test_every_kernel_of_the_norms_is_reached(run):
+    """What norm.cu builds and what some call of its two operators launches is the same."""
+    built, left = run("""
+        reached = set()
+        for R in (1, 700, 5000):
+            for d in (8, 264, 520, 1000, 1344, 2048, 2056, 4104, 8192):
+                for typ in (0, 1, 2):
+                    for gate_rows in (1, 7, R):
+                        cfg = B.make_norm(R, d, typ, gate_rows)
+                        for post, gate, pre, out, y, x in ((i & 1, i & 2, i & 4, i & 8, i & 16, i & 32) for i in range(64)):
+                            w = lambda v: P if v else None
+                            if (y or x and not post and not gate) and (out or pre):
+                                reached |= {l.kernel for l in norm(R, d, typ, gate_rows, w(x), w(y), w(post), w(gate), w(pre),
+                                                                   w(out), w(pre))}
+                            if y or not post and not gate:
+                                reached |= {l.kernel for l in launches(lambda: lib.moe_w4a16_norm_backward(
+                                    ctypes.byref(cfg), w(y), w(post), w(gate), P, w(pre), P, w(pre), w(x or not pre), w(y), w(post),
+                                    w(gate), w(pre), P, 1 << 40, None))}
+        built = kernels("norm_cu")
+        print(json.dumps([len(built), sorted(name for k, name in built.items() if k not in reached)]))
+    """)
+    assert built > 100 and left == []

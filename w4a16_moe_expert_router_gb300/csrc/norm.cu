@@ -716,9 +716,11 @@ int fitting(int registers, int threads, size_t smem) {
   return std::max(std::min({warps / (threads / 32), 226 * 1024 / (int(smem) + 2048), 4}), 1);
 }
 
-template <int kType, int kPieces, int kDepth>
+// kGates: with a gate row per row, without, or either.
+enum { kNeverByRow, kAlwaysByRow, kMaybeByRow };
+template <int kType, int kPieces, int kDepth, int kGates>
 cudaError_t forward(Args a, cudaStream_t st) {
-  const bool by_row = a.gate && a.gate_rows == 1;
+  const bool by_row = kGates == kMaybeByRow ? a.gate && a.gate_rows == 1 : kGates == kAlwaysByRow;
   GroupShape g = group_shape(a.R, a.nvec, kPieces, INT32_MAX);
   const int threads = g.group * g.groups;
   const size_t smem = size_t(kDepth) * (2 + (by_row ? kType == 2 ? 1 : 2 : 0)) * kPieces * threads * 16;
@@ -729,25 +731,29 @@ cudaError_t forward(Args a, cudaStream_t st) {
   a.group = g.group;
   a.units = g.units;
   static std::atomic<uint64_t> room[6];
-  if (!a.y)
-    return a.u ? launch(norm_kernel<kType, kPieces, kDepth, false, true, false>, room[0], g, smem, st, a)
-               : launch(norm_kernel<kType, kPieces, kDepth, false, false, false>, room[5], g, smem, st, a);
-  if (by_row)
-    return a.u ? launch(norm_kernel<kType, kPieces, kDepth, true, true, true>, room[1], g, smem, st, a)
-               : launch(norm_kernel<kType, kPieces, kDepth, true, false, true>, room[2], g, smem, st, a);
-  return a.u ? launch(norm_kernel<kType, kPieces, kDepth, true, true, false>, room[3], g, smem, st, a)
-             : launch(norm_kernel<kType, kPieces, kDepth, true, false, false>, room[4], g, smem, st, a);
+  if constexpr (kGates != kNeverByRow)
+    if (by_row)
+      return a.u ? launch(norm_kernel<kType, kPieces, kDepth, true, true, true>, room[0], g, smem, st, a)
+                 : launch(norm_kernel<kType, kPieces, kDepth, true, false, true>, room[1], g, smem, st, a);
+  if constexpr (kGates != kAlwaysByRow) {
+    if (!a.y)
+      return a.u ? launch(norm_kernel<kType, kPieces, kDepth, false, true, false>, room[2], g, smem, st, a)
+                 : launch(norm_kernel<kType, kPieces, kDepth, false, false, false>, room[3], g, smem, st, a);
+    return a.u ? launch(norm_kernel<kType, kPieces, kDepth, true, true, false>, room[4], g, smem, st, a)
+               : launch(norm_kernel<kType, kPieces, kDepth, true, false, false>, room[5], g, smem, st, a);
+  }
 }
 // Pieces per thread: four, where there are rows enough (a barrier less often), two where four would leave a fifth of
 // the threads without columns (8000 rows of 1344 bf16 columns 15.8 -> 14.6 us), one where latency counts.
 template <int kType>
 cudaError_t forward(const Args& a, cudaStream_t st) {
-  if (a.nvec <= 32 || (a.nvec <= 512 && a.R <= 4 * kNormSms)) return forward<kType, 1, 3>(a, st);
+  if (a.nvec <= 32 || (a.nvec <= 512 && a.R <= 4 * kNormSms)) return forward<kType, 1, 3, kMaybeByRow>(a, st);
   const bool by_row = a.gate && a.gate_rows == 1;  // the ring holds the gate too
   const bool full = 4 * ((a.nvec + 127) / 128 * 128) <= 5 * a.nvec;
-  if ((a.nvec <= 256 && !full) || (by_row && a.nvec <= 1024)) return forward<kType, 2, 3>(a, st);
-  if (kType == 2 && by_row) return forward<2, 4, 2>(a, st);
-  return forward<kType, 4, 3>(a, st);
+  if ((a.nvec <= 256 && !full) || (by_row && a.nvec <= 1024)) return forward<kType, 2, 3, kMaybeByRow>(a, st);
+  if constexpr (kType == 2)  // (rows of 16 bits have 1024 pieces at most)
+    if (by_row) return forward<2, 4, 2, kAlwaysByRow>(a, st);
+  return forward<kType, 4, 3, kNeverByRow>(a, st);
 }
 
 // Rows of a ring: with four tensors four rows of one piece, three of two (two with the gates) and one of four (a row of
