@@ -454,8 +454,12 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_linear_backward(const moe_w4a16_linear_
  *   out[t] = residual[t] + sum over the k chosen experts of w[t][r] Wd gelu(Wg x) (Wu x)
  * with the choice and the weights of moe_w4a16_route (bit for bit).  The codes are multiplied
  * as they are and a group's scale and second value applied to its fp32 sum, h is kept in two
- * values of the type (22 bits for fp16, 16 for bf16; its range is the type's), everything else in
- * fp32, rounded once.  A token's output does not depend on the other tokens.
+ * values of the type (22 bits or 2^-25 for fp16, 16 bits for bf16), everything else in fp32,
+ * rounded once.  h's range is the type's: a value beyond it leaves its token's output without
+ * numbers.  A token's output does not depend on the other tokens.
+ *   For fp16 tokens there are two ways to the same layer.  This call is the faster one up to about
+ * 128 pairs (tokens x top_k; 64 where d and f are twice 2048 and 704); with more, moe_w4a16_route and
+ * moe_w4a16_forward are, which unpack an expert once for up to 16 of its tokens, this call for four.
  *   shape       as for the layer, tokens 0..MOE_W4A16_FEW_TOKENS (ERR_SHAPE above); `reduction`
  *               has no effect
  *   type        MOE_W4A16_FP16 or _BF16: type of x, residual and out
@@ -479,7 +483,9 @@ MOE_W4A16_API moe_w4a16_status moe_w4a16_few(const moe_w4a16_shape* shape, int32
  *   v   = gamma_post y / sqrt(mean(y^2) + eps)          (gamma_post NULL: v = y)
  *   out = residual_scale x + gate v                     (gate NULL: ones; x NULL: no residual)
  *   u   = gamma_pre out / sqrt(mean(out^2) + eps)
- * in fp32 from load to store (u is the norm of out before its rounding).
+ * in fp32 from load to store (u is the norm of out before its rounding).  A row's sum of squares has
+ * to stay in fp32's range: above it (rows of about 1e19 / sqrt(d)) the norm is zero, and without eps
+ * rows below 1e-19 have none.
  *   rows            R, 0..2^22
  *   hidden          d, a multiple of 8, 8..8192
  *   type            MOE_W4A16_FP16, _BF16 or _FP32: type of the rows

@@ -617,7 +617,9 @@ def moe_w4a16_clip_workspace_bytes(tensors) -> int:
 
 
 def moe_w4a16_clip(tensors, max_norm: float, norm, workspace, stream=None) -> None:
-    """tensors: a TensorList, or tensors to be scaled in place.  max_norm may be math.inf: the norm alone."""
+    """tensors: a TensorList, or tensors to be scaled in place.  max_norm may be math.inf: the norm alone.
+    Plain tensors are checked in every call, which takes about 1 us each on the host (400 of them 450 us, the call
+    with a TensorList 10); a program that clips the same gradients in every step keeps a list (make_tensors)."""
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors, None)
     _, _, f32, device, current = _CONTEXT or _context()

@@ -13,8 +13,9 @@
 // there on: an fp64 addition per element would be the bound (its rate is a hundredth of fp32's), one
 // per chunk is not seen. Where such a sum leaves the range in which fp32 squares keep their digits,
 // it is taken again in fp64. All orders are fixed: the same bits in every run.
-// Measured: 554 million bf16 values from one place to another 516 us (3.3 GB in the two passes, 6.5 TB/s);
-// 400 tensors of 47 MB in all below the bound 13.4 us; five small ones 4.9 us, of which a launch is the most.
+// Measured: 554 million bf16 values from one place to another 509 us (3.3 GB in the two passes, 6.5 TB/s), in
+// place 518; 400 tensors of 47 MB in all below the bound 13.9 us, above it in place 15.3; five small ones 5.2 us, of which
+// a launch is the most.
 #include <cfloat>
 #include <climits>
 #include <cmath>

@@ -12,18 +12,20 @@
 //    memory does not fit beside the other's, or its warps there are too few; it gets the lists then);
 //  - the contraction is shared by the warps of a CTA (gate_up) or by the CTAs of a cluster (down);
 //    each warp streams its own stages with cp.async, some ahead, also across work items.
-// Measured in a replayed graph: 1 token 13.3 us (1.5 TB/s), 4 tokens of bf16 33.0 (2.1), 16 tokens 58.1 (3.5).
+// Measured in a replayed graph over the weights of as many layers as exceed L2: 1 token 14.1 us (1.4 TB/s), 4 tokens of
+// bf16 34.2 (2.0), 16 tokens 62.1 (3.2); one layer's again and again, from L2, 13.7, 32.1 and 62.7.
 // One token is bound by the chain routing 2.0 us, first weights 2.3, products 2, the way to the down
-// launch 0.9, its h, products and sums 3.5; sixteen by the issue of instructions (some 180 to take a
-// 16 x 128 strip of codes through, a third of them masks and shifts of the codes) and by the parts
-// in which no weights move: routing 3.8, the lists' way 1.5, both ends' sums 4.
+// launch 0.9, its h, products and sums 3.5. Sixteen are bound by the latency of the chain from a stage's arrival over its
+// loads from shared memory, the unpacking and the matrix instructions to the groups' scales, which four warps a scheduler
+// do not hide (issue slots 42 and 39 %, memory at half its rate), and by the parts in which no weights move: routing 3.8,
+// the lists' way 1.5, both ends' sums 4.
 //
-// The weights stay integers: a group's codes are multiplied as they are (exact products in the fp32
-// accumulators), then scale and zero-point are applied to the group's sum,
+// The weights stay integers: a group's codes are multiplied as they are (exact products, summed in the fp32
+// accumulators to 2^-23 of a group's sum), then scale and zero-point are applied to the group's sum,
 //   sum_k w_k x_k = s sum_k q_k x_k + c sum_k x_k,   c = -s z (affine: the bias).
 // The sums of x come from one more matrix instruction with ones for two or four strips, the sums of h
 // from the gate_up launch. h is kept as two 16-bit values, h = hi + lo, which take two columns of
-// one instruction (four tokens per instruction, not eight): 22 bits of h for fp16, 16 for bf16. Every
+// one instruction (four tokens per instruction, not eight): 22 bits of h for fp16 (or 2^-25), 16 for bf16. Every
 // sum has an order of its own (stages, then warps or CTAs in their order; a token's experts in rank
 // order), so the result does not depend on the other tokens and is the same in every run.
 #include <algorithm>
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kUpThreads, kBeside ? 2 : 1) few_gate_up_kerne
     struct Place {
       int unit, item, group;
     };
-    Place put{unit0, static_cast<int>((unit0 + 0.5f) * a.per_item_inv), 0}, got;  // exact: below 2^14
+    Place put{unit0, static_cast<int>((unit0 + 0.5f) * a.per_item_inv), 0}, got;  // exact: at most 2^8 items of 2^10 units
     put.group = unit0 - put.item * a.per_item;
     got = put;
     const auto step = [&](Place& p) {
@@ -1001,7 +1003,7 @@ cudaError_t launch_few(const Dims& s, int type, const void* x, const float* logi
   }
   // Where few strips and stages leave SMs without work, more CTAs share the items, as long as each of their warps has
   // one (8 tokens of top-3 lose 1.3 us to a larger cluster). Which experts meet is not known here; their number is
-  // about that of evenly chosen ones.
+  // about that of evenly chosen ones. (Where they have more than four tokens, there are more items than that.)
   const double items = s.E * (1.0 - std::pow(1.0 - double(s.k) / s.E, s.T));
   a.parts = 1;
   for (int p = 2; a.strips == 2 && p <= 8 / a.stage_ranks && items >= kDownWarps * p; ++p)

@@ -5,7 +5,7 @@
 //   out = scale x + gate v
 //   u   = gamma_pre out r2,  r2 = 1 / sqrt(mean out^2 + eps)
 // and backwards, with n = out r2, m = y r1 and means over a row's columns,
-//   g  = dout + r2 (gamma_pre du - n mean(n gamma_pre du))        dx = scale g
+//   g  = dout + r2 (gamma_pre du - n c),  c = mean(n gamma_pre du)        dx = scale g
 //   dv = gate g       dy = r1 (gamma_post dv - m mean(m gamma_post dv))
 //   dgamma_pre = sum du n,  dgamma_post = sum dv m,  dgate = sum g v  (over the rows they are shared by)
 //
@@ -19,7 +19,7 @@
 // The arithmetic is fp32 from load to store, on pairs (the gradient spent 53 instructions an element, 63 %
 // of the issue slots, one value at a time); u is the norm of the unrounded out.
 // Measured: 16384 rows of 2048 bf16 columns with both norms and a gate 48.9 us (5.5 TB/s), their gradient
-// 71 us (5.6 TB/s, 45 instructions an element); one row 2.1 us.
+// 72.9 us (5.5 TB/s, 46 instructions an element); one row 2.3 us.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const Args a) {
 // ---------------------------------------------------------------- backward
 //
 // What the gradient needs of a whole row is linear in sums that the loaded values give at once,
-//   mean(m gamma_post dv) = r1 / d (sum w y dout + r2 sum w y (gamma_pre du) - r2^2 c sum w y out),
-//   w = gamma_post gate, c = mean(n gamma_pre du),
+//   mean(m gamma_post dv) = r1 / d (sum w y dout + r2 sum w y (gamma_pre du) - (r2 c) (r2 sum w y out)),
+//   w = gamma_post gate,
 // so six sums of a row go through one reduction and one barrier. The gate's and gamma_post's gradients
 // come from the same sum over the rows of a gate row, P = sum g m: dgate = gamma_post P, dgamma_post +=
 // gate P, held in registers over a unit like gamma_pre's.

@@ -108,7 +108,8 @@ def alloc_few(wl: Workload, tokens: int, type: int = 0, device="cuda") -> FewBuf
 
 def run_few(buf: FewBuffers, x: torch.Tensor, logits: torch.Tensor, w: PreparedWeights,
             residual: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """The whole layer (plus `residual`) for a few tokens, in two launches; returns the output tensor."""
+    """The whole layer (plus `residual`) for a few tokens, in two launches; returns the output tensor.  Of fp16 tokens
+    with more than about 128 pairs (tokens times top_k) ``run_layer`` is the faster one."""
     o = buf.out if out is None else out
     B.moe_w4a16_few(buf.shape, buf.type, x, logits, w.gate_up, w.down, residual, buf.topk_idx, buf.topk_w, o,
                     buf.workspace, stream)
@@ -274,7 +275,7 @@ class Block16:
         return out
 
     def clip(self, grads, max_norm: float, stream=None) -> torch.Tensor:
-        """Scales a step's gradients (tensors, or a list from B.make_tensors) down to `max_norm` over all of them;
-        returns their norm, a tensor of one element."""
+        """Scales a step's gradients (tensors, or a list from B.make_tensors, which spares some 1 us a tensor and call)
+        down to `max_norm` over all of them; returns their norm, a tensor of one element."""
         B.moe_w4a16_clip(grads, max_norm, self.grad_norm, self.ws, stream)
         return self.grad_norm
